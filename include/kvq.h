@@ -117,6 +117,8 @@ typedef int32_t kvq_status;
 #define KVQ_DEV_ERR_TIMEOUT       4u  /* a bounded wait on a shared-memory barrier gave up                 */
 #define KVQ_DEV_ERR_PAGE          8u  /* a page_table entry lies outside [0, n_pages) (paged layout)        */
 #define KVQ_DEV_ERR_OUTLIER      16u  /* an outlier_idx row is not strictly increasing inside [0, head_dim) */
+#define KVQ_DEV_ERR_NO_ROOM      32u  /* kvq_page_update: no free page or no row left for a sequence's tokens */
+#define KVQ_DEV_ERR_ROW          64u  /* kvq_qk_norm_rope: dst_row at or past n_dst_rows                       */
 
 /*
  * The cache descriptor.  Body planes hold the packed payload of every block:
@@ -350,6 +352,162 @@ KVQ_API kvq_status kvq_prefill_attention(const kvq_cache* c, const void* q, int3
                                  int32_t causal, int32_t chunk, float scale, void* out,
                                  int32_t out_dtype, void* workspace, size_t ws_bytes,
                                  void* stream);
+
+/*
+ * Norms of queries and keys per head and the position rotation, in one pass:
+ * from the rows of a projection to what kvq_rotate_quantize_append takes as k
+ * and v and the attention calls take as q.  Library addition: the pages
+ * describe the cache and its attention, not what stands before them.
+ * The plan (weights and frequencies; a caller keeps one per layer):
+ */
+typedef struct kvq_rope_norm {
+  int32_t rot_dim;        /* rotated channels of a head, the first ones: a multiple of 16 in [0, head_dim] */
+  int32_t interleaved;    /* 0: pairs (i, i + rot_dim/2); 1: pairs (2i, 2i + 1)                   */
+  float eps;              /* added to the mean square (>= 0)                                      */
+  int32_t weight_dtype;   /* KVQ_F32 / KVQ_BF16 / KVQ_F16 of the weights                          */
+  const void* q_weight;   /* device [head_dim], 16-byte aligned; NULL: queries are not normed     */
+  const void* k_weight;   /* the same for keys                                                    */
+  const float* inv_freq;  /* device fp32 [rot_dim / 2], 4-byte aligned: radians per position, |.| <= 1024
+                             (NULL only with rot_dim 0)                                           */
+} kvq_rope_norm;
+/*
+ *   q, k, v   device rows of `dtype`: head h of row r starts at element
+ *             r * stride + h * head_dim, so the three may be parts of one fused
+ *             projection.  16-byte aligned, strides in elements, a multiple of
+ *             16 bytes and at least heads * head_dim.  v and v_out may both be
+ *             NULL (no values to move).
+ *   pos       device int32 [n_rows]: each row's position, any int32
+ *   dst_row   device int32 [n_rows] or NULL (row r goes to row r; n_dst_rows is
+ *             then at least n_rows).  A negative entry leaves the row out; one
+ *             at or past n_dst_rows leaves it out and sets KVQ_DEV_ERR_ROW.  Of
+ *             rows with the same entry any one's heads may be found there.
+ *   q_out     device [n_dst_rows][n_q_heads][head_dim] of `dtype`
+ *   k_out, v_out  device [n_dst_rows][n_kv_heads][head_dim] of `dtype`
+ * Per head: y = x * 1/sqrt(mean(x^2) + eps) * weight (queries and keys with a
+ * weight only), then every pair (a, b) of the rotated channels becomes (a cos t
+ * - b sin t, a sin t + b cos t), t = pos * inv_freq[pair]; values are copied.
+ * All of it in fp32 -- the angle modulo one turn is exact to 2^-31 turns at
+ * every position -- and rounded once, to nearest even.  Rows of the outputs that no
+ * row goes to keep what they held.  An output may be its own input (same
+ * pointer, stride heads * head_dim, dst_row NULL); no other overlap is allowed.
+ * n_rows 0 is a no-op.  Of the cache only head_dim, n_kv_heads and status are
+ * used; head_dim: every multiple of 32 up to 512.
+ */
+KVQ_API kvq_status kvq_qk_norm_rope(const kvq_cache* c, const kvq_rope_norm* r, int32_t dtype, int32_t n_q_heads,
+                                    const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                    const void* v, int64_t v_stride, const int32_t* pos, const int32_t* dst_row,
+                                    int32_t n_rows, int32_t n_dst_rows, void* q_out, void* k_out, void* v_out,
+                                    void* stream);
+
+/*
+ * The page table and the row maps of a step, built on the GPU from what each
+ * sequence asks for.  Library addition beside the paged layout.
+ * The pool: a ring of page ids of which `count` from `head` on are free.
+ */
+typedef struct kvq_page_pool {
+  int32_t* ring;         /* device [n_pages]                                                */
+  const int32_t* state;  /* device [2]: head in [0, n_pages), count in [0, n_pages]          */
+  int32_t* next;         /* device [2]: the state after the call (may be `state` itself)     */
+} kvq_page_pool;
+#define KVQ_PAGE_RELEASE (-1)
+/*
+ *   n_new      device int32 [batch]: tokens sequence b is about to append, in
+ *              [0, n_new_max], or KVQ_PAGE_RELEASE: it is done, its pages go
+ *              back.  Any other value, or tokens that would pass max_ctx, sets
+ *              KVQ_DEV_ERR_APPEND_RANGE and counts as 0.
+ *   granted    device int32 [batch]: the tokens it may append (n_new or 0), to
+ *              be given to the append as n_new_per_seq.  Sequences are served
+ *              in order; the first that finds too few free pages (those free
+ *              before the call: released ones can be had from the next call
+ *              on) or too few rows gets nothing, as do all after it that need
+ *              any (a page, or a row), and KVQ_DEV_ERR_NO_ROOM is set.
+ *   c->page_table  is written at the new pages of granted tokens: pages
+ *              ceil(seq_len / page_tokens) on, in ring order.  Nothing else in
+ *              it changes; a released row keeps its entries, which mean nothing
+ *              once its length is 0.
+ *   Row maps (each device int32 [max_rows] or NULL): the new tokens of all
+ *   sequences in order are rows 0, 1, ...; token i of sequence b has position
+ *   row_pos = seq_len[b] + i, its row in a padded [batch][n_new_max] layout
+ *   row_dst = b * n_new_max + i, and its token slot in the pool row_slot = page *
+ *   page_tokens + position % page_tokens.  row_dst and row_slot are -1 where
+ *   nothing was granted, and on the rows behind the last token, whose row_pos is 0.
+ *   seq_len_out  device int32 [batch] or NULL: the lengths with released
+ *              sequences at 0 (may be c->seq_len itself, which is what a
+ *              serving loop wants).  Granted tokens are not added: the append
+ *              does that.
+ * A state outside its ranges sets KVQ_DEV_ERR_PAGE; nothing is granted or
+ * released then, and `next` gets the state as it was.  Requires the paged
+ * layout and batch * n_new_max < 2^31.  Uses status word 2 as a completion counter.
+ * Of the cache's planes only seq_len, status and page_table are touched.
+ */
+KVQ_API kvq_status kvq_page_update(const kvq_cache* c, const kvq_page_pool* pool, const int32_t* n_new,
+                                   int32_t n_new_max, int32_t* granted, int32_t max_rows, int32_t* row_pos,
+                                   int32_t* row_dst, int32_t* row_slot, int32_t* seq_len_out, void* stream);
+
+/*
+ * Sparse attention over blocks of a sequence: an index holds the mean key of
+ * every block of block_tokens positions, kvq_select_blocks ranks the blocks by
+ * it for each query, and kvq_sparse_decode_attention reads the selected ones
+ * only.  Library addition beside kvq_decode_attention, for long sequences.
+ * Requirements of all three: head_dim in {64, 128, 192, 256, 320}, n_outlier 0
+ * (else KVQ_ERR_UNSUPPORTED); block_tokens a multiple of 64, at most 65536.
+ * nblk = ceil(max_ctx / block_tokens).
+ */
+typedef struct kvq_block_index {
+  int32_t block_tokens;
+  int8_t* codes;   /* device [batch][n_kv_heads][nblk][head_dim], 16-byte aligned */
+  float* scales;   /* device [batch][n_kv_heads][nblk], 4-byte aligned            */
+} kvq_block_index;
+/*
+ * Brings the index up to date with the cache.
+ *   n_last  0: every block; else the blocks that hold any of the last n_last
+ *           tokens of a sequence (after an append of up to n_last tokens)
+ * For a block's tokens below seq_len[b], x_t = the dequantized rotated key of
+ * the body (which holds every token, those of the bf16 tail too): mean m = (sum
+ * of x_t) / count, scale = max |m| / 127, code = m / scale rounded to the nearest,
+ * half to even (all codes 0 with a scale of 0), in fp32 with this order of
+ * sums, so that the codes are the same wherever they are computed: token t of the
+ * block is added to partial sum t % 8 in token order; then s0+s1, s2+s3, s4+s5,
+ * s6+s7; (s0+s1)+(s2+s3), ...; the last two.  Blocks that hold no token keep what
+ * they held.  A page id outside the pool sets KVQ_DEV_ERR_PAGE; its tokens count
+ * as zeros.
+ */
+KVQ_API kvq_status kvq_block_index_update(const kvq_cache* c, const kvq_block_index* x, int32_t n_last, void* stream);
+/*
+ * The blocks that decode attention of q should read, per sequence and KV head.
+ *   q         device [batch][n_q_heads][head_dim] of q_dtype (unrotated), at most
+ *             128 query heads per KV head
+ *   n_first, n_last  blocks at a sequence's beginning and end that are always
+ *             selected (n_first + n_last <= n_select)
+ *   sel       device int32 [batch][n_kv_heads][n_select]: the selected blocks in
+ *             ascending order, -1 behind them.  A sequence of no more than
+ *             n_select blocks has them all.
+ * Of the other blocks those with the highest score are taken, on equal scores
+ * the lower ones: the query is rotated like the keys (channels paired at
+ * distance 1, 2, 4, ..., then times fp32(1/sqrt(G))), coded in 8 bits (scale sq =
+ * max |q'| / 127, code = q' / sq to the nearest, half to even), and score = max
+ * over the group's heads of fp32(fp32(dot * sq) * scale), dot the integer product
+ * of the codes.  Eight bits for the query as for the means: the score only ranks
+ * blocks, and integers make the ranking the same wherever it is computed.  A NaN
+ * score ranks last.  Requires nblk <= 49152 (take larger blocks for a longer
+ * max_ctx, else KVQ_ERR_UNSUPPORTED) and n_select in [1, 49152].
+ */
+KVQ_API kvq_status kvq_select_blocks(const kvq_cache* c, const kvq_block_index* x, const void* q, int32_t q_dtype,
+                                     int32_t n_q_heads, int32_t n_first, int32_t n_last, int32_t n_select,
+                                     int32_t* sel, void* stream);
+/*
+ * Decode attention over selected blocks: kvq_decode_attention with the softmax
+ * over the tokens of the listed blocks alone.
+ *   sel       device int32 [batch][n_kv_heads][n_select]: block numbers, in any
+ *             order; entries outside [0, ceil(seq_len / block_tokens)) are left
+ *             out, a block listed twice counts twice
+ *   q, out, scale  as in kvq_decode_attention (every K / V format pair, contiguous
+ *             or paged, positions of the last tail_len tokens from the bf16 tail)
+ * A (sequence, KV head) with no listed token yields zeros.  No workspace.
+ */
+KVQ_API kvq_status kvq_sparse_decode_attention(const kvq_cache* c, const void* q, int32_t q_dtype, int32_t n_q_heads,
+                                               float scale, int32_t block_tokens, const int32_t* sel,
+                                               int32_t n_select, void* out, int32_t out_dtype, void* stream);
 
 /*
  * Inspection of stored tokens (test aid): the stored blocks in the GGUF

@@ -11,6 +11,7 @@
 
 namespace {
 
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool valid_type(int t) { return t >= KVQ_TYPE_Q4_0 && t <= KVQ_TYPE_Q5_1; }
 bool has_qh(int t) { return t == KVQ_TYPE_Q5_0 || t == KVQ_TYPE_Q5_1; }
@@ -98,6 +99,19 @@ kvq_status resolve(const kvq_cache* c, kvq::Rot* r) {
   r->k = want_k;
   r->v = want_v;
   return KVQ_OK;
+}
+
+bool block_tokens_ok(int32_t bt) { return bt > 0 && bt % 64 == 0 && bt <= 65536; }
+// block index and sparse decode: the decode's head dims, without outlier channels
+bool sparse_supported(const kvq_cache* c) {
+  return c->n_outlier == 0 && kvq::decode_supported(c->head_dim, c->k_type, c->v_type, 0);
+}
+kvq_status check_index(const kvq_cache* c, const kvq_block_index* x) {
+  const kvq_status s = check_cache(c);
+  if (s != KVQ_OK) return s;
+  if (!x || !block_tokens_ok(x->block_tokens)) return KVQ_ERR_INVALID_ARG;
+  if (!x->codes || !x->scales || !aligned16(x->codes) || !aligned4(x->scales)) return KVQ_ERR_INVALID_ARG;
+  return sparse_supported(c) ? KVQ_OK : KVQ_ERR_UNSUPPORTED;
 }
 
 kvq_status from_cuda(cudaError_t e) { return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA; }
@@ -273,6 +287,109 @@ kvq_status kvq_prefill_attention(const kvq_cache* c, const void* q, int32_t q_dt
   const float sc = scale == 0.0f ? 1.0f / sqrtf(float(c->head_dim)) : scale;
   return from_cuda(kvq::launch_prefill(*c, r, q, q_dtype, n_q_heads, n_tokens, q_pos0, causal, sc, out, out_dtype,
                                        workspace, static_cast<cudaStream_t>(stream)));
+}
+
+kvq_status kvq_qk_norm_rope(const kvq_cache* c, const kvq_rope_norm* r, int32_t dtype, int32_t n_q_heads, const void* q,
+                            int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                            const int32_t* pos, const int32_t* dst_row, int32_t n_rows, int32_t n_dst_rows, void* q_out,
+                            void* k_out, void* v_out, void* stream) {
+  if (!shape_ok(c) || !r) return KVQ_ERR_INVALID_ARG;
+  if (!c->status || !aligned16(c->status)) return KVQ_ERR_INVALID_ARG;
+  const int d = c->head_dim;
+  if (r->rot_dim < 0 || r->rot_dim > d || r->rot_dim % 16 || (r->rot_dim && !r->inv_freq)) return KVQ_ERR_INVALID_ARG;
+  if (!valid_dtype(r->weight_dtype) || !(r->eps >= 0.0f) || r->eps > 1e30f) return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(r->q_weight) || !aligned16(r->k_weight) || !aligned4(r->inv_freq)) return KVQ_ERR_INVALID_ARG;
+  if (!valid_dtype(dtype) || n_q_heads <= 0 || n_q_heads > (1 << 20)) return KVQ_ERR_INVALID_ARG;
+  if (n_rows < 0 || n_dst_rows < 0 || (!dst_row && n_dst_rows < n_rows)) return KVQ_ERR_INVALID_ARG;
+  if (!v != !v_out) return KVQ_ERR_INVALID_ARG;
+  const int es = dtype == KVQ_F32 ? 4 : 2;
+  const void* in[] = {q, k, v};
+  void* out[] = {q_out, k_out, v_out};
+  const int64_t stride[] = {q_stride, k_stride, v_stride};
+  kvq::RopeArgs a{};
+  for (int i = 0; i < 3; ++i) {
+    const int64_t heads = i == 0 ? n_q_heads : c->n_kv_heads;
+    if (i == 2 && !v) break;
+    if (n_rows > 0 && (!in[i] || !out[i] || !aligned16(in[i]) || !aligned16(out[i]))) return KVQ_ERR_INVALID_ARG;
+    // offsets stay far below 2^62 bytes
+    if (stride[i] < heads * d || stride[i] > (int64_t(1) << 40) || stride[i] * es % 16) return KVQ_ERR_INVALID_ARG;
+    a.in[i] = in[i];
+    a.out[i] = out[i];
+    a.stride[i] = stride[i];
+  }
+  if (n_rows == 0) return KVQ_OK;
+  if (!pos || !aligned4(pos) || !aligned4(dst_row)) return KVQ_ERR_INVALID_ARG;
+  a.pos = pos; a.dst_row = dst_row;
+  a.n_rows = n_rows; a.n_dst_rows = n_dst_rows;
+  a.n_q_heads = n_q_heads; a.n_kv_heads = c->n_kv_heads; a.head_dim = d;
+  a.status = c->status;
+  return from_cuda(kvq::launch_qk_norm_rope(a, *r, dtype, static_cast<cudaStream_t>(stream)));
+}
+
+kvq_status kvq_page_update(const kvq_cache* c, const kvq_page_pool* pool, const int32_t* n_new, int32_t n_new_max,
+                           int32_t* granted, int32_t max_rows, int32_t* row_pos, int32_t* row_dst, int32_t* row_slot,
+                           int32_t* seq_len_out, void* stream) {
+  if (!shape_ok(c) || !pool || !c->page_tokens) return KVQ_ERR_INVALID_ARG;
+  if (!c->seq_len || !c->status || !c->page_table || !aligned16(c->seq_len) || !aligned16(c->status) ||
+      !aligned4(c->page_table))
+    return KVQ_ERR_INVALID_ARG;
+  const void* must[] = {pool->ring, pool->state, pool->next, n_new, granted};
+  for (const void* p : must)
+    if (!p || !aligned4(p)) return KVQ_ERR_INVALID_ARG;
+  if (!aligned4(row_pos) || !aligned4(row_dst) || !aligned4(row_slot) || !aligned4(seq_len_out)) return KVQ_ERR_INVALID_ARG;
+  if (n_new_max < 0 || max_rows < 0 || (long long)c->batch * n_new_max > 0x7fffffffLL) return KVQ_ERR_INVALID_ARG;
+  // a pool slot is an int32
+  if ((long long)c->n_pages * c->page_tokens > 0x7fffffffLL) return KVQ_ERR_INVALID_ARG;
+  kvq::PageArgs a{};
+  a.seq_len = c->seq_len; a.status = c->status;
+  a.table = const_cast<int32_t*>(c->page_table);
+  a.batch = c->batch; a.max_ctx = c->max_ctx; a.page_tokens = c->page_tokens; a.n_pages = c->n_pages;
+  a.pool = *pool;
+  a.n_new = n_new; a.n_new_max = n_new_max; a.max_rows = max_rows;
+  a.granted = granted; a.row_pos = row_pos; a.row_dst = row_dst; a.row_slot = row_slot; a.seq_len_out = seq_len_out;
+  return from_cuda(kvq::launch_page_update(a, static_cast<cudaStream_t>(stream)));
+}
+
+kvq_status kvq_block_index_update(const kvq_cache* c, const kvq_block_index* x, int32_t n_last, void* stream) {
+  kvq_status s = check_index(c, x);
+  if (s != KVQ_OK) return s;
+  if (n_last < 0) return KVQ_ERR_INVALID_ARG;
+  return from_cuda(kvq::launch_block_index_update(*c, *x, n_last, static_cast<cudaStream_t>(stream)));
+}
+
+kvq_status kvq_select_blocks(const kvq_cache* c, const kvq_block_index* x, const void* q, int32_t q_dtype,
+                             int32_t n_q_heads, int32_t n_first, int32_t n_last, int32_t n_select, int32_t* sel,
+                             void* stream) {
+  kvq_status s = check_index(c, x);
+  if (s != KVQ_OK) return s;
+  kvq::Rot r{};
+  if ((s = resolve(c, &r)) != KVQ_OK) return s;
+  if (!valid_dtype(q_dtype) || n_q_heads <= 0 || n_q_heads % c->n_kv_heads) return KVQ_ERR_INVALID_ARG;
+  if (!q || !aligned16(q) || !sel || !aligned4(sel)) return KVQ_ERR_INVALID_ARG;
+  if (n_first < 0 || n_last < 0 || n_select < 1 || (long long)n_first + n_last > n_select) return KVQ_ERR_INVALID_ARG;
+  if (n_q_heads / c->n_kv_heads > 128 || n_select > kvq::kMaxIndexBlocks ||
+      (c->max_ctx + (long long)x->block_tokens - 1) / x->block_tokens > kvq::kMaxIndexBlocks)
+    return KVQ_ERR_UNSUPPORTED;
+  return from_cuda(kvq::launch_select_blocks(*c, r, *x, q, q_dtype, n_q_heads, n_first, n_last, n_select, sel,
+                                             static_cast<cudaStream_t>(stream)));
+}
+
+kvq_status kvq_sparse_decode_attention(const kvq_cache* c, const void* q, int32_t q_dtype, int32_t n_q_heads, float scale,
+                                       int32_t block_tokens, const int32_t* sel, int32_t n_select, void* out,
+                                       int32_t out_dtype, void* stream) {
+  kvq_status s = check_cache(c);
+  if (s != KVQ_OK) return s;
+  kvq::Rot r{};
+  if ((s = resolve(c, &r)) != KVQ_OK) return s;
+  if (!block_tokens_ok(block_tokens) || n_select < 0) return KVQ_ERR_INVALID_ARG;
+  if (!valid_dtype(q_dtype) || !valid_dtype(out_dtype)) return KVQ_ERR_INVALID_ARG;
+  if (n_q_heads <= 0 || n_q_heads % c->n_kv_heads || n_q_heads / c->n_kv_heads > 4096) return KVQ_ERR_INVALID_ARG;
+  if (!q || !out || !aligned16(q) || !aligned16(out) || (n_select && !sel) || !aligned4(sel)) return KVQ_ERR_INVALID_ARG;
+  if (!(scale >= 0.0f) || scale > 1e30f) return KVQ_ERR_INVALID_ARG;
+  if (!sparse_supported(c)) return KVQ_ERR_UNSUPPORTED;
+  const float sc = scale == 0.0f ? 1.0f / sqrtf(float(c->head_dim)) : scale;
+  return from_cuda(kvq::launch_sparse_decode(*c, r, q, q_dtype, n_q_heads, sc, block_tokens, sel, n_select, out,
+                                             out_dtype, static_cast<cudaStream_t>(stream)));
 }
 
 kvq_status kvq_dequant_debug(const kvq_cache* c, int32_t seq, int32_t kv_head, int32_t which, int32_t t0,

@@ -127,4 +127,41 @@ cudaError_t launch_prefill(const kvq_cache& c, Rot rot, const void* q, int q_dty
                            const int32_t* q_pos0, int causal, float scale, void* out, int out_dtype,
                            void* ws, cudaStream_t st);
 
+// Norms and position rotation of query / key rows (kvq_qk_norm_rope).
+struct RopeArgs {
+  const void* in[3];        // q, k, v rows (v may be NULL)
+  long long stride[3];      // elements between rows
+  void* out[3];
+  const int32_t* pos;
+  const int32_t* dst_row;   // may be NULL
+  int n_rows, n_dst_rows, n_q_heads, n_kv_heads, head_dim;
+  uint32_t* status;
+};
+cudaError_t launch_qk_norm_rope(const RopeArgs& a, const kvq_rope_norm& r, int dtype, cudaStream_t st);
+
+struct PageArgs {
+  const int32_t* seq_len;
+  uint32_t* status;
+  int32_t* table;
+  int batch, max_ctx, page_tokens, n_pages;
+  kvq_page_pool pool;
+  const int32_t* n_new;
+  int n_new_max, max_rows;
+  int32_t* granted;
+  int32_t* row_pos;
+  int32_t* row_dst;
+  int32_t* row_slot;
+  int32_t* seq_len_out;
+};
+cudaError_t launch_page_update(const PageArgs& a, cudaStream_t st);
+
+// Block index and sparse decode (the decode's head dims, no outlier channels).
+constexpr int kMaxIndexBlocks = 49152;  // keys of a row in shared memory: 192 KB
+cudaError_t launch_block_index_update(const kvq_cache& c, const kvq_block_index& x, int n_last, cudaStream_t st);
+cudaError_t launch_select_blocks(const kvq_cache& c, Rot rot, const kvq_block_index& x, const void* q, int q_dtype,
+                                 int n_q_heads, int n_first, int n_last, int n_select, int32_t* sel, cudaStream_t st);
+cudaError_t launch_sparse_decode(const kvq_cache& c, Rot rot, const void* q, int q_dtype, int n_q_heads, float scale,
+                                 int block_tokens, const int32_t* sel, int n_select, void* out, int out_dtype,
+                                 cudaStream_t st);
+
 }  // namespace kvq

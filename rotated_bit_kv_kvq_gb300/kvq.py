@@ -36,6 +36,8 @@ KVQ_INPUT_PREROTATED = 1
 KVQ_NUM_PLANES = 12
 KVQ_DEV_ERR_APPEND_RANGE, KVQ_DEV_ERR_PREFILL_RANGE, KVQ_DEV_ERR_TIMEOUT, KVQ_DEV_ERR_PAGE = 1, 2, 4, 8
 KVQ_DEV_ERR_OUTLIER = 16
+KVQ_DEV_ERR_NO_ROOM, KVQ_DEV_ERR_ROW = 32, 64
+KVQ_PAGE_RELEASE = -1
 
 
 class kvq_cache(ctypes.Structure):
@@ -51,6 +53,22 @@ class kvq_cache(ctypes.Structure):
         ("n_outlier", ctypes.c_int32), ("outlier_idx", ctypes.c_void_p),
         ("outl", ctypes.c_void_p),
     ]
+
+
+class kvq_rope_norm(ctypes.Structure):
+    _fields_ = [
+        ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("eps", ctypes.c_float),
+        ("weight_dtype", ctypes.c_int32), ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+        ("inv_freq", ctypes.c_void_p),
+    ]
+
+
+class kvq_page_pool(ctypes.Structure):
+    _fields_ = [("ring", ctypes.c_void_p), ("state", ctypes.c_void_p), ("next", ctypes.c_void_p)]
+
+
+class kvq_block_index(ctypes.Structure):
+    _fields_ = [("block_tokens", ctypes.c_int32), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
 
 
 # every symbol include/kvq.h declares, with its C signature
@@ -80,6 +98,22 @@ SIGNATURES = {
                                                ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_float,
                                                ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t,
                                                ctypes.c_void_p]),
+    "kvq_qk_norm_rope": (ctypes.c_int32, [_P, ctypes.POINTER(kvq_rope_norm), ctypes.c_int32, ctypes.c_int32,
+                                          ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
+                                          ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p,
+                                          ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
+                                          ctypes.c_void_p, ctypes.c_void_p]),
+    "kvq_page_update": (ctypes.c_int32, [_P, ctypes.POINTER(kvq_page_pool), ctypes.c_void_p, ctypes.c_int32,
+                                         ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
+                                         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "kvq_block_index_update": (ctypes.c_int32, [_P, ctypes.POINTER(kvq_block_index), ctypes.c_int32,
+                                                ctypes.c_void_p]),
+    "kvq_select_blocks": (ctypes.c_int32, [_P, ctypes.POINTER(kvq_block_index), ctypes.c_void_p, ctypes.c_int32,
+                                           ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                                           ctypes.c_void_p, ctypes.c_void_p]),
+    "kvq_sparse_decode_attention": (ctypes.c_int32, [_P, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32,
+                                                     ctypes.c_float, ctypes.c_int32, ctypes.c_void_p, ctypes.c_int32,
+                                                     ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p]),
     "kvq_dequant_debug": (ctypes.c_int32, [_P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
                                            ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
                                            ctypes.c_void_p]),
@@ -201,6 +235,154 @@ def kvq_prefill_attention(cache: kvq_cache, q, out, workspace, q_pos0=None, caus
                                        _ptr(q_pos0), 1 if causal else 0, chunk, float(scale), _ptr(out),
                                        _dtype_id(out), _ptr(workspace), wsb, _stream(stream)),
            "kvq_prefill_attention")
+
+
+def _expect(what: str, shape, dtypes, *tensors, contiguous=True):
+    """ValueError unless the tensors (None allowed) lie on the current device and have that shape and a type of `dtypes`."""
+    import torch
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is None:
+            continue
+        if t.get_device() != dev:
+            raise ValueError(f"{what}: a tensor is not on the current CUDA device")
+        if t.dtype not in dtypes or (shape is not None and tuple(t.shape) != shape):
+            raise ValueError(f"{what}: expected {shape} of {dtypes}, got {tuple(t.shape)} of {t.dtype}")
+        if contiguous and not t.is_contiguous():
+            raise ValueError(f"{what}: a tensor is not contiguous")
+
+
+def _heads_row_stride(what: str, t, heads: int, d: int, n_rows: int, like) -> int:
+    """Row stride (elements) of projection rows [n_rows][heads * d] or [n_rows][heads][d] whose heads lie side by side."""
+    ok = t.dtype == like.dtype and t.get_device() == like.get_device() and t.shape[0] == n_rows
+    if t.dim() == 2:
+        ok = ok and t.shape[1] == heads * d and (t.stride(1) == 1 or n_rows == 0)
+    else:
+        ok = ok and t.dim() == 3 and t.shape[1] == heads and t.shape[2] == d and \
+            (n_rows == 0 or (t.stride(2) == 1 and (heads == 1 or t.stride(1) == d)))
+    if not ok:
+        raise ValueError(f"{what}: expected {n_rows} rows of {heads} x {d} values of {like.dtype}, heads side by side")
+    # (the stride of a single row is free: torch may report any number)
+    return t.stride(0) if n_rows > 1 else max(t.stride(0), heads * d)
+
+
+class RopeNorm:
+    """The plan of kvq_qk_norm_rope: inv_freq fp32 [rot_dim / 2] (None: no rotation), weights [head_dim] or None."""
+
+    def __init__(self, inv_freq=None, q_weight=None, k_weight=None, eps=1e-6, interleaved=False):
+        import torch
+        floats = (torch.float32, torch.bfloat16, torch.float16)
+        _expect("RopeNorm", None, (torch.float32,), inv_freq)
+        _expect("RopeNorm", None, floats, q_weight, k_weight)
+        if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
+            raise ValueError("RopeNorm: q_weight and k_weight differ in type")
+        self.inv_freq, self.q_weight, self.k_weight = inv_freq, q_weight, k_weight  # kept alive
+        self.desc = kvq_rope_norm()
+        self.desc.rot_dim = 0 if inv_freq is None else 2 * inv_freq.numel()
+        self.desc.interleaved = 1 if interleaved else 0
+        self.desc.eps = eps
+        w = q_weight if q_weight is not None else k_weight
+        self.desc.weight_dtype = KVQ_F32 if w is None else _dtype_id(w)
+        self.desc.q_weight, self.desc.k_weight = _ptr(q_weight), _ptr(k_weight)
+        self.desc.inv_freq = None if self.desc.rot_dim == 0 else _ptr(inv_freq)
+
+
+def kvq_qk_norm_rope(cache: kvq_cache, rope: RopeNorm, q, k, v, pos, q_out, k_out, v_out, dst_row=None, stream=None):
+    """Rows q [n][heads * d] or [n][heads][d] (any row stride, e.g. parts of one projection), k and v (or None) the same
+    with the KV heads; pos int32 [n], dst_row int32 [n] or None.  Outputs [rows][heads][d], or [..][heads][d] contiguous."""
+    import torch
+    d, hkv, hq, n = cache.head_dim, cache.n_kv_heads, q_out.shape[-2], q.shape[0]
+    rows = q_out.numel() // max(1, hq * d)
+    for w in (rope.q_weight, rope.k_weight):
+        if w is not None and w.numel() != d:
+            raise ValueError("kvq_qk_norm_rope: a weight has not head_dim values")
+    _expect("kvq_qk_norm_rope: pos, dst_row", (n,), (torch.int32,), pos, dst_row)
+    _expect("kvq_qk_norm_rope: outputs", None, (q.dtype,), q_out, k_out, v_out)
+    if q_out.shape[-1] != d or k_out.numel() != rows * hkv * d or (v_out is not None and v_out.numel() != rows * hkv * d):
+        raise ValueError("kvq_qk_norm_rope: the outputs differ in rows, heads or head_dim")
+    qs = _heads_row_stride("kvq_qk_norm_rope: q", q, hq, d, n, q_out)
+    ks = _heads_row_stride("kvq_qk_norm_rope: k", k, hkv, d, n, q_out)
+    vs = 0 if v is None else _heads_row_stride("kvq_qk_norm_rope: v", v, hkv, d, n, q_out)
+    _check(lib().kvq_qk_norm_rope(ctypes.byref(cache), ctypes.byref(rope.desc), _dtype_id(q), hq, _ptr(q), qs, _ptr(k),
+                                  ks, _ptr(v), vs, _ptr(pos), _ptr(dst_row), n, rows, _ptr(q_out), _ptr(k_out),
+                                  _ptr(v_out), _stream(stream)),
+           "kvq_qk_norm_rope")
+
+
+class PagePool:
+    """The free pages of a paged cache: at first all of them, or those listed in `free`."""
+
+    def __init__(self, cache: kvq_cache, free=None, device="cuda"):
+        import torch
+        n = cache.n_pages
+        free = range(n) if free is None else free
+        self.ring = torch.full((max(n, 1),), -1, dtype=torch.int32, device=device)
+        ids = torch.as_tensor(list(free), dtype=torch.int32)
+        if len(ids) > n:
+            raise ValueError("PagePool: more free pages than the cache has")
+        self.ring[:len(ids)] = ids.to(device)
+        self.state = torch.tensor([0, len(ids)], dtype=torch.int32, device=device)
+        self.desc = kvq_page_pool(self.ring.data_ptr(), self.state.data_ptr(), self.state.data_ptr())
+
+
+def kvq_page_update(cache: kvq_cache, pool, n_new, n_new_max: int, granted, row_pos=None, row_dst=None, row_slot=None,
+                    seq_len_out=None, stream=None):
+    """pool: PagePool or kvq_page_pool; n_new, granted, seq_len_out int32 [batch]; the row maps int32 [max_rows]."""
+    import torch
+    _expect("kvq_page_update", (cache.batch,), (torch.int32,), n_new, granted, seq_len_out)
+    rows = next((t.numel() for t in (row_pos, row_dst, row_slot) if t is not None), None)
+    if rows is None:
+        rows = min(cache.batch * n_new_max, 0x7fffffff)  # no maps: no limit of rows
+    else:
+        _expect("kvq_page_update: row maps", (rows,), (torch.int32,), row_pos, row_dst, row_slot)
+    desc = pool.desc if isinstance(pool, PagePool) else pool
+    _check(lib().kvq_page_update(ctypes.byref(cache), ctypes.byref(desc), _ptr(n_new), n_new_max, _ptr(granted), rows,
+                                 _ptr(row_pos), _ptr(row_dst), _ptr(row_slot), _ptr(seq_len_out), _stream(stream)),
+           "kvq_page_update")
+
+
+class BlockIndex:
+    """The int8 mean keys of a cache's blocks, allocated with torch."""
+
+    def __init__(self, cache: kvq_cache, block_tokens: int, device="cuda"):
+        import torch
+        nblk = -(-cache.max_ctx // block_tokens)
+        self.codes = torch.zeros(cache.batch, cache.n_kv_heads, nblk, cache.head_dim, dtype=torch.int8, device=device)
+        self.scales = torch.zeros(cache.batch, cache.n_kv_heads, nblk, dtype=torch.float32, device=device)
+        self.desc = kvq_block_index(block_tokens, self.codes.data_ptr(), self.scales.data_ptr())
+
+
+def _index_desc(index):
+    return index.desc if isinstance(index, BlockIndex) else index
+
+
+def kvq_block_index_update(cache: kvq_cache, index, n_last: int = 0, stream=None):
+    """index: BlockIndex or kvq_block_index; n_last 0: every block, else those of the last n_last tokens."""
+    _check(lib().kvq_block_index_update(ctypes.byref(cache), ctypes.byref(_index_desc(index)), n_last, _stream(stream)),
+           "kvq_block_index_update")
+
+
+def kvq_select_blocks(cache: kvq_cache, index, q, sel, n_first: int = 1, n_last: int = 1, stream=None):
+    """q [batch][n_q_heads][head_dim]; sel int32 [batch][n_kv_heads][n_select]."""
+    import torch
+    _expect("kvq_select_blocks: q", (cache.batch, q.shape[1], cache.head_dim),
+            (torch.float32, torch.bfloat16, torch.float16), q)
+    _expect("kvq_select_blocks: sel", (cache.batch, cache.n_kv_heads, sel.shape[-1]), (torch.int32,), sel)
+    _check(lib().kvq_select_blocks(ctypes.byref(cache), ctypes.byref(_index_desc(index)), _ptr(q), _dtype_id(q),
+                                   q.shape[1], n_first, n_last, sel.shape[-1], _ptr(sel), _stream(stream)),
+           "kvq_select_blocks")
+
+
+def kvq_sparse_decode_attention(cache: kvq_cache, q, sel, out, block_tokens: int, scale: float = 0.0, stream=None):
+    """q, out [batch][n_q_heads][head_dim]; sel int32 [batch][n_kv_heads][n_select] block numbers (negative: none)."""
+    import torch
+    _expect("kvq_sparse_decode_attention: q, out", (cache.batch, q.shape[1], cache.head_dim),
+            (torch.float32, torch.bfloat16, torch.float16), q, out)
+    _expect("kvq_sparse_decode_attention: sel", (cache.batch, cache.n_kv_heads, sel.shape[-1]), (torch.int32,), sel)
+    _check(lib().kvq_sparse_decode_attention(ctypes.byref(cache), _ptr(q), _dtype_id(q), q.shape[1], float(scale),
+                                             block_tokens, _ptr(sel), sel.shape[-1], _ptr(out), _dtype_id(out),
+                                             _stream(stream)),
+           "kvq_sparse_decode_attention")
 
 
 def kvq_dequant_debug(cache: kvq_cache, seq, kv_head, which, t0, count, out=None, blocks=None,

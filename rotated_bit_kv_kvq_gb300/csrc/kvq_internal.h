@@ -25,6 +25,11 @@ inline int rotation_group(int d) {
 }
 
 size_t qs_row_bytes_host(int qt, int d);
+// rows of the body planes
+inline long long body_row_count(const kvq_cache& c) {
+  return c.page_tokens ? (long long)c.n_pages * c.n_kv_heads * c.page_tokens
+                       : (long long)c.batch * c.n_kv_heads * c.max_ctx;
+}
 
 // Raises a kernel's dynamic shared-memory limit once per device (again only for
 // a larger size), so that steady-state calls make no attribute call and can be

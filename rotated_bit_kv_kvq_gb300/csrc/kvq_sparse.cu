@@ -1,134 +1,769 @@
 // Decode attention over selected blocks (kvq_sparse_decode_attention).
 //
-// One CTA per (query head, sequence): a warp takes a token at a time, lane l its channels
-// l, l + 32, ...; online softmax per warp, the warps merged at the end.
+// A row of work is one (sequence, KV head, group of up to eight query heads).  A cluster of
+// CTAs shares a row: its warps take the listed blocks' tiles (kRows<D> tokens) in turn, each
+// with its own ring of shared-memory stages filled by TMA and its own online softmax, and the
+// partials of all its warps are merged through distributed shared memory -- one launch, no
+// workspace.
+//
+// Scores of a tile, heads x tokens, on the tensor cores: A = the query (16 rows: fp16 high
+// parts of eight heads, then the low parts; the two rows of a head are added, so one mma does
+// both parts), B = the codes.  4-, 5- and 8-bit codes u go in as the fp16 subnormals u * 2^-24
+// -- the code's bits are the half's bits, so a mask (or a byte permute) is the whole
+// conversion -- with the offset's part, -offset * (sum of the block's q), as the mma's initial
+// value; the factor 2^24 goes to the finished score.  The query is scaled by a power of two
+// (its largest value below 2^11) so that its low parts stay far above fp16's smallest step.
+// The mma's result has exactly the layout of P as the B operand of P.V, so P never moves
+// between lanes.  P.V is the decode's: A = centred codes (channels x tokens), B = P times the
+// block's scale as fp16 high and low parts.  (Subnormal codes do not serve there: all weights
+// are positive, the offset's part would grow with the number of tokens and cancel.)
 
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <math.h>
+#include <cooperative_groups.h>
+#include <string.h>
 
-#include "kvq_device.cuh"
-#include "kvq_internal.h"
-#include "kvq_quant.cuh"
+#include <algorithm>
+
+#include "kvq_decode_impl.cuh"
 
 namespace kvq {
 namespace {
 
-constexpr int kSpWarps = 8;
+namespace cg = cooperative_groups;
 
-struct SparseArgs {
+constexpr int kTailRows = 8;   // tokens of a tail tile
+constexpr int kMaxStages = 4;
+constexpr int kMaxCluster = 8;
+
+template <int D> constexpr int kRows = D <= 128 ? 32 : 16;               // tokens of a body tile
+template <int D> constexpr int kW = D <= 128 ? 8 : D <= 256 ? 6 : 8;      // warps of a CTA
+template <int D> constexpr int kSpCtas = D <= 256 ? 2 : 1;                // CTAs of an SM
+
+// a stage's layout: K codes, V codes (1024-aligned: TMA swizzle), headers, high bits; or K and V tail rows
+struct SpStage {
+  int v, kd, vd, kqh, vqh, vt, bytes, stages;
+  int kh, vh;  // bytes of a row's K and V headers
+  uint32_t tx;
+};
+
+struct SpArgs {
   kvq_cache c;
+  SpStage s;
   const void* q;
   const int32_t* sel;
   void* out;
-  int q_dtype, out_dtype, n_q_heads, group, block_tokens, n_select, rot_k, rot_v;
+  int q_dtype, out_dtype, n_q_heads, group, head_groups, heads_per_cta, block_tokens, n_select, rot_k, rot_v;
   float scale_log2;
 };
 
-// channel 32 * blk + lane of a body row
-__device__ __forceinline__ float body_value(const kvq_cache& c, bool v, long long row, int blk, int lane) {
-  const int qt = v ? c.v_type : c.k_type, d = c.head_dim, nb = d / 32;
-  const uint8_t* qs = static_cast<const uint8_t*>(v ? c.v_qs : c.k_qs);
-  const __half* hd = static_cast<const __half*>(v ? c.v_d : c.k_d);
-  const long long e = row * nb + blk;
-  if (qt == KVQ_TYPE_Q8_0) return float(int(qs[row * d + 32 * blk + lane]) - 128) * __half2float(hd[e]);
-  int code = (qs[row * (d / 2) + 16 * blk + (lane & 15)] >> (lane & 16 ? 4 : 0)) & 15;
-  if (type_has_qh(qt)) code |= int((qh_get(v ? c.v_qh : c.k_qh, !v, size_t(row), nb, blk) >> lane) & 1u) << 4;
-  if (type_has_min(qt)) return fmaf(float(code), __half2float(hd[2 * e]), __half2float(hd[2 * e + 1]));
-  return float(code - type_code_offset(qt)) * __half2float(hd[e]);
+// codes of the low (H16 false) or high nibbles as fp16 subnormals: bits 0-4 / 16-20, or
+// bits 4-8 / 20-24 (16 times the value), the 5-bit formats' high bits in place already
+template <bool H16>
+__device__ __forceinline__ uint32_t nib_sub(uint32_t r, uint32_t hb) {
+  return (r & (H16 ? 0x00F000F0u : 0x000F000Fu)) | hb;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kSpWarps * 32) sparse_kernel(SparseArgs a) {
-  constexpr int G = (D & (D - 1)) == 0 ? D : 64, E = D / 32;
-  __shared__ float s_x[D], s_acc[kSpWarps][D], s_m[kSpWarps], s_l[kSpWarps];
-  const kvq_cache& c = a.c;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int hq = blockIdx.x, b = blockIdx.y, h = hq / a.group, T = c.tail_len;
-  const int n = min(max(c.seq_len[b], 0), c.max_ctx);
-  const long long bh = (long long)b * c.n_kv_heads + h;
-  const int32_t* sel = a.sel + bh * a.n_select;
-  if (warp == 0) {
-    float v[E];
-    const size_t row = ((size_t)b * a.n_q_heads + hq) * D;
+// D = A * B + C with C apart from D (the initial values are shared by several mma)
+__device__ __forceinline__ void mma16816_from(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%11,%11};"
+               : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(0.0f));
+}
+
+// Scores of a body tile (st: its stage): S[hh][t][e] of tokens 16hh + 8t + 2tig + e and head g.
+template <int D, int KT>
+__device__ __forceinline__ void body_scores(const uint8_t* st, const SpStage& L, const uint4* qf, const float* qsum, int lane,
+                                            float (&S)[kRows<D> / 16][2][2]) {
+  constexpr int NB = D / 32, RB = kRows<D>, HB = RB / 16, ROW = KT == KVQ_TYPE_Q8_0 ? D : D / 2, W = box_w(ROW);
+  constexpr bool K1 = type_has_min(KT), K5 = type_has_qh(KT);
+  constexpr int KHH = K1 ? 2 : 1, HW = NB * KHH / 2;
+  const int g = lane >> 2, tig = lane & 3, mi = lane >> 3, rr = (lane & 7) + 8 * (mi & 1);
+  const uint32_t kb = smem_u32(st);
+  uint32_t lb[W / 32];
+  swz_lane<W>(rr, mi >> 1, lb);
+  uint32_t hd[HB][4][HW];  // headers of tokens 16hh + 2tig, + 1, + 8, + 9
 #pragma unroll
-    for (int gi = 0; gi < D / G; ++gi) load_vals<G / 32>(a.q, a.q_dtype, row + gi * G + lane * (G / 32), v + gi * (G / 32));
-    if (a.rot_k) warp_fwht<D, G>(v, lane);
-    const float s = a.scale_log2 * (a.rot_k ? inv_sqrt_group<G>() : 1.0f);
+  for (int hh = 0; hh < HB; ++hh)
 #pragma unroll
-    for (int e = 0; e < E; ++e) s_x[fwht_channel<D, G>(lane, e)] = v[e] * s;
-  }
-  __syncthreads();
-  float q[E], acc[E], m = -INFINITY, l = 0.0f;
+    for (int i = 0; i < 4; ++i)
+      lds_words<NB * 2 * KHH>(st + L.kd + (16 * hh + 2 * tig + (i & 1) + 8 * (i >> 1)) * NB * 2 * KHH, hd[hh][i]);
+  const float off = KT == KVQ_TYPE_Q8_0 ? 128.0f : float(type_code_offset(KT));
+  // operands of the two k-steps of block blk for the 8-token tiles of half hh
+  auto dots = [&](int blk, int hh, const uint32_t (&b)[2][4], const uint32_t (&a0)[4], const uint32_t (&a1)[4], float qs) {
 #pragma unroll
-  for (int e = 0; e < E; ++e) { q[e] = s_x[32 * e + lane]; acc[e] = 0.0f; }
-  __syncthreads();
-  const RowMap rm = row_map(c);
-  for (int i = 0; i < a.n_select; ++i) {
-    const int blk = sel[i];
-    if (blk < 0 || (long long)blk * a.block_tokens >= n) continue;
-    const int t0 = blk * a.block_tokens, t1 = min(n, t0 + a.block_tokens);
-    for (int t = t0 + warp; t < t1; t += kSpWarps) {
-      const bool tail = t >= n - T;
-      const long long row = tail ? bh * T + t % T : body_row(rm, b, h, t);
-      if (row < 0) {
-        if (lane == 0) atomicOr(c.status, KVQ_DEV_ERR_PAGE);
-        continue;
+    for (int t = 0; t < 2; ++t) {
+      float cc[4];
+      mma16816_from(cc, a0, b[t][0], b[t][1], K1 ? 0.0f : -off * qs);
+      mma16816(cc, a1, b[t][2], b[t][3]);
+      const float s0 = cc[0] + cc[2], s1 = cc[1] + cc[3];
+      S[hh][t][0] = fmaf(hdr_scale<KHH>(hd[hh][2 * t], blk), s0, S[hh][t][0]);
+      S[hh][t][1] = fmaf(hdr_scale<KHH>(hd[hh][2 * t + 1], blk), s1, S[hh][t][1]);
+      if constexpr (K1) {
+        S[hh][t][0] = fmaf(h2f(hd[hh][2 * t][blk], 1), qs, S[hh][t][0]);
+        S[hh][t][1] = fmaf(h2f(hd[hh][2 * t + 1][blk], 1), qs, S[hh][t][1]);
       }
-      float s = 0.0f;
+    }
+  };
+  const uint32_t k0 = uint32_t(8 * (tig >> 1) + 2 * (tig & 1) - 4) & 31u, k1 = (k0 + 1) & 31u;
+  constexpr int BP = KT == KVQ_TYPE_Q8_0 ? 1 : 2;  // blocks of one ldmatrix
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float x = tail ? bf16_bits_to_f32(static_cast<const uint16_t*>(c.k_tail)[row * D + 32 * e + lane])
-                             : body_value(c, false, row, e, lane);
-        s = fmaf(q[e], x, s);
-      }
+  for (int bp = 0; bp < NB; bp += BP) {
+    uint32_t r[HB][4];
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      const float nm = fmaxf(m, s);
-      const float f = m == -INFINITY ? 0.0f : exp2f(m - nm), p = exp2f(s - nm);
-      m = nm;
-      l = l * f + p;
+    for (int hh = 0; hh < HB; ++hh) {
+      const int j = KT == KVQ_TYPE_Q8_0 ? 2 * bp : bp;  // its first 16-byte chunk
+      ldsm_x4(kb + hh * 16 * W + lb[swz_lane_idx<W>(j)] + swz_box_off<W, RB>(j), r[hh][0], r[hh][1], r[hh][2], r[hh][3]);
+    }
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float x = tail ? bf16_bits_to_f32(static_cast<const uint16_t*>(c.v_tail)[row * D + 32 * e + lane])
-                             : body_value(c, true, row, e, lane);
-        acc[e] = fmaf(acc[e], f, p * x);
+    for (int e = 0; e < BP; ++e) {
+      const int blk = bp + e;
+      const uint4 qa = qf[(blk * 2) * 32 + lane], qb = qf[(blk * 2 + 1) * 32 + lane];
+      const uint32_t a0[4] = {qa.x, qa.y, qa.z, qa.w}, a1[4] = {qb.x, qb.y, qb.z, qb.w};
+      const float qs = qsum[blk * kMaxHeads + g];
+#pragma unroll
+      for (int hh = 0; hh < HB; ++hh) {
+        uint32_t b[2][4];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if constexpr (KT == KVQ_TYPE_Q8_0) {  // r[t]: channels 4tig .. of the first half block, r[2 + t] of the second
+            b[t][0] = __byte_perm(r[hh][t], 0, 0x4240);
+            b[t][1] = __byte_perm(r[hh][t], 0, 0x4341);
+            b[t][2] = __byte_perm(r[hh][2 + t], 0, 0x4240);
+            b[t][3] = __byte_perm(r[hh][2 + t], 0, 0x4341);
+          } else {
+            const uint32_t w = r[hh][2 * e + t], w8 = w >> 8;
+            uint32_t h0 = 0, h1 = 0;
+            if constexpr (K5) {  // rotated: the pairs' bits at 4 / 20 (low nibbles) and 8 / 24
+              const uint32_t h = reinterpret_cast<const uint32_t*>(st + L.kqh)[(16 * hh + 8 * t + g) * NB + blk];
+              h0 = __funnelshift_r(h, h, k0);
+              h1 = __funnelshift_r(h, h, k1);
+            }
+            b[t][0] = nib_sub<false>(w, h0 & 0x00100010u);
+            b[t][1] = nib_sub<false>(w8, h1 & 0x00100010u);
+            b[t][2] = nib_sub<true>(w, h0 & 0x01000100u);
+            b[t][3] = nib_sub<true>(w8, h1 & 0x01000100u);
+          }
+        }
+        dots(blk, hh, b, a0, a1, qs);
       }
     }
   }
+}
+
+// acc += codes_V^T . (P * scale) of 16 body rows: rows 2g (acc .. [0], [1]) and 2g + 1 of each
+// 16 channels, columns heads 2tig, 2tig + 1; dmin += the blocks' minima . P (rows blocks g, g + 8).
+// ok[i]: token i of the lane's four lies below the tile's end.
+template <int D, int VT>
+__device__ __forceinline__ void body_values(uint32_t vb, const uint8_t* st, const SpStage& L, int row0, const uint32_t (&ph)[2],
+                                            const uint32_t (&pl)[2], bool partial, const bool (&ok)[4], int lane,
+                                            float (&acc)[D / 32][2][4], float (&dmin)[4]) {
+  constexpr int NB = D / 32, RB = kRows<D>, ROW = VT == KVQ_TYPE_Q8_0 ? D : D / 2, W = box_w(ROW);
+  constexpr bool V1 = type_has_min(VT), V5 = type_has_qh(VT);
+  constexpr int VHH = V1 ? 2 : 1, VW = NB * VHH / 2;
+  const int g = lane >> 2, tig = lane & 3, mi = lane >> 3, rr = (lane & 7) + 8 * (mi & 1);
+  uint32_t lb[W / 32];
+  swz_lane<W>(rr, mi >> 1, lb);
+  const uint8_t* vd = st + L.vd + (row0 + 2 * tig) * NB * 2 * VHH;
+  uint32_t vh[4][VW];
 #pragma unroll
-  for (int e = 0; e < E; ++e) s_acc[warp][32 * e + lane] = acc[e];
-  if (lane == 0) { s_m[warp] = m; s_l[warp] = l; }
+  for (int i = 0; i < 4; ++i) {
+    lds_words<NB * 2 * VHH>(vd + ((i & 1) + 8 * (i >> 1)) * NB * 2 * VHH, vh[i]);
+    if (partial) {  // rows past the end hold anything: their headers become zero
+#pragma unroll
+      for (int j = 0; j < VW; ++j) vh[i][j] = ok[i] ? vh[i][j] : 0u;
+    }
+  }
+  auto scales = [&](int blk, int a, int b) -> uint32_t {
+    if constexpr (VHH == 1) return __byte_perm(vh[a][blk >> 1], vh[b][blk >> 1], (blk & 1) ? 0x7632 : 0x5410);
+    else return __byte_perm(vh[a][blk], vh[b][blk], 0x5410);
+  };
+  auto block = [&](int blk, const uint32_t (&a0)[4], const uint32_t (&a1)[4]) {
+    uint32_t h0, l0, h1, l1;
+    hscale_split(ph[0], pl[0], scales(blk, 0, 1), h0, l0);
+    hscale_split(ph[1], pl[1], scales(blk, 2, 3), h1, l1);
+    mma16816(acc[blk][0], a0, h0, h1);
+    mma16816(acc[blk][0], a0, l0, l1);
+    mma16816(acc[blk][1], a1, h0, h1);
+    mma16816(acc[blk][1], a1, l0, l1);
+  };
+  if constexpr (V1) {
+    auto lo2 = [&](int blk, int i) -> uint32_t {
+      const int bb = blk < NB ? blk : NB - 1;
+      uint32_t w0 = *reinterpret_cast<const uint32_t*>(vd + (8 * (i >> 1) * NB + bb) * 4);
+      uint32_t w1 = *reinterpret_cast<const uint32_t*>(vd + ((8 * (i >> 1) + 1) * NB + bb) * 4);
+      if (partial) { w0 = ok[i] ? w0 : 0u; w1 = ok[i + 1] ? w1 : 0u; }
+      return blk < NB ? __byte_perm(w0, w1, 0x7632) : 0u;
+    };
+    const uint32_t al[4] = {lo2(g, 0), NB > 8 ? lo2(g + 8, 0) : 0u, lo2(g, 2), NB > 8 ? lo2(g + 8, 2) : 0u};
+    mma16816(dmin, al, ph[0], ph[1]);
+    mma16816(dmin, al, pl[0], pl[1]);
+  }
+  if constexpr (VT == KVQ_TYPE_Q8_0) {
+#pragma unroll
+    for (int blk = 0; blk < NB; ++blk) {
+      uint32_t r0, r1, r2, r3;
+      ldsm_x4_t(vb + lb[swz_lane_idx<W>(2 * blk)] + swz_box_off<W, RB>(2 * blk), r0, r1, r2, r3);
+      const uint32_t a0[4] = {i8_pair<0, 2>(r0), i8_pair<1, 3>(r0), i8_pair<0, 2>(r1), i8_pair<1, 3>(r1)};
+      const uint32_t a1[4] = {i8_pair<0, 2>(r2), i8_pair<1, 3>(r2), i8_pair<0, 2>(r3), i8_pair<1, 3>(r3)};
+      block(blk, a0, a1);
+    }
+  } else {
+    constexpr uint32_t OFF = (0x6400u + uint32_t(type_code_offset(VT))) * 0x10001u;
+    constexpr uint32_t OFF16 = neg_off_x16_bits(type_code_offset(VT));
+    const uint32_t v0 = uint32_t(8 * ((g & 3) >> 1) + 2 * (g & 1) - 4) & 31u, v1 = (v0 + 1) & 31u;
+#pragma unroll
+    for (int bp = 0; bp < NB; bp += 2) {
+      uint32_t r[4];
+      ldsm_x4_t(vb + lb[swz_lane_idx<W>(bp)] + swz_box_off<W, RB>(bp), r[0], r[1], r[2], r[3]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int blk = bp + e;
+        uint32_t a0[4], a1[4];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {  // tokens 0-7, 8-15
+          const uint32_t w = r[2 * e + t], w8 = w >> 8;
+          uint32_t m0 = 0x64006400u, m1 = m0, m2 = m0, m3 = m0;
+          if constexpr (V5) {  // the lane's part word of rows 8t + 2tig, + 1
+            const uint32_t h = *reinterpret_cast<const uint32_t*>(
+                st + L.vqh + (((row0 / 2 + 4 * t + tig) * NB + blk) * 2 + (g >> 2)) * 4);
+            const uint32_t h0 = __funnelshift_r(h, h, v0), h1 = __funnelshift_r(h, h, v1);
+            m0 = vhb(h0, 0x00100010u); m1 = vhb(h1, 0x00100010u);
+            m2 = vhb(h0, 0x01000100u); m3 = vhb(h1, 0x01000100u);
+          }
+          a0[2 * t] = nib_pair(w, 0, m0, OFF);
+          a0[2 * t + 1] = nib_pair(w8, 0, m1, OFF);
+          a1[2 * t] = nib_pair_x16(w, m2, OFF16);
+          a1[2 * t + 1] = nib_pair_x16(w8, m3, OFF16);
+        }
+        block(blk, a0, a1);
+      }
+    }
+  }
+}
+
+// a bf16 pair times a power of two as an fp16 pair
+__device__ __forceinline__ uint32_t bf16x2_times(uint32_t b, float f) {
+  return pack_h2(__uint_as_float(b << 16) * f, __uint_as_float(b & 0xFFFF0000u) * f);
+}
+
+template <int D>
+__global__ void __launch_bounds__(32 * kW<D>, kSpCtas<D>)
+sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+              const __grid_constant__ CUtensorMap tmKt, const __grid_constant__ CUtensorMap tmVt) {
+  constexpr int NB = D / 32, RB = kRows<D>, HB = RB / 16, G = (D & (D - 1)) == 0 ? D : 64;
+  constexpr int WT = box_w(2 * D), kWarps = kW<D>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const kvq_cache& c = a.c;
+  const int S = int(cg::this_cluster().num_blocks()), rank = int(cg::this_cluster().block_rank());
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const int g = lane >> 2, tig = lane & 3;
+  const int row = blockIdx.x / S, plane = row % (c.n_kv_heads * a.head_groups), b = row / (c.n_kv_heads * a.head_groups);
+  const int kvh = plane / a.head_groups, hg = plane % a.head_groups;
+  const int head0 = kvh * a.group + hg * a.heads_per_cta, nheads = min(a.heads_per_cta, a.group - hg * a.heads_per_cta);
+  const int T = c.tail_len, NS = a.s.stages;
+  // shared memory: stages [kWarps][NS] (the partials of the merge afterwards), query fragments,
+  // block sums of the query, partial (m, l), score factors, barriers, jobs
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* wst = smem + warp * NS * a.s.bytes;
+  const bool nib = c.k_type != KVQ_TYPE_Q8_0;
+  uint8_t* sp = smem + kWarps * NS * a.s.bytes;
+  float* sq = reinterpret_cast<float*>(sp);                             // [8][D], then the fragments
+  uint4* qf = reinterpret_cast<uint4*>(sp);
+  sp += 32 * D;
+  float* qsum = reinterpret_cast<float*>(sp);                           // [NB][8]
+  float* s_m = qsum + NB * kMaxHeads;                                   // [kWarps][8]
+  float* s_l = s_m + kWarps * kMaxHeads;
+  float* s_f = s_l + kWarps * kMaxHeads;                                // [8]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s_f + kMaxHeads);        // [kWarps][kMaxStages]
+  int2* jobs = reinterpret_cast<int2*>(bars + kWarps * kMaxStages);     // [kWarps][kMaxStages]
+
+  const int n = min(max(c.seq_len[b], 0), c.max_ctx);
+  const long long bh = (long long)b * c.n_kv_heads + kvh;
+  const int32_t* sel = a.sel + bh * a.n_select;
+  uint64_t* wbar = bars + warp * kMaxStages;
+  int2* wjob = jobs + warp * kMaxStages;
+  if (lane == 0) {
+    for (int i = 0; i < NS; ++i) mbar_init(&wbar[i], 1);
+    fence_barrier_init();
+    if (warp == 0) {
+      prefetch_tmap(&tmK); prefetch_tmap(&tmV);
+      if (T > 0) { prefetch_tmap(&tmKt); prefetch_tmap(&tmVt); }
+    }
+  }
+  __syncwarp();
+
+  // ---- producer: the warp's tiles, in order.  Tile ordinal k is tile wid + k * nw of the list;
+  // lane l holds ordinal 32 * (chunk) + l: its first position (-1: not listed) and body row
+  const int tpb = a.block_tokens / RB, body_end = n - T;
+  const long long tiles = (long long)a.n_select * tpb;
+  const int wid = rank * kWarps + warp, nw = S * kWarps;
+  const RowMap rm = row_map(c);
+  long long chunk = 0;     // ordinal of lane 0's tile
+  int my_t0 = -1, my_row = 0;
+  auto fetch = [&]() {
+    const long long u = wid + (chunk + lane) * nw;
+    my_t0 = -1;
+    if (u < tiles) {
+      const int blk = sel[u / tpb];
+      if (blk >= 0 && (long long)blk * a.block_tokens < n) {
+        const int t0 = blk * a.block_tokens + int(u % tpb) * RB;
+        if (t0 < n) {
+          my_t0 = t0;
+          my_row = -1;
+          if (t0 < body_end) {
+            const long long r = body_row(rm, b, kvh, t0);  // rows of a tile lie in one page
+            my_row = int(r);
+            if (r < 0) atomicOr(c.status, KVQ_DEV_ERR_PAGE);
+          }
+        }
+      }
+    }
+  };
+  fetch();
+  int at = 0, pos = -1;    // next ordinal of the chunk; next position of the tile in hand (-1: none)
+  int end = 0, trow = 0;   // its end and body row
+  bool done = false;
+  // the next job (p, count): count > 0 body rows, < 0 tail rows, 0 none left; copies issued by one lane
+  auto produce = [&](int s) {
+    while (!done && pos < 0) {
+      if (at == 32) {
+        chunk += 32;
+        at = 0;
+        if (wid + chunk * nw >= tiles) { done = true; break; }
+        fetch();
+      }
+      const unsigned live = __ballot_sync(0xffffffffu, my_t0 >= 0) >> at;
+      if (!live) { at = 32; continue; }
+      at += __ffs(live) - 1;
+      const int t0 = __shfl_sync(0xffffffffu, my_t0, at);
+      trow = __shfl_sync(0xffffffffu, my_row, at);
+      ++at;
+      end = min(n, t0 + RB);
+      pos = t0;
+      if (pos < body_end && trow < 0) {  // a page outside the pool: its body rows are left out
+        pos = min(end, body_end);
+        if (pos >= end) pos = -1;
+      }
+    }
+    int2 job = make_int2(0, 0);
+    if (!done) {
+      if (pos < body_end) {
+        job = make_int2(pos, min(end, body_end) - pos);
+      } else {
+        job = make_int2(pos, -min(min(kTailRows, end - pos), T - pos % T));  // (a tail tile ends where the ring wraps)
+      }
+    }
+    if (lane == 0) {
+      wjob[s] = job;
+      uint8_t* st = wst + s * a.s.bytes;
+      if (job.y > 0) {
+        const size_t r = size_t(trow);
+        mbar_arrive_expect_tx(&wbar[s], a.s.tx);
+        tma_3d_g2s(st, &tmK, trow, &wbar[s]);
+        tma_3d_g2s(st + a.s.v, &tmV, trow, &wbar[s]);
+        bulk_g2s(st + a.s.kd, static_cast<const uint8_t*>(c.k_d) + r * a.s.kh, RB * a.s.kh, &wbar[s]);
+        bulk_g2s(st + a.s.vd, static_cast<const uint8_t*>(c.v_d) + r * a.s.vh, RB * a.s.vh, &wbar[s]);
+        if (c.k_qh) bulk_g2s(st + a.s.kqh, static_cast<const uint32_t*>(c.k_qh) + r * NB, RB * NB * 4, &wbar[s]);
+        if (c.v_qh) bulk_g2s(st + a.s.vqh, static_cast<const uint32_t*>(c.v_qh) + r * NB, RB * NB * 4, &wbar[s]);
+      } else if (job.y < 0) {
+        const int r = int(bh * T + pos % T);
+        mbar_arrive_expect_tx(&wbar[s], 2 * kTailRows * 2 * D);
+        tma_3d_g2s(st, &tmKt, r, &wbar[s]);
+        tma_3d_g2s(st + a.s.vt, &tmVt, r, &wbar[s]);
+      }
+    }
+    if (job.y != 0) {
+      pos += abs(job.y);
+      if (pos >= end) pos = -1;
+    }
+    return job.y != 0;
+  };
+  int issued = 0;
+  for (int i = 0; i < NS; ++i) issued += produce(i) ? 1 : 0;
+
+  // ---- queries: rotate, scale, fragments (a warp per head)
+  for (int hh = warp; hh < kMaxHeads; hh += kWarps) {
+    float v[NB];
+    load_q_fwht<D, G>(a.q, a.q_dtype, (size_t)b * a.n_q_heads + head0 + hh, hh < nheads, lane, v);
+    if (a.rot_k) warp_fwht<D, G>(v, lane);
+    const float sc = a.scale_log2 * (a.rot_k ? inv_sqrt_group<G>() : 1.0f);
+    float mx = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      v[j] *= sc;
+      mx = fmaxf(mx, fabsf(v[j]));
+    }
+    mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
+    // a power of two that brings the largest value into [2^10, 2^11)
+    const int e = min(max(137 - int(__float_as_uint(mx) >> 23), -100), 100);
+    const float up = __uint_as_float(uint32_t(127 + e) << 23);
+#pragma unroll
+    for (int j = 0; j < NB; ++j) sq[hh * D + fwht_channel<D, G>(lane, j)] = v[j] * up;
+    if (lane == 0) s_f[hh] = __uint_as_float(uint32_t(127 - e) << 23);
+  }
   __syncthreads();
-  if (warp != 0) return;
-  float M = -INFINITY, L = 0.0f;
-  for (int w = 0; w < kSpWarps; ++w) M = fmaxf(M, s_m[w]);
-  float f[kSpWarps];
-  for (int w = 0; w < kSpWarps; ++w) {
-    f[w] = s_m[w] == -INFINITY ? 0.0f : exp2f(s_m[w] - M);
-    L += s_l[w] * f[w];
-  }
-  const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-  float x[E];
+  {
+    constexpr int BPW = (NB + kWarps - 1) / kWarps;
+    uint4 fb[BPW][2];
+    float qs[BPW];
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const int ch = fwht_channel<D, G>(lane, e);
-    x[e] = 0.0f;
-    for (int w = 0; w < kSpWarps; ++w) x[e] = fmaf(s_acc[w][ch], f[w], x[e]);
-    x[e] *= inv;
-  }
-  if (a.rot_v) {
-    warp_fwht<D, G>(x, lane);
+    for (int u = 0; u < BPW; ++u) {
+      const int blk = warp + kWarps * u;
+      qs[u] = 0.0f;
+      if (blk < NB) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) x[e] *= inv_sqrt_group<G>();
-  }
+        for (int hf = 0; hf < 2; ++hf) {
+          const float4 x = *reinterpret_cast<const float4*>(sq + g * D + 32 * blk + 16 * hf + 4 * tig);
+          qs[u] += (x.x + x.y) + (x.z + x.w);
+          // (the high nibbles come 16 times too large)
+          const float w = hf && nib ? 0.0625f : 1.0f;
+          uint4 f;
+          split_h2(x.x * w, x.z * w, f.x, f.y);  // channels 4tig, 4tig + 2: high parts (row g), low parts (row g + 8)
+          split_h2(x.y * w, x.w * w, f.z, f.w);
+          fb[u][hf] = f;
+        }
+        qs[u] += __shfl_xor_sync(0xffffffffu, qs[u], 1);
+        qs[u] += __shfl_xor_sync(0xffffffffu, qs[u], 2);
+      }
+    }
+    __syncthreads();  // every warp has read the staged queries
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const size_t o = ((size_t)b * a.n_q_heads + hq) * D + fwht_channel<D, G>(lane, e);
-    if (a.out_dtype == KVQ_F32) static_cast<float*>(a.out)[o] = x[e];
-    else if (a.out_dtype == KVQ_BF16) static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(x[e]);
-    else static_cast<__half*>(a.out)[o] = __float2half_rn(x[e]);
+    for (int u = 0; u < BPW; ++u) {
+      const int blk = warp + kWarps * u;
+      if (blk < NB) {
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) qf[(blk * 2 + hf) * 32 + lane] = fb[u][hf];
+        if (tig == 0) qsum[blk * kMaxHeads + g] = qs[u] * 5.9604644775390625e-8f;  // in the mma's units, 2^-24
+      }
+    }
   }
+  __syncthreads();
+  const float f_tail = s_f[g] * 256.0f, f_body = s_f[g] * 16777216.0f;  // (tail rows go in times 2^-8)
+
+  // ---- main loop
+  float acc[NB][2][4];
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[i][j][r] = 0.0f;
+  float dmin[4] = {0.f, 0.f, 0.f, 0.f};
+  float m = -INFINITY, l = 0.0f;
+  bool timed_out = false;
+  int k = 0;
+  for (; k < issued; ++k) {
+    const int s = k % NS;
+    const bool arrived = mbar_wait_bounded(&wbar[s], (k / NS) & 1, kWaitCycles);
+    if (!__all_sync(0xffffffffu, arrived)) { timed_out = true; break; }
+    const int2 job = wjob[s];
+    const uint8_t* st = wst + s * a.s.bytes;
+    const int cnt = abs(job.y);
+    float sc[HB][2][2];
+#pragma unroll
+    for (int hh = 0; hh < HB; ++hh) sc[hh][0][0] = sc[hh][0][1] = sc[hh][1][0] = sc[hh][1][1] = 0.0f;
+    float f = f_body;
+    if (job.y > 0) {
+#define KVQ_SCORES(KT) \
+  case KT: body_scores<D, KT>(st, a.s, qf, qsum, lane, sc); break;
+      switch (c.k_type) {
+        KVQ_SCORES(KVQ_TYPE_Q4_0)
+        KVQ_SCORES(KVQ_TYPE_Q5_0)
+        KVQ_SCORES(KVQ_TYPE_Q8_0)
+        KVQ_SCORES(KVQ_TYPE_Q4_1)
+        KVQ_SCORES(KVQ_TYPE_Q5_1)
+      }
+#undef KVQ_SCORES
+    } else {
+      f = f_tail;
+      float cc[4] = {0.f, 0.f, 0.f, 0.f};
+      const float f1 = nib ? 0.0625f : 0.00390625f;  // times 16 where the fragments are 16 times smaller
+#pragma unroll 2
+      for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const uint2 x = *reinterpret_cast<const uint2*>(st + swz_off<WT>(g, 2 * (32 * i + 16 * hf + 4 * tig), kTailRows));
+          const uint4 q = qf[(2 * i + hf) * 32 + lane];
+          const uint32_t qa[4] = {q.x, q.y, q.z, q.w};
+          const float f0 = hf ? f1 : 0.00390625f;
+          mma16816(cc, qa, bf16x2_times(__byte_perm(x.x, x.y, 0x5410), f0), bf16x2_times(__byte_perm(x.x, x.y, 0x7632), f0));
+        }
+      sc[0][0][0] = cc[0] + cc[2];
+      sc[0][0][1] = cc[1] + cc[3];
+    }
+    // ---- online softmax (base 2) of head g; the tokens are 16hh + 8t + 2tig + e
+    const bool partial = cnt < RB;
+    float mx = -INFINITY;
+#pragma unroll
+    for (int hh = 0; hh < HB; ++hh)
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float& x = sc[hh][t][e];
+          x *= f;
+          if (partial && 16 * hh + 8 * t + 2 * tig + e >= cnt) x = -INFINITY;
+          mx = fmaxf(mx, x);
+        }
+    // m is a reference kLazyMax above the maximum at its last move (weights stay <= 1), so the
+    // rescale runs only when a score passes it
+    if (__any_sync(0xffffffffu, mx > m)) {
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const float nm = mx > m ? mx + kLazyMax : m;
+      const float r = m == -INFINITY ? 0.0f : fast_exp2(m - nm);
+      l *= r;
+      m = nm;
+      const float r0 = __shfl_sync(0xffffffffu, r, 8 * tig), r1 = __shfl_sync(0xffffffffu, r, 8 * tig + 4);
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) { acc[i][j][0] *= r0; acc[i][j][1] *= r1; acc[i][j][2] *= r0; acc[i][j][3] *= r1; }
+      dmin[0] *= r0; dmin[1] *= r1; dmin[2] *= r0; dmin[3] *= r1;
+    }
+    const float ms = m == -INFINITY ? 0.0f : m;
+    float p[HB][2][2];
+#pragma unroll
+    for (int hh = 0; hh < HB; ++hh)
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          p[hh][t][e] = fast_exp2(sc[hh][t][e] - ms);
+          l += p[hh][t][e];
+        }
+    // ---- P.V
+    if (job.y > 0) {
+      uint32_t ph[HB][2], pl[HB][2];
+      bool ok[HB][4];
+#pragma unroll
+      for (int hh = 0; hh < HB; ++hh)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          split_h2(p[hh][t][0], p[hh][t][1], ph[hh][t], pl[hh][t]);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) ok[hh][2 * t + e] = 16 * hh + 8 * t + 2 * tig + e < cnt;
+        }
+#define KVQ_VALUES(VT)                                                                                               \
+  case VT:                                                                                                           \
+    _Pragma("unroll") for (int hh = 0; hh < HB; ++hh) body_values<D, VT>(                                            \
+        smem_u32(st + a.s.v) + hh * 16 * box_w(VT == KVQ_TYPE_Q8_0 ? D : D / 2), st, a.s, 16 * hh, ph[hh], pl[hh], partial, \
+        ok[hh], lane, acc, dmin);                                                                                    \
+    break;
+      switch (c.v_type) {
+        KVQ_VALUES(KVQ_TYPE_Q4_0)
+        KVQ_VALUES(KVQ_TYPE_Q5_0)
+        KVQ_VALUES(KVQ_TYPE_Q8_0)
+        KVQ_VALUES(KVQ_TYPE_Q4_1)
+        KVQ_VALUES(KVQ_TYPE_Q5_1)
+      }
+#undef KVQ_VALUES
+    } else {
+      uint32_t bh_, bl_;
+      split_h2(p[0][0][0] * 256.0f, p[0][0][1] * 256.0f, bh_, bl_);
+      const bool ok0 = 2 * tig < cnt, ok1 = 2 * tig + 1 < cnt;
+      const uint8_t* vt = st + a.s.vt;
+#pragma unroll
+      for (int i = 0; i < 2 * NB; ++i) {  // channels 16i + 2g, + 1 of tokens 2tig, 2tig + 1
+        uint32_t w0 = *reinterpret_cast<const uint32_t*>(vt + swz_off<WT>(2 * tig, 2 * (16 * i + 2 * g), kTailRows));
+        uint32_t w1 = *reinterpret_cast<const uint32_t*>(vt + swz_off<WT>(2 * tig + 1, 2 * (16 * i + 2 * g), kTailRows));
+        w0 = ok0 ? w0 : 0u;
+        w1 = ok1 ? w1 : 0u;
+        const uint32_t av[4] = {bf16x2_to_h2_scaled(__byte_perm(w0, w1, 0x5410)),
+                                bf16x2_to_h2_scaled(__byte_perm(w0, w1, 0x7632)), 0u, 0u};
+        mma16816(acc[i / 2][i % 2], av, bh_, 0u);
+        mma16816(acc[i / 2][i % 2], av, bl_, 0u);
+      }
+    }
+    __syncwarp();
+    if (lane == 0) fence_proxy_async_smem();
+    issued += produce(s) ? 1 : 0;
+    __syncwarp();
+  }
+  if (timed_out) {
+    if (lane == 0) atomicOr(c.status, KVQ_DEV_ERR_TIMEOUT);
+    for (; k < issued; ++k) mbar_wait_bounded(&wbar[k % NS], (k / NS) & 1, kWaitCycles);  // copies still in flight
+  }
+
+  // ---- merge: every warp's partial to its CTA's shared memory, then each head by one warp of the cluster
+  l += __shfl_xor_sync(0xffffffffu, l, 1);
+  l += __shfl_xor_sync(0xffffffffu, l, 2);
+  if (tig == 0) {
+    s_m[warp * kMaxHeads + g] = m;
+    s_l[warp * kMaxHeads + g] = l;
+  }
+  __syncthreads();  // the stages are free
+  float* macc = reinterpret_cast<float*>(smem);  // [kWarps][8][D]
+#pragma unroll
+  for (int blk = 0; blk < NB; ++blk)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float* o = macc + (size_t)(warp * kMaxHeads + 2 * tig) * D + 32 * blk + 16 * j + 2 * g;
+      *reinterpret_cast<float2*>(o) = make_float2(acc[blk][j][0], acc[blk][j][2]);
+      *reinterpret_cast<float2*>(o + D) = make_float2(acc[blk][j][1], acc[blk][j][3]);
+    }
+  if (type_has_min(c.v_type)) {
+    __syncwarp();
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int blk = g + 8 * half;
+      if (blk < NB) {
+        float* o = macc + (size_t)(warp * kMaxHeads + 2 * tig) * D + 32 * blk;
+#pragma unroll 8
+        for (int i = 0; i < 32; ++i) {
+          o[i] += dmin[2 * half];
+          o[D + i] += dmin[2 * half + 1];
+        }
+      }
+    }
+  }
+  // the CTA's warps: every thread sums its (head, channel) elements, in the frame of the CTA's maximum
+  __syncthreads();
+  float* s_cta = s_f;  // [8]: the CTA's maximum per head; its sum goes to s_l[head] (the factors are done with)
+  for (int i = tid; i < kMaxHeads * D / 4; i += 32 * kWarps) {
+    const int hh = i / (D / 4);
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w * kMaxHeads + hh]);
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float mw = s_m[w * kMaxHeads + hh];
+      const float f = mw == -INFINITY ? 0.0f : fast_exp2(mw - M);  // (a warp without tokens: zeros)
+      const float4 x = reinterpret_cast<const float4*>(macc)[w * (kMaxHeads * D / 4) + i];
+      v.x = fmaf(x.x, f, v.x); v.y = fmaf(x.y, f, v.y); v.z = fmaf(x.z, f, v.z); v.w = fmaf(x.w, f, v.w);
+    }
+    reinterpret_cast<float4*>(macc)[i] = v;  // (only this thread reads element i of warp 0's partial)
+  }
+  float cm = -INFINITY, csum = 0.0f;
+  if (tid < kMaxHeads) {
+    for (int w = 0; w < kWarps; ++w) cm = fmaxf(cm, s_m[w * kMaxHeads + tid]);
+    for (int w = 0; w < kWarps; ++w) {
+      const float mw = s_m[w * kMaxHeads + tid];
+      if (mw != -INFINITY) csum = fmaf(s_l[w * kMaxHeads + tid], fast_exp2(mw - cm), csum);
+    }
+  }
+  __syncthreads();
+  if (tid < kMaxHeads) {
+    s_cta[tid] = cm;
+    s_l[tid] = csum;
+  }
+  // the cluster's CTAs: head hh by warp hh / S of rank hh % S
+  cg::cluster_group cl = cg::this_cluster();
+  cl.sync();
+  for (int hh = rank + S * warp; hh < nheads; hh += S * kWarps) {
+    float cmx[kMaxCluster], cl_[kMaxCluster], xs[kMaxCluster][NB], x[NB];
+    float M = -INFINITY, Lsum = 0.0f;
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) {  // every load before the first use
+      if (r < S) {
+        cmx[r] = cl.map_shared_rank(s_cta, r)[hh];
+        cl_[r] = cl.map_shared_rank(s_l, r)[hh];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NB; ++j) x[j] = 0.0f;
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r)
+      if (r < S) M = fmaxf(M, cmx[r]);
+#pragma unroll
+    for (int r0 = 0; r0 < kMaxCluster; r0 += 4) {
+#pragma unroll
+      for (int r = r0; r < r0 + 4; ++r)
+        if (r < S) {
+          const float* ra = cl.map_shared_rank(macc, r) + hh * D;
+#pragma unroll
+          for (int j = 0; j < NB; ++j) xs[r][j] = ra[fwht_channel<D, G>(lane, j)];
+        }
+#pragma unroll
+      for (int r = r0; r < r0 + 4; ++r)
+        if (r < S) {
+          const float f = cmx[r] == -INFINITY ? 0.0f : fast_exp2(cmx[r] - M);
+          Lsum = fmaf(cl_[r], f, Lsum);
+#pragma unroll
+          for (int j = 0; j < NB; ++j) x[j] = fmaf(xs[r][j], f, x[j]);
+        }
+    }
+    const float inv = Lsum > 0.0f ? 1.0f / Lsum : 0.0f;
+#pragma unroll
+    for (int j = 0; j < NB; ++j) x[j] *= inv;
+    if (a.rot_v) {
+      warp_fwht<D, G>(x, lane);
+#pragma unroll
+      for (int j = 0; j < NB; ++j) x[j] *= inv_sqrt_group<G>();
+    }
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      const size_t o = ((size_t)b * a.n_q_heads + head0 + hh) * D + fwht_channel<D, G>(lane, j);
+      if (a.out_dtype == KVQ_F32) static_cast<float*>(a.out)[o] = x[j];
+      else if (a.out_dtype == KVQ_BF16) static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(x[j]);
+      else static_cast<__half*>(a.out)[o] = __float2half_rn(x[j]);
+    }
+  }
+  cl.sync();  // no CTA leaves while another reads its partials
+}
+
+template <int D>
+cudaError_t run_sparse(SpArgs& a, cudaStream_t st) {
+  constexpr int NB = D / 32, RB = kRows<D>, kWarps = kW<D>;
+  const kvq_cache& c = a.c;
+  const int rowK = int(qs_row_bytes_host(c.k_type, D)), rowV = int(qs_row_bytes_host(c.v_type, D));
+  const int kh = NB * (type_has_min(c.k_type) ? 4 : 2), vh = NB * (type_has_min(c.v_type) ? 4 : 2);
+  SpStage& s = a.s;
+  s.kh = kh;
+  s.vh = vh;
+  s.v = align_up(RB * rowK, 1024);
+  s.kd = s.v + RB * rowV;
+  s.vd = s.kd + RB * kh;
+  s.kqh = s.vd + RB * vh;
+  s.vqh = s.kqh + (type_has_qh(c.k_type) ? RB * NB * 4 : 0);
+  const int body = s.vqh + (type_has_qh(c.v_type) ? RB * NB * 4 : 0);
+  s.tx = uint32_t(RB * (rowK + rowV + kh + vh) + (type_has_qh(c.k_type) ? RB * NB * 4 : 0) +
+                  (type_has_qh(c.v_type) ? RB * NB * 4 : 0));
+  s.vt = align_up(kTailRows * 2 * D, 1024);
+  const int tail = c.tail_len > 0 ? s.vt + kTailRows * 2 * D : 0;
+  s.bytes = align_up(std::max(body, tail), 1024);
+  const int rest = 32 * D + (NB + 2 * kWarps + 1) * kMaxHeads * 4 + kWarps * kMaxStages * 16 + 1024;
+  // as many stages as leave room for kSpCtas<D> CTAs on an SM (228 KB, 1 KB of it reserved per CTA), two at
+  // least (the merge's partials, 32 * D bytes per warp, fit two stages of any pair: 2 * RB * D)
+  const int room = 228 * 1024 / kSpCtas<D> - 1024 - rest;
+  s.stages = std::min(kMaxStages, std::max(2, room / (kWarps * s.bytes)));
+  const int bytes = kWarps * s.stages * s.bytes + rest;
+
+  alignas(64) CUtensorMap mk, mv, mkt, mvt;
+  memset(&mkt, 0, sizeof(mkt));
+  memset(&mvt, 0, sizeof(mvt));
+  if (!make_map(&mk, c.k_qs, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, body_rows(c), rowK, box_w(rowK), RB) ||
+      !make_map(&mv, c.v_qs, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, body_rows(c), rowV, box_w(rowV), RB))
+    return cudaErrorInvalidValue;
+  if (c.tail_len > 0) {
+    const long long trows = (long long)c.batch * c.n_kv_heads * c.tail_len;
+    if (!make_map(&mkt, c.k_tail, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, trows, 2 * D, box_w(2 * D), kTailRows) ||
+        !make_map(&mvt, c.v_tail, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, trows, 2 * D, box_w(2 * D), kTailRows))
+      return cudaErrorInvalidValue;
+  }
+  auto kern = sparse_kernel<D>;
+  cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), bytes);
+  if (e != cudaSuccess) return e;
+  // CTAs per row: as many as one wave holds, a tile per warp at least.  (Clusters of 8 do not fill
+  // every SM group to the last SM: with 7/8 of the slots the wave stays one.)
+  const long long rows = (long long)c.batch * c.n_kv_heads * a.head_groups;
+  const long long tiles = (long long)a.n_select * (a.block_tokens / RB);
+  const int sms = device_sm_count();
+  const int per_sm = std::min(kSpCtas<D>, 228 * 1024 / (bytes + 1024));
+  const long long slots = (long long)(sms > 0 ? sms : 148) * per_sm;
+  const int S = int(std::max<long long>(1, std::min<long long>({kMaxCluster, slots * 7 / 8 / rows, tiles / kWarps})));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(rows * S));
+  cfg.blockDim = dim3(32 * kWarps);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = S;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, a, mk, mv, mkt, mvt);
 }
 
 }  // namespace
@@ -136,18 +771,21 @@ __global__ void __launch_bounds__(kSpWarps * 32) sparse_kernel(SparseArgs a) {
 cudaError_t launch_sparse_decode(const kvq_cache& c, Rot rot, const void* q, int q_dtype, int n_q_heads, float scale,
                                  int block_tokens, const int32_t* sel, int n_select, void* out, int out_dtype,
                                  cudaStream_t st) {
-  SparseArgs a{c, q, sel, out, q_dtype, out_dtype, n_q_heads, n_q_heads / c.n_kv_heads, block_tokens, n_select,
-               rot.k, rot.v, scale * 1.4426950408889634f};
-  const dim3 grid(n_q_heads, c.batch);
+  SpArgs a{};
+  a.c = c; a.q = q; a.sel = sel; a.out = out;
+  a.q_dtype = q_dtype; a.out_dtype = out_dtype; a.n_q_heads = n_q_heads; a.group = n_q_heads / c.n_kv_heads;
+  a.head_groups = (a.group + kMaxHeads - 1) / kMaxHeads;
+  a.heads_per_cta = (a.group + a.head_groups - 1) / a.head_groups;
+  a.block_tokens = block_tokens; a.n_select = n_select; a.rot_k = rot.k; a.rot_v = rot.v;
+  a.scale_log2 = scale * kLog2e;
   switch (c.head_dim) {
-    case 64: sparse_kernel<64><<<grid, kSpWarps * 32, 0, st>>>(a); break;
-    case 128: sparse_kernel<128><<<grid, kSpWarps * 32, 0, st>>>(a); break;
-    case 192: sparse_kernel<192><<<grid, kSpWarps * 32, 0, st>>>(a); break;
-    case 256: sparse_kernel<256><<<grid, kSpWarps * 32, 0, st>>>(a); break;
-    case 320: sparse_kernel<320><<<grid, kSpWarps * 32, 0, st>>>(a); break;
+    case 64: return run_sparse<64>(a, st);
+    case 128: return run_sparse<128>(a, st);
+    case 192: return run_sparse<192>(a, st);
+    case 256: return run_sparse<256>(a, st);
+    case 320: return run_sparse<320>(a, st);
     default: return cudaErrorInvalidValue;
   }
-  return cudaGetLastError();
 }
 
 }  // namespace kvq

@@ -159,18 +159,34 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+_raw_stream = None  # device index -> its current stream's handle
+_dtype_ids = None
+
+
 def _stream(stream) -> Optional[int]:
+    global _raw_stream
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _raw_stream is None:
+            # the handle without a torch.cuda.Stream object around it: 0.1 us instead of 2.9 us a call
+            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+                (lambda device: torch.cuda.current_stream(device).cuda_stream)
+        return _raw_stream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
 
 
+def _dtypes() -> dict:
+    global _dtype_ids
+    if _dtype_ids is None:
+        import torch
+        _dtype_ids = {torch.float32: KVQ_F32, torch.bfloat16: KVQ_BF16, torch.float16: KVQ_F16}
+    return _dtype_ids
+
+
 def _dtype_id(t) -> int:
-    import torch
-    return {torch.float32: KVQ_F32, torch.bfloat16: KVQ_BF16, torch.float16: KVQ_F16}[t.dtype]
+    return _dtypes()[t.dtype]
 
 
 # ---- the C entry points, same names -----------------------------------------
@@ -237,33 +253,32 @@ def kvq_prefill_attention(cache: kvq_cache, q, out, workspace, q_pos0=None, caus
            "kvq_prefill_attention")
 
 
-def _expect(what: str, shape, dtypes, *tensors, contiguous=True):
-    """ValueError unless the tensors (None allowed) lie on the current device and have that shape and a type of `dtypes`."""
+def _expect(what: str, shape, dtype, *tensors):
+    """ValueError unless the tensors (None allowed) are contiguous, on the current device and of that shape and type
+    (None: any shape; any of the q / k / v types)."""
     import torch
     dev = torch.cuda.current_device()
     for t in tensors:
         if t is None:
             continue
-        if t.get_device() != dev:
-            raise ValueError(f"{what}: a tensor is not on the current CUDA device")
-        if t.dtype not in dtypes or (shape is not None and tuple(t.shape) != shape):
-            raise ValueError(f"{what}: expected {shape} of {dtypes}, got {tuple(t.shape)} of {t.dtype}")
-        if contiguous and not t.is_contiguous():
-            raise ValueError(f"{what}: a tensor is not contiguous")
+        if (t.get_device() != dev or not t.is_contiguous() or (shape is not None and t.shape != shape) or
+                (t.dtype is not dtype if dtype is not None else t.dtype not in _dtypes())):
+            raise ValueError(f"{what}: expected {shape or 'any shape'} of {dtype or 'fp32, bf16 or fp16'}, contiguous, on "
+                             f"CUDA device {dev}; got {tuple(t.shape)} of {t.dtype} on {t.device}")
 
 
 def _heads_row_stride(what: str, t, heads: int, d: int, n_rows: int, like) -> int:
     """Row stride (elements) of projection rows [n_rows][heads * d] or [n_rows][heads][d] whose heads lie side by side."""
-    ok = t.dtype == like.dtype and t.get_device() == like.get_device() and t.shape[0] == n_rows
-    if t.dim() == 2:
-        ok = ok and t.shape[1] == heads * d and (t.stride(1) == 1 or n_rows == 0)
-    else:
-        ok = ok and t.dim() == 3 and t.shape[1] == heads and t.shape[2] == d and \
-            (n_rows == 0 or (t.stride(2) == 1 and (heads == 1 or t.stride(1) == d)))
-    if not ok:
-        raise ValueError(f"{what}: expected {n_rows} rows of {heads} x {d} values of {like.dtype}, heads side by side")
-    # (the stride of a single row is free: torch may report any number)
-    return t.stride(0) if n_rows > 1 else max(t.stride(0), heads * d)
+    shape, stride = t.shape, t.stride()
+    if t.dtype is like.dtype and t.get_device() == like.get_device() and shape[0] == n_rows:
+        if len(shape) == 2:
+            ok = shape[1] == heads * d and (stride[1] == 1 or n_rows == 0)
+        else:
+            ok = shape[1:] == (heads, d) and (n_rows == 0 or (stride[2] == 1 and (heads == 1 or stride[1] == d)))
+        if ok:
+            # (the stride of a single row is free: torch may report any number)
+            return stride[0] if n_rows > 1 else heads * d
+    raise ValueError(f"{what}: expected {n_rows} rows of {heads} x {d} values of {like.dtype}, heads side by side")
 
 
 class RopeNorm:
@@ -271,9 +286,8 @@ class RopeNorm:
 
     def __init__(self, inv_freq=None, q_weight=None, k_weight=None, eps=1e-6, interleaved=False):
         import torch
-        floats = (torch.float32, torch.bfloat16, torch.float16)
-        _expect("RopeNorm", None, (torch.float32,), inv_freq)
-        _expect("RopeNorm", None, floats, q_weight, k_weight)
+        _expect("RopeNorm", None, torch.float32, inv_freq)
+        _expect("RopeNorm", None, None, q_weight, k_weight)
         if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
             raise ValueError("RopeNorm: q_weight and k_weight differ in type")
         self.inv_freq, self.q_weight, self.k_weight = inv_freq, q_weight, k_weight  # kept alive
@@ -282,6 +296,9 @@ class RopeNorm:
         self.desc.interleaved = 1 if interleaved else 0
         self.desc.eps = eps
         w = q_weight if q_weight is not None else k_weight
+        self.weight_dim = 0 if w is None else w.numel()
+        if k_weight is not None and k_weight.numel() != self.weight_dim:
+            raise ValueError("RopeNorm: q_weight and k_weight differ in size")
         self.desc.weight_dtype = KVQ_F32 if w is None else _dtype_id(w)
         self.desc.q_weight, self.desc.k_weight = _ptr(q_weight), _ptr(k_weight)
         self.desc.inv_freq = None if self.desc.rot_dim == 0 else _ptr(inv_freq)
@@ -291,14 +308,13 @@ def kvq_qk_norm_rope(cache: kvq_cache, rope: RopeNorm, q, k, v, pos, q_out, k_ou
     """Rows q [n][heads * d] or [n][heads][d] (any row stride, e.g. parts of one projection), k and v (or None) the same
     with the KV heads; pos int32 [n], dst_row int32 [n] or None.  Outputs [rows][heads][d], or [..][heads][d] contiguous."""
     import torch
-    d, hkv, hq, n = cache.head_dim, cache.n_kv_heads, q_out.shape[-2], q.shape[0]
+    d, hkv, (hq, dq), n = cache.head_dim, cache.n_kv_heads, q_out.shape[-2:], q.shape[0]
     rows = q_out.numel() // max(1, hq * d)
-    for w in (rope.q_weight, rope.k_weight):
-        if w is not None and w.numel() != d:
-            raise ValueError("kvq_qk_norm_rope: a weight has not head_dim values")
-    _expect("kvq_qk_norm_rope: pos, dst_row", (n,), (torch.int32,), pos, dst_row)
-    _expect("kvq_qk_norm_rope: outputs", None, (q.dtype,), q_out, k_out, v_out)
-    if q_out.shape[-1] != d or k_out.numel() != rows * hkv * d or (v_out is not None and v_out.numel() != rows * hkv * d):
+    if rope.weight_dim not in (0, d):
+        raise ValueError("kvq_qk_norm_rope: a weight has not head_dim values")
+    _expect("kvq_qk_norm_rope: pos, dst_row", (n,), torch.int32, pos, dst_row)
+    _expect("kvq_qk_norm_rope: outputs", None, q.dtype, q_out, k_out, v_out)
+    if dq != d or k_out.numel() != rows * hkv * d or (v_out is not None and v_out.numel() != rows * hkv * d):
         raise ValueError("kvq_qk_norm_rope: the outputs differ in rows, heads or head_dim")
     qs = _heads_row_stride("kvq_qk_norm_rope: q", q, hq, d, n, q_out)
     ks = _heads_row_stride("kvq_qk_norm_rope: k", k, hkv, d, n, q_out)
@@ -329,12 +345,12 @@ def kvq_page_update(cache: kvq_cache, pool, n_new, n_new_max: int, granted, row_
                     seq_len_out=None, stream=None):
     """pool: PagePool or kvq_page_pool; n_new, granted, seq_len_out int32 [batch]; the row maps int32 [max_rows]."""
     import torch
-    _expect("kvq_page_update", (cache.batch,), (torch.int32,), n_new, granted, seq_len_out)
+    _expect("kvq_page_update", (cache.batch,), torch.int32, n_new, granted, seq_len_out)
     rows = next((t.numel() for t in (row_pos, row_dst, row_slot) if t is not None), None)
     if rows is None:
         rows = min(cache.batch * n_new_max, 0x7fffffff)  # no maps: no limit of rows
     else:
-        _expect("kvq_page_update: row maps", (rows,), (torch.int32,), row_pos, row_dst, row_slot)
+        _expect("kvq_page_update: row maps", (rows,), torch.int32, row_pos, row_dst, row_slot)
     desc = pool.desc if isinstance(pool, PagePool) else pool
     _check(lib().kvq_page_update(ctypes.byref(cache), ctypes.byref(desc), _ptr(n_new), n_new_max, _ptr(granted), rows,
                                  _ptr(row_pos), _ptr(row_dst), _ptr(row_slot), _ptr(seq_len_out), _stream(stream)),
@@ -365,9 +381,8 @@ def kvq_block_index_update(cache: kvq_cache, index, n_last: int = 0, stream=None
 def kvq_select_blocks(cache: kvq_cache, index, q, sel, n_first: int = 1, n_last: int = 1, stream=None):
     """q [batch][n_q_heads][head_dim]; sel int32 [batch][n_kv_heads][n_select]."""
     import torch
-    _expect("kvq_select_blocks: q", (cache.batch, q.shape[1], cache.head_dim),
-            (torch.float32, torch.bfloat16, torch.float16), q)
-    _expect("kvq_select_blocks: sel", (cache.batch, cache.n_kv_heads, sel.shape[-1]), (torch.int32,), sel)
+    _expect("kvq_select_blocks: q", (cache.batch, q.shape[1], cache.head_dim), None, q)
+    _expect("kvq_select_blocks: sel", (cache.batch, cache.n_kv_heads, sel.shape[-1]), torch.int32, sel)
     _check(lib().kvq_select_blocks(ctypes.byref(cache), ctypes.byref(_index_desc(index)), _ptr(q), _dtype_id(q),
                                    q.shape[1], n_first, n_last, sel.shape[-1], _ptr(sel), _stream(stream)),
            "kvq_select_blocks")
@@ -376,9 +391,8 @@ def kvq_select_blocks(cache: kvq_cache, index, q, sel, n_first: int = 1, n_last:
 def kvq_sparse_decode_attention(cache: kvq_cache, q, sel, out, block_tokens: int, scale: float = 0.0, stream=None):
     """q, out [batch][n_q_heads][head_dim]; sel int32 [batch][n_kv_heads][n_select] block numbers (negative: none)."""
     import torch
-    _expect("kvq_sparse_decode_attention: q, out", (cache.batch, q.shape[1], cache.head_dim),
-            (torch.float32, torch.bfloat16, torch.float16), q, out)
-    _expect("kvq_sparse_decode_attention: sel", (cache.batch, cache.n_kv_heads, sel.shape[-1]), (torch.int32,), sel)
+    _expect("kvq_sparse_decode_attention: q, out", (cache.batch, q.shape[1], cache.head_dim), None, q, out)
+    _expect("kvq_sparse_decode_attention: sel", (cache.batch, cache.n_kv_heads, sel.shape[-1]), torch.int32, sel)
     _check(lib().kvq_sparse_decode_attention(ctypes.byref(cache), _ptr(q), _dtype_id(q), q.shape[1], float(scale),
                                              block_tokens, _ptr(sel), sel.shape[-1], _ptr(out), _dtype_id(out),
                                              _stream(stream)),

@@ -387,9 +387,10 @@ kvq_status kvq_sparse_decode_attention(const kvq_cache* c, const void* q, int32_
   if (!q || !out || !aligned16(q) || !aligned16(out) || (n_select && !sel) || !aligned4(sel)) return KVQ_ERR_INVALID_ARG;
   if (!(scale >= 0.0f) || scale > 1e30f) return KVQ_ERR_INVALID_ARG;
   if (!sparse_supported(c)) return KVQ_ERR_UNSUPPORTED;
-  // rows of the planes are 32-bit copy coordinates; up to 8 CTAs per (sequence, KV head, 8 query heads)
+  // rows of the planes are 32-bit copy coordinates; up to 16 CTAs per (sequence, KV head, 8 query heads)
   const long long prow = (long long)c->batch * c->n_kv_heads, groups = (n_q_heads / c->n_kv_heads + 7) / 8;
-  if (kvq::body_row_count(*c) > 0x7fffffffLL || prow * c->tail_len > 0x7fffffffLL || prow * groups * 8 > 0x7fffffffLL)
+  if (kvq::body_row_count(*c) > 0x7fffffffLL || prow * c->tail_len > 0x7fffffffLL || prow * groups * 16 > 0x7fffffffLL ||
+      (long long)n_select * (block_tokens / 16) > 0x3fffffffLL)
     return KVQ_ERR_UNSUPPORTED;
   const float sc = scale == 0.0f ? 1.0f / sqrtf(float(c->head_dim)) : scale;
   return from_cuda(kvq::launch_sparse_decode(*c, r, q, q_dtype, n_q_heads, sc, block_tokens, sel, n_select, out,

@@ -50,6 +50,21 @@ inline cudaError_t ensure_dynamic_smem(const void* kernel, int bytes) {
   return e;
 }
 
+// Allows a kernel clusters of more than 8 CTAs, once per device.
+inline cudaError_t allow_large_clusters(const void* kernel) {
+  constexpr int kMaxDevices = 64;
+  static std::mutex mu;
+  static std::unordered_map<const void*, bool[kMaxDevices]> done;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(mu);
+  if (dev >= 0 && dev < kMaxDevices && done[kernel][dev]) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess && dev >= 0 && dev < kMaxDevices) done[kernel][dev] = true;
+  return e;
+}
+
 // Launchers (arguments already validated by the API layer).
 // SMs of the current device (0 when the query fails).
 int device_sm_count();

@@ -32,7 +32,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kTailRows = 8;   // tokens of a tail tile
 constexpr int kMaxStages = 4;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
 
 template <int D> constexpr int kRows = D <= 128 ? 32 : 16;               // tokens of a body tile
 template <int D> constexpr int kW = D <= 128 ? 8 : D <= 256 ? 6 : 8;      // warps of a CTA
@@ -52,8 +52,48 @@ struct SpArgs {
   const int32_t* sel;
   void* out;
   int q_dtype, out_dtype, n_q_heads, group, head_groups, heads_per_cta, block_tokens, n_select, rot_k, rot_v;
+  int tiles, pages_per_seq;                 // tiles of a list; page table entries of a sequence
+  DivU32 by_block, by_page, by_tail, by_plane;  // tiles of a block, tokens of a page, tail slots, planes of a sequence
   float scale_log2;
 };
+
+// Shared-memory loads by 32-bit address: from generic pointers into the stages the compiler
+// makes generic loads with 64-bit address arithmetic.
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t r;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 r;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
+  return r;
+}
+// BYTES as words, in the widest loads that rows of BYTES bytes from a 16-byte aligned base allow
+template <int BYTES>
+__device__ __forceinline__ void lds_row(uint32_t a, uint32_t (&w)[BYTES / 4]) {
+  if constexpr (BYTES % 16 == 0) {
+#pragma unroll
+    for (int i = 0; i < BYTES / 16; ++i) {
+      const uint4 v = lds128(a + 16 * i);
+      w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+    }
+  } else if constexpr (BYTES % 8 == 0) {
+#pragma unroll
+    for (int i = 0; i < BYTES / 8; ++i) {
+      const uint2 v = lds64(a + 8 * i);
+      w[2 * i] = v.x; w[2 * i + 1] = v.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < BYTES / 4; ++i) w[i] = lds32(a + 4 * i);
+  }
+}
 
 // codes of the low (H16 false) or high nibbles as fp16 subnormals: bits 0-4 / 16-20, or
 // bits 4-8 / 20-24 (16 times the value), the 5-bit formats' high bits in place already
@@ -69,15 +109,14 @@ __device__ __forceinline__ void mma16816_from(float (&d)[4], const uint32_t (&a)
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(0.0f));
 }
 
-// Scores of a body tile (st: its stage): S[hh][t][e] of tokens 16hh + 8t + 2tig + e and head g.
+// Scores of a body tile (st, qf, qsum: shared addresses of its stage, the query fragments and block sums): S[hh][t][e] of tokens 16hh + 8t + 2tig + e and head g.
 template <int D, int KT>
-__device__ __forceinline__ void body_scores(const uint8_t* st, const SpStage& L, const uint4* qf, const float* qsum, int lane,
+__device__ __forceinline__ void body_scores(uint32_t st, const SpStage& L, uint32_t qf, uint32_t qsum, int lane,
                                             float (&S)[kRows<D> / 16][2][2]) {
   constexpr int NB = D / 32, RB = kRows<D>, HB = RB / 16, ROW = KT == KVQ_TYPE_Q8_0 ? D : D / 2, W = box_w(ROW);
   constexpr bool K1 = type_has_min(KT), K5 = type_has_qh(KT);
   constexpr int KHH = K1 ? 2 : 1, HW = NB * KHH / 2;
   const int g = lane >> 2, tig = lane & 3, mi = lane >> 3, rr = (lane & 7) + 8 * (mi & 1);
-  const uint32_t kb = smem_u32(st);
   uint32_t lb[W / 32];
   swz_lane<W>(rr, mi >> 1, lb);
   uint32_t hd[HB][4][HW];  // headers of tokens 16hh + 2tig, + 1, + 8, + 9
@@ -85,7 +124,7 @@ __device__ __forceinline__ void body_scores(const uint8_t* st, const SpStage& L,
   for (int hh = 0; hh < HB; ++hh)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      lds_words<NB * 2 * KHH>(st + L.kd + (16 * hh + 2 * tig + (i & 1) + 8 * (i >> 1)) * NB * 2 * KHH, hd[hh][i]);
+      lds_row<NB * 2 * KHH>(st + L.kd + 2 * tig * NB * 2 * KHH + (16 * hh + (i & 1) + 8 * (i >> 1)) * NB * 2 * KHH, hd[hh][i]);
   const float off = KT == KVQ_TYPE_Q8_0 ? 128.0f : float(type_code_offset(KT));
   // operands of the two k-steps of block blk for the 8-token tiles of half hh
   auto dots = [&](int blk, int hh, const uint32_t (&b)[2][4], const uint32_t (&a0)[4], const uint32_t (&a1)[4], float qs) {
@@ -111,14 +150,14 @@ __device__ __forceinline__ void body_scores(const uint8_t* st, const SpStage& L,
 #pragma unroll
     for (int hh = 0; hh < HB; ++hh) {
       const int j = KT == KVQ_TYPE_Q8_0 ? 2 * bp : bp;  // its first 16-byte chunk
-      ldsm_x4(kb + hh * 16 * W + lb[swz_lane_idx<W>(j)] + swz_box_off<W, RB>(j), r[hh][0], r[hh][1], r[hh][2], r[hh][3]);
+      ldsm_x4(st + hh * 16 * W + lb[swz_lane_idx<W>(j)] + swz_box_off<W, RB>(j), r[hh][0], r[hh][1], r[hh][2], r[hh][3]);
     }
 #pragma unroll
     for (int e = 0; e < BP; ++e) {
       const int blk = bp + e;
-      const uint4 qa = qf[(blk * 2) * 32 + lane], qb = qf[(blk * 2 + 1) * 32 + lane];
+      const uint4 qa = lds128(qf + lane * 16 + blk * 1024), qb = lds128(qf + lane * 16 + blk * 1024 + 512);
       const uint32_t a0[4] = {qa.x, qa.y, qa.z, qa.w}, a1[4] = {qb.x, qb.y, qb.z, qb.w};
-      const float qs = qsum[blk * kMaxHeads + g];
+      const float qs = __uint_as_float(lds32(qsum + g * 4 + blk * (kMaxHeads * 4)));
 #pragma unroll
       for (int hh = 0; hh < HB; ++hh) {
         uint32_t b[2][4];
@@ -133,7 +172,7 @@ __device__ __forceinline__ void body_scores(const uint8_t* st, const SpStage& L,
             const uint32_t w = r[hh][2 * e + t], w8 = w >> 8;
             uint32_t h0 = 0, h1 = 0;
             if constexpr (K5) {  // rotated: the pairs' bits at 4 / 20 (low nibbles) and 8 / 24
-              const uint32_t h = reinterpret_cast<const uint32_t*>(st + L.kqh)[(16 * hh + 8 * t + g) * NB + blk];
+              const uint32_t h = lds32(st + L.kqh + g * NB * 4 + ((16 * hh + 8 * t) * NB + blk) * 4);
               h0 = __funnelshift_r(h, h, k0);
               h1 = __funnelshift_r(h, h, k1);
             }
@@ -149,12 +188,12 @@ __device__ __forceinline__ void body_scores(const uint8_t* st, const SpStage& L,
   }
 }
 
-// acc += codes_V^T . (P * scale) of 16 body rows: rows 2g (acc .. [0], [1]) and 2g + 1 of each
+// acc += codes_V^T . (P * scale) of the 16 body rows from row0: rows 2g (acc .. [0], [1]) and 2g + 1 of each
 // 16 channels, columns heads 2tig, 2tig + 1; dmin += the blocks' minima . P (rows blocks g, g + 8).
-// ok[i]: token i of the lane's four lies below the tile's end.
+// cnt: the tile's tokens.
 template <int D, int VT>
-__device__ __forceinline__ void body_values(uint32_t vb, const uint8_t* st, const SpStage& L, int row0, const uint32_t (&ph)[2],
-                                            const uint32_t (&pl)[2], bool partial, const bool (&ok)[4], int lane,
+__device__ __forceinline__ void body_values(uint32_t st, const SpStage& L, int row0, const uint32_t (&ph)[2],
+                                            const uint32_t (&pl)[2], int cnt, int lane,
                                             float (&acc)[D / 32][2][4], float (&dmin)[4]) {
   constexpr int NB = D / 32, RB = kRows<D>, ROW = VT == KVQ_TYPE_Q8_0 ? D : D / 2, W = box_w(ROW);
   constexpr bool V1 = type_has_min(VT), V5 = type_has_qh(VT);
@@ -162,15 +201,17 @@ __device__ __forceinline__ void body_values(uint32_t vb, const uint8_t* st, cons
   const int g = lane >> 2, tig = lane & 3, mi = lane >> 3, rr = (lane & 7) + 8 * (mi & 1);
   uint32_t lb[W / 32];
   swz_lane<W>(rr, mi >> 1, lb);
-  const uint8_t* vd = st + L.vd + (row0 + 2 * tig) * NB * 2 * VHH;
+  const uint32_t vb = st + L.v + row0 * W, vd = st + L.vd + (row0 + 2 * tig) * NB * 2 * VHH;
   uint32_t vh[4][VW];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    lds_words<NB * 2 * VHH>(vd + ((i & 1) + 8 * (i >> 1)) * NB * 2 * VHH, vh[i]);
-    if (partial) {  // rows past the end hold anything: their headers become zero
+  for (int i = 0; i < 4; ++i) lds_row<NB * 2 * VHH>(vd + ((i & 1) + 8 * (i >> 1)) * NB * 2 * VHH, vh[i]);
+  auto ok = [&](int i) { return row0 + (i & 1) + 8 * (i >> 1) < cnt - 2 * tig; };  // token i of the lane's four is one
+  const bool partial = cnt < RB;
+  if (partial) {  // rows past the end hold anything: their headers become zero
 #pragma unroll
-      for (int j = 0; j < VW; ++j) vh[i][j] = ok[i] ? vh[i][j] : 0u;
-    }
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < VW; ++j) vh[i][j] = ok(i) ? vh[i][j] : 0u;
   }
   auto scales = [&](int blk, int a, int b) -> uint32_t {
     if constexpr (VHH == 1) return __byte_perm(vh[a][blk >> 1], vh[b][blk >> 1], (blk & 1) ? 0x7632 : 0x5410);
@@ -188,9 +229,9 @@ __device__ __forceinline__ void body_values(uint32_t vb, const uint8_t* st, cons
   if constexpr (V1) {
     auto lo2 = [&](int blk, int i) -> uint32_t {
       const int bb = blk < NB ? blk : NB - 1;
-      uint32_t w0 = *reinterpret_cast<const uint32_t*>(vd + (8 * (i >> 1) * NB + bb) * 4);
-      uint32_t w1 = *reinterpret_cast<const uint32_t*>(vd + ((8 * (i >> 1) + 1) * NB + bb) * 4);
-      if (partial) { w0 = ok[i] ? w0 : 0u; w1 = ok[i + 1] ? w1 : 0u; }
+      uint32_t w0 = lds32(vd + (8 * (i >> 1) * NB + bb) * 4);
+      uint32_t w1 = lds32(vd + ((8 * (i >> 1) + 1) * NB + bb) * 4);
+      if (partial) { w0 = ok(i) ? w0 : 0u; w1 = ok(i + 1) ? w1 : 0u; }
       return blk < NB ? __byte_perm(w0, w1, 0x7632) : 0u;
     };
     const uint32_t al[4] = {lo2(g, 0), NB > 8 ? lo2(g + 8, 0) : 0u, lo2(g, 2), NB > 8 ? lo2(g + 8, 2) : 0u};
@@ -223,8 +264,7 @@ __device__ __forceinline__ void body_values(uint32_t vb, const uint8_t* st, cons
           const uint32_t w = r[2 * e + t], w8 = w >> 8;
           uint32_t m0 = 0x64006400u, m1 = m0, m2 = m0, m3 = m0;
           if constexpr (V5) {  // the lane's part word of rows 8t + 2tig, + 1
-            const uint32_t h = *reinterpret_cast<const uint32_t*>(
-                st + L.vqh + (((row0 / 2 + 4 * t + tig) * NB + blk) * 2 + (g >> 2)) * 4);
+            const uint32_t h = lds32(st + L.vqh + (tig * NB * 2 + (g >> 2)) * 4 + ((row0 / 2 + 4 * t) * NB + blk) * 8);
             const uint32_t h0 = __funnelshift_r(h, h, v0), h1 = __funnelshift_r(h, h, v1);
             m0 = vhb(h0, 0x00100010u); m1 = vhb(h1, 0x00100010u);
             m2 = vhb(h0, 0x01000100u); m3 = vhb(h1, 0x01000100u);
@@ -240,9 +280,11 @@ __device__ __forceinline__ void body_values(uint32_t vb, const uint8_t* st, cons
   }
 }
 
-// a bf16 pair times a power of two as an fp16 pair
-__device__ __forceinline__ uint32_t bf16x2_times(uint32_t b, float f) {
-  return pack_h2(__uint_as_float(b << 16) * f, __uint_as_float(b & 0xFFFF0000u) * f);
+// a bf16 pair times a pair of powers of two (bf16, exact) as an fp16 pair
+__device__ __forceinline__ uint32_t bf16x2_times(uint32_t b, uint32_t f) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(b), "r"(f));
+  return pack_h2(__uint_as_float(r << 16), __uint_as_float(r & 0xFFFF0000u));
 }
 
 template <int D>
@@ -250,14 +292,15 @@ __global__ void __launch_bounds__(32 * kW<D>, kSpCtas<D>)
 sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
               const __grid_constant__ CUtensorMap tmKt, const __grid_constant__ CUtensorMap tmVt) {
   constexpr int NB = D / 32, RB = kRows<D>, HB = RB / 16, G = (D & (D - 1)) == 0 ? D : 64;
-  constexpr int WT = box_w(2 * D), kWarps = kW<D>;
+  constexpr int WT = 128, kWarps = kW<D>;  // (tail rows of 2 D bytes are whole 128-byte columns)
+  static_assert(box_w(2 * D) == WT && kTailRows == 8, "tail rows' swizzle");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const kvq_cache& c = a.c;
   const int S = int(cg::this_cluster().num_blocks()), rank = int(cg::this_cluster().block_rank());
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int g = lane >> 2, tig = lane & 3;
-  const int row = blockIdx.x / S, plane = row % (c.n_kv_heads * a.head_groups), b = row / (c.n_kv_heads * a.head_groups);
-  const int kvh = plane / a.head_groups, hg = plane % a.head_groups;
+  const int row = (blockIdx.x - rank) / S, b = int(div_u32(uint32_t(row), a.by_plane));
+  const int plane = row - b * c.n_kv_heads * a.head_groups, kvh = plane / a.head_groups, hg = plane % a.head_groups;
   const int head0 = kvh * a.group + hg * a.heads_per_cta, nheads = min(a.heads_per_cta, a.group - hg * a.heads_per_cta);
   const int T = c.tail_len, NS = a.s.stages;
   // shared memory: stages [kWarps][NS] (the partials of the merge afterwards), query fragments,
@@ -293,53 +336,54 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
 
   // ---- producer: the warp's tiles, in order.  Tile ordinal k is tile wid + k * nw of the list;
   // lane l holds ordinal 32 * (chunk) + l: its first position (-1: not listed) and body row
-  const int tpb = a.block_tokens / RB, body_end = n - T;
-  const long long tiles = (long long)a.n_select * tpb;
-  const int wid = rank * kWarps + warp, nw = S * kWarps;
-  const RowMap rm = row_map(c);
-  long long chunk = 0;     // ordinal of lane 0's tile
+  const int body_end = n - T, wid = rank * kWarps + warp, nw = S * kWarps;
+  auto slot_of = [&](int p) { return p - int(div_u32(uint32_t(p), a.by_tail)) * T; };
+  int chunk = 0;           // ordinal of lane 0's tile
   int my_t0 = -1, my_row = 0;
   auto fetch = [&]() {
-    const long long u = wid + (chunk + lane) * nw;
+    const uint32_t u = uint32_t(wid) + uint32_t(chunk + lane) * uint32_t(nw);  // (below 2^32: see the launch)
     my_t0 = -1;
-    if (u < tiles) {
-      const int blk = sel[u / tpb];
+    if (u < uint32_t(a.tiles)) {
+      const uint32_t e = div_u32(u, a.by_block);
+      const int blk = sel[e];
       if (blk >= 0 && (long long)blk * a.block_tokens < n) {
-        const int t0 = blk * a.block_tokens + int(u % tpb) * RB;
+        const int t0 = blk * a.block_tokens + int(u - e * a.by_block.d) * RB;
         if (t0 < n) {
           my_t0 = t0;
-          my_row = -1;
-          if (t0 < body_end) {
-            const long long r = body_row(rm, b, kvh, t0);  // rows of a tile lie in one page
-            my_row = int(r);
-            if (r < 0) atomicOr(c.status, KVQ_DEV_ERR_PAGE);
+          my_row = int(bh) * c.max_ctx + t0;
+          if (c.page_tokens && t0 < body_end) {  // (rows of a tile lie in one page)
+            const int i = int(div_u32(uint32_t(t0), a.by_page));
+            const int pg = c.page_table[(long long)b * a.pages_per_seq + i];
+            my_row = pg >= 0 && pg < c.n_pages ? (pg * c.n_kv_heads + kvh) * c.page_tokens + t0 - i * c.page_tokens : -1;
+            if (my_row < 0) atomicOr(c.status, KVQ_DEV_ERR_PAGE);
           }
         }
       }
     }
   };
   fetch();
-  int at = 0, pos = -1;    // next ordinal of the chunk; next position of the tile in hand (-1: none)
+  unsigned live = __ballot_sync(0xffffffffu, my_t0 >= 0);  // the chunk's tiles still to come
+  int pos = -1;            // next position of the tile in hand (-1: none)
   int end = 0, trow = 0;   // its end and body row
   bool done = false;
-  // the next job (p, count): count > 0 body rows, < 0 tail rows, 0 none left; copies issued by one lane
+  // the next job: y > 0 body rows, y < 0 tail rows from slot x, 0 none left; copies issued by one lane
   auto produce = [&](int s) {
-    while (!done && pos < 0) {
-      if (at == 32) {
+    while (pos < 0 && !done) {
+      if (!live) {
         chunk += 32;
-        at = 0;
-        if (wid + chunk * nw >= tiles) { done = true; break; }
-        fetch();
+        done = wid + chunk * nw >= a.tiles;
+        if (!done) {
+          fetch();
+          live = __ballot_sync(0xffffffffu, my_t0 >= 0);
+        }
+        continue;
       }
-      const unsigned live = __ballot_sync(0xffffffffu, my_t0 >= 0) >> at;
-      if (!live) { at = 32; continue; }
-      at += __ffs(live) - 1;
-      const int t0 = __shfl_sync(0xffffffffu, my_t0, at);
-      trow = __shfl_sync(0xffffffffu, my_row, at);
-      ++at;
-      end = min(n, t0 + RB);
-      pos = t0;
-      if (pos < body_end && trow < 0) {  // a page outside the pool: its body rows are left out
+      const int src = __ffs(live) - 1;
+      live &= live - 1;
+      pos = __shfl_sync(0xffffffffu, my_t0, src);
+      trow = __shfl_sync(0xffffffffu, my_row, src);
+      end = min(n, pos + RB);
+      if (trow < 0 && pos < body_end) {  // a page outside the pool: its body rows are left out
         pos = min(end, body_end);
         if (pos >= end) pos = -1;
       }
@@ -349,7 +393,8 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
       if (pos < body_end) {
         job = make_int2(pos, min(end, body_end) - pos);
       } else {
-        job = make_int2(pos, -min(min(kTailRows, end - pos), T - pos % T));  // (a tail tile ends where the ring wraps)
+        job = make_int2(slot_of(pos), -min(kTailRows, end - pos));
+        job.y = max(job.y, job.x - T);  // (a tail tile ends where the ring wraps)
       }
     }
     if (lane == 0) {
@@ -365,7 +410,7 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
         if (c.k_qh) bulk_g2s(st + a.s.kqh, static_cast<const uint32_t*>(c.k_qh) + r * NB, RB * NB * 4, &wbar[s]);
         if (c.v_qh) bulk_g2s(st + a.s.vqh, static_cast<const uint32_t*>(c.v_qh) + r * NB, RB * NB * 4, &wbar[s]);
       } else if (job.y < 0) {
-        const int r = int(bh * T + pos % T);
+        const int r = int(bh) * T + job.x;
         mbar_arrive_expect_tx(&wbar[s], 2 * kTailRows * 2 * D);
         tma_3d_g2s(st, &tmKt, r, &wbar[s]);
         tma_3d_g2s(st + a.s.vt, &tmVt, r, &wbar[s]);
@@ -440,6 +485,7 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
   const float f_tail = s_f[g] * 256.0f, f_body = s_f[g] * 16777216.0f;  // (tail rows go in times 2^-8)
 
   // ---- main loop
+  const uint32_t wst_s = smem_u32(wst), qf_s = smem_u32(qf), qsum_s = smem_u32(qsum);
   float acc[NB][2][4];
 #pragma unroll
   for (int i = 0; i < NB; ++i)
@@ -456,7 +502,7 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
     const bool arrived = mbar_wait_bounded(&wbar[s], (k / NS) & 1, kWaitCycles);
     if (!__all_sync(0xffffffffu, arrived)) { timed_out = true; break; }
     const int2 job = wjob[s];
-    const uint8_t* st = wst + s * a.s.bytes;
+    const uint32_t st = wst_s + s * a.s.bytes;
     const int cnt = abs(job.y);
     float sc[HB][2][2];
 #pragma unroll
@@ -464,7 +510,7 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
     float f = f_body;
     if (job.y > 0) {
 #define KVQ_SCORES(KT) \
-  case KT: body_scores<D, KT>(st, a.s, qf, qsum, lane, sc); break;
+  case KT: body_scores<D, KT>(st, a.s, qf_s, qsum_s, lane, sc); break;
       switch (c.k_type) {
         KVQ_SCORES(KVQ_TYPE_Q4_0)
         KVQ_SCORES(KVQ_TYPE_Q5_0)
@@ -476,17 +522,18 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
     } else {
       f = f_tail;
       float cc[4] = {0.f, 0.f, 0.f, 0.f};
-      const float f1 = nib ? 0.0625f : 0.00390625f;  // times 16 where the fragments are 16 times smaller
-#pragma unroll 2
-      for (int i = 0; i < NB; ++i)
+      // the second half blocks' channels times 16 more where the fragments are 16 times smaller
+      const uint32_t f1 = nib ? 0x3D803D80u : 0x3B803B80u;
+      // token g, bytes 8tig .. of half block 0; half block j lies 32 bytes further, its 16-byte chunks swizzled
+      const uint32_t k0 = st + g * WT + (((tig >> 1) ^ g) << 4) + (tig & 1) * 8;
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const uint2 x = *reinterpret_cast<const uint2*>(st + swz_off<WT>(g, 2 * (32 * i + 16 * hf + 4 * tig), kTailRows));
-          const uint4 q = qf[(2 * i + hf) * 32 + lane];
-          const uint32_t qa[4] = {q.x, q.y, q.z, q.w};
-          const float f0 = hf ? f1 : 0.00390625f;
-          mma16816(cc, qa, bf16x2_times(__byte_perm(x.x, x.y, 0x5410), f0), bf16x2_times(__byte_perm(x.x, x.y, 0x7632), f0));
-        }
+      for (int j = 0; j < 2 * NB; ++j) {
+        const uint2 x = lds64((k0 ^ ((2 * (j & 3)) << 4)) + (j >> 2) * (kTailRows * WT));
+        const uint4 q = lds128(qf_s + lane * 16 + j * 512);
+        const uint32_t qa[4] = {q.x, q.y, q.z, q.w};
+        const uint32_t fj = j & 1 ? f1 : 0x3B803B80u;  // bf16 2^-8, or 2^-4
+        mma16816(cc, qa, bf16x2_times(__byte_perm(x.x, x.y, 0x5410), fj), bf16x2_times(__byte_perm(x.x, x.y, 0x7632), fj));
+      }
       sc[0][0][0] = cc[0] + cc[2];
       sc[0][0][1] = cc[1] + cc[3];
     }
@@ -498,12 +545,14 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float& x = sc[hh][t][e];
-          x *= f;
-          if (partial && 16 * hh + 8 * t + 2 * tig + e >= cnt) x = -INFINITY;
-          mx = fmaxf(mx, x);
-        }
+        for (int e = 0; e < 2; ++e) sc[hh][t][e] *= f;
+    if (partial) {
+#pragma unroll
+      for (int i = 0; i < 4 * HB; ++i)
+        if (16 * (i >> 2) + 8 * ((i >> 1) & 1) + (i & 1) >= cnt - 2 * tig) sc[i >> 2][(i >> 1) & 1][i & 1] = -INFINITY;
+    }
+#pragma unroll
+    for (int i = 0; i < 4 * HB; ++i) mx = fmaxf(mx, sc[i >> 2][(i >> 1) & 1][i & 1]);
     // m is a reference kLazyMax above the maximum at its last move (weights stay <= 1), so the
     // rescale runs only when a score passes it
     if (__any_sync(0xffffffffu, mx > m)) {
@@ -534,20 +583,14 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
     // ---- P.V
     if (job.y > 0) {
       uint32_t ph[HB][2], pl[HB][2];
-      bool ok[HB][4];
 #pragma unroll
       for (int hh = 0; hh < HB; ++hh)
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          split_h2(p[hh][t][0], p[hh][t][1], ph[hh][t], pl[hh][t]);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) ok[hh][2 * t + e] = 16 * hh + 8 * t + 2 * tig + e < cnt;
-        }
+        for (int t = 0; t < 2; ++t) split_h2(p[hh][t][0], p[hh][t][1], ph[hh][t], pl[hh][t]);
 #define KVQ_VALUES(VT)                                                                                               \
   case VT:                                                                                                           \
-    _Pragma("unroll") for (int hh = 0; hh < HB; ++hh) body_values<D, VT>(                                            \
-        smem_u32(st + a.s.v) + hh * 16 * box_w(VT == KVQ_TYPE_Q8_0 ? D : D / 2), st, a.s, 16 * hh, ph[hh], pl[hh], partial, \
-        ok[hh], lane, acc, dmin);                                                                                    \
+    _Pragma("unroll") for (int hh = 0; hh < HB; ++hh) body_values<D, VT>(st, a.s, 16 * hh, ph[hh], pl[hh], cnt, lane, acc, \
+                                                                          dmin);                                    \
     break;
       switch (c.v_type) {
         KVQ_VALUES(KVQ_TYPE_Q4_0)
@@ -560,18 +603,19 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
     } else {
       uint32_t bh_, bl_;
       split_h2(p[0][0][0] * 256.0f, p[0][0][1] * 256.0f, bh_, bl_);
-      const bool ok0 = 2 * tig < cnt, ok1 = 2 * tig + 1 < cnt;
-      const uint8_t* vt = st + a.s.vt;
+      // tokens 2tig and 2tig + 1, channels 2g, 2g + 1; 16 channels further 32 bytes, swizzled.  Rows past the
+      // end hold anything: masked
+      const uint32_t m0 = 2 * tig < cnt ? 0xFFFFFFFFu : 0u, m1 = 2 * tig + 1 < cnt ? 0xFFFFFFFFu : 0u;
+      const uint32_t v0 = st + a.s.vt + 2 * tig * WT + (((g >> 2) ^ (2 * tig)) << 4) + (g & 3) * 4;
+      const uint32_t v1 = st + a.s.vt + (2 * tig + 1) * WT + (((g >> 2) ^ (2 * tig + 1)) << 4) + (g & 3) * 4;
 #pragma unroll
-      for (int i = 0; i < 2 * NB; ++i) {  // channels 16i + 2g, + 1 of tokens 2tig, 2tig + 1
-        uint32_t w0 = *reinterpret_cast<const uint32_t*>(vt + swz_off<WT>(2 * tig, 2 * (16 * i + 2 * g), kTailRows));
-        uint32_t w1 = *reinterpret_cast<const uint32_t*>(vt + swz_off<WT>(2 * tig + 1, 2 * (16 * i + 2 * g), kTailRows));
-        w0 = ok0 ? w0 : 0u;
-        w1 = ok1 ? w1 : 0u;
-        const uint32_t av[4] = {bf16x2_to_h2_scaled(__byte_perm(w0, w1, 0x5410)),
-                                bf16x2_to_h2_scaled(__byte_perm(w0, w1, 0x7632)), 0u, 0u};
-        mma16816(acc[i / 2][i % 2], av, bh_, 0u);
-        mma16816(acc[i / 2][i % 2], av, bl_, 0u);
+      for (int j = 0; j < 2 * NB; ++j) {
+        const uint32_t w0 = lds32((v0 ^ ((2 * (j & 3)) << 4)) + (j >> 2) * (kTailRows * WT)) & m0;
+        const uint32_t w1 = lds32((v1 ^ ((2 * (j & 3)) << 4)) + (j >> 2) * (kTailRows * WT)) & m1;
+        const uint32_t av[4] = {bf16x2_times(__byte_perm(w0, w1, 0x5410), 0x3B803B80u),
+                                bf16x2_times(__byte_perm(w0, w1, 0x7632), 0x3B803B80u), 0u, 0u};
+        mma16816(acc[j / 2][j % 2], av, bh_, 0u);
+        mma16816(acc[j / 2][j % 2], av, bl_, 0u);
       }
     }
     __syncwarp();
@@ -651,37 +695,24 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
   cg::cluster_group cl = cg::this_cluster();
   cl.sync();
   for (int hh = rank + S * warp; hh < nheads; hh += S * kWarps) {
-    float cmx[kMaxCluster], cl_[kMaxCluster], xs[kMaxCluster][NB], x[NB];
-    float M = -INFINITY, Lsum = 0.0f;
+    // lane r: the maximum and sum of rank r
+    const float mr = lane < S ? cl.map_shared_rank(s_cta, lane)[hh] : -INFINITY;
+    const float lr = lane < S ? cl.map_shared_rank(s_l, lane)[hh] : 0.0f;
+    float M = mr, x[NB];
 #pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r) {  // every load before the first use
-      if (r < S) {
-        cmx[r] = cl.map_shared_rank(s_cta, r)[hh];
-        cl_[r] = cl.map_shared_rank(s_l, r)[hh];
-      }
-    }
+    for (int o = 1; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float fr = mr == -INFINITY ? 0.0f : fast_exp2(mr - M);
+    float Lsum = lr * fr;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) Lsum += __shfl_xor_sync(0xffffffffu, Lsum, o);
 #pragma unroll
     for (int j = 0; j < NB; ++j) x[j] = 0.0f;
+#pragma unroll 4
+    for (int r = 0; r < S; ++r) {
+      const float* ra = cl.map_shared_rank(macc, r) + hh * D;
+      const float f = __shfl_sync(0xffffffffu, fr, r);
 #pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r)
-      if (r < S) M = fmaxf(M, cmx[r]);
-#pragma unroll
-    for (int r0 = 0; r0 < kMaxCluster; r0 += 4) {
-#pragma unroll
-      for (int r = r0; r < r0 + 4; ++r)
-        if (r < S) {
-          const float* ra = cl.map_shared_rank(macc, r) + hh * D;
-#pragma unroll
-          for (int j = 0; j < NB; ++j) xs[r][j] = ra[fwht_channel<D, G>(lane, j)];
-        }
-#pragma unroll
-      for (int r = r0; r < r0 + 4; ++r)
-        if (r < S) {
-          const float f = cmx[r] == -INFINITY ? 0.0f : fast_exp2(cmx[r] - M);
-          Lsum = fmaf(cl_[r], f, Lsum);
-#pragma unroll
-          for (int j = 0; j < NB; ++j) x[j] = fmaf(xs[r][j], f, x[j]);
-        }
+      for (int j = 0; j < NB; ++j) x[j] = fmaf(ra[fwht_channel<D, G>(lane, j)], f, x[j]);
     }
     const float inv = Lsum > 0.0f ? 1.0f / Lsum : 0.0f;
 #pragma unroll
@@ -744,14 +775,22 @@ cudaError_t run_sparse(SpArgs& a, cudaStream_t st) {
   auto kern = sparse_kernel<D>;
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), bytes);
   if (e != cudaSuccess) return e;
+  if ((e = allow_large_clusters(reinterpret_cast<const void*>(kern))) != cudaSuccess) return e;
   // CTAs per row: as many as one wave holds, a tile per warp at least.  (Clusters of 8 do not fill
   // every SM group to the last SM: with 7/8 of the slots the wave stays one.)
   const long long rows = (long long)c.batch * c.n_kv_heads * a.head_groups;
   const long long tiles = (long long)a.n_select * (a.block_tokens / RB);
+  if (tiles > 0x3fffffffLL) return cudaErrorInvalidValue;  // (the API refuses such lists)
+  a.tiles = int(tiles);
+  a.by_block = make_divu32(uint32_t(a.block_tokens / RB));
+  a.pages_per_seq = c.page_tokens ? c.max_ctx / c.page_tokens : 0;
+  a.by_page = make_divu32(uint32_t(std::max(1, c.page_tokens)));
+  a.by_tail = make_divu32(uint32_t(std::max(1, c.tail_len)));
+  a.by_plane = make_divu32(uint32_t(c.n_kv_heads * a.head_groups));
   const int sms = device_sm_count();
   const int per_sm = std::min(kSpCtas<D>, 228 * 1024 / (bytes + 1024));
   const long long slots = (long long)(sms > 0 ? sms : 148) * per_sm;
-  const int S = int(std::max<long long>(1, std::min<long long>({kMaxCluster, slots * 7 / 8 / rows, tiles / kWarps})));
+  const int S = int(std::max<long long>(1, std::min<long long>({8, slots * 7 / 8 / rows, tiles / kWarps})));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(rows * S));
   cfg.blockDim = dim3(32 * kWarps);

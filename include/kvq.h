@@ -489,8 +489,9 @@ KVQ_API kvq_status kvq_block_index_update(const kvq_cache* c, const kvq_block_in
  * over the group's heads of fp32(fp32(dot * sq) * scale), dot the integer product
  * of the codes.  Eight bits for the query as for the means: the score only ranks
  * blocks, and integers make the ranking the same wherever it is computed.  A NaN
- * score ranks last.  Requires nblk <= 49152 (take larger blocks for a longer
- * max_ctx, else KVQ_ERR_UNSUPPORTED) and n_select in [1, 49152].
+ * score ranks last.  Requires n_select in [1, 49152], nblk <= 49152 (take larger
+ * blocks for a longer max_ctx) and 4 nblk + (head_dim + 20) * (query heads per KV
+ * head, rounded up to 8) <= 216 KB, else KVQ_ERR_UNSUPPORTED.
  */
 KVQ_API kvq_status kvq_select_blocks(const kvq_cache* c, const kvq_block_index* x, const void* q, int32_t q_dtype,
                                      int32_t n_q_heads, int32_t n_first, int32_t n_last, int32_t n_select,

@@ -367,9 +367,12 @@ kvq_status kvq_select_blocks(const kvq_cache* c, const kvq_block_index* x, const
   if (!valid_dtype(q_dtype) || n_q_heads <= 0 || n_q_heads % c->n_kv_heads) return KVQ_ERR_INVALID_ARG;
   if (!q || !aligned16(q) || !sel || !aligned4(sel)) return KVQ_ERR_INVALID_ARG;
   if (n_first < 0 || n_last < 0 || n_select < 1 || (long long)n_first + n_last > n_select) return KVQ_ERR_INVALID_ARG;
-  if (n_q_heads / c->n_kv_heads > 128 || n_select > kvq::kMaxIndexBlocks ||
-      (c->max_ctx + (long long)x->block_tokens - 1) / x->block_tokens > kvq::kMaxIndexBlocks)
-    return KVQ_ERR_UNSUPPORTED;
+  const long long nblk = (c->max_ctx + (long long)x->block_tokens - 1) / x->block_tokens;
+  const int group = n_q_heads / c->n_kv_heads;
+  if (group > 128 || n_select > kvq::kMaxIndexBlocks || nblk > kvq::kMaxIndexBlocks) return KVQ_ERR_UNSUPPORTED;
+  // the blocks' scores and the coded queries share a CTA's shared memory
+  if (4 * nblk + (group + 7) / 8 * 8 * (c->head_dim + 20) > 216 * 1024) return KVQ_ERR_UNSUPPORTED;
+  if ((long long)c->batch * c->n_kv_heads * 8 > 0x7fffffffLL) return KVQ_ERR_UNSUPPORTED;
   return from_cuda(kvq::launch_select_blocks(*c, r, *x, q, q_dtype, n_q_heads, n_first, n_last, n_select, sel,
                                              static_cast<cudaStream_t>(stream)));
 }

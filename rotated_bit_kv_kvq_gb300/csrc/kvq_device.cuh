@@ -13,6 +13,7 @@
 #include <stdint.h>
 
 #include "kvq.h"
+#include "kvq_divu32.h"
 
 namespace kvq {
 
@@ -140,27 +141,6 @@ __device__ __forceinline__ uint32_t qh_get(const void* plane, bool k_plane, size
   if (k_plane) return qh_k_to_gguf(static_cast<const uint32_t*>(plane)[row * size_t(nb) + size_t(blk)]);
   const uint16_t* p = static_cast<const uint16_t*>(plane);
   return qh_v_to_gguf(uint32_t(p[qh_v_half(row, nb, blk, 0)]) | (uint32_t(p[qh_v_half(row, nb, blk, 1)]) << 16));
-}
-
-// ---------------------------------------------------------------------------
-// Unsigned 32-bit division by a run-time invariant divisor d >= 1 with one
-// high multiply (Granlund and Montgomery, "Division by invariant integers
-// using multiplication", 1994, section 4): l = ceil(log2 d),
-// m = floor(2^32 (2^l - d) / d) + 1, q = (t + ((n - t) >> min(l, 1))) >>
-// max(l - 1, 0) with t = mulhi(m, n); exact for every 32-bit n.
-// ---------------------------------------------------------------------------
-struct DivU32 {
-  uint32_t d, m, s1, s2;
-};
-inline DivU32 make_divu32(uint32_t d) {
-  uint32_t l = 0;
-  while (l < 32 && (uint64_t(1) << l) < d) ++l;
-  const uint32_t m = uint32_t(((uint64_t(1) << 32) * ((uint64_t(1) << l) - d)) / d + 1);
-  return DivU32{d, m, l < 1 ? l : 1u, l > 1 ? l - 1 : 0u};
-}
-__device__ __forceinline__ uint32_t div_u32(uint32_t n, const DivU32& v) {
-  const uint32_t t = __umulhi(v.m, n);
-  return (t + ((n - t) >> v.s1)) >> v.s2;
 }
 
 // ---------------------------------------------------------------------------

@@ -1,6 +1,7 @@
 // Block index of a cache: mean keys of its blocks as int8 codes
 // (kvq_block_index_update), and the selection of blocks by them (kvq_select_blocks).
 
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <math.h>
 
@@ -13,6 +14,8 @@
 namespace kvq {
 namespace {
 
+namespace cg = cooperative_groups;
+
 // ---------------------------------------------------------------------------
 // Index update: one CTA per (block, KV head, sequence), one warp per 32-channel
 // quantization block.  Lane (j, s) of a warp adds the tokens j, j + 8, ... of its
@@ -22,45 +25,69 @@ namespace {
 // depend on the launch.  Every product code * d is exact in fp32 (8 x 11 bits), so a
 // fused multiply-add rounds as the sum of the two does.
 // ---------------------------------------------------------------------------
+// four bytes as exact floats, less `off`: a byte in the low bits of 2^23's significand
+__device__ __forceinline__ void bytes_f32(uint32_t w, float off, float2& a, float2& b) {
+  const float2 m = make_float2(-8388608.0f - off, -8388608.0f - off);
+  a = __fadd2_rn(make_float2(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440)),
+                             __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7441))), m);
+  b = __fadd2_rn(make_float2(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7442)),
+                             __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7443))), m);
+}
+
+// what lane s reads of one token's quantization block
 template <int KT>
-__device__ __forceinline__ void add_token(const kvq_cache& c, long long row, int blk, int s, float (&acc)[8]) {
-  const int d = c.head_dim, nb = d / 32;
+struct Token {
+  uint32_t w[KT == KVQ_TYPE_Q8_0 ? 2 : 1], hd, qh;
+};
+template <int KT, int D>
+__device__ __forceinline__ Token<KT> load_token(const kvq_cache& c, long long row, int blk, int s) {
+  constexpr int d = D, nb = D / 32;
+  Token<KT> t;
   if constexpr (KT == KVQ_TYPE_Q8_0) {
     const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(c.k_qs) + row * d + 32 * blk + 8 * s);
-    const float dk = __half2float(static_cast<const __half*>(c.k_d)[row * nb + blk]);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int u = ((i < 4 ? w.x : w.y) >> (8 * (i & 3))) & 255;
-      acc[i] = fmaf(float(u - 128), dk, acc[i]);
-    }
+    t.w[0] = w.x;
+    t.w[1] = w.y;
   } else {
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(c.k_qs) + row * (d / 2) +
-                                                          16 * blk + 4 * s);
-    uint32_t hb = 0;
-    if constexpr (type_has_qh(KT)) hb = qh_k_to_gguf(static_cast<const uint32_t*>(c.k_qh)[row * nb + blk]);
-    float dk, lo = 0.0f;
-    if constexpr (type_has_min(KT)) {
-      const float2 f = __half22float2(static_cast<const __half2*>(c.k_d)[row * nb + blk]);
-      dk = f.x;
-      lo = f.y;
-    } else {
-      dk = __half2float(static_cast<const __half*>(c.k_d)[row * nb + blk]);
+    t.w[0] = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(c.k_qs) + row * (d / 2) + 16 * blk + 4 * s);
+  }
+  if constexpr (type_has_qh(KT)) t.qh = static_cast<const uint32_t*>(c.k_qh)[row * nb + blk];
+  if constexpr (type_has_min(KT)) t.hd = static_cast<const uint32_t*>(c.k_d)[row * nb + blk];
+  else t.hd = static_cast<const uint16_t*>(c.k_d)[row * nb + blk];
+  return t;
+}
+template <int KT>
+__device__ __forceinline__ void add_token(const Token<KT>& t, int s, float2 (&acc)[4]) {
+  float2 x[4];
+  const float2 hd = __half22float2(u32_as_h2(t.hd)), dk = make_float2(hd.x, hd.x);
+  if constexpr (KT == KVQ_TYPE_Q8_0) {
+    bytes_f32(t.w[0], 128.0f, x[0], x[1]);
+    bytes_f32(t.w[1], 128.0f, x[2], x[3]);
+  } else {
+    uint32_t lo = t.w[0] & 0x0F0F0F0Fu, hi = (t.w[0] >> 4) & 0x0F0F0F0Fu;
+    if constexpr (type_has_qh(KT)) {
+      // the K plane's order: channels 4s .. 4s+3 at bits 0, 1, 16, 17 of the word moved down by
+      // 8 (s / 2) + 2 (s % 2), channels 16 further at 4 bits above; to bit 4 of their bytes
+      const uint32_t h = t.qh >> (8 * (s >> 1) + 2 * (s & 1));
+      lo |= ((h << 4) & 0x00100010u) | ((h << 11) & 0x10001000u);
+      hi |= (h & 0x00100010u) | ((h << 7) & 0x10001000u);
     }
+    const float off = type_has_min(KT) ? 0.0f : float(type_code_offset(KT));
+    bytes_f32(lo, off, x[0], x[1]);
+    bytes_f32(hi, off, x[2], x[3]);
+  }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      int code = (w >> (8 * (i & 3) + (i < 4 ? 0 : 4))) & 15;
-      if constexpr (type_has_qh(KT)) code |= ((hb >> (4 * s + (i & 3) + (i < 4 ? 0 : 16))) & 1) << 4;
-      if constexpr (type_has_min(KT)) acc[i] = __fadd_rn(acc[i], fmaf(float(code), dk, lo));
-      else acc[i] = fmaf(float(code - type_code_offset(KT)), dk, acc[i]);
-    }
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (type_has_min(KT)) acc[i] = __fadd2_rn(acc[i], __ffma2_rn(x[i], dk, make_float2(hd.y, hd.y)));
+    else acc[i] = __ffma2_rn(x[i], dk, acc[i]);
   }
 }
 
-template <int KT>
-__global__ void __launch_bounds__(320) index_update_kernel(kvq_cache c, kvq_block_index x, int n_last, int nblk) {
-  __shared__ float s_max[10];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  const int h = blockIdx.y, b = blockIdx.z, bt = x.block_tokens, d = c.head_dim;
+template <int KT, int D>
+__global__ void __launch_bounds__(D) index_update_kernel(kvq_cache c, kvq_block_index x, int n_last, int nblk) {
+  __shared__ uint32_t s_max[10];
+  constexpr int nw = D / 32, d = D;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int h = blockIdx.y, b = blockIdx.z, bt = x.block_tokens;
   const int n = min(max(c.seq_len[b], 0), c.max_ctx);
   const long long j0 = n_last ? max(0, n - n_last) / bt : 0;
   const long long blk = j0 + blockIdx.x;
@@ -68,62 +95,72 @@ __global__ void __launch_bounds__(320) index_update_kernel(kvq_cache c, kvq_bloc
   const RowMap rm = row_map(c);
   const int t0 = int(blk * bt), cnt = min(bt, n - t0);
   const int j = lane >> 2, s = lane & 3;
-  float acc[8];
+  float2 acc[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
+  for (int i = 0; i < 4; ++i) acc[i] = make_float2(0.0f, 0.0f);
   bool bad = false;
   for (int u = 0; u < cnt; u += 64) {  // 64 positions lie in one page
-    const long long row = body_row(rm, b, h, t0 + u);
-    if (row < 0) { bad = true; continue; }
+    const long long row0 = body_row(rm, b, h, t0 + u);
+    if (row0 < 0) { bad = true; continue; }
+    const long long row = row0 + j;
     const int m = min(64, cnt - u);
+    Token<KT> t[8];  // (every load before the first use)
+    if (m == 64) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (8 * i + j < m) add_token<KT>(c, row + 8 * i + j, warp, s, acc);
+      for (int i = 0; i < 8; ++i) t[i] = load_token<KT, D>(c, row + 8 * i, warp, s);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) add_token<KT>(t[i], s, acc);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (8 * i + j < m) t[i] = load_token<KT, D>(c, row + 8 * i, warp, s);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (8 * i + j < m) add_token<KT>(t[i], s, acc);
+    }
   }
   if (bad && threadIdx.x == 0) atomicOr(c.status, KVQ_DEV_ERR_PAGE);
-  float mean[8], mx = 0.0f;
+  // the partial sums in pairs (j, j ^ 1), (j, j ^ 2), (j, j ^ 4), each lane keeping half of its
+  // channels at every step: lane (j, s) ends with channel e of the eight
+  float v[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float v = acc[i];
+  for (int i = 0; i < 8; ++i) v[i] = i & 1 ? acc[i / 2].y : acc[i / 2].x;
 #pragma unroll
-    for (int o = 4; o < 32; o <<= 1) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, o));
-    mean[i] = __fdiv_rn(v, float(cnt));
-    mx = fmaxf(mx, fabsf(mean[i]));
+  for (int step = 0; step < 3; ++step) {
+    const int half = 4 >> step;
+    const bool up = (j >> step) & 1;
+#pragma unroll
+    for (int i = 0; i < half; ++i) {
+      const float give = up ? v[i] : v[i + half], keep = up ? v[i + half] : v[i];
+      v[i] = __fadd_rn(keep, __shfl_xor_sync(0xffffffffu, give, 4 << step));
+    }
   }
-  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+  const int e = 4 * (j & 1) + (j & 2) + (j >> 2);
+  // (a product with the power of two 1 / count is the quotient)
+  const float mean = (cnt & (cnt - 1)) == 0 ? __fmul_rn(v[0], __uint_as_float(uint32_t(127 - (31 - __clz(cnt))) << 23))
+                                            : __fdiv_rn(v[0], float(cnt));
+  uint32_t mx = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(mean)));
   if (lane == 0) s_max[warp] = mx;
   __syncthreads();
-  for (int w = 0; w < nw; ++w) mx = fmaxf(mx, s_max[w]);
-  const float scale = __fdiv_rn(mx, 127.0f);
-  const long long e = ((long long)b * c.n_kv_heads + h) * nblk + blk;
-  if (threadIdx.x == 0) x.scales[e] = scale;
-  if (j == 0) {
-    uint32_t w[2] = {0, 0};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int code = scale > 0.0f ? __float2int_rn(__fdiv_rn(mean[i], scale)) : 0;
-      w[i >> 2] |= (uint32_t(code) & 255u) << (8 * (i & 3));
-    }
-    uint8_t* dst = reinterpret_cast<uint8_t*>(x.codes) + e * d + 32 * warp;
-    if constexpr (KT == KVQ_TYPE_Q8_0) {
-      *reinterpret_cast<uint2*>(dst + 8 * s) = make_uint2(w[0], w[1]);
-    } else {
-      *reinterpret_cast<uint32_t*>(dst + 4 * s) = w[0];
-      *reinterpret_cast<uint32_t*>(dst + 16 + 4 * s) = w[1];
-    }
-  }
+  for (int w = 0; w < nw; ++w) mx = max(mx, s_max[w]);
+  const float scale = __fdiv_rn(__uint_as_float(mx), 127.0f);
+  const long long at = ((long long)b * c.n_kv_heads + h) * nblk + blk;
+  if (threadIdx.x == 0) x.scales[at] = scale;
+  const int ch = KT == KVQ_TYPE_Q8_0 ? 8 * s + e : e < 4 ? 4 * s + e : 12 + 4 * s + e;
+  x.codes[at * d + 32 * warp + ch] = int8_t(scale > 0.0f ? __float2int_rn(__fdiv_rn(mean, scale)) : 0);
 }
 
 // ---------------------------------------------------------------------------
-// Selection: one CTA per (KV head, sequence).  The queries of the group are rotated
-// and coded, 16 blocks x 8 heads at a time scored on the tensor cores (int8 mma:
-// integers, so every order gives the same sum), the scores kept in shared memory as
-// order-preserving integers; then the n_select-th largest is found by histograms of
-// ever finer bins and the blocks at or above it are written in order.
+// Selection: a cluster of CTAs per (KV head, sequence).  The queries of the group are
+// rotated and coded, 16 blocks x 8 heads at a time scored on the tensor cores (int8 mma:
+// integers, so every order gives the same sum), the scores collected in the first CTA's
+// shared memory as order-preserving integers; there the n_select-th largest is found by
+// histograms of ever finer bins and the blocks at or above it are written in order.
 // ---------------------------------------------------------------------------
-constexpr int kSelThreads = 512;
 constexpr int kBins = 2048;
+constexpr int kMaxSelCluster = 8;
+constexpr int kFewBlocks = 256;  // up to these a thread ranks each block
 
 // D = A (16x32 int8, row) * B (32x8 int8, col) + C, int32
 __device__ __forceinline__ void mma16832_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -147,40 +184,63 @@ struct SelArgs {
 template <int D>
 constexpr int sel_pitch() { return D + 16; }
 template <int D>
-int sel_q_bytes(int group) { return (group + 7) / 8 * 8 * (sel_pitch<D>() + 4); }
+int sel_q_bytes(int group) { return (group + 7) / 8 * 8 * (sel_pitch<D>() + 4); }  // (the API checks the sum, see there)
 
-template <int D>
-__global__ void __launch_bounds__(kSelThreads) select_kernel(SelArgs a) {
+template <int D, int kThreads>
+__global__ void __launch_bounds__(kThreads) select_kernel(SelArgs a) {
   constexpr int G = (D & (D - 1)) == 0 ? D : 64;
-  constexpr int E = D / 32, SEG = D / 64, QP = sel_pitch<D>();
+  constexpr int E = D / 32, SEG = D / 64, QP = sel_pitch<D>(), kW = kThreads / 32;
   extern __shared__ __align__(16) uint8_t smem[];
+  cg::cluster_group cl = cg::this_cluster();
+  const int S = int(cl.num_blocks()), rank = int(cl.block_rank());
+  cl.barrier_arrive();  // (no CTA touches the first one's shared memory before it runs)
   const int heads8 = (a.group + 7) / 8 * 8;
   uint8_t* s_q = smem;                                                  // [heads8][QP]
   float* s_qs = reinterpret_cast<float*>(smem + heads8 * QP);           // [heads8]
-  uint32_t* s_key = reinterpret_cast<uint32_t*>(s_qs + heads8);         // [blocks of the sequence]
+  uint32_t* s_key = reinterpret_cast<uint32_t*>(s_qs + heads8);         // [blocks of the sequence] (first CTA's)
   __shared__ uint32_t s_hist[kBins];
-  __shared__ int s_warp[2][kSelThreads / 32];
-  __shared__ uint32_t s_lim[2];
+  __shared__ int s_warp[2][32];
+  __shared__ uint32_t s_lim[2][32];
+  __shared__ uint32_t s_range[kMaxSelCluster][2];  // smallest and largest key of each CTA (first CTA's)
   __shared__ int s_bin, s_above, s_in;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int h = blockIdx.x, b = blockIdx.y;
+  const int row = blockIdx.x / S, h = row % a.n_kv_heads, b = row / a.n_kv_heads;
   const long long bh = (long long)b * a.n_kv_heads + h;
   int32_t* sel = a.sel + bh * a.n_select;
   const int n = min(max(a.seq_len[b], 0), a.max_ctx);
   const int nb = int(((long long)n + a.block_tokens - 1) / a.block_tokens);
   if (nb <= a.n_select) {  // all of them
-    for (int i = tid; i < a.n_select; i += kSelThreads) sel[i] = i < nb ? i : -1;
+    if (rank == 0)
+      for (int i = tid; i < a.n_select; i += kThreads) sel[i] = i < nb ? i : -1;
+    cl.barrier_wait();
     return;
   }
+  // ---- the first 16 blocks' codes of a warp are on their way while the queries are coded: lane
+  // (g, tig) loads 16 channels of rows g and g + 8 at a time
+  const int g = lane >> 2, tig = lane & 3;
+  const int8_t* codes = a.codes + bh * a.nblk * D;
+  const float* scales = a.scales + bh * a.nblk;
+  uint4 xa[SEG], xb[SEG];
+  auto load = [&](int r0) {
+    const int ra = min(r0 + g, nb - 1), rb = min(r0 + g + 8, nb - 1);
+#pragma unroll
+    for (int s = 0; s < SEG; ++s) {
+      xa[s] = *reinterpret_cast<const uint4*>(codes + (long long)ra * D + 64 * s + 16 * tig);
+      xb[s] = *reinterpret_cast<const uint4*>(codes + (long long)rb * D + 64 * s + 16 * tig);
+    }
+  };
+  const int step = 16 * kW * S;
+  int r0 = 16 * (rank * kW + warp);
+  if (r0 < nb) load(r0);
   // ---- queries: rotate, code
-  for (int i = warp; i < heads8; i += kSelThreads / 32) {
+  for (int i = warp; i < heads8; i += kW) {
     float v[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) v[e] = 0.0f;
     if (i < a.group) {
-      const size_t row = ((size_t)b * a.n_q_heads + (size_t)h * a.group + i) * D;
+      const size_t qrow = ((size_t)b * a.n_q_heads + (size_t)h * a.group + i) * D;
 #pragma unroll
-      for (int gi = 0; gi < D / G; ++gi) load_vals<G / 32>(a.q, a.q_dtype, row + gi * G + lane * (G / 32), v + gi * (G / 32));
+      for (int gi = 0; gi < D / G; ++gi) load_vals<G / 32>(a.q, a.q_dtype, qrow + gi * G + lane * (G / 32), v + gi * (G / 32));
     }
     if (a.rot_k) {
       warp_fwht<D, G>(v, lane);
@@ -190,8 +250,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(SelArgs a) {
     float mx = 0.0f;
 #pragma unroll
     for (int e = 0; e < E; ++e) mx = fmaxf(mx, fabsf(v[e]));
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
     const float sq = __fdiv_rn(mx, 127.0f);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
@@ -200,22 +259,13 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(SelArgs a) {
     }
     if (lane == 0) s_qs[i] = sq;
   }
-  if (tid == 0) { s_lim[0] = 0xFFFFFFFFu; s_lim[1] = 0; }
   __syncthreads();
-  // ---- scores: lane (g, tig) loads 16 channels of rows g and g + 8 at a time; two mma
-  // take them as their 32-wide inner index in an order of their own, the query's too
-  const int g = lane >> 2, tig = lane & 3;
-  const int8_t* codes = a.codes + bh * a.nblk * D;
-  const float* scales = a.scales + bh * a.nblk;
+  cl.barrier_wait();
+  uint32_t* keys = S > 1 ? cl.map_shared_rank(s_key, 0) : s_key;
+  // ---- scores: two mma take the 16 channels of a lane as their 32-wide inner index, in an
+  // order of their own that is the query's too
   uint32_t lo = 0xFFFFFFFFu, hi = 0;
-  for (int r0 = 16 * warp; r0 < nb; r0 += 16 * (kSelThreads / 32)) {
-    const int ra = min(r0 + g, nb - 1), rb = min(r0 + g + 8, nb - 1);
-    uint4 xa[SEG], xb[SEG];
-#pragma unroll
-    for (int s = 0; s < SEG; ++s) {
-      xa[s] = *reinterpret_cast<const uint4*>(codes + (long long)ra * D + 64 * s + 16 * tig);
-      xb[s] = *reinterpret_cast<const uint4*>(codes + (long long)rb * D + 64 * s + 16 * tig);
-    }
+  for (; r0 < nb; r0 += step) {
     float ma = -INFINITY, mb = -INFINITY;
     for (int h0 = 0; h0 < a.group; h0 += 8) {
       int acc[4] = {0, 0, 0, 0};
@@ -234,6 +284,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(SelArgs a) {
         }
       }
     }
+    if (r0 + step < nb) load(r0 + step);
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
       ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, o));
@@ -248,7 +299,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(SelArgs a) {
         uint32_t key = (u >> 31) ? ~u : (u | 0x80000000u);
         if (sc != sc) key = 0;
         if (r < a.n_first || r >= nb - a.n_last) key = 0xFFFFFFFFu;
-        s_key[r] = key;
+        keys[r] = key;
         lo = min(lo, key);
         hi = max(hi, key);
       }
@@ -256,10 +307,47 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(SelArgs a) {
   }
   lo = __reduce_min_sync(0xffffffffu, lo);
   hi = __reduce_max_sync(0xffffffffu, hi);
-  if (lane == 0) { atomicMin(&s_lim[0], lo); atomicMax(&s_lim[1], hi); }
+  if (lane == 0) { s_lim[0][warp] = lo; s_lim[1][warp] = hi; }
   __syncthreads();
-  lo = s_lim[0];
-  hi = s_lim[1];
+  if (warp == 0) {
+    lo = __reduce_min_sync(0xffffffffu, lane < kW ? s_lim[0][lane] : 0xFFFFFFFFu);
+    hi = __reduce_max_sync(0xffffffffu, lane < kW ? s_lim[1][lane] : 0u);
+    if (lane == 0) {
+      uint32_t* o = S > 1 ? cl.map_shared_rank(&s_range[0][0], 0) : &s_range[0][0];
+      o[2 * rank] = lo;
+      o[2 * rank + 1] = hi;
+    }
+  }
+  if (S > 1) cl.sync(); else __syncthreads();
+  if (rank != 0) return;
+  lo = 0xFFFFFFFFu;
+  hi = 0;
+  for (int r = 0; r < S; ++r) {
+    lo = min(lo, s_range[r][0]);
+    hi = max(hi, s_range[r][1]);
+  }
+  if constexpr (kThreads == kFewBlocks) {
+    if (nb <= kFewBlocks) {
+      // few blocks: a thread per block counts the keys above its own and those equal to it
+      const uint32_t k = tid < nb ? s_key[tid] : 0u;
+      int gt = 0, ge = 0, ties_before = 0;
+      for (int i = 0; i < nb; ++i) {
+        const uint32_t o = s_key[i];
+        gt += o > k;
+        ge += o >= k;
+      }
+      const bool tie = tid < nb && gt < a.n_select && ge > a.n_select;  // equal keys on both sides of the border
+      if (tie)
+        for (int i = 0; i < tid; ++i) ties_before += s_key[i] == k;
+      const bool in = tid < nb && gt + ties_before < a.n_select && (tie || ge <= a.n_select);
+      const unsigned m = __ballot_sync(0xffffffffu, in);
+      if (lane == 0) s_warp[0][warp] = __popc(m);
+      __syncthreads();
+      const int at = int(__reduce_add_sync(0xffffffffu, lane < warp ? unsigned(s_warp[0][lane]) : 0u));
+      if (in) sel[at + __popc(m & ((1u << lane) - 1u))] = tid;
+      return;
+    }
+  }
   // ---- the n_select-th largest key: bins of 2^sh keys over [lo, hi], then the same in the
   // bin that holds it, until a bin is one key wide or taken whole
   int need = a.n_select;   // keys to take from [lo, hi]; all above hi are taken
@@ -267,14 +355,14 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(SelArgs a) {
   for (;;) {
     const uint32_t range = hi - lo;
     const int sh = range < kBins ? 0 : 32 - __clz(range) - 11;
-    for (int i = tid; i < kBins; i += kSelThreads) s_hist[i] = 0;
+    for (int i = tid; i < kBins; i += kThreads) s_hist[i] = 0;
     __syncthreads();
-    for (int i = tid; i < nb; i += kSelThreads) {
+    for (int i = tid; i < nb; i += kThreads) {
       const uint32_t k = s_key[i];
       if (k >= lo && k <= hi) atomicAdd(&s_hist[(k - lo) >> sh], 1u);
     }
     __syncthreads();
-    constexpr int BPT = kBins / kSelThreads;  // bins per thread, from the top
+    constexpr int BPT = kBins / kThreads;  // bins per thread, from the top
     int cnt[BPT], sum = 0;
 #pragma unroll
     for (int i = 0; i < BPT; ++i) {
@@ -289,8 +377,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(SelArgs a) {
     }
     if (lane == 31) s_warp[0][warp] = inc;
     __syncthreads();
-    int above = inc - sum;
-    for (int w = 0; w < warp; ++w) above += s_warp[0][w];
+    int above = inc - sum + int(__reduce_add_sync(0xffffffffu, lane < warp ? unsigned(s_warp[0][lane]) : 0u));
 #pragma unroll
     for (int i = 0; i < BPT; ++i) {
       if (above < need && above + cnt[i] >= need) { s_bin = kBins - 1 - (tid * BPT + i); s_above = above; s_in = cnt[i]; }
@@ -304,45 +391,60 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(SelArgs a) {
     if (whole) break;
     if (sh == 0) { ties = true; break; }
   }
-  // ---- the blocks above, and of those equal the first `need`, in order
-  const int per = (nb + kSelThreads - 1) / kSelThreads;
-  const int i0 = min(nb, tid * per), i1 = min(nb, i0 + per);
+  // ---- the blocks above, and of those equal the first `need`, in order: a warp takes a run of
+  // blocks, 32 at a time
+  const int per = ((nb + kW - 1) / kW + 31) / 32 * 32, i0 = warp * per, i1 = min(nb, i0 + per);
   int gt = 0, eq = 0;
-  for (int i = i0; i < i1; ++i) {
-    const uint32_t k = s_key[i];
-    if (ties && k == lo) ++eq;
-    else if (k >= lo) ++gt;
+  for (int i = i0; i < i1; i += 32) {
+    const uint32_t k = i + lane < i1 ? s_key[i + lane] : 0u;
+    const bool in = i + lane < i1 && k >= lo, tie = in && ties && k == lo;
+    eq += __popc(__ballot_sync(0xffffffffu, tie));
+    gt += __popc(__ballot_sync(0xffffffffu, in && !tie));
   }
-  int ig = gt, ie = eq;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int yg = __shfl_up_sync(0xffffffffu, ig, o), ye = __shfl_up_sync(0xffffffffu, ie, o);
-    if (lane >= o) { ig += yg; ie += ye; }
-  }
-  if (lane == 31) { s_warp[0][warp] = ig; s_warp[1][warp] = ie; }
+  if (lane == 0) { s_warp[0][warp] = gt; s_warp[1][warp] = eq; }
   __syncthreads();
-  int bg = ig - gt, be = ie - eq;
-  for (int w = 0; w < warp; ++w) { bg += s_warp[0][w]; be += s_warp[1][w]; }
-  for (int i = i0; i < i1; ++i) {
-    const uint32_t k = s_key[i];
-    if (ties && k == lo) {
-      if (be < need) sel[bg + be] = i;
-      ++be;
-    } else if (k >= lo) {
-      sel[bg + min(be, need)] = i;
-      ++bg;
-    }
+  int bg = int(__reduce_add_sync(0xffffffffu, lane < warp ? unsigned(s_warp[0][lane]) : 0u));
+  int be = int(__reduce_add_sync(0xffffffffu, lane < warp ? unsigned(s_warp[1][lane]) : 0u));
+  const unsigned below = (1u << lane) - 1u;
+  for (int i = i0; i < i1; i += 32) {
+    const uint32_t k = i + lane < i1 ? s_key[i + lane] : 0u;
+    const bool in = i + lane < i1 && k >= lo, tie = in && ties && k == lo;
+    const unsigned mt = __ballot_sync(0xffffffffu, tie), mg = __ballot_sync(0xffffffffu, in && !tie);
+    const int e = be + __popc(mt & below), at = bg + __popc(mg & below) + min(e, need);
+    if (in && (!tie || e < need)) sel[at] = i + lane;
+    be += __popc(mt);
+    bg += __popc(mg);
   }
 }
 
-template <int D>
-cudaError_t select_d(const SelArgs& a, int batch, cudaStream_t st) {
+template <int D, int kThreads>
+cudaError_t select_t(const SelArgs& a, int batch, cudaStream_t st) {
   const int bytes = sel_q_bytes<D>(a.group) + 4 * a.nblk;
-  auto kern = select_kernel<D>;
+  auto kern = select_kernel<D, kThreads>;
   const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), bytes);
   if (e != cudaSuccess) return e;
-  kern<<<dim3(a.n_kv_heads, batch), kSelThreads, bytes, st>>>(a);
-  return cudaGetLastError();
+  // CTAs per row while each has 16 blocks per warp to score and the GPU has SMs for them
+  const long long rows = (long long)a.n_kv_heads * batch;
+  const int sms = device_sm_count();
+  const int S = int(std::max<long long>(1, std::min<long long>({kMaxSelCluster, (sms > 0 ? sms : 148) / rows,
+                                                               a.nblk / (16 * kThreads / 32)})));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(rows * S));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = S;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, a);
+}
+template <int D>
+cudaError_t select_d(const SelArgs& a, int batch, cudaStream_t st) {
+  // few blocks: barriers of few warps
+  return a.nblk <= 2048 ? select_t<D, kFewBlocks>(a, batch, st) : select_t<D, 1024>(a, batch, st);
 }
 
 }  // namespace
@@ -353,14 +455,24 @@ cudaError_t launch_block_index_update(const kvq_cache& c, const kvq_block_index&
   // blocks that can hold any of the last n_last tokens
   const int nx = n_last ? int(std::min<long long>(nblk, ((long long)n_last + bt - 2) / bt + 1)) : nblk;
   const dim3 grid(nx, c.n_kv_heads, c.batch);
-  const int threads = c.head_dim;
+#define KVQ_INDEX(KT, D) index_update_kernel<KT, D><<<grid, D, 0, st>>>(c, x, n_last, nblk)
+#define KVQ_INDEX_KT(KT)                        \
+  case KT:                                      \
+    if (c.head_dim == 64) KVQ_INDEX(KT, 64);    \
+    else if (c.head_dim == 128) KVQ_INDEX(KT, 128); \
+    else if (c.head_dim == 192) KVQ_INDEX(KT, 192); \
+    else if (c.head_dim == 256) KVQ_INDEX(KT, 256); \
+    else KVQ_INDEX(KT, 320);                    \
+    break;
   switch (c.k_type) {
-    case KVQ_TYPE_Q4_0: index_update_kernel<KVQ_TYPE_Q4_0><<<grid, threads, 0, st>>>(c, x, n_last, nblk); break;
-    case KVQ_TYPE_Q5_0: index_update_kernel<KVQ_TYPE_Q5_0><<<grid, threads, 0, st>>>(c, x, n_last, nblk); break;
-    case KVQ_TYPE_Q8_0: index_update_kernel<KVQ_TYPE_Q8_0><<<grid, threads, 0, st>>>(c, x, n_last, nblk); break;
-    case KVQ_TYPE_Q4_1: index_update_kernel<KVQ_TYPE_Q4_1><<<grid, threads, 0, st>>>(c, x, n_last, nblk); break;
-    default: index_update_kernel<KVQ_TYPE_Q5_1><<<grid, threads, 0, st>>>(c, x, n_last, nblk); break;
+    KVQ_INDEX_KT(KVQ_TYPE_Q4_0)
+    KVQ_INDEX_KT(KVQ_TYPE_Q5_0)
+    KVQ_INDEX_KT(KVQ_TYPE_Q8_0)
+    KVQ_INDEX_KT(KVQ_TYPE_Q4_1)
+    KVQ_INDEX_KT(KVQ_TYPE_Q5_1)
   }
+#undef KVQ_INDEX_KT
+#undef KVQ_INDEX
   return cudaGetLastError();
 }
 

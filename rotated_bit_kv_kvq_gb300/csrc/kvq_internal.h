@@ -9,6 +9,7 @@
 #include <unordered_map>
 
 #include "kvq.h"
+#include "kvq_divu32.h"
 
 namespace kvq {
 
@@ -172,8 +173,9 @@ struct PageArgs {
   int32_t* row_dst;
   int32_t* row_slot;
   int32_t* seq_len_out;
+  DivU32 by_page;  // set at the launch
 };
-cudaError_t launch_page_update(const PageArgs& a, cudaStream_t st);
+cudaError_t launch_page_update(PageArgs a, cudaStream_t st);
 
 // Block index and sparse decode (the decode's head dims, no outlier channels).
 constexpr int kMaxIndexBlocks = 49152;  // keys of a row in shared memory: 192 KB

@@ -20,7 +20,6 @@
 namespace kvq {
 namespace {
 
-constexpr int kRopeThreads = 128;
 constexpr int kMaxPairs = 256;
 
 // floor(2^64 / 2pi)
@@ -65,41 +64,36 @@ __device__ __forceinline__ void store8(void* p, long long elem, const Raw8<DT>& 
   if constexpr (DT == KVQ_F32) d[1] = r.w[1];
 }
 template <int DT>
-__device__ __forceinline__ void to_f32(const Raw8<DT>& r, float (&x)[8]) {
-  if constexpr (DT == KVQ_F32) {
-    const uint32_t w[8] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w, r.w[1].x, r.w[1].y, r.w[1].z, r.w[1].w};
+__device__ __forceinline__ void to_f32(const Raw8<DT>& r, float2 (&x)[4]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
-  } else {
-    const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (DT == KVQ_BF16) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-      } else {
-        const float2 f = __half22float2(u32_as_h2(w[i]));
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
-      }
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (DT == KVQ_F32) {
+      const uint4& q = r.w[i / 2];
+      x[i] = i & 1 ? make_float2(__uint_as_float(q.z), __uint_as_float(q.w)) : make_float2(__uint_as_float(q.x), __uint_as_float(q.y));
+    } else {
+      const uint32_t v = i == 0 ? r.w[0].x : i == 1 ? r.w[0].y : i == 2 ? r.w[0].z : r.w[0].w;
+      if constexpr (DT == KVQ_BF16) x[i] = make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+      else x[i] = __half22float2(u32_as_h2(v));
     }
   }
 }
 template <int DT>
-__device__ __forceinline__ Raw8<DT> from_f32(const float (&x)[8]) {
+__device__ __forceinline__ Raw8<DT> from_f32(const float2 (&x)[4]) {
   Raw8<DT> r;
   if constexpr (DT == KVQ_F32) {
-    r.w[0] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
-    r.w[1] = make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]));
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      r.w[i] = make_uint4(__float_as_uint(x[2 * i].x), __float_as_uint(x[2 * i].y), __float_as_uint(x[2 * i + 1].x),
+                          __float_as_uint(x[2 * i + 1].y));
   } else {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if constexpr (DT == KVQ_BF16) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x[i].x, x[i].y);
         w[i] = *reinterpret_cast<const uint32_t*>(&h);
       } else {
-        w[i] = pack_h2(x[2 * i], x[2 * i + 1]);
+        w[i] = pack_h2(x[i].x, x[i].y);
       }
     }
     r.w[0] = make_uint4(w[0], w[1], w[2], w[3]);
@@ -107,10 +101,10 @@ __device__ __forceinline__ Raw8<DT> from_f32(const float (&x)[8]) {
   return r;
 }
 
-__device__ __forceinline__ void load_weights(const void* w, int dt, int ch, float (&x)[8]) {
+__device__ __forceinline__ void load_weights(const void* w, int dt, int ch, float2 (&x)[4]) {
   if (!w) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = 1.0f;
+    for (int i = 0; i < 4; ++i) x[i] = make_float2(1.0f, 1.0f);
   } else if (dt == KVQ_F32) {
     to_f32<KVQ_F32>(load8<KVQ_F32>(w, ch), x);
   } else if (dt == KVQ_BF16) {
@@ -120,146 +114,195 @@ __device__ __forceinline__ void load_weights(const void* w, int dt, int ch, floa
   }
 }
 
-// One CTA per row.  A head lies on L lanes, NC chunks of 8 channels each; a warp takes
-// 32 / L heads at a time.
-template <int DT, int L, int NC>
-__global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(RopeArgs a, kvq_rope_norm r) {
-  __shared__ __align__(16) float s_cos[kMaxPairs], s_sin[kMaxPairs];
-  constexpr int HW = 32 / L;  // heads per warp
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int row = blockIdx.x, d = a.head_dim, half = r.rot_dim / 2;
-  const int dst = a.dst_row ? a.dst_row[row] : row;
-  if (dst < 0 || dst >= a.n_dst_rows) {
-    if (dst >= 0 && threadIdx.x == 0) atomicOr(a.status, KVQ_DEV_ERR_ROW);
-    return;
+// A row is shared by WPR warps of a CTA of W.  A head lies on L lanes, NC chunks of 8 channels
+// each; a warp takes 32 / L heads at a time and has the loads of the next kAhead - 1 times in
+// flight, the first ones issued before the row's angles are computed.
+// The channels' factors (norm weight times cosine or sine) are worked out once per warp and row,
+// so with many rows a warp takes a whole row, and with few a row's heads spread over 8 warps.
+template <int DT, int L, int NC, int W, int WPR>
+__global__ void __launch_bounds__(32 * W, W == 4 ? (NC == 1 ? 6 : 4) : 2) qk_norm_rope_kernel(RopeArgs a, kvq_rope_norm r) {
+  constexpr int RPC = W / WPR, HW = 32 / L;  // rows of a CTA, heads of a warp
+  constexpr int kAhead = DT == KVQ_F32 || NC > 1 ? 2 : 4;
+  __shared__ __align__(16) float s_cos[RPC][kMaxPairs], s_sin[RPC][kMaxPairs];
+  const int lane = threadIdx.x & 31, sub = lane / L, l = lane % L;
+  const int rc = (threadIdx.x >> 5) / WPR, warp = (threadIdx.x >> 5) % WPR, rt = warp * 32 + lane;  // row of the CTA, place in it
+  const int row = blockIdx.x * RPC + rc, d = a.head_dim, half = r.rot_dim / 2;
+  int dst = row < a.n_rows ? (a.dst_row ? a.dst_row[row] : row) : -1;
+  if (dst >= a.n_dst_rows) {
+    if (rt == 0) atomicOr(a.status, KVQ_DEV_ERR_ROW);
+    dst = -1;
   }
-  const int pos = a.pos[row];
-  for (int i = threadIdx.x; i < half; i += kRopeThreads) {
+  if (WPR == W && dst < 0) return;  // (the CTA's only row)
+  const bool live = dst >= 0;
+  // the warp's units, HW heads each: the queries' (filled up to whole rounds of kAhead), then the keys'
+  const int nq = ((a.n_q_heads + HW - 1) / HW - warp + WPR - 1) / WPR, nk = ((a.n_kv_heads + HW - 1) / HW - warp + WPR - 1) / WPR;
+  const int nqp = (max(nq, 0) + kAhead - 1) / kAhead * kAhead;
+  const long long qbase = row * a.stride[0], kbase = row * a.stride[1];
+  Raw8<DT> raw[kAhead][NC];
+  auto load = [&](int u, int n) {  // unit n into raw[u]
+    const bool key = n >= nqp;
+    const int h = (warp + (key ? n - nqp : n) * WPR) * HW + sub, heads = key ? a.n_kv_heads : a.n_q_heads;
+    const void* in = key ? a.in[1] : a.in[0];
+    const long long base = key ? kbase : qbase;
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      const int ch = 8 * (l + 32 * j);  // (NC > 1 only with L = 32)
+      if (live && h < heads && ch < d) {
+        raw[u][j] = load8<DT>(in, base + h * d + ch);
+      } else {
+#pragma unroll
+        for (auto& q : raw[u][j].w) q = make_uint4(0, 0, 0, 0);
+      }
+    }
+  };
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) load(u, u);
+  const int pos = live ? a.pos[row] : 0;
+  if (a.in[2] && live) {  // values: one run of n_kv_heads * head_dim elements
+    const int n8 = a.n_kv_heads * d / 8;
+    const long long from = row * a.stride[2], to = (long long)dst * a.n_kv_heads * d;
+    for (int i = rt; i < n8; i += 32 * WPR) store8<DT>(a.out[2], to + 8 * i, load8<DT>(a.in[2], from + 8 * i));
+  }
+  for (int i = rt; i < half; i += 32 * WPR) {
     const unsigned long long t = (unsigned long long)(long long)pos * turns64(r.inv_freq[i]);
     // the upper 32 bits as a signed fraction of a turn in half turns: [-1, 1)
-    sincospif(float(int32_t(t >> 32)) * 4.656612873077393e-10f, &s_sin[i], &s_cos[i]);
+    sincospif(float(int32_t(t >> 32)) * 4.656612873077393e-10f, &s_sin[rc][i], &s_cos[rc][i]);
   }
-  __syncthreads();
-  const int sub = lane / L, l = lane % L;
+  if (WPR == 1) __syncwarp(); else __syncthreads();
+  if (!live) return;
+  const float inv_d = 1.0f / float(d);
 
+#pragma unroll 1
   for (int part = 0; part < 2; ++part) {  // queries, keys
     const int heads = part ? a.n_kv_heads : a.n_q_heads;
     const void* w = part ? r.k_weight : r.q_weight;
-    const void* in = a.in[part];
-    void* out = a.out[part];
-    float A[NC][8], B[NC][8];
-    int from[NC];     // lane (of L) and chunk the partner channels come from; -1: not rotated, -2: own chunk
+    void* out = part ? a.out[1] : a.out[0];
+    const int first = part ? nqp : 0, count = part ? nk : nqp;
+    float2 A[NC][4], B[NC][4];
+    int from[NC];     // chunk (of the head) the partner channels come from; -1: not rotated, -2: own chunk
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-      const int ck = l + 32 * j, ch = 8 * ck;  // (NC > 1 only with L = 32)
+      const int ck = l + 32 * j, ch = 8 * ck;
       from[j] = -1;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) A[j][i] = B[j][i] = make_float2(0.0f, 0.0f);
       if (ch < d) {
         load_weights(w, r.weight_dtype, ch, A[j]);
-        if (ch < r.rot_dim) {
-          if (r.interleaved) {
-            from[j] = -2;
+        if (ch < r.rot_dim && r.interleaved) {
+          from[j] = -2;
+          const float4 c = *reinterpret_cast<const float4*>(&s_cos[rc][ch / 2]), s = *reinterpret_cast<const float4*>(&s_sin[rc][ch / 2]);
+          const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-              const float c = s_cos[ch / 2 + i / 2], s = s_sin[ch / 2 + i / 2];
-              B[j][i] = -A[j][i + 1] * s;
-              B[j][i + 1] = A[j][i] * s;
-              A[j][i] *= c;
-              A[j][i + 1] *= c;
-            }
-          } else {
-            const bool second = ch >= half;
-            const int c0 = second ? ch - half : ch;
-            from[j] = second ? ck - half / 8 : ck + half / 8;
-            float wp[8];
-            load_weights(w, r.weight_dtype, 8 * from[j], wp);
+          for (int i = 0; i < 4; ++i) {
+            B[j][i] = make_float2(-A[j][i].y * ss[i], A[j][i].x * ss[i]);
+            A[j][i] = make_float2(A[j][i].x * cc[i], A[j][i].y * cc[i]);
+          }
+        } else if (ch < r.rot_dim) {
+          const bool second = ch >= half;
+          const int c0 = second ? ch - half : ch;
+          from[j] = second ? ck - half / 8 : ck + half / 8;
+          load_weights(w, r.weight_dtype, 8 * from[j], B[j]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float c = s_cos[c0 + i], s = s_sin[c0 + i];
-              A[j][i] *= c;
-              B[j][i] = second ? wp[i] * s : -wp[i] * s;
-            }
+          for (int i = 0; i < 4; ++i) {
+            const float2 c = *reinterpret_cast<const float2*>(&s_cos[rc][c0 + 2 * i]);
+            float2 s = *reinterpret_cast<const float2*>(&s_sin[rc][c0 + 2 * i]);
+            if (!second) s = make_float2(-s.x, -s.y);
+            A[j][i] = __fmul2_rn(A[j][i], c);
+            B[j][i] = __fmul2_rn(B[j][i], s);
           }
         }
       }
     }
-    for (int h0 = warp * HW; h0 < heads; h0 += (kRopeThreads / 32) * HW) {
-      const int h = h0 + sub;
-      Raw8<DT> raw[NC];
-      float x[NC][8], ss = 0.0f;
+#pragma unroll 1
+    for (int n0 = 0; n0 < count; n0 += kAhead) {
 #pragma unroll
-      for (int j = 0; j < NC; ++j) {
-        const int ch = 8 * (l + 32 * j);
-        if (h < heads && ch < d) {
-          raw[j] = load8<DT>(in, row * a.stride[part] + (long long)h * d + ch);
-        } else {
+      for (int u = 0; u < kAhead; ++u) {
+        const int h = (warp + (n0 + u) * WPR) * HW + sub;
+        if (h - sub < heads) {  // (warp-uniform)
+          float2 x[NC][4], sq = make_float2(0.0f, 0.0f);
 #pragma unroll
-          for (auto& q : raw[j].w) q = make_uint4(0, 0, 0, 0);
-        }
-        to_f32<DT>(raw[j], x[j]);
+          for (int j = 0; j < NC; ++j) {
+            to_f32<DT>(raw[u][j], x[j]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(x[j][i], x[j][i], ss);
-      }
-      float scale = 1.0f;
-      if (w) {
-#pragma unroll
-        for (int o = 1; o < L; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        scale = 1.0f / sqrtf(ss / float(d) + r.eps);
-      }
-#pragma unroll
-      for (int j = 0; j < NC; ++j) {
-        float xp[8], y[8];
-        if (r.interleaved || half == 0) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) xp[i] = x[j][i ^ 1];
-        } else {
-          // the partner's eight values; lanes that do not rotate read their own
-          Raw8<DT> rp;
-          const int fl = from[j] >= 0 ? from[j] % 32 : l, fj = from[j] >= 0 ? from[j] / 32 : j;
-          const int src = sub * L + fl;
-#pragma unroll
-          for (int q = 0; q < int(sizeof(rp.w) / 16); ++q) {
-            uint32_t t[4] = {0, 0, 0, 0};
-#pragma unroll
-            for (int jj = 0; jj < NC; ++jj) {
-              const uint32_t g[4] = {__shfl_sync(0xffffffffu, raw[jj].w[q].x, src),
-                                     __shfl_sync(0xffffffffu, raw[jj].w[q].y, src),
-                                     __shfl_sync(0xffffffffu, raw[jj].w[q].z, src),
-                                     __shfl_sync(0xffffffffu, raw[jj].w[q].w, src)};
-              if (fj == jj) { t[0] = g[0]; t[1] = g[1]; t[2] = g[2]; t[3] = g[3]; }
-            }
-            rp.w[q] = make_uint4(t[0], t[1], t[2], t[3]);
+            for (int i = 0; i < 4; ++i) sq = __ffma2_rn(x[j][i], x[j][i], sq);
           }
-          to_f32<DT>(rp, xp);
-        }
-        const int ch = 8 * (l + 32 * j);
-        if (h < heads && ch < d) {
+          float scale = 1.0f;
+          if (w) {
+            float ss = sq.x + sq.y;
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            y[i] = scale * (from[j] == -1 ? x[j][i] * A[j][i] : fmaf(x[j][i], A[j][i], xp[i] * B[j][i]));
-          store8<DT>(out, ((long long)dst * heads + h) * d + ch, from_f32<DT>(y));
+            for (int o = 1; o < L; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            scale = rsqrtf(fmaf(ss, inv_d, r.eps));
+          }
+          const float2 scale2 = make_float2(scale, scale);
+#pragma unroll
+          for (int j = 0; j < NC; ++j) {
+            float2 xp[4], y[4];
+            if (r.interleaved || half == 0) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) xp[i] = make_float2(x[j][i].y, x[j][i].x);
+            } else {
+              // the partner's eight values; lanes that do not rotate read their own
+              Raw8<DT> rp;
+              const int fl = from[j] >= 0 ? from[j] % 32 : l, fj = from[j] >= 0 ? from[j] / 32 : j;
+              const int src = sub * L + fl;
+#pragma unroll
+              for (int q = 0; q < int(sizeof(rp.w) / 16); ++q) {
+                uint4 t = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int jj = 0; jj < NC; ++jj) {
+                  const uint4 g = make_uint4(__shfl_sync(0xffffffffu, raw[u][jj].w[q].x, src),
+                                             __shfl_sync(0xffffffffu, raw[u][jj].w[q].y, src),
+                                             __shfl_sync(0xffffffffu, raw[u][jj].w[q].z, src),
+                                             __shfl_sync(0xffffffffu, raw[u][jj].w[q].w, src));
+                  if (NC == 1 || fj == jj) t = g;
+                }
+                rp.w[q] = t;
+              }
+              to_f32<DT>(rp, xp);
+            }
+            if (from[j] == -1) {  // (B is zero, but not where the partner is no number)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) xp[i] = make_float2(0.0f, 0.0f);
+            }
+            const int ch = 8 * (l + 32 * j);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              y[i] = __fmul2_rn(scale2, __ffma2_rn(x[j][i], A[j][i], __fmul2_rn(xp[i], B[j][i])));
+            if (h < heads && ch < d)
+              store8<DT>(out, ((long long)dst * heads + h) * d + ch, from_f32<DT>(y));
+          }
         }
+        load(u, first + n0 + u + kAhead);
       }
     }
-  }
-  if (a.in[2]) {  // values: one run of n_kv_heads * head_dim elements
-    const int n8 = a.n_kv_heads * d / 8;
-    for (int i = threadIdx.x; i < n8; i += kRopeThreads)
-      store8<DT>(a.out[2], (long long)dst * a.n_kv_heads * d + 8 * i, load8<DT>(a.in[2], row * a.stride[2] + 8 * i));
   }
 }
 
 template <int DT>
 cudaError_t launch_dt(const RopeArgs& a, const kvq_rope_norm& r, cudaStream_t st) {
   const int n = a.head_dim / 8;
-  auto go = [&](auto kern) {
-    kern<<<unsigned(a.n_rows), kRopeThreads, 0, st>>>(a, r);
+  const int sms = device_sm_count();
+  // As many warps per row as one wave holds: the factors of a row are worked out in each of its
+  // warps, and a second wave costs a whole one (1001 rows of 48 heads of 128: 4 warps a row
+  // 8.6 us, 2 TWO us; 8192 rows: 4 warps 52.6 us, 1 warp 38.8 us; 4 rows of 32 heads of 256:
+  // 4 warps 6.0 us, 8 warps 4.5 us).
+  auto go = [&](auto w8, auto w4, auto w2, auto w1) {
+    const long long n = a.n_rows, m = sms > 0 ? sms : 148;
+    if (n <= 2 * m) w8<<<unsigned(n), 256, 0, st>>>(a, r);
+    else if (n <= 6 * m) w4<<<unsigned(n), 128, 0, st>>>(a, r);
+    else if (n <= 12 * m) w2<<<unsigned((n + 1) / 2), 128, 0, st>>>(a, r);
+    else w1<<<unsigned((n + 3) / 4), 128, 0, st>>>(a, r);
     return cudaGetLastError();
   };
-  if (n <= 4) return go(qk_norm_rope_kernel<DT, 4, 1>);
-  if (n <= 8) return go(qk_norm_rope_kernel<DT, 8, 1>);
-  if (n <= 16) return go(qk_norm_rope_kernel<DT, 16, 1>);
-  if (n <= 32) return go(qk_norm_rope_kernel<DT, 32, 1>);
-  return go(qk_norm_rope_kernel<DT, 32, 2>);
+#define KVQ_ROPE(L, NC) \
+  go(qk_norm_rope_kernel<DT, L, NC, 8, 8>, qk_norm_rope_kernel<DT, L, NC, 4, 4>, \
+     qk_norm_rope_kernel<DT, L, NC, 4, 2>, qk_norm_rope_kernel<DT, L, NC, 4, 1>)
+  if (n <= 4) return KVQ_ROPE(4, 1);
+  if (n <= 8) return KVQ_ROPE(8, 1);
+  if (n <= 16) return KVQ_ROPE(16, 1);
+  if (n <= 32) return KVQ_ROPE(32, 1);
+  return KVQ_ROPE(32, 2);
+#undef KVQ_ROPE
 }
 
 }  // namespace

@@ -253,74 +253,86 @@ def kvq_prefill_attention(cache: kvq_cache, q, out, workspace, q_pos0=None, caus
            "kvq_prefill_attention")
 
 
-def _expect(what: str, shape, dtype, *tensors):
-    """ValueError unless the tensors (None allowed) are contiguous, on the current device and of that shape and type
+def _expect(what: str, dev: int, shape, dtype, *tensors):
+    """ValueError unless the tensors (None allowed) are contiguous, on CUDA device `dev` and of that shape and type
     (None: any shape; any of the q / k / v types)."""
-    import torch
-    dev = torch.cuda.current_device()
     for t in tensors:
-        if t is None:
-            continue
-        if (t.get_device() != dev or not t.is_contiguous() or (shape is not None and t.shape != shape) or
-                (t.dtype is not dtype if dtype is not None else t.dtype not in _dtypes())):
+        if t is not None and (t.get_device() != dev or not t.is_contiguous() or
+                              (t.dtype is not dtype if dtype is not None else t.dtype not in _dtypes()) or
+                              (shape is not None and t.shape != shape)):
             raise ValueError(f"{what}: expected {shape or 'any shape'} of {dtype or 'fp32, bf16 or fp16'}, contiguous, on "
                              f"CUDA device {dev}; got {tuple(t.shape)} of {t.dtype} on {t.device}")
 
 
-def _heads_row_stride(what: str, t, heads: int, d: int, n_rows: int, like) -> int:
+def _heads_row_stride(what: str, t, dev: int, dtype, heads: int, d: int, n_rows: int) -> int:
     """Row stride (elements) of projection rows [n_rows][heads * d] or [n_rows][heads][d] whose heads lie side by side."""
-    shape, stride = t.shape, t.stride()
-    if t.dtype is like.dtype and t.get_device() == like.get_device() and shape[0] == n_rows:
+    if t.dtype is dtype and t.get_device() == dev:
+        shape, stride = t.shape, t.stride()
         if len(shape) == 2:
-            ok = shape[1] == heads * d and (stride[1] == 1 or n_rows == 0)
+            ok = shape == (n_rows, heads * d) and (stride[1] == 1 or n_rows == 0)
         else:
-            ok = shape[1:] == (heads, d) and (n_rows == 0 or (stride[2] == 1 and (heads == 1 or stride[1] == d)))
+            ok = shape == (n_rows, heads, d) and (n_rows == 0 or (stride[2] == 1 and (heads == 1 or stride[1] == d)))
         if ok:
             # (the stride of a single row is free: torch may report any number)
             return stride[0] if n_rows > 1 else heads * d
-    raise ValueError(f"{what}: expected {n_rows} rows of {heads} x {d} values of {like.dtype}, heads side by side")
+    raise ValueError(f"{what}: expected {n_rows} rows of {heads} x {d} values of {dtype}, heads side by side, on CUDA "
+                     f"device {dev}; got {tuple(t.shape)} of {t.dtype} on {t.device}")
+
+
+_torch = None  # torch, its current-device query and int32, looked up once
+_device = None
+_int32 = None
+
+
+def _torch_ready():
+    global _torch, _device, _int32
+    if _torch is None:
+        import torch
+        _device, _int32, _torch = torch.cuda.current_device, torch.int32, torch
+    return _torch
 
 
 class RopeNorm:
     """The plan of kvq_qk_norm_rope: inv_freq fp32 [rot_dim / 2] (None: no rotation), weights [head_dim] or None."""
 
     def __init__(self, inv_freq=None, q_weight=None, k_weight=None, eps=1e-6, interleaved=False):
-        import torch
-        _expect("RopeNorm", None, torch.float32, inv_freq)
-        _expect("RopeNorm", None, None, q_weight, k_weight)
-        if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
-            raise ValueError("RopeNorm: q_weight and k_weight differ in type")
+        torch = _torch_ready()
+        dev = _device()
+        _expect("RopeNorm", dev, None, torch.float32, inv_freq)
+        _expect("RopeNorm", dev, None, None, q_weight, k_weight)
+        weights = [w for w in (q_weight, k_weight) if w is not None]
+        if any(w.dtype != weights[0].dtype or w.shape != weights[0].shape or w.dim() != 1 or not w.numel() for w in weights):
+            raise ValueError("RopeNorm: the weights are vectors of one type and size")
         self.inv_freq, self.q_weight, self.k_weight = inv_freq, q_weight, k_weight  # kept alive
+        self.weight_dim = weights[0].numel() if weights else None
         self.desc = kvq_rope_norm()
         self.desc.rot_dim = 0 if inv_freq is None else 2 * inv_freq.numel()
         self.desc.interleaved = 1 if interleaved else 0
         self.desc.eps = eps
-        w = q_weight if q_weight is not None else k_weight
-        self.weight_dim = 0 if w is None else w.numel()
-        if k_weight is not None and k_weight.numel() != self.weight_dim:
-            raise ValueError("RopeNorm: q_weight and k_weight differ in size")
-        self.desc.weight_dtype = KVQ_F32 if w is None else _dtype_id(w)
+        self.desc.weight_dtype = _dtype_id(weights[0]) if weights else KVQ_F32
         self.desc.q_weight, self.desc.k_weight = _ptr(q_weight), _ptr(k_weight)
         self.desc.inv_freq = None if self.desc.rot_dim == 0 else _ptr(inv_freq)
 
 
 def kvq_qk_norm_rope(cache: kvq_cache, rope: RopeNorm, q, k, v, pos, q_out, k_out, v_out, dst_row=None, stream=None):
     """Rows q [n][heads * d] or [n][heads][d] (any row stride, e.g. parts of one projection), k and v (or None) the same
-    with the KV heads; pos int32 [n], dst_row int32 [n] or None.  Outputs [rows][heads][d], or [..][heads][d] contiguous."""
-    import torch
-    d, hkv, (hq, dq), n = cache.head_dim, cache.n_kv_heads, q_out.shape[-2:], q.shape[0]
+    with the KV heads; pos int32 [n], dst_row int32 [n] or None.  Outputs [..][heads][d], contiguous, of the same rows."""
+    _torch_ready()
+    dev, dtype, d, hkv = _device(), q.dtype, cache.head_dim, cache.n_kv_heads
+    shape, n = q_out.shape, q.shape[0]
+    hq = shape[-2]
     rows = q_out.numel() // max(1, hq * d)
-    if rope.weight_dim not in (0, d):
-        raise ValueError("kvq_qk_norm_rope: a weight has not head_dim values")
-    _expect("kvq_qk_norm_rope: pos, dst_row", (n,), torch.int32, pos, dst_row)
-    _expect("kvq_qk_norm_rope: outputs", None, q.dtype, q_out, k_out, v_out)
-    if dq != d or k_out.numel() != rows * hkv * d or (v_out is not None and v_out.numel() != rows * hkv * d):
+    if rope.weight_dim is not None and rope.weight_dim != d:
+        raise ValueError("kvq_qk_norm_rope: the weights have not head_dim values")
+    _expect("kvq_qk_norm_rope: pos, dst_row", dev, (n,), _int32, pos, dst_row)
+    _expect("kvq_qk_norm_rope: outputs", dev, None, dtype, q_out, k_out, v_out)
+    if shape[-1] != d or k_out.numel() != rows * hkv * d or (v_out is not None and v_out.numel() != rows * hkv * d):
         raise ValueError("kvq_qk_norm_rope: the outputs differ in rows, heads or head_dim")
-    qs = _heads_row_stride("kvq_qk_norm_rope: q", q, hq, d, n, q_out)
-    ks = _heads_row_stride("kvq_qk_norm_rope: k", k, hkv, d, n, q_out)
-    vs = 0 if v is None else _heads_row_stride("kvq_qk_norm_rope: v", v, hkv, d, n, q_out)
-    _check(lib().kvq_qk_norm_rope(ctypes.byref(cache), ctypes.byref(rope.desc), _dtype_id(q), hq, _ptr(q), qs, _ptr(k),
-                                  ks, _ptr(v), vs, _ptr(pos), _ptr(dst_row), n, rows, _ptr(q_out), _ptr(k_out),
+    qs = _heads_row_stride("kvq_qk_norm_rope: q", q, dev, dtype, hq, d, n)
+    ks = _heads_row_stride("kvq_qk_norm_rope: k", k, dev, dtype, hkv, d, n)
+    vs = 0 if v is None else _heads_row_stride("kvq_qk_norm_rope: v", v, dev, dtype, hkv, d, n)
+    _check(lib().kvq_qk_norm_rope(cache, rope.desc, _dtypes()[dtype], hq, q.data_ptr(), qs, k.data_ptr(), ks, _ptr(v), vs,
+                                  pos.data_ptr(), _ptr(dst_row), n, rows, q_out.data_ptr(), k_out.data_ptr(),
                                   _ptr(v_out), _stream(stream)),
            "kvq_qk_norm_rope")
 
@@ -344,15 +356,17 @@ class PagePool:
 def kvq_page_update(cache: kvq_cache, pool, n_new, n_new_max: int, granted, row_pos=None, row_dst=None, row_slot=None,
                     seq_len_out=None, stream=None):
     """pool: PagePool or kvq_page_pool; n_new, granted, seq_len_out int32 [batch]; the row maps int32 [max_rows]."""
-    import torch
-    _expect("kvq_page_update", (cache.batch,), torch.int32, n_new, granted, seq_len_out)
-    rows = next((t.numel() for t in (row_pos, row_dst, row_slot) if t is not None), None)
-    if rows is None:
-        rows = min(cache.batch * n_new_max, 0x7fffffff)  # no maps: no limit of rows
+    _torch_ready()
+    dev, batch = _device(), cache.batch
+    _expect("kvq_page_update", dev, (batch,), _int32, n_new, granted, seq_len_out)
+    a_map = row_dst if row_dst is not None else row_pos if row_pos is not None else row_slot
+    if a_map is None:
+        rows = min(batch * n_new_max, 0x7fffffff)  # no maps: no limit of rows
     else:
-        _expect("kvq_page_update: row maps", (rows,), torch.int32, row_pos, row_dst, row_slot)
+        rows = a_map.numel()
+        _expect("kvq_page_update: row maps", dev, (rows,), _int32, row_pos, row_dst, row_slot)
     desc = pool.desc if isinstance(pool, PagePool) else pool
-    _check(lib().kvq_page_update(ctypes.byref(cache), ctypes.byref(desc), _ptr(n_new), n_new_max, _ptr(granted), rows,
+    _check(lib().kvq_page_update(cache, desc, _ptr(n_new), n_new_max, _ptr(granted), rows,
                                  _ptr(row_pos), _ptr(row_dst), _ptr(row_slot), _ptr(seq_len_out), _stream(stream)),
            "kvq_page_update")
 
@@ -374,28 +388,29 @@ def _index_desc(index):
 
 def kvq_block_index_update(cache: kvq_cache, index, n_last: int = 0, stream=None):
     """index: BlockIndex or kvq_block_index; n_last 0: every block, else those of the last n_last tokens."""
-    _check(lib().kvq_block_index_update(ctypes.byref(cache), ctypes.byref(_index_desc(index)), n_last, _stream(stream)),
+    _check(lib().kvq_block_index_update(cache, _index_desc(index), n_last, _stream(stream)),
            "kvq_block_index_update")
 
 
 def kvq_select_blocks(cache: kvq_cache, index, q, sel, n_first: int = 1, n_last: int = 1, stream=None):
     """q [batch][n_q_heads][head_dim]; sel int32 [batch][n_kv_heads][n_select]."""
-    import torch
-    _expect("kvq_select_blocks: q", (cache.batch, q.shape[1], cache.head_dim), None, q)
-    _expect("kvq_select_blocks: sel", (cache.batch, cache.n_kv_heads, sel.shape[-1]), torch.int32, sel)
-    _check(lib().kvq_select_blocks(ctypes.byref(cache), ctypes.byref(_index_desc(index)), _ptr(q), _dtype_id(q),
-                                   q.shape[1], n_first, n_last, sel.shape[-1], _ptr(sel), _stream(stream)),
+    _torch_ready()
+    dev, batch, hq, n = _device(), cache.batch, q.shape[1], sel.shape[-1]
+    _expect("kvq_select_blocks: q", dev, (batch, hq, cache.head_dim), None, q)
+    _expect("kvq_select_blocks: sel", dev, (batch, cache.n_kv_heads, n), _int32, sel)
+    _check(lib().kvq_select_blocks(cache, _index_desc(index), q.data_ptr(), _dtypes()[q.dtype], hq, n_first, n_last, n,
+                                   sel.data_ptr(), _stream(stream)),
            "kvq_select_blocks")
 
 
 def kvq_sparse_decode_attention(cache: kvq_cache, q, sel, out, block_tokens: int, scale: float = 0.0, stream=None):
     """q, out [batch][n_q_heads][head_dim]; sel int32 [batch][n_kv_heads][n_select] block numbers (negative: none)."""
-    import torch
-    _expect("kvq_sparse_decode_attention: q, out", (cache.batch, q.shape[1], cache.head_dim), None, q, out)
-    _expect("kvq_sparse_decode_attention: sel", (cache.batch, cache.n_kv_heads, sel.shape[-1]), torch.int32, sel)
-    _check(lib().kvq_sparse_decode_attention(ctypes.byref(cache), _ptr(q), _dtype_id(q), q.shape[1], float(scale),
-                                             block_tokens, _ptr(sel), sel.shape[-1], _ptr(out), _dtype_id(out),
-                                             _stream(stream)),
+    _torch_ready()
+    dev, batch, hq, n, ids = _device(), cache.batch, q.shape[1], sel.shape[-1], _dtypes()
+    _expect("kvq_sparse_decode_attention: q, out", dev, (batch, hq, cache.head_dim), None, q, out)
+    _expect("kvq_sparse_decode_attention: sel", dev, (batch, cache.n_kv_heads, n), _int32, sel)
+    _check(lib().kvq_sparse_decode_attention(cache, q.data_ptr(), ids[q.dtype], hq, scale, block_tokens, sel.data_ptr(), n,
+                                             out.data_ptr(), ids[out.dtype], _stream(stream)),
            "kvq_sparse_decode_attention")
 
 

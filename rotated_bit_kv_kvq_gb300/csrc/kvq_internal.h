@@ -5,7 +5,9 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <map>
 #include <mutex>
+#include <tuple>
 #include <unordered_map>
 
 #include "kvq.h"
@@ -64,6 +66,42 @@ inline cudaError_t allow_large_clusters(const void* kernel) {
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess && dev >= 0 && dev < kMaxDevices) done[kernel][dev] = true;
   return e;
+}
+
+// How many clusters of k CTAs of a kernel the device runs at once (a cluster stays within a
+// group of SMs, and the groups differ in size), for k = 2 .. kMaxCluster; asked once per kernel,
+// shared-memory size and device.  NULL when the query fails.
+constexpr int kMaxCluster = 16;
+struct ClusterLimits {
+  int clusters[kMaxCluster + 1];
+};
+inline const ClusterLimits* cluster_limits(const void* kernel, int threads, int smem) {
+  static std::mutex mu;
+  static std::map<std::tuple<const void*, int, int>, ClusterLimits> known;  // (a map's values never move)
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
+  std::lock_guard<std::mutex> lock(mu);
+  const auto key = std::make_tuple(kernel, smem, dev);
+  const auto it = known.find(key);
+  if (it != known.end()) return &it->second;
+  ClusterLimits lim{};
+  for (int k = 2; k <= kMaxCluster; ++k) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(k));
+    cfg.blockDim = dim3(unsigned(threads));
+    cfg.dynamicSmemBytes = size_t(smem);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = unsigned(k);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&lim.clusters[k], kernel, &cfg) != cudaSuccess) {
+      cudaGetLastError();  // (this size is not available)
+      lim.clusters[k] = 0;
+    }
+  }
+  return &known.emplace(key, lim).first->second;
 }
 
 // Launchers (arguments already validated by the API layer).

@@ -32,7 +32,6 @@ namespace cg = cooperative_groups;
 
 constexpr int kTailRows = 8;   // tokens of a tail tile
 constexpr int kMaxStages = 4;
-constexpr int kMaxCluster = 16;
 
 template <int D> constexpr int kRows = D <= 128 ? 32 : 16;               // tokens of a body tile
 template <int D> constexpr int kW = D <= 128 ? 8 : D <= 256 ? 6 : 8;      // warps of a CTA
@@ -102,6 +101,23 @@ __device__ __forceinline__ uint32_t nib_sub(uint32_t r, uint32_t hb) {
   return (r & (H16 ? 0x00F000F0u : 0x000F000Fu)) | hb;
 }
 
+// ldmatrix rows of a 16-row tile in W-byte box columns (R rows each): the lane's row and its
+// swizzle key, and the address of 16-byte chunk j + (lane's half), j even, may be a run-time value
+template <int W>
+struct LdRow {
+  uint32_t row, key;
+  __device__ explicit LdRow(uint32_t base, int lane) {
+    const int r = (lane & 7) + 8 * ((lane >> 3) & 1);
+    const int k = W == 128 ? (r & 7) : W == 64 ? ((r >> 1) & 3) : ((r >> 2) & 1);
+    row = base + r * W;
+    key = uint32_t((k ^ (lane >> 4)) << 4);
+  }
+  template <int R>
+  __device__ uint32_t at(int j) const {
+    return row + (uint32_t((j % (W / 16)) << 4) ^ key) + (j / (W / 16)) * (R * W);
+  }
+};
+
 // D = A * B + C with C apart from D (the initial values are shared by several mma)
 __device__ __forceinline__ void mma16816_from(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%11,%11};"
@@ -115,64 +131,52 @@ __device__ __forceinline__ void body_scores(uint32_t st, const SpStage& L, uint3
                                             float (&S)[kRows<D> / 16][2][2]) {
   constexpr int NB = D / 32, RB = kRows<D>, HB = RB / 16, ROW = KT == KVQ_TYPE_Q8_0 ? D : D / 2, W = box_w(ROW);
   constexpr bool K1 = type_has_min(KT), K5 = type_has_qh(KT);
-  constexpr int KHH = K1 ? 2 : 1, HW = NB * KHH / 2;
-  const int g = lane >> 2, tig = lane & 3, mi = lane >> 3, rr = (lane & 7) + 8 * (mi & 1);
-  uint32_t lb[W / 32];
-  swz_lane<W>(rr, mi >> 1, lb);
-  uint32_t hd[HB][4][HW];  // headers of tokens 16hh + 2tig, + 1, + 8, + 9
-#pragma unroll
-  for (int hh = 0; hh < HB; ++hh)
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      lds_row<NB * 2 * KHH>(st + L.kd + 2 * tig * NB * 2 * KHH + (16 * hh + (i & 1) + 8 * (i >> 1)) * NB * 2 * KHH, hd[hh][i]);
+  constexpr int KHH = K1 ? 2 : 1, HP = NB * 2 * KHH;  // halves of a block header, bytes of a row's
+  const int g = lane >> 2, tig = lane & 3;
+  const LdRow<W> ld(st, lane);
   const float off = KT == KVQ_TYPE_Q8_0 ? 128.0f : float(type_code_offset(KT));
-  // operands of the two k-steps of block blk for the 8-token tiles of half hh
-  auto dots = [&](int blk, int hh, const uint32_t (&b)[2][4], const uint32_t (&a0)[4], const uint32_t (&a1)[4], float qs) {
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      float cc[4];
-      mma16816_from(cc, a0, b[t][0], b[t][1], K1 ? 0.0f : -off * qs);
-      mma16816(cc, a1, b[t][2], b[t][3]);
-      const float s0 = cc[0] + cc[2], s1 = cc[1] + cc[3];
-      S[hh][t][0] = fmaf(hdr_scale<KHH>(hd[hh][2 * t], blk), s0, S[hh][t][0]);
-      S[hh][t][1] = fmaf(hdr_scale<KHH>(hd[hh][2 * t + 1], blk), s1, S[hh][t][1]);
-      if constexpr (K1) {
-        S[hh][t][0] = fmaf(h2f(hd[hh][2 * t][blk], 1), qs, S[hh][t][0]);
-        S[hh][t][1] = fmaf(h2f(hd[hh][2 * t + 1][blk], 1), qs, S[hh][t][1]);
-      }
-    }
-  };
   const uint32_t k0 = uint32_t(8 * (tig >> 1) + 2 * (tig & 1) - 4) & 31u, k1 = (k0 + 1) & 31u;
-  constexpr int BP = KT == KVQ_TYPE_Q8_0 ? 1 : 2;  // blocks of one ldmatrix
-#pragma unroll
-  for (int bp = 0; bp < NB; bp += BP) {
-    uint32_t r[HB][4];
+  const uint32_t hd0 = st + L.kd + 2 * tig * HP, qh0 = st + L.kqh + g * NB * 4, qf0 = qf + lane * 16, qs0 = qsum + g * 4;
+  // Two blocks at a time.  Large heads keep the loop rolled: a call lasts a few tiles per warp, and
+  // straight-line code of 8 or 10 blocks is fetched once for each of them.
+  constexpr int kUnroll = D <= 128 ? NB / 2 : 1;
+#pragma unroll kUnroll
+  for (int bp = 0; bp < NB; bp += 2) {
+    uint32_t r[HB][KT == KVQ_TYPE_Q8_0 ? 2 : 1][4], hd[HB][4][KHH];
 #pragma unroll
     for (int hh = 0; hh < HB; ++hh) {
-      const int j = KT == KVQ_TYPE_Q8_0 ? 2 * bp : bp;  // its first 16-byte chunk
-      ldsm_x4(st + hh * 16 * W + lb[swz_lane_idx<W>(j)] + swz_box_off<W, RB>(j), r[hh][0], r[hh][1], r[hh][2], r[hh][3]);
+      if constexpr (KT == KVQ_TYPE_Q8_0) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          ldsm_x4(ld.template at<RB>(2 * (bp + e)) + hh * 16 * W, r[hh][e][0], r[hh][e][1], r[hh][e][2], r[hh][e][3]);
+      } else {
+        ldsm_x4(ld.template at<RB>(bp) + hh * 16 * W, r[hh][0][0], r[hh][0][1], r[hh][0][2], r[hh][0][3]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)  // headers of tokens 16hh + 2tig, + 1, + 8, + 9
+        lds_row<4 * KHH>(hd0 + (16 * hh + (i & 1) + 8 * (i >> 1)) * HP + bp * 2 * KHH, hd[hh][i]);
     }
 #pragma unroll
-    for (int e = 0; e < BP; ++e) {
+    for (int e = 0; e < 2; ++e) {
       const int blk = bp + e;
-      const uint4 qa = lds128(qf + lane * 16 + blk * 1024), qb = lds128(qf + lane * 16 + blk * 1024 + 512);
+      const uint4 qa = lds128(qf0 + blk * 1024), qb = lds128(qf0 + blk * 1024 + 512);
       const uint32_t a0[4] = {qa.x, qa.y, qa.z, qa.w}, a1[4] = {qb.x, qb.y, qb.z, qb.w};
-      const float qs = __uint_as_float(lds32(qsum + g * 4 + blk * (kMaxHeads * 4)));
+      const float qs = __uint_as_float(lds32(qs0 + blk * (kMaxHeads * 4)));
 #pragma unroll
       for (int hh = 0; hh < HB; ++hh) {
-        uint32_t b[2][4];
+        uint32_t b[2][4];  // operands of the two k-steps for the 8-token tiles of half hh
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           if constexpr (KT == KVQ_TYPE_Q8_0) {  // r[t]: channels 4tig .. of the first half block, r[2 + t] of the second
-            b[t][0] = __byte_perm(r[hh][t], 0, 0x4240);
-            b[t][1] = __byte_perm(r[hh][t], 0, 0x4341);
-            b[t][2] = __byte_perm(r[hh][2 + t], 0, 0x4240);
-            b[t][3] = __byte_perm(r[hh][2 + t], 0, 0x4341);
+            b[t][0] = __byte_perm(r[hh][e][t], 0, 0x4240);
+            b[t][1] = __byte_perm(r[hh][e][t], 0, 0x4341);
+            b[t][2] = __byte_perm(r[hh][e][2 + t], 0, 0x4240);
+            b[t][3] = __byte_perm(r[hh][e][2 + t], 0, 0x4341);
           } else {
-            const uint32_t w = r[hh][2 * e + t], w8 = w >> 8;
+            const uint32_t w = r[hh][0][2 * e + t], w8 = w >> 8;
             uint32_t h0 = 0, h1 = 0;
             if constexpr (K5) {  // rotated: the pairs' bits at 4 / 20 (low nibbles) and 8 / 24
-              const uint32_t h = lds32(st + L.kqh + g * NB * 4 + ((16 * hh + 8 * t) * NB + blk) * 4);
+              const uint32_t h = lds32(qh0 + ((16 * hh + 8 * t) * NB + blk) * 4);
               h0 = __funnelshift_r(h, h, k0);
               h1 = __funnelshift_r(h, h, k1);
             }
@@ -182,7 +186,18 @@ __device__ __forceinline__ void body_scores(uint32_t st, const SpStage& L, uint3
             b[t][3] = nib_sub<true>(w8, h1 & 0x01000100u);
           }
         }
-        dots(blk, hh, b, a0, a1, qs);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          float cc[4];
+          mma16816_from(cc, a0, b[t][0], b[t][1], K1 ? 0.0f : -off * qs);
+          mma16816(cc, a1, b[t][2], b[t][3]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t (&w)[KHH] = hd[hh][2 * t + i];
+            S[hh][t][i] = fmaf(KHH == 1 ? h2f(w[0], e) : h2f(w[e % KHH], 0), cc[i] + cc[2 + i], S[hh][t][i]);
+            if constexpr (K1) S[hh][t][i] = fmaf(h2f(w[e % KHH], 1), qs, S[hh][t][i]);
+          }
+        }
       }
     }
   }
@@ -197,30 +212,31 @@ __device__ __forceinline__ void body_values(uint32_t st, const SpStage& L, int r
                                             float (&acc)[D / 32][2][4], float (&dmin)[4]) {
   constexpr int NB = D / 32, RB = kRows<D>, ROW = VT == KVQ_TYPE_Q8_0 ? D : D / 2, W = box_w(ROW);
   constexpr bool V1 = type_has_min(VT), V5 = type_has_qh(VT);
-  constexpr int VHH = V1 ? 2 : 1, VW = NB * VHH / 2;
-  const int g = lane >> 2, tig = lane & 3, mi = lane >> 3, rr = (lane & 7) + 8 * (mi & 1);
-  uint32_t lb[W / 32];
-  swz_lane<W>(rr, mi >> 1, lb);
-  const uint32_t vb = st + L.v + row0 * W, vd = st + L.vd + (row0 + 2 * tig) * NB * 2 * VHH;
-  uint32_t vh[4][VW];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) lds_row<NB * 2 * VHH>(vd + ((i & 1) + 8 * (i >> 1)) * NB * 2 * VHH, vh[i]);
+  constexpr int VHH = V1 ? 2 : 1;
+  constexpr int HP = NB * 2 * VHH;
+  const int g = lane >> 2, tig = lane & 3;
+  const LdRow<W> ld(st + L.v + row0 * W, lane);
+  const uint32_t vd = st + L.vd + (row0 + 2 * tig) * HP;
   auto ok = [&](int i) { return row0 + (i & 1) + 8 * (i >> 1) < cnt - 2 * tig; };  // token i of the lane's four is one
   const bool partial = cnt < RB;
-  if (partial) {  // rows past the end hold anything: their headers become zero
+  // headers of the lane's four tokens for blocks bp, bp + 1; rows past the end hold anything: theirs become zero
+  auto headers = [&](int bp, uint32_t (&w)[4][VHH]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4; ++i) lds_row<4 * VHH>(vd + ((i & 1) + 8 * (i >> 1)) * HP + bp * 2 * VHH, w[i]);
+    if (partial) {
 #pragma unroll
-      for (int j = 0; j < VW; ++j) vh[i][j] = ok(i) ? vh[i][j] : 0u;
-  }
-  auto scales = [&](int blk, int a, int b) -> uint32_t {
-    if constexpr (VHH == 1) return __byte_perm(vh[a][blk >> 1], vh[b][blk >> 1], (blk & 1) ? 0x7632 : 0x5410);
-    else return __byte_perm(vh[a][blk], vh[b][blk], 0x5410);
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < VHH; ++j) w[i][j] = ok(i) ? w[i][j] : 0u;
+    }
   };
-  auto block = [&](int blk, const uint32_t (&a0)[4], const uint32_t (&a1)[4]) {
+  auto block = [&](int blk, const uint32_t (&w)[4][VHH], const uint32_t (&a0)[4], const uint32_t (&a1)[4]) {
+    const int e = blk & 1;
+    const uint32_t d0 = VHH == 1 ? __byte_perm(w[0][0], w[1][0], e ? 0x7632 : 0x5410) : __byte_perm(w[0][e % VHH], w[1][e % VHH], 0x5410);
+    const uint32_t d1 = VHH == 1 ? __byte_perm(w[2][0], w[3][0], e ? 0x7632 : 0x5410) : __byte_perm(w[2][e % VHH], w[3][e % VHH], 0x5410);
     uint32_t h0, l0, h1, l1;
-    hscale_split(ph[0], pl[0], scales(blk, 0, 1), h0, l0);
-    hscale_split(ph[1], pl[1], scales(blk, 2, 3), h1, l1);
+    hscale_split(ph[0], pl[0], d0, h0, l0);
+    hscale_split(ph[1], pl[1], d1, h1, l1);
     mma16816(acc[blk][0], a0, h0, h1);
     mma16816(acc[blk][0], a0, l0, l1);
     mma16816(acc[blk][1], a1, h0, h1);
@@ -238,43 +254,46 @@ __device__ __forceinline__ void body_values(uint32_t st, const SpStage& L, int r
     mma16816(dmin, al, ph[0], ph[1]);
     mma16816(dmin, al, pl[0], pl[1]);
   }
-  if constexpr (VT == KVQ_TYPE_Q8_0) {
+  constexpr uint32_t OFF = (0x6400u + uint32_t(type_code_offset(VT))) * 0x10001u;
+  constexpr uint32_t OFF16 = neg_off_x16_bits(type_code_offset(VT));
+  const uint32_t v0 = uint32_t(8 * ((g & 3) >> 1) + 2 * (g & 1) - 4) & 31u, v1 = (v0 + 1) & 31u;
+  const uint32_t qh0 = st + L.vqh + (tig * NB * 2 + (g >> 2)) * 4 + row0 * NB * 4;
 #pragma unroll
-    for (int blk = 0; blk < NB; ++blk) {
-      uint32_t r0, r1, r2, r3;
-      ldsm_x4_t(vb + lb[swz_lane_idx<W>(2 * blk)] + swz_box_off<W, RB>(2 * blk), r0, r1, r2, r3);
-      const uint32_t a0[4] = {i8_pair<0, 2>(r0), i8_pair<1, 3>(r0), i8_pair<0, 2>(r1), i8_pair<1, 3>(r1)};
-      const uint32_t a1[4] = {i8_pair<0, 2>(r2), i8_pair<1, 3>(r2), i8_pair<0, 2>(r3), i8_pair<1, 3>(r3)};
-      block(blk, a0, a1);
-    }
-  } else {
-    constexpr uint32_t OFF = (0x6400u + uint32_t(type_code_offset(VT))) * 0x10001u;
-    constexpr uint32_t OFF16 = neg_off_x16_bits(type_code_offset(VT));
-    const uint32_t v0 = uint32_t(8 * ((g & 3) >> 1) + 2 * (g & 1) - 4) & 31u, v1 = (v0 + 1) & 31u;
+  for (int bp = 0; bp < NB; bp += 2) {
+    uint32_t w[4][VHH];
+    headers(bp, w);
+    if constexpr (VT == KVQ_TYPE_Q8_0) {
 #pragma unroll
-    for (int bp = 0; bp < NB; bp += 2) {
+      for (int e = 0; e < 2; ++e) {
+        uint32_t r0, r1, r2, r3;
+        ldsm_x4_t(ld.template at<RB>(2 * (bp + e)), r0, r1, r2, r3);
+        const uint32_t a0[4] = {i8_pair<0, 2>(r0), i8_pair<1, 3>(r0), i8_pair<0, 2>(r1), i8_pair<1, 3>(r1)};
+        const uint32_t a1[4] = {i8_pair<0, 2>(r2), i8_pair<1, 3>(r2), i8_pair<0, 2>(r3), i8_pair<1, 3>(r3)};
+        block(bp + e, w, a0, a1);
+      }
+    } else {
       uint32_t r[4];
-      ldsm_x4_t(vb + lb[swz_lane_idx<W>(bp)] + swz_box_off<W, RB>(bp), r[0], r[1], r[2], r[3]);
+      ldsm_x4_t(ld.template at<RB>(bp), r[0], r[1], r[2], r[3]);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int blk = bp + e;
         uint32_t a0[4], a1[4];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {  // tokens 0-7, 8-15
-          const uint32_t w = r[2 * e + t], w8 = w >> 8;
+          const uint32_t c = r[2 * e + t], c8 = c >> 8;
           uint32_t m0 = 0x64006400u, m1 = m0, m2 = m0, m3 = m0;
           if constexpr (V5) {  // the lane's part word of rows 8t + 2tig, + 1
-            const uint32_t h = lds32(st + L.vqh + (tig * NB * 2 + (g >> 2)) * 4 + ((row0 / 2 + 4 * t) * NB + blk) * 8);
+            const uint32_t h = lds32(qh0 + (4 * t * NB + blk) * 8);
             const uint32_t h0 = __funnelshift_r(h, h, v0), h1 = __funnelshift_r(h, h, v1);
             m0 = vhb(h0, 0x00100010u); m1 = vhb(h1, 0x00100010u);
             m2 = vhb(h0, 0x01000100u); m3 = vhb(h1, 0x01000100u);
           }
-          a0[2 * t] = nib_pair(w, 0, m0, OFF);
-          a0[2 * t + 1] = nib_pair(w8, 0, m1, OFF);
-          a1[2 * t] = nib_pair_x16(w, m2, OFF16);
-          a1[2 * t + 1] = nib_pair_x16(w8, m3, OFF16);
+          a0[2 * t] = nib_pair(c, 0, m0, OFF);
+          a0[2 * t + 1] = nib_pair(c8, 0, m1, OFF);
+          a1[2 * t] = nib_pair_x16(c, m2, OFF16);
+          a1[2 * t + 1] = nib_pair_x16(c8, m3, OFF16);
         }
-        block(blk, a0, a1);
+        block(blk, w, a0, a1);
       }
     }
   }
@@ -776,8 +795,7 @@ cudaError_t run_sparse(SpArgs& a, cudaStream_t st) {
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), bytes);
   if (e != cudaSuccess) return e;
   if ((e = allow_large_clusters(reinterpret_cast<const void*>(kern))) != cudaSuccess) return e;
-  // CTAs per row: as many as one wave holds, a tile per warp at least.  (Clusters of 8 do not fill
-  // every SM group to the last SM: with 7/8 of the slots the wave stays one.)
+  // CTAs per row: as many as let all rows' clusters run at once, a tile per warp at least
   const long long rows = (long long)c.batch * c.n_kv_heads * a.head_groups;
   const long long tiles = (long long)a.n_select * (a.block_tokens / RB);
   if (tiles > 0x3fffffffLL) return cudaErrorInvalidValue;  // (the API refuses such lists)
@@ -787,10 +805,11 @@ cudaError_t run_sparse(SpArgs& a, cudaStream_t st) {
   a.by_page = make_divu32(uint32_t(std::max(1, c.page_tokens)));
   a.by_tail = make_divu32(uint32_t(std::max(1, c.tail_len)));
   a.by_plane = make_divu32(uint32_t(c.n_kv_heads * a.head_groups));
-  const int sms = device_sm_count();
-  const int per_sm = std::min(kSpCtas<D>, 228 * 1024 / (bytes + 1024));
-  const long long slots = (long long)(sms > 0 ? sms : 148) * per_sm;
-  const int S = int(std::max<long long>(1, std::min<long long>({8, slots * 7 / 8 / rows, tiles / kWarps})));
+  const ClusterLimits* lim = cluster_limits(reinterpret_cast<const void*>(kern), 32 * kWarps, bytes);
+  int S = 1;
+  if (lim)
+    for (int k = 2; k <= kMaxCluster && (long long)k * kWarps <= tiles; ++k)
+      if (lim->clusters[k] >= rows) S = k;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(rows * S));
   cfg.blockDim = dim3(32 * kWarps);

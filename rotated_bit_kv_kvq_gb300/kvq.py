@@ -163,8 +163,10 @@ _raw_stream = None  # device index -> its current stream's handle
 _dtype_ids = None
 
 
-def _stream(stream) -> Optional[int]:
+def _stream(stream, device=None) -> Optional[int]:
     global _raw_stream
+    if stream is None and device is not None and _raw_stream is not None:
+        return _raw_stream(device)
     if stream is None:
         import torch
         if _raw_stream is None:
@@ -333,7 +335,7 @@ def kvq_qk_norm_rope(cache: kvq_cache, rope: RopeNorm, q, k, v, pos, q_out, k_ou
     vs = 0 if v is None else _heads_row_stride("kvq_qk_norm_rope: v", v, dev, dtype, hkv, d, n)
     _check(lib().kvq_qk_norm_rope(cache, rope.desc, _dtypes()[dtype], hq, q.data_ptr(), qs, k.data_ptr(), ks, _ptr(v), vs,
                                   pos.data_ptr(), _ptr(dst_row), n, rows, q_out.data_ptr(), k_out.data_ptr(),
-                                  _ptr(v_out), _stream(stream)),
+                                  _ptr(v_out), _stream(stream, dev)),
            "kvq_qk_norm_rope")
 
 
@@ -367,7 +369,7 @@ def kvq_page_update(cache: kvq_cache, pool, n_new, n_new_max: int, granted, row_
         _expect("kvq_page_update: row maps", dev, (rows,), _int32, row_pos, row_dst, row_slot)
     desc = pool.desc if isinstance(pool, PagePool) else pool
     _check(lib().kvq_page_update(cache, desc, _ptr(n_new), n_new_max, _ptr(granted), rows,
-                                 _ptr(row_pos), _ptr(row_dst), _ptr(row_slot), _ptr(seq_len_out), _stream(stream)),
+                                 _ptr(row_pos), _ptr(row_dst), _ptr(row_slot), _ptr(seq_len_out), _stream(stream, dev)),
            "kvq_page_update")
 
 
@@ -399,7 +401,7 @@ def kvq_select_blocks(cache: kvq_cache, index, q, sel, n_first: int = 1, n_last:
     _expect("kvq_select_blocks: q", dev, (batch, hq, cache.head_dim), None, q)
     _expect("kvq_select_blocks: sel", dev, (batch, cache.n_kv_heads, n), _int32, sel)
     _check(lib().kvq_select_blocks(cache, _index_desc(index), q.data_ptr(), _dtypes()[q.dtype], hq, n_first, n_last, n,
-                                   sel.data_ptr(), _stream(stream)),
+                                   sel.data_ptr(), _stream(stream, dev)),
            "kvq_select_blocks")
 
 
@@ -410,7 +412,7 @@ def kvq_sparse_decode_attention(cache: kvq_cache, q, sel, out, block_tokens: int
     _expect("kvq_sparse_decode_attention: q, out", dev, (batch, hq, cache.head_dim), None, q, out)
     _expect("kvq_sparse_decode_attention: sel", dev, (batch, cache.n_kv_heads, n), _int32, sel)
     _check(lib().kvq_sparse_decode_attention(cache, q.data_ptr(), ids[q.dtype], hq, scale, block_tokens, sel.data_ptr(), n,
-                                             out.data_ptr(), ids[out.dtype], _stream(stream)),
+                                             out.data_ptr(), ids[out.dtype], _stream(stream, dev)),
            "kvq_sparse_decode_attention")
 
 

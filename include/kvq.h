@@ -367,15 +367,15 @@ typedef struct kvq_rope_norm {
   int32_t weight_dtype;   /* KVQ_F32 / KVQ_BF16 / KVQ_F16 of the weights                          */
   const void* q_weight;   /* device [head_dim], 16-byte aligned; NULL: queries are not normed     */
   const void* k_weight;   /* the same for keys                                                    */
-  const float* inv_freq;  /* device fp32 [rot_dim / 2], 4-byte aligned: radians per position, |.| <= 1024
-                             (NULL only with rot_dim 0)                                           */
+  const float* inv_freq;  /* device fp32 [rot_dim / 2], 4-byte aligned: radians per position, finite and
+                             at most 1024 in magnitude (NULL only with rot_dim 0)                 */
 } kvq_rope_norm;
 /*
  *   q, k, v   device rows of `dtype`: head h of row r starts at element
  *             r * stride + h * head_dim, so the three may be parts of one fused
  *             projection.  16-byte aligned, strides in elements, a multiple of
- *             16 bytes and at least heads * head_dim.  v and v_out may both be
- *             NULL (no values to move).
+ *             16 bytes and at least heads * head_dim; rows * stride below 2^60.
+ *             v and v_out may both be NULL (no values to move).
  *   pos       device int32 [n_rows]: each row's position, any int32
  *   dst_row   device int32 [n_rows] or NULL (row r goes to row r; n_dst_rows is
  *             then at least n_rows).  A negative entry leaves the row out; one
@@ -387,7 +387,8 @@ typedef struct kvq_rope_norm {
  * weight only), then every pair (a, b) of the rotated channels becomes (a cos t
  * - b sin t, a sin t + b cos t), t = pos * inv_freq[pair]; values are copied.
  * All of it in fp32 -- the angle modulo one turn is exact to 2^-31 turns at
- * every position -- and rounded once, to nearest even.  Rows of the outputs that no
+ * every position, for |inv_freq| <= 1 (to 2^(k - 31) up to 2^k) -- and rounded
+ * once, to nearest even.  Rows of the outputs that no
  * row goes to keep what they held.  An output may be its own input (same
  * pointer, stride heads * head_dim, dst_row NULL); no other overlap is allowed.
  * n_rows 0 is a no-op.  Of the cache only head_dim, n_kv_heads and status are
@@ -436,8 +437,11 @@ typedef struct kvq_page_pool {
  *              serving loop wants).  Granted tokens are not added: the append
  *              does that.
  * A state outside its ranges sets KVQ_DEV_ERR_PAGE; nothing is granted or
- * released then, and `next` gets the state as it was.  Requires the paged
- * layout and batch * n_new_max < 2^31.  Uses status word 2 as a completion counter.
+ * released then, and `next` gets the state as it was.  Free and released pages
+ * that together pass n_pages set it too, and the released ones are lost, as does
+ * a page id outside [0, n_pages) (its rows get slot -1).  Requires the paged
+ * layout and batch * n_new_max < 2^31, and n_pages * page_tokens < 2^31.  Uses
+ * status word 2 as a completion counter.  No array may overlap another but as said above.
  * Of the cache's planes only seq_len, status and page_table are touched.
  */
 KVQ_API kvq_status kvq_page_update(const kvq_cache* c, const kvq_page_pool* pool, const int32_t* n_new,
@@ -504,7 +508,9 @@ KVQ_API kvq_status kvq_select_blocks(const kvq_cache* c, const kvq_block_index* 
  *             out, a block listed twice counts twice
  *   q, out, scale  as in kvq_decode_attention (every K / V format pair, contiguous
  *             or paged, positions of the last tail_len tokens from the bf16 tail)
- * A (sequence, KV head) with no listed token yields zeros.  No workspace.
+ * A (sequence, KV head) with no listed token yields zeros.  No workspace: calls
+ * that only read a cache may run at the same time.  The first call for a
+ * head_dim asks the device for its limits; make it before a stream capture.
  * Body planes of 2^31 rows or more (and as many tail rows) give
  * KVQ_ERR_UNSUPPORTED.  The arithmetic keeps fp32's precision, as the decode's,
  * for |rotated key| < 1e6 in the bf16 tail and |rotated value| < 1.6e7 there.

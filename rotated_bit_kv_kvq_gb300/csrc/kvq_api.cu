@@ -311,8 +311,8 @@ kvq_status kvq_qk_norm_rope(const kvq_cache* c, const kvq_rope_norm* r, int32_t 
     const int64_t heads = i == 0 ? n_q_heads : c->n_kv_heads;
     if (i == 2 && !v) break;
     if (n_rows > 0 && (!in[i] || !out[i] || !aligned16(in[i]) || !aligned16(out[i]))) return KVQ_ERR_INVALID_ARG;
-    // offsets stay far below 2^62 bytes
-    if (stride[i] < heads * d || stride[i] > (int64_t(1) << 40) || stride[i] * es % 16) return KVQ_ERR_INVALID_ARG;
+    if (stride[i] < heads * d || stride[i] > (int64_t(1) << 60) || stride[i] * es % 16) return KVQ_ERR_INVALID_ARG;
+    if (double(stride[i]) * n_rows > 1.15e18) return KVQ_ERR_INVALID_ARG;  // offsets below 2^62 bytes
     a.in[i] = in[i];
     a.out[i] = out[i];
     a.stride[i] = stride[i];

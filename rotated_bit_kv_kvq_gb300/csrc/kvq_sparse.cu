@@ -369,8 +369,10 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
         const int t0 = blk * a.block_tokens + int(u - e * a.by_block.d) * RB;
         if (t0 < n) {
           my_t0 = t0;
-          my_row = int(bh) * c.max_ctx + t0;
-          if (c.page_tokens && t0 < body_end) {  // (rows of a tile lie in one page)
+          my_row = 0;
+          if (!c.page_tokens) {
+            my_row = int(bh) * c.max_ctx + t0;
+          } else if (t0 < body_end) {  // (rows of a tile lie in one page)
             const int i = int(div_u32(uint32_t(t0), a.by_page));
             const int pg = c.page_table[(long long)b * a.pages_per_seq + i];
             my_row = pg >= 0 && pg < c.n_pages ? (pg * c.n_kv_heads + kvh) * c.page_tokens + t0 - i * c.page_tokens : -1;

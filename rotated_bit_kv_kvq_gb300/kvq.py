@@ -347,9 +347,10 @@ class PagePool:
         n = cache.n_pages
         free = range(n) if free is None else free
         self.ring = torch.full((max(n, 1),), -1, dtype=torch.int32, device=device)
-        ids = torch.as_tensor(list(free), dtype=torch.int32)
-        if len(ids) > n:
-            raise ValueError("PagePool: more free pages than the cache has")
+        ids = [int(i) for i in free]
+        if len(set(ids)) != len(ids) or any(i < 0 or i >= n for i in ids):
+            raise ValueError("PagePool: free pages are distinct and in [0, n_pages)")
+        ids = torch.tensor(ids, dtype=torch.int32)
         self.ring[:len(ids)] = ids.to(device)
         self.state = torch.tensor([0, len(ids)], dtype=torch.int32, device=device)
         self.desc = kvq_page_pool(self.ring.data_ptr(), self.state.data_ptr(), self.state.data_ptr())
@@ -367,7 +368,11 @@ def kvq_page_update(cache: kvq_cache, pool, n_new, n_new_max: int, granted, row_
     else:
         rows = a_map.numel()
         _expect("kvq_page_update: row maps", dev, (rows,), _int32, row_pos, row_dst, row_slot)
-    desc = pool.desc if isinstance(pool, PagePool) else pool
+    desc = pool
+    if isinstance(pool, PagePool):
+        desc = pool.desc
+        if pool.ring.numel() < cache.n_pages:
+            raise ValueError("kvq_page_update: the pool was made for fewer pages")
     _check(lib().kvq_page_update(cache, desc, _ptr(n_new), n_new_max, _ptr(granted), rows,
                                  _ptr(row_pos), _ptr(row_dst), _ptr(row_slot), _ptr(seq_len_out), _stream(stream, dev)),
            "kvq_page_update")
@@ -378,19 +383,26 @@ class BlockIndex:
 
     def __init__(self, cache: kvq_cache, block_tokens: int, device="cuda"):
         import torch
+        if block_tokens <= 0 or block_tokens % 64:
+            raise ValueError("BlockIndex: block_tokens is a multiple of 64")
         nblk = -(-cache.max_ctx // block_tokens)
+        self.sizes = (cache.batch, cache.n_kv_heads, cache.max_ctx, cache.head_dim)
         self.codes = torch.zeros(cache.batch, cache.n_kv_heads, nblk, cache.head_dim, dtype=torch.int8, device=device)
         self.scales = torch.zeros(cache.batch, cache.n_kv_heads, nblk, dtype=torch.float32, device=device)
         self.desc = kvq_block_index(block_tokens, self.codes.data_ptr(), self.scales.data_ptr())
 
 
-def _index_desc(index):
-    return index.desc if isinstance(index, BlockIndex) else index
+def _index_desc(cache, index):
+    if not isinstance(index, BlockIndex):
+        return index
+    if index.sizes != (cache.batch, cache.n_kv_heads, cache.max_ctx, cache.head_dim):
+        raise ValueError("BlockIndex: made for a cache of other sizes")
+    return index.desc
 
 
 def kvq_block_index_update(cache: kvq_cache, index, n_last: int = 0, stream=None):
     """index: BlockIndex or kvq_block_index; n_last 0: every block, else those of the last n_last tokens."""
-    _check(lib().kvq_block_index_update(cache, _index_desc(index), n_last, _stream(stream)),
+    _check(lib().kvq_block_index_update(cache, _index_desc(cache, index), n_last, _stream(stream)),
            "kvq_block_index_update")
 
 
@@ -400,7 +412,7 @@ def kvq_select_blocks(cache: kvq_cache, index, q, sel, n_first: int = 1, n_last:
     dev, batch, hq, n = _device(), cache.batch, q.shape[1], sel.shape[-1]
     _expect("kvq_select_blocks: q", dev, (batch, hq, cache.head_dim), None, q)
     _expect("kvq_select_blocks: sel", dev, (batch, cache.n_kv_heads, n), _int32, sel)
-    _check(lib().kvq_select_blocks(cache, _index_desc(index), q.data_ptr(), _dtypes()[q.dtype], hq, n_first, n_last, n,
+    _check(lib().kvq_select_blocks(cache, _index_desc(cache, index), q.data_ptr(), _dtypes()[q.dtype], hq, n_first, n_last, n,
                                    sel.data_ptr(), _stream(stream, dev)),
            "kvq_select_blocks")
 

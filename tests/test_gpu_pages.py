@@ -106,8 +106,9 @@ def test_pool_class_refusals():
     c = kvq.descriptor(2, 1, 64, 256, 0, "q4_0", "q4_0", page_tokens=64, n_pages=3)
     pool = kvq.PagePool(c, free=[2, 0])
     assert pool.state.tolist() == [0, 2] and pool.ring.tolist() == [2, 0, -1]
-    with pytest.raises(ValueError):
-        kvq.PagePool(c, free=range(4))
+    for free in (range(4), [0, 0], [-1], [3]):
+        with pytest.raises(ValueError):
+            kvq.PagePool(c, free=free)
     i = torch.zeros(2, dtype=torch.int32, device="cuda")
     for bad in (i.long(), i[:1], i.cpu()):
         with pytest.raises(ValueError):

@@ -244,3 +244,93 @@ def test_sparse_binding_refuses_tensors():
             kvq.kvq_sparse_decode_attention(gc.desc, **{**dict(q=q, sel=sel, out=torch.empty_like(q), block_tokens=64), **kw})
     with pytest.raises(kvq.KvqError):
         kvq.kvq_select_blocks(gc.desc, x, q, sel, n_first=2, n_last=2)
+
+
+def test_index_of_another_cache_is_refused():
+    torch = require_gpu()
+    from rotated_bit_kv_kvq_gb300 import kvq
+    small, large = (kvq.KVCache(1, 1, 64, n, 0, "q4_0", "q4_0") for n in (256, 512))
+    x = kvq.BlockIndex(small.desc, 64)
+    q = torch.zeros(1, 1, 64, device="cuda")
+    with pytest.raises(ValueError):
+        kvq.kvq_block_index_update(large.desc, x)
+    with pytest.raises(ValueError):
+        kvq.kvq_select_blocks(large.desc, x, q, torch.zeros(1, 1, 4, dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError):
+        kvq.BlockIndex(small.desc, 96)
+
+
+@pytest.mark.parametrize("d,hkv,kt,vt,T", [(128, 8, "q8_0", "q4_0", 0), (64, 16, "q5_1", "q8_0", 40)])
+def test_the_end_of_a_long_cache(d, hkv, kt, vt, T):
+    """Planes past 2^32 bytes: the last tokens of four million, against the same tokens in a small cache."""
+    torch = require_gpu()
+    from rotated_bit_kv_kvq_gb300 import kvq
+    rng = np.random.default_rng(28)
+    ctx, n = 1 << 22, 300
+    start = ctx - 320                    # five blocks of 64 from the end
+    long, short = (kvq.KVCache(1, hkv, d, c, T, kt, vt) for c in (ctx, 320))
+    k, v = (to_dev(rng.standard_normal((1, n, hkv, d)), "bf16", torch) for _ in range(2))
+    long.seq_len.fill_(start)
+    for c in (long, short):
+        kvq.kvq_rotate_quantize_append(c.desc, k, v)
+    q = to_dev(rng.standard_normal((1, 2 * hkv, d)), "f32", torch)
+    out = []
+    for c, first in ((long, start // 64), (short, 0)):
+        x = kvq.BlockIndex(c.desc, 64)
+        kvq.kvq_block_index_update(c.desc, x, n_last=n)
+        sel = torch.tensor([4, 2, 0, 1], dtype=torch.int32, device="cuda").expand(1, hkv, 4).add(first).contiguous()
+        o = torch.empty_like(q)
+        kvq.kvq_sparse_decode_attention(c.desc, q, sel, o, 64)
+        out.append((o, x.codes[:, :, first:first + 5], x.scales[:, :, first:first + 5]))
+        assert kvq.kvq_sync_status(c.desc)[0] == 0
+    assert torch.equal(out[0][1], out[1][1]) and torch.equal(out[0][2], out[1][2])
+    # (the tail's slots differ, the sums may be split elsewhere: a few fp32 roundings)
+    assert torch.allclose(out[0][0], out[1][0], atol=1e-5, rtol=1e-5)
+
+
+def test_calls_on_a_stream_of_their_own_and_at_once():
+    """Two selections and sparse decodes of one cache on two streams at once give what they give alone."""
+    torch = require_gpu()
+    from rotated_bit_kv_kvq_gb300 import kvq
+    rng = np.random.default_rng(29)
+    gc, oc = _pair(torch, kvq, rng, 2, 2, 128, 4096, 64, "q8_0", "q4_0", [4000, 3000])
+    x = kvq.BlockIndex(gc.desc, 64)
+    kvq.kvq_block_index_update(gc.desc, x)
+    qs = [to_dev(rng.standard_normal((2, 8, 128)), "bf16", torch) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    res = [(torch.empty(2, 2, 9, dtype=torch.int32, device="cuda"), torch.empty(2, 8, 128, device="cuda")) for _ in range(2)]
+
+    def one(i, stream):
+        kvq.kvq_select_blocks(gc.desc, x, qs[i], res[i][0], stream=stream)
+        kvq.kvq_sparse_decode_attention(gc.desc, qs[i], res[i][0], res[i][1], 64, stream=stream)
+
+    alone = []
+    for i in range(2):
+        one(i, None)
+        torch.cuda.synchronize()
+        alone.append([t.clone() for t in res[i]])
+        for t in res[i]:
+            t.fill_(0)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i in range(2):
+            one(i, streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert torch.equal(res[i][0], alone[i][0]) and torch.equal(res[i][1], alone[i][1])
+        codes, scales = x.codes.cpu().numpy(), x.scales.cpu().numpy()
+        assert np.array_equal(alone[i][0].cpu().numpy(), so.select_blocks(qs[i].float().cpu().numpy(), codes, scales, oc.seq_len, 64, 1, 1, 9, True))
+        _close(alone[i][1].cpu().numpy().astype(np.float64), so.sparse_decode(oc, qs[i].float().cpu().numpy(), alone[i][0].cpu().numpy(), 64))
+
+
+@pytest.mark.parametrize("B,hkv,g,nsel", [(300, 3, 2, 3), (1, 1, 8, 16), (2, 1, 100, 5)])
+def test_sparse_decode_many_rows_and_many_heads(B, hkv, g, nsel):
+    torch = require_gpu()
+    from rotated_bit_kv_kvq_gb300 import kvq
+    rng = np.random.default_rng(30)
+    lens = [int(n) for n in rng.integers(0, 257, B)]
+    gc, oc = _pair(torch, kvq, rng, B, hkv, 64, 256, 10, "q4_0", "q5_0", lens)
+    sel = rng.integers(-1, 4, (B, hkv, nsel))
+    q = rng.standard_normal((B, hkv * g, 64)).astype(np.float32)
+    got, qn = _sparse(torch, kvq, gc, q, "f16", sel, 64)
+    _close(got, so.sparse_decode(oc, qn, sel, 64))

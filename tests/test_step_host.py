@@ -34,7 +34,7 @@ def _norm_rope(c=None, r=None, **kw):
     dict(dtype=3), dict(n_q_heads=0), dict(q=None), dict(k=None), dict(q_out=None), dict(v=None), dict(v_out=None),
     dict(q=FAKE + 8), dict(v_out=FAKE + 2), dict(q_stride=1023), dict(q_stride=512), dict(k_stride=508),
     dict(k_stride=513), dict(pos=None), dict(pos=FAKE + 2), dict(dst_row=FAKE + 1), dict(n_rows=-1),
-    dict(n_dst_rows=3), dict(n_dst_rows=-1), dict(v_stride=1 << 41),
+    dict(n_dst_rows=3), dict(n_dst_rows=-1), dict(v_stride=1 << 61), dict(q_stride=1 << 59),
 ])
 def test_norm_rope_refuses(built_lib_path, kw):
     assert _norm_rope(**kw) == INVALID

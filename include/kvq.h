@@ -513,7 +513,7 @@ KVQ_API kvq_status kvq_select_blocks(const kvq_cache* c, const kvq_block_index* 
  * head_dim asks the device for its limits; make it before a stream capture.
  * Body planes of 2^31 rows or more (and as many tail rows) give
  * KVQ_ERR_UNSUPPORTED.  The arithmetic keeps fp32's precision, as the decode's,
- * for |rotated key| < 1e6 in the bf16 tail and |rotated value| < 1.6e7 there.
+ * for rotated keys and values below 5e5 in magnitude.
  */
 KVQ_API kvq_status kvq_sparse_decode_attention(const kvq_cache* c, const void* q, int32_t q_dtype, int32_t n_q_heads,
                                                float scale, int32_t block_tokens, const int32_t* sel,

@@ -33,6 +33,14 @@ namespace cg = cooperative_groups;
 constexpr int kTailRows = 8;   // tokens of a tail tile
 constexpr int kMaxStages = 4;
 
+// Weights P = 2^(score - lim + kHead), lim a reference kLazyMax above the largest score at its last
+// move, are at most 2^kHead: P times a V scale, split in two fp16 parts, keeps an absolute error of
+// 2^-25 (fp16's smallest step), so the weights have to be large.  2^7: the tail takes P times 2^8.
+// Scales from kBigScale on (codes of q8_0 go in divided by 16, their scales times 16) would overflow:
+// a warp that meets one takes P down to 1 from there on.
+constexpr float kHead = 7.0f;
+__device__ __forceinline__ uint32_t big_scale(int vt) { return vt == KVQ_TYPE_Q8_0 ? 0x5000u : 0x6000u; }  // fp16 32, 512
+
 template <int D> constexpr int kRows = D <= 128 ? 32 : 16;               // tokens of a body tile
 template <int D> constexpr int kW = D <= 128 ? 8 : D <= 256 ? 6 : 8;      // warps of a CTA
 template <int D> constexpr int kSpCtas = D <= 256 ? 2 : 1;                // CTAs of an SM
@@ -203,9 +211,15 @@ __device__ __forceinline__ void body_scores(uint32_t st, const SpStage& L, uint3
   }
 }
 
+// bytes I0, I1 of offset-binary codes as the fp16 pair code / 16 (exact: 1152 / 16 = 72)
+template <int I0, int I1>
+__device__ __forceinline__ uint32_t i8_sixteenth(uint32_t r) {
+  return hfma2_bits(__byte_perm(r, 0x64646464u, I0 | (4 << 4) | (I1 << 8) | (4 << 12)), 0x2C002C00u, 0xD480D480u);
+}
+
 // acc += codes_V^T . (P * scale) of the 16 body rows from row0: rows 2g (acc .. [0], [1]) and 2g + 1 of each
 // 16 channels, columns heads 2tig, 2tig + 1; dmin += the blocks' minima . P (rows blocks g, g + 8).
-// cnt: the tile's tokens.
+// cnt: the tile's tokens; P comes times 16 where the codes are divided by 16 (q8_0).
 template <int D, int VT>
 __device__ __forceinline__ void body_values(uint32_t st, const SpStage& L, int row0, const uint32_t (&ph)[2],
                                             const uint32_t (&pl)[2], int cnt, int lane,
@@ -267,8 +281,8 @@ __device__ __forceinline__ void body_values(uint32_t st, const SpStage& L, int r
       for (int e = 0; e < 2; ++e) {
         uint32_t r0, r1, r2, r3;
         ldsm_x4_t(ld.template at<RB>(2 * (bp + e)), r0, r1, r2, r3);
-        const uint32_t a0[4] = {i8_pair<0, 2>(r0), i8_pair<1, 3>(r0), i8_pair<0, 2>(r1), i8_pair<1, 3>(r1)};
-        const uint32_t a1[4] = {i8_pair<0, 2>(r2), i8_pair<1, 3>(r2), i8_pair<0, 2>(r3), i8_pair<1, 3>(r3)};
+        const uint32_t a0[4] = {i8_sixteenth<0, 2>(r0), i8_sixteenth<1, 3>(r0), i8_sixteenth<0, 2>(r1), i8_sixteenth<1, 3>(r1)};
+        const uint32_t a1[4] = {i8_sixteenth<0, 2>(r2), i8_sixteenth<1, 3>(r2), i8_sixteenth<0, 2>(r3), i8_sixteenth<1, 3>(r3)};
         block(bp + e, w, a0, a1);
       }
     } else {
@@ -515,7 +529,9 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
 #pragma unroll
       for (int r = 0; r < 4; ++r) acc[i][j][r] = 0.0f;
   float dmin[4] = {0.f, 0.f, 0.f, 0.f};
-  float m = -INFINITY, l = 0.0f;
+  float lim = -INFINITY, l = 0.0f, head = kHead;
+  const float vs = c.v_type == KVQ_TYPE_Q8_0 ? 16.0f : 1.0f;
+  const uint32_t hmask = type_has_min(c.v_type) ? 0x00007FFFu : 0x7FFF7FFFu, big = big_scale(c.v_type);
   bool timed_out = false;
   int k = 0;
   for (; k < issued; ++k) {
@@ -574,15 +590,21 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
     }
 #pragma unroll
     for (int i = 0; i < 4 * HB; ++i) mx = fmaxf(mx, sc[i >> 2][(i >> 1) & 1][i & 1]);
-    // m is a reference kLazyMax above the maximum at its last move (weights stay <= 1), so the
-    // rescale runs only when a score passes it
-    if (__any_sync(0xffffffffu, mx > m)) {
+    // The rescale runs only when a score passes the reference, or when a tile's scales ask for smaller weights.
+    bool down = false;
+    if (job.y > 0 && head != 0.0f) {
+      uint32_t mxs = 0;
+      for (int i = lane; i < RB * a.s.vh / 4; i += 32) mxs = __vmaxu2(mxs, lds32(st + a.s.vd + 4 * i) & hmask);
+      down = __any_sync(0xffffffffu, (mxs & 0xFFFFu) >= big || (mxs >> 16) >= big);
+    }
+    if (__any_sync(0xffffffffu, mx > lim) || down) {
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const float nm = mx > m ? mx + kLazyMax : m;
-      const float r = m == -INFINITY ? 0.0f : fast_exp2(m - nm);
+      const float nl = mx > lim ? mx + kLazyMax : lim, nh = down ? 0.0f : head;
+      const float r = lim == -INFINITY ? 0.0f : fast_exp2((lim - nl) + (nh - head));
       l *= r;
-      m = nm;
+      lim = nl;
+      head = nh;
       const float r0 = __shfl_sync(0xffffffffu, r, 8 * tig), r1 = __shfl_sync(0xffffffffu, r, 8 * tig + 4);
 #pragma unroll
       for (int i = 0; i < NB; ++i)
@@ -590,7 +612,7 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
         for (int j = 0; j < 2; ++j) { acc[i][j][0] *= r0; acc[i][j][1] *= r1; acc[i][j][2] *= r0; acc[i][j][3] *= r1; }
       dmin[0] *= r0; dmin[1] *= r1; dmin[2] *= r0; dmin[3] *= r1;
     }
-    const float ms = m == -INFINITY ? 0.0f : m;
+    const float ms = lim == -INFINITY ? 0.0f : lim - head;
     float p[HB][2][2];
 #pragma unroll
     for (int hh = 0; hh < HB; ++hh)
@@ -607,7 +629,7 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
 #pragma unroll
       for (int hh = 0; hh < HB; ++hh)
 #pragma unroll
-        for (int t = 0; t < 2; ++t) split_h2(p[hh][t][0], p[hh][t][1], ph[hh][t], pl[hh][t]);
+        for (int t = 0; t < 2; ++t) split_h2(p[hh][t][0] * vs, p[hh][t][1] * vs, ph[hh][t], pl[hh][t]);
 #define KVQ_VALUES(VT)                                                                                               \
   case VT:                                                                                                           \
     _Pragma("unroll") for (int hh = 0; hh < HB; ++hh) body_values<D, VT>(st, a.s, 16 * hh, ph[hh], pl[hh], cnt, lane, acc, \
@@ -653,7 +675,7 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
   l += __shfl_xor_sync(0xffffffffu, l, 1);
   l += __shfl_xor_sync(0xffffffffu, l, 2);
   if (tig == 0) {
-    s_m[warp * kMaxHeads + g] = m;
+    s_m[warp * kMaxHeads + g] = lim == -INFINITY ? -INFINITY : lim - head;
     s_l[warp * kMaxHeads + g] = l;
   }
   __syncthreads();  // the stages are free

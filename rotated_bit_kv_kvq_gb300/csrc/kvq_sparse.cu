@@ -8,15 +8,16 @@
 //
 // Scores of a tile, heads x tokens, on the tensor cores: A = the query (16 rows: fp16 high
 // parts of eight heads, then the low parts; the two rows of a head are added, so one mma does
-// both parts), B = the codes.  4-, 5- and 8-bit codes u go in as the fp16 subnormals u * 2^-24
-// -- the code's bits are the half's bits, so a mask (or a byte permute) is the whole
-// conversion -- with the offset's part, -offset * (sum of the block's q), as the mma's initial
-// value; the factor 2^24 goes to the finished score.  The query is scaled by a power of two
-// (its largest value below 2^11) so that its low parts stay far above fp16's smallest step.
-// The mma's result has exactly the layout of P as the B operand of P.V, so P never moves
-// between lanes.  P.V is the decode's: A = centred codes (channels x tokens), B = P times the
-// block's scale as fp16 high and low parts.  (Subnormal codes do not serve there: all weights
-// are positive, the offset's part would grow with the number of tokens and cancel.)
+// both parts), B = the codes less their offset, exact in fp16, a block's result times its scale
+// in fp32.  The query is scaled by a power of two (its largest value below 2^11) so that its low
+// parts stay far above fp16's smallest step.  The mma's result has exactly the layout of P as
+// the B operand of P.V, so P never moves between lanes.  P.V is the decode's: A = centred codes
+// (channels x tokens), B = P times the block's scale as fp16 high and low parts.
+//
+// Codes are centred everywhere.  Uncentred they could go in as fp16 subnormals, a mask or byte
+// permute each, with the offset as the mma's initial value: 3% faster, but the sums are then
+// some times larger than their result, and fp32 outputs were 1.4e-6 off instead of 1.5e-7.  The
+// scale + minimum formats are centred too: code - c with the minimum + c * scale.
 
 #include <cooperative_groups.h>
 #include <string.h>
@@ -102,11 +103,9 @@ __device__ __forceinline__ void lds_row(uint32_t a, uint32_t (&w)[BYTES / 4]) {
   }
 }
 
-// codes of the low (H16 false) or high nibbles as fp16 subnormals: bits 0-4 / 16-20, or
-// bits 4-8 / 20-24 (16 times the value), the 5-bit formats' high bits in place already
-template <bool H16>
-__device__ __forceinline__ uint32_t nib_sub(uint32_t r, uint32_t hb) {
-  return (r & (H16 ? 0x00F000F0u : 0x000F000Fu)) | hb;
+// What the codes of a type are centred by; q8_0's are offset binary, centred by their conversion.
+__host__ __device__ constexpr int code_centre(int qt) {
+  return qt == KVQ_TYPE_Q8_0 ? 0 : type_has_qh(qt) ? 16 : 8;
 }
 
 // ldmatrix rows of a 16-row tile in W-byte box columns (R rows each): the lane's row and its
@@ -126,13 +125,6 @@ struct LdRow {
   }
 };
 
-// D = A * B + C with C apart from D (the initial values are shared by several mma)
-__device__ __forceinline__ void mma16816_from(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%11,%11};"
-               : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(0.0f));
-}
-
 // Scores of a body tile (st, qf, qsum: shared addresses of its stage, the query fragments and block sums): S[hh][t][e] of tokens 16hh + 8t + 2tig + e and head g.
 template <int D, int KT>
 __device__ __forceinline__ void body_scores(uint32_t st, const SpStage& L, uint32_t qf, uint32_t qsum, int lane,
@@ -142,7 +134,7 @@ __device__ __forceinline__ void body_scores(uint32_t st, const SpStage& L, uint3
   constexpr int KHH = K1 ? 2 : 1, HP = NB * 2 * KHH;  // halves of a block header, bytes of a row's
   const int g = lane >> 2, tig = lane & 3;
   const LdRow<W> ld(st, lane);
-  const float off = KT == KVQ_TYPE_Q8_0 ? 128.0f : float(type_code_offset(KT));
+  constexpr uint32_t OFF = (0x6400u + uint32_t(code_centre(KT))) * 0x10001u, OFF16 = neg_off_x16_bits(code_centre(KT));
   const uint32_t k0 = uint32_t(8 * (tig >> 1) + 2 * (tig & 1) - 4) & 31u, k1 = (k0 + 1) & 31u;
   const uint32_t hd0 = st + L.kd + 2 * tig * HP, qh0 = st + L.kqh + g * NB * 4, qf0 = qf + lane * 16, qs0 = qsum + g * 4;
   // Two blocks at a time.  Large heads keep the loop rolled: a call lasts a few tiles per warp, and
@@ -169,46 +161,54 @@ __device__ __forceinline__ void body_scores(uint32_t st, const SpStage& L, uint3
       const int blk = bp + e;
       const uint4 qa = lds128(qf0 + blk * 1024), qb = lds128(qf0 + blk * 1024 + 512);
       const uint32_t a0[4] = {qa.x, qa.y, qa.z, qa.w}, a1[4] = {qb.x, qb.y, qb.z, qb.w};
-      const float qs = __uint_as_float(lds32(qs0 + blk * (kMaxHeads * 4)));
+      const float qs = K1 ? __uint_as_float(lds32(qs0 + blk * (kMaxHeads * 4))) : 0.0f;
 #pragma unroll
       for (int hh = 0; hh < HB; ++hh) {
         uint32_t b[2][4];  // operands of the two k-steps for the 8-token tiles of half hh
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           if constexpr (KT == KVQ_TYPE_Q8_0) {  // r[t]: channels 4tig .. of the first half block, r[2 + t] of the second
-            b[t][0] = __byte_perm(r[hh][e][t], 0, 0x4240);
-            b[t][1] = __byte_perm(r[hh][e][t], 0, 0x4341);
-            b[t][2] = __byte_perm(r[hh][e][2 + t], 0, 0x4240);
-            b[t][3] = __byte_perm(r[hh][e][2 + t], 0, 0x4341);
+            b[t][0] = i8_pair<0, 2>(r[hh][e][t]);
+            b[t][1] = i8_pair<1, 3>(r[hh][e][t]);
+            b[t][2] = i8_pair<0, 2>(r[hh][e][2 + t]);
+            b[t][3] = i8_pair<1, 3>(r[hh][e][2 + t]);
           } else {
             const uint32_t w = r[hh][0][2 * e + t], w8 = w >> 8;
-            uint32_t h0 = 0, h1 = 0;
+            uint32_t m0 = 0x64006400u, m1 = m0, m2 = m0, m3 = m0;
             if constexpr (K5) {  // rotated: the pairs' bits at 4 / 20 (low nibbles) and 8 / 24
               const uint32_t h = lds32(qh0 + ((16 * hh + 8 * t) * NB + blk) * 4);
-              h0 = __funnelshift_r(h, h, k0);
-              h1 = __funnelshift_r(h, h, k1);
+              const uint32_t h0 = __funnelshift_r(h, h, k0), h1 = __funnelshift_r(h, h, k1);
+              m0 = khb(h0, 0x00100010u); m1 = khb(h1, 0x00100010u);
+              m2 = khb(h0, 0x01000100u); m3 = khb(h1, 0x01000100u);
             }
-            b[t][0] = nib_sub<false>(w, h0 & 0x00100010u);
-            b[t][1] = nib_sub<false>(w8, h1 & 0x00100010u);
-            b[t][2] = nib_sub<true>(w, h0 & 0x01000100u);
-            b[t][3] = nib_sub<true>(w8, h1 & 0x01000100u);
+            b[t][0] = nib_pair(w, 0, m0, OFF);
+            b[t][1] = nib_pair(w8, 0, m1, OFF);
+            b[t][2] = nib_pair_x16(w, m2, OFF16);
+            b[t][3] = nib_pair_x16(w8, m3, OFF16);
           }
         }
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          float cc[4];
-          mma16816_from(cc, a0, b[t][0], b[t][1], K1 ? 0.0f : -off * qs);
+          float cc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          mma16816(cc, a0, b[t][0], b[t][1]);
           mma16816(cc, a1, b[t][2], b[t][3]);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const uint32_t (&w)[KHH] = hd[hh][2 * t + i];
-            S[hh][t][i] = fmaf(KHH == 1 ? h2f(w[0], e) : h2f(w[e % KHH], 0), cc[i] + cc[2 + i], S[hh][t][i]);
-            if constexpr (K1) S[hh][t][i] = fmaf(h2f(w[e % KHH], 1), qs, S[hh][t][i]);
+            const float dk = KHH == 1 ? h2f(w[0], e) : h2f(w[e % KHH], 0);
+            S[hh][t][i] = fmaf(dk, cc[i] + cc[2 + i], S[hh][t][i]);
+            if constexpr (K1) S[hh][t][i] = fmaf(fmaf(dk, float(code_centre(KT)), h2f(w[e % KHH], 1)), qs, S[hh][t][i]);
           }
         }
       }
     }
   }
+}
+
+__device__ __forceinline__ uint32_t hadd2_bits(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
 // bytes I0, I1 of offset-binary codes as the fp16 pair code / 16 (exact: 1152 / 16 = 72)
@@ -257,19 +257,32 @@ __device__ __forceinline__ void body_values(uint32_t st, const SpStage& L, int r
     mma16816(acc[blk][1], a1, l0, l1);
   };
   if constexpr (V1) {
-    auto lo2 = [&](int blk, int i) -> uint32_t {
+    // blocks' minima + centre * scale at tokens i, i + 1 of the lane's four, as fp16 high and low parts: the
+    // product with the centre, a power of two, is exact, and so is the remainder of the sum
+    constexpr uint32_t C2 = (code_centre(VT) == 16 ? 0x4C00u : 0x4800u) * 0x10001u;
+    auto minimum = [&](int blk, int i, uint32_t& hi, uint32_t& lo) {
       const int bb = blk < NB ? blk : NB - 1;
       uint32_t w0 = lds32(vd + (8 * (i >> 1) * NB + bb) * 4);
       uint32_t w1 = lds32(vd + ((8 * (i >> 1) + 1) * NB + bb) * 4);
       if (partial) { w0 = ok(i) ? w0 : 0u; w1 = ok(i + 1) ? w1 : 0u; }
-      return blk < NB ? __byte_perm(w0, w1, 0x7632) : 0u;
+      const uint32_t m = __byte_perm(w0, w1, 0x7632), p = hmul2_bits(__byte_perm(w0, w1, 0x5410), C2);
+      hi = hadd2_bits(p, m);
+      const uint32_t mm = hsub2_bits(hi, p);  // the part of m in the sum
+      lo = hadd2_bits(hsub2_bits(p, hsub2_bits(hi, mm)), hsub2_bits(m, mm));
+      if (blk >= NB) hi = lo = 0u;
     };
-    const uint32_t al[4] = {lo2(g, 0), NB > 8 ? lo2(g + 8, 0) : 0u, lo2(g, 2), NB > 8 ? lo2(g + 8, 2) : 0u};
+    uint32_t ah[4] = {0, 0, 0, 0}, al[4] = {0, 0, 0, 0};
+    minimum(g, 0, ah[0], al[0]);
+    minimum(g, 2, ah[2], al[2]);
+    if constexpr (NB > 8) {
+      minimum(g + 8, 0, ah[1], al[1]);
+      minimum(g + 8, 2, ah[3], al[3]);
+    }
+    mma16816(dmin, ah, ph[0], ph[1]);
+    mma16816(dmin, ah, pl[0], pl[1]);
     mma16816(dmin, al, ph[0], ph[1]);
-    mma16816(dmin, al, pl[0], pl[1]);
   }
-  constexpr uint32_t OFF = (0x6400u + uint32_t(type_code_offset(VT))) * 0x10001u;
-  constexpr uint32_t OFF16 = neg_off_x16_bits(type_code_offset(VT));
+  constexpr uint32_t OFF = (0x6400u + uint32_t(code_centre(VT))) * 0x10001u, OFF16 = neg_off_x16_bits(code_centre(VT));
   const uint32_t v0 = uint32_t(8 * ((g & 3) >> 1) + 2 * (g & 1) - 4) & 31u, v1 = (v0 + 1) & 31u;
   const uint32_t qh0 = st + L.vqh + (tig * NB * 2 + (g >> 2)) * 4 + row0 * NB * 4;
 #pragma unroll
@@ -313,10 +326,10 @@ __device__ __forceinline__ void body_values(uint32_t st, const SpStage& L, int r
   }
 }
 
-// a bf16 pair times a pair of powers of two (bf16, exact) as an fp16 pair
-__device__ __forceinline__ uint32_t bf16x2_times(uint32_t b, uint32_t f) {
+// a bf16 pair times 2^-8 (exact) as an fp16 pair
+__device__ __forceinline__ uint32_t bf16x2_scaled(uint32_t b) {
   uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(b), "r"(f));
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(b), "r"(0x3B803B80u));
   return pack_h2(__uint_as_float(r << 16), __uint_as_float(r & 0xFFFF0000u));
 }
 
@@ -340,7 +353,6 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
   // block sums of the query, partial (m, l), score factors, barriers, jobs
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* wst = smem + warp * NS * a.s.bytes;
-  const bool nib = c.k_type != KVQ_TYPE_Q8_0;
   uint8_t* sp = smem + kWarps * NS * a.s.bytes;
   float* sq = reinterpret_cast<float*>(sp);                             // [8][D], then the fragments
   uint4* qf = reinterpret_cast<uint4*>(sp);
@@ -494,11 +506,9 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
         for (int hf = 0; hf < 2; ++hf) {
           const float4 x = *reinterpret_cast<const float4*>(sq + g * D + 32 * blk + 16 * hf + 4 * tig);
           qs[u] += (x.x + x.y) + (x.z + x.w);
-          // (the high nibbles come 16 times too large)
-          const float w = hf && nib ? 0.0625f : 1.0f;
           uint4 f;
-          split_h2(x.x * w, x.z * w, f.x, f.y);  // channels 4tig, 4tig + 2: high parts (row g), low parts (row g + 8)
-          split_h2(x.y * w, x.w * w, f.z, f.w);
+          split_h2(x.x, x.z, f.x, f.y);  // channels 4tig, 4tig + 2: high parts (row g), low parts (row g + 8)
+          split_h2(x.y, x.w, f.z, f.w);
           fb[u][hf] = f;
         }
         qs[u] += __shfl_xor_sync(0xffffffffu, qs[u], 1);
@@ -512,12 +522,12 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
       if (blk < NB) {
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) qf[(blk * 2 + hf) * 32 + lane] = fb[u][hf];
-        if (tig == 0) qsum[blk * kMaxHeads + g] = qs[u] * 5.9604644775390625e-8f;  // in the mma's units, 2^-24
+        if (tig == 0) qsum[blk * kMaxHeads + g] = qs[u];
       }
     }
   }
   __syncthreads();
-  const float f_tail = s_f[g] * 256.0f, f_body = s_f[g] * 16777216.0f;  // (tail rows go in times 2^-8)
+  const float f_body = s_f[g], f_tail = f_body * 256.0f;  // (tail rows go in times 2^-8)
 
   // ---- main loop
   const uint32_t wst_s = smem_u32(wst), qf_s = smem_u32(qf), qsum_s = smem_u32(qsum);
@@ -559,8 +569,6 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
     } else {
       f = f_tail;
       float cc[4] = {0.f, 0.f, 0.f, 0.f};
-      // the second half blocks' channels times 16 more where the fragments are 16 times smaller
-      const uint32_t f1 = nib ? 0x3D803D80u : 0x3B803B80u;
       // token g, bytes 8tig .. of half block 0; half block j lies 32 bytes further, its 16-byte chunks swizzled
       const uint32_t k0 = st + g * WT + (((tig >> 1) ^ g) << 4) + (tig & 1) * 8;
 #pragma unroll
@@ -568,8 +576,7 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
         const uint2 x = lds64((k0 ^ ((2 * (j & 3)) << 4)) + (j >> 2) * (kTailRows * WT));
         const uint4 q = lds128(qf_s + lane * 16 + j * 512);
         const uint32_t qa[4] = {q.x, q.y, q.z, q.w};
-        const uint32_t fj = j & 1 ? f1 : 0x3B803B80u;  // bf16 2^-8, or 2^-4
-        mma16816(cc, qa, bf16x2_times(__byte_perm(x.x, x.y, 0x5410), fj), bf16x2_times(__byte_perm(x.x, x.y, 0x7632), fj));
+        mma16816(cc, qa, bf16x2_scaled(__byte_perm(x.x, x.y, 0x5410)), bf16x2_scaled(__byte_perm(x.x, x.y, 0x7632)));
       }
       sc[0][0][0] = cc[0] + cc[2];
       sc[0][0][1] = cc[1] + cc[3];
@@ -655,8 +662,8 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
       for (int j = 0; j < 2 * NB; ++j) {
         const uint32_t w0 = lds32((v0 ^ ((2 * (j & 3)) << 4)) + (j >> 2) * (kTailRows * WT)) & m0;
         const uint32_t w1 = lds32((v1 ^ ((2 * (j & 3)) << 4)) + (j >> 2) * (kTailRows * WT)) & m1;
-        const uint32_t av[4] = {bf16x2_times(__byte_perm(w0, w1, 0x5410), 0x3B803B80u),
-                                bf16x2_times(__byte_perm(w0, w1, 0x7632), 0x3B803B80u), 0u, 0u};
+        const uint32_t av[4] = {bf16x2_scaled(__byte_perm(w0, w1, 0x5410)),
+                                bf16x2_scaled(__byte_perm(w0, w1, 0x7632)), 0u, 0u};
         mma16816(acc[j / 2][j % 2], av, bh_, 0u);
         mma16816(acc[j / 2][j % 2], av, bl_, 0u);
       }

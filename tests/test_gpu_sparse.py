@@ -159,8 +159,35 @@ def test_sparse_decode_formats(kt, vt):
     q = rng.standard_normal((3, 8, 128)).astype(np.float32)
     sel = np.array([[[9, 0, 4, 5], [1, -1, 9, 2]], [[1, 0, -1, 5], [0, -1, -1, -1]], [[9, 8, 7, 6], [2, 2, 0, 99]]])
     got, qn = _sparse(torch, kvq, gc, q, "f32", sel, 64)
-    _close(got, so.sparse_decode(oc, qn, sel, 64))
+    ref = so.sparse_decode(oc, qn, sel, 64)
+    _close(got, ref)
+    # fp32's precision: a weight times a V scale is held to 2^-25, the weights within 2^6 of the largest
+    # (2^5 .. 2^7) times scales from 2^-6 on to 2^-18 of themselves and less; scores and weights add 2^-21
+    assert np.linalg.norm(got - ref) <= 2.0 ** -18 * np.linalg.norm(ref)
     assert kvq.kvq_sync_status(gc.desc)[0] == 0
+
+
+@pytest.mark.parametrize("vt,T", [(t, T) for t in TYPES for T in (0, 40)])
+def test_sparse_decode_of_large_values(vt, T):
+    """V scales past what the weights leave room for in fp16, in some blocks of some tokens only."""
+    torch = require_gpu()
+    from rotated_bit_kv_kvq_gb300 import kvq
+    rng = np.random.default_rng(33)
+    gc, oc = (kvq.KVCache(1, 1, 128, 512, T, "q8_0", vt, flags=kvq.KVQ_ROT_AUTO | kvq.KVQ_ROT_V_OFF),
+              ko.OracleCache(1, 1, 128, 512, T, "q8_0", vt, True, False))
+    k, v = rng.standard_normal((2, 1, 500, 1, 128)).astype(np.float32)
+    v[:, 200:210, :, 40:50] *= 1e4
+    v[:, 490, :, 3] *= 3e4
+    append_both(gc, oc, k, v, torch=torch)
+    q = rng.standard_normal((1, 5, 128)).astype(np.float32)
+    sel = np.array([[[0, 1, 2, 3, 4, 6, 7]]])
+    got, qn = _sparse(torch, kvq, gc, q, "f32", sel, 64)
+    ref = so.sparse_decode(oc, qn, sel, 64)
+    assert np.all(np.isfinite(got))
+    assert np.linalg.norm(got - ref) <= RTOL * np.linalg.norm(ref)
+    # the channels without large values on their own
+    calm = [c for c in range(128) if not 32 <= c < 64 and c >= 32]
+    assert np.abs(got[..., calm] - ref[..., calm]).max() <= ATOL
 
 
 @pytest.mark.parametrize("d,g,T,bt,qd,od,page", [

@@ -3,6 +3,8 @@
 ``ensure_built()`` compiles every ``csrc/*.cu`` translation unit in parallel
 with nvcc for ``sm_103a`` and links ``_build/libkvq.so`` when any source or
 header is newer than the library.  No other architecture is built.
+``ensure_binding()`` compiles ``csrc/kvq_torch.cpp`` (host code, for the torch
+that is installed) to the extension module ``_build/_kvq_torch.so`` beside it.
 """
 
 from __future__ import annotations
@@ -19,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libkvq.so")
+BINDING = os.path.join(BUILD, "_kvq_torch.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -69,7 +72,8 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
         objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), _sources()))
     tmp = LIB + ".tmp"
-    r = subprocess.run([nvcc(), *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
+    r = subprocess.run([nvcc(), *ARCH, "-shared", "-Xlinker", "-soname=libkvq.so", "-o", tmp, *objs],
+                       capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
@@ -78,6 +82,34 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
 
 def ensure_built() -> str:
     return build(force=False)
+
+
+def _binding_sources():
+    return [os.path.join(CSRC, "kvq_torch.cpp"), os.path.join(INCLUDE, "kvq.h"), os.path.abspath(__file__)]
+
+
+def ensure_binding() -> str:
+    """Compile the extension module if a source of it is newer; returns its path.  It finds libkvq.so beside itself."""
+    lib = ensure_built()
+    if os.path.exists(BINDING) and all(os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in _binding_sources()):
+        return BINDING
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    inc = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(root, "include"),
+           os.path.join(root, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include")]
+    tmp = BINDING + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{p}" for p in inc),
+           _binding_sources()[0], "-o", tmp, lib, f"-L{os.path.join(root, 'lib')}", "-ltorch_python", "-ltorch_cpu", "-lc10",
+           "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{os.path.join(root, 'lib')}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed for kvq_torch.cpp:\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 if __name__ == "__main__":

@@ -9,6 +9,10 @@
 // The angle modulo one turn is taken in integers: F = inv_freq / 2pi as a 64-bit fraction
 // of a turn, pos * F modulo 2^64 its position (the overflow is whole turns), of which the
 // upper 32 bits feed sincospi.  No fp64, and as exact at position 2^30 as at 1.
+//
+// Bound by memory with many rows: 8192 rows of 48 heads of 128 in bf16, 201 MB in 38.9 us,
+// 5.2 TB/s (78% of the card's measured copy rate); by the chain position - angle - factors -
+// store with few: 4 rows of 32 heads of 256 4.5 us.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -284,7 +288,8 @@ cudaError_t launch_dt(const RopeArgs& a, const kvq_rope_norm& r, cudaStream_t st
   const int sms = device_sm_count();
   // As many warps per row as one wave holds: the factors of a row are worked out in each of its
   // warps, and a second wave costs a whole one (1001 rows of 48 heads of 128: 4 warps a row
-  // 8.6 us, 2 TWO us; 8192 rows: 4 warps 52.6 us, 1 warp 38.8 us; 4 rows of 32 heads of 256:
+  // 8.6 us, 2
+  // 7.6 us; 8192 rows: 4 warps 52.6 us, 1 warp 38.8 us; 4 rows of 32 heads of 256:
   // 4 warps 6.0 us, 8 warps 4.5 us).
   auto go = [&](auto w8, auto w4, auto w2, auto w1) {
     const long long n = a.n_rows, m = sms > 0 ? sms : 148;

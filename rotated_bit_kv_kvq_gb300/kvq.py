@@ -159,21 +159,13 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
-_raw_stream = None  # device index -> its current stream's handle
 _dtype_ids = None
 
 
-def _stream(stream, device=None) -> Optional[int]:
-    global _raw_stream
-    if stream is None and device is not None and _raw_stream is not None:
-        return _raw_stream(device)
+def _stream(stream) -> Optional[int]:
     if stream is None:
         import torch
-        if _raw_stream is None:
-            # the handle without a torch.cuda.Stream object around it: 0.1 us instead of 2.9 us a call
-            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-                (lambda device: torch.cuda.current_stream(device).cuda_stream)
-        return _raw_stream(torch.cuda.current_device())
+        return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -255,58 +247,46 @@ def kvq_prefill_attention(cache: kvq_cache, q, out, workspace, q_pos0=None, caus
            "kvq_prefill_attention")
 
 
-def _expect(what: str, dev: int, shape, dtype, *tensors):
-    """ValueError unless the tensors (None allowed) are contiguous, on CUDA device `dev` and of that shape and type
-    (None: any shape; any of the q / k / v types)."""
+_native = None
+
+
+def native():
+    """The extension module that takes the step operators' tensors (built in-tree on first use if stale)."""
+    global _native
+    if _native is None:
+        import importlib.util
+
+        import torch  # noqa: F401  (its libraries are the module's)
+        lib()
+        path = _build.ensure_binding()
+        spec = importlib.util.spec_from_file_location("_kvq_torch", path)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        _native = mod
+    return _native
+
+
+def _expect_plan(what: str, dtypes, *tensors):
+    import torch
     for t in tensors:
-        if t is not None and (t.get_device() != dev or not t.is_contiguous() or
-                              (t.dtype is not dtype if dtype is not None else t.dtype not in _dtypes()) or
-                              (shape is not None and t.shape != shape)):
-            raise ValueError(f"{what}: expected {shape or 'any shape'} of {dtype or 'fp32, bf16 or fp16'}, contiguous, on "
-                             f"CUDA device {dev}; got {tuple(t.shape)} of {t.dtype} on {t.device}")
-
-
-def _heads_row_stride(what: str, t, dev: int, dtype, heads: int, d: int, n_rows: int) -> int:
-    """Row stride (elements) of projection rows [n_rows][heads * d] or [n_rows][heads][d] whose heads lie side by side."""
-    if t.dtype is dtype and t.get_device() == dev:
-        shape, stride = t.shape, t.stride()
-        if len(shape) == 2:
-            ok = shape == (n_rows, heads * d) and (stride[1] == 1 or n_rows == 0)
-        else:
-            ok = shape == (n_rows, heads, d) and (n_rows == 0 or (stride[2] == 1 and (heads == 1 or stride[1] == d)))
-        if ok:
-            # (the stride of a single row is free: torch may report any number)
-            return stride[0] if n_rows > 1 else heads * d
-    raise ValueError(f"{what}: expected {n_rows} rows of {heads} x {d} values of {dtype}, heads side by side, on CUDA "
-                     f"device {dev}; got {tuple(t.shape)} of {t.dtype} on {t.device}")
-
-
-_torch = None  # torch, its current-device query and int32, looked up once
-_device = None
-_int32 = None
-
-
-def _torch_ready():
-    global _torch, _device, _int32
-    if _torch is None:
-        import torch
-        _device, _int32, _torch = torch.cuda.current_device, torch.int32, torch
-    return _torch
+        if t is not None and (t.get_device() != torch.cuda.current_device() or not t.is_contiguous() or t.dim() != 1 or
+                              t.dtype not in dtypes):
+            raise ValueError(f"{what}: expected a contiguous vector of {dtypes} on the current CUDA device; got "
+                             f"{tuple(t.shape)} of {t.dtype} on {t.device}")
 
 
 class RopeNorm:
     """The plan of kvq_qk_norm_rope: inv_freq fp32 [rot_dim / 2] (None: no rotation), weights [head_dim] or None."""
 
     def __init__(self, inv_freq=None, q_weight=None, k_weight=None, eps=1e-6, interleaved=False):
-        torch = _torch_ready()
-        dev = _device()
-        _expect("RopeNorm", dev, None, torch.float32, inv_freq)
-        _expect("RopeNorm", dev, None, None, q_weight, k_weight)
+        import torch
+        _expect_plan("RopeNorm", (torch.float32,), inv_freq)
+        _expect_plan("RopeNorm", tuple(_dtypes()), q_weight, k_weight)
         weights = [w for w in (q_weight, k_weight) if w is not None]
-        if any(w.dtype != weights[0].dtype or w.shape != weights[0].shape or w.dim() != 1 or not w.numel() for w in weights):
+        if any(w.dtype != weights[0].dtype or w.shape != weights[0].shape or not w.numel() for w in weights):
             raise ValueError("RopeNorm: the weights are vectors of one type and size")
         self.inv_freq, self.q_weight, self.k_weight = inv_freq, q_weight, k_weight  # kept alive
-        self.weight_dim = weights[0].numel() if weights else None
+        self.weight_dim = weights[0].numel() if weights else 0
         self.desc = kvq_rope_norm()
         self.desc.rot_dim = 0 if inv_freq is None else 2 * inv_freq.numel()
         self.desc.interleaved = 1 if interleaved else 0
@@ -319,24 +299,8 @@ class RopeNorm:
 def kvq_qk_norm_rope(cache: kvq_cache, rope: RopeNorm, q, k, v, pos, q_out, k_out, v_out, dst_row=None, stream=None):
     """Rows q [n][heads * d] or [n][heads][d] (any row stride, e.g. parts of one projection), k and v (or None) the same
     with the KV heads; pos int32 [n], dst_row int32 [n] or None.  Outputs [..][heads][d], contiguous, of the same rows."""
-    _torch_ready()
-    dev, dtype, d, hkv = _device(), q.dtype, cache.head_dim, cache.n_kv_heads
-    shape, n = q_out.shape, q.shape[0]
-    hq = shape[-2]
-    rows = q_out.numel() // max(1, hq * d)
-    if rope.weight_dim is not None and rope.weight_dim != d:
-        raise ValueError("kvq_qk_norm_rope: the weights have not head_dim values")
-    _expect("kvq_qk_norm_rope: pos, dst_row", dev, (n,), _int32, pos, dst_row)
-    _expect("kvq_qk_norm_rope: outputs", dev, None, dtype, q_out, k_out, v_out)
-    if shape[-1] != d or k_out.numel() != rows * hkv * d or (v_out is not None and v_out.numel() != rows * hkv * d):
-        raise ValueError("kvq_qk_norm_rope: the outputs differ in rows, heads or head_dim")
-    qs = _heads_row_stride("kvq_qk_norm_rope: q", q, dev, dtype, hq, d, n)
-    ks = _heads_row_stride("kvq_qk_norm_rope: k", k, dev, dtype, hkv, d, n)
-    vs = 0 if v is None else _heads_row_stride("kvq_qk_norm_rope: v", v, dev, dtype, hkv, d, n)
-    _check(lib().kvq_qk_norm_rope(cache, rope.desc, _dtypes()[dtype], hq, q.data_ptr(), qs, k.data_ptr(), ks, _ptr(v), vs,
-                                  pos.data_ptr(), _ptr(dst_row), n, rows, q_out.data_ptr(), k_out.data_ptr(),
-                                  _ptr(v_out), _stream(stream, dev)),
-           "kvq_qk_norm_rope")
+    _check((_native or native()).qk_norm_rope(cache, rope.desc, rope.weight_dim, q, k, v, pos, q_out, k_out, v_out, dst_row,
+                                              stream), "kvq_qk_norm_rope")
 
 
 class PagePool:
@@ -346,6 +310,7 @@ class PagePool:
         import torch
         n = cache.n_pages
         free = range(n) if free is None else free
+        self.pages = n
         self.ring = torch.full((max(n, 1),), -1, dtype=torch.int32, device=device)
         ids = [int(i) for i in free]
         if len(set(ids)) != len(ids) or any(i < 0 or i >= n for i in ids):
@@ -359,23 +324,11 @@ class PagePool:
 def kvq_page_update(cache: kvq_cache, pool, n_new, n_new_max: int, granted, row_pos=None, row_dst=None, row_slot=None,
                     seq_len_out=None, stream=None):
     """pool: PagePool or kvq_page_pool; n_new, granted, seq_len_out int32 [batch]; the row maps int32 [max_rows]."""
-    _torch_ready()
-    dev, batch = _device(), cache.batch
-    _expect("kvq_page_update", dev, (batch,), _int32, n_new, granted, seq_len_out)
-    a_map = row_dst if row_dst is not None else row_pos if row_pos is not None else row_slot
-    if a_map is None:
-        rows = min(batch * n_new_max, 0x7fffffff)  # no maps: no limit of rows
-    else:
-        rows = a_map.numel()
-        _expect("kvq_page_update: row maps", dev, (rows,), _int32, row_pos, row_dst, row_slot)
-    desc = pool
+    pages = 0x7fffffff  # a descriptor of the caller's own: its sizes are theirs
     if isinstance(pool, PagePool):
-        desc = pool.desc
-        if pool.ring.numel() < cache.n_pages:
-            raise ValueError("kvq_page_update: the pool was made for fewer pages")
-    _check(lib().kvq_page_update(cache, desc, _ptr(n_new), n_new_max, _ptr(granted), rows,
-                                 _ptr(row_pos), _ptr(row_dst), _ptr(row_slot), _ptr(seq_len_out), _stream(stream, dev)),
-           "kvq_page_update")
+        pool, pages = pool.desc, pool.pages
+    _check((_native or native()).page_update(cache, pool, pages, n_new, n_new_max, granted, row_pos, row_dst, row_slot,
+                                             seq_len_out, stream), "kvq_page_update")
 
 
 class BlockIndex:
@@ -402,29 +355,19 @@ def _index_desc(cache, index):
 
 def kvq_block_index_update(cache: kvq_cache, index, n_last: int = 0, stream=None):
     """index: BlockIndex or kvq_block_index; n_last 0: every block, else those of the last n_last tokens."""
-    _check(lib().kvq_block_index_update(cache, _index_desc(cache, index), n_last, _stream(stream)),
+    _check((_native or native()).block_index_update(cache, _index_desc(cache, index), n_last, stream),
            "kvq_block_index_update")
 
 
 def kvq_select_blocks(cache: kvq_cache, index, q, sel, n_first: int = 1, n_last: int = 1, stream=None):
     """q [batch][n_q_heads][head_dim]; sel int32 [batch][n_kv_heads][n_select]."""
-    _torch_ready()
-    dev, batch, hq, n = _device(), cache.batch, q.shape[1], sel.shape[-1]
-    _expect("kvq_select_blocks: q", dev, (batch, hq, cache.head_dim), None, q)
-    _expect("kvq_select_blocks: sel", dev, (batch, cache.n_kv_heads, n), _int32, sel)
-    _check(lib().kvq_select_blocks(cache, _index_desc(cache, index), q.data_ptr(), _dtypes()[q.dtype], hq, n_first, n_last, n,
-                                   sel.data_ptr(), _stream(stream, dev)),
+    _check((_native or native()).select_blocks(cache, _index_desc(cache, index), q, sel, n_first, n_last, stream),
            "kvq_select_blocks")
 
 
 def kvq_sparse_decode_attention(cache: kvq_cache, q, sel, out, block_tokens: int, scale: float = 0.0, stream=None):
     """q, out [batch][n_q_heads][head_dim]; sel int32 [batch][n_kv_heads][n_select] block numbers (negative: none)."""
-    _torch_ready()
-    dev, batch, hq, n, ids = _device(), cache.batch, q.shape[1], sel.shape[-1], _dtypes()
-    _expect("kvq_sparse_decode_attention: q, out", dev, (batch, hq, cache.head_dim), None, q, out)
-    _expect("kvq_sparse_decode_attention: sel", dev, (batch, cache.n_kv_heads, n), _int32, sel)
-    _check(lib().kvq_sparse_decode_attention(cache, q.data_ptr(), ids[q.dtype], hq, scale, block_tokens, sel.data_ptr(), n,
-                                             out.data_ptr(), ids[out.dtype], _stream(stream, dev)),
+    _check((_native or native()).sparse_decode_attention(cache, q, sel, out, block_tokens, scale, stream),
            "kvq_sparse_decode_attention")
 
 

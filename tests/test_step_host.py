@@ -184,3 +184,21 @@ def test_oracle_selection_and_means():
     oc.append(rng.standard_normal((1, 150, 1, 64)), rng.standard_normal((1, 150, 1, 64)))
     q = rng.standard_normal((1, 2, 64))
     assert np.allclose(so.sparse_decode(oc, q, np.array([[[2, 0, 1, -1]]]), 64), ko.decode_attention(oc, q), atol=1e-12)
+
+
+def test_binding_module_builds_and_refuses_descriptors():
+    """The extension module loads without a GPU and tells descriptors apart before it looks at a tensor."""
+    torch = pytest.importorskip("torch")
+    n = kvq.native()
+    c, x = kvq.descriptor(1, 1, 64, 64, 0, "q4_0", "q4_0"), kvq.kvq_block_index(64, FAKE, FAKE)
+    t = torch.zeros(1, 1, 64)
+    for args in ((c, c, 0, 0), (x, x, 0, 0), (None, x, 0, 0), (c, x, 1 << 40, 0), (c, x, "1", 0), (c, x, 0, "s"), (c, x)):
+        with pytest.raises(ValueError):
+            n.block_index_update(*args)
+    assert n.block_index_update(_full_desc(), x, -1, 0) == INVALID           # through to the C ABI's own checks
+    with pytest.raises(ValueError):
+        n.select_blocks(c, x, [1.0], t, 1, 1, None)
+    with pytest.raises(ValueError):
+        n.sparse_decode_attention(c, t, None, t, 64, 0.0, None)
+    with pytest.raises(ValueError):
+        n.page_update(c, kvq.kvq_page_pool(FAKE, FAKE, FAKE), 0, None, 1, t, None, None, None, None, None)

@@ -89,6 +89,7 @@ __device__ __forceinline__ void add_token(const Token<KT>& t, int s, float2 (&ac
 
 template <int KT, int D>
 __global__ void __launch_bounds__(D) index_update_kernel(kvq_cache c, kvq_block_index x, int n_last, int nblk) {
+  pdl_begin();
   __shared__ uint32_t s_max[10];
   constexpr int nw = D / 32, d = D;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -202,6 +203,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(SelArgs a) {
   constexpr int G = (D & (D - 1)) == 0 ? D : 64;
   constexpr int E = D / 32, SEG = D / 64, QP = sel_pitch<D>(), kW = kThreads / 32;
   extern __shared__ __align__(16) uint8_t smem[];
+  pdl_begin();
   cg::cluster_group cl = cg::this_cluster();
   const int S = int(cl.num_blocks()), rank = int(cl.block_rank());
   cl.barrier_arrive();  // (no CTA touches the first one's shared memory before it runs)
@@ -439,18 +441,7 @@ cudaError_t select_t(const SelArgs& a, int batch, cudaStream_t st) {
   const int sms = device_sm_count();
   const int S = int(std::max<long long>(1, std::min<long long>({kMaxSelCluster, (sms > 0 ? sms : 148) / rows,
                                                                a.nblk / (16 * kThreads / 32)})));
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(rows * S));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = bytes;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = S;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, a);
+  return launch_dependent(kern, unsigned(rows * S), kThreads, bytes, st, S, a);
 }
 template <int D>
 cudaError_t select_d(const SelArgs& a, int batch, cudaStream_t st) {
@@ -466,7 +457,7 @@ cudaError_t launch_block_index_update(const kvq_cache& c, const kvq_block_index&
   // blocks that can hold any of the last n_last tokens
   const int nx = n_last ? int(std::min<long long>(nblk, ((long long)n_last + bt - 2) / bt + 1)) : nblk;
   const dim3 grid(nx, c.n_kv_heads, c.batch);
-#define KVQ_INDEX(KT, D) index_update_kernel<KT, D><<<grid, D, 0, st>>>(c, x, n_last, nblk)
+#define KVQ_INDEX(KT, D) return launch_dependent(index_update_kernel<KT, D>, grid, D, 0, st, 1, c, x, n_last, nblk)
 #define KVQ_INDEX_KT(KT)                        \
   case KT:                                      \
     if (c.head_dim == 64) KVQ_INDEX(KT, 64);    \

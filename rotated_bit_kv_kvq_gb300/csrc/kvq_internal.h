@@ -68,6 +68,29 @@ inline cudaError_t allow_large_clusters(const void* kernel) {
   return e;
 }
 
+// Launches a kernel as a programmatic dependent of what runs before it on the stream, in clusters
+// of `cluster` CTAs.  Its CTAs may become resident before that has finished, so such a kernel begins
+// with pdl_begin() (kvq_device.cuh), in every thread and ahead of every access to memory; what this
+// saves is the launch latency between two calls.
+template <class... P, class... A>
+inline cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t st, int cluster,
+                                    const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = size_t(smem);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = unsigned(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // How many clusters of k CTAs of a kernel the device runs at once (a cluster stays within a
 // group of SMs, and the groups differ in size), for k = 2 .. kMaxCluster; asked once per kernel,
 // shared-memory size and device.  NULL when the query fails.

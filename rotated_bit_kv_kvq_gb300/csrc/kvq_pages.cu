@@ -67,6 +67,7 @@ __device__ __forceinline__ Sums warp_scan(Sums v, int lane) {  // inclusive
 }
 
 __global__ void __launch_bounds__(kMaxPageThreads) page_update_kernel(PageArgs a) {
+  pdl_begin();
   __shared__ Sums s_warp[32];
   __shared__ int s_row[kMaxPageThreads], s_need[kMaxPageThreads], s_n[kMaxPageThreads], s_held[kMaxPageThreads];
   __shared__ int s_get[kMaxPageThreads], s_put[kMaxPageThreads];  // pages to hand out (-1: nothing granted) and to take back
@@ -193,8 +194,7 @@ cudaError_t launch_page_update(PageArgs a, cudaStream_t st) {
   const int threads = std::min(kMaxPageThreads, std::max(128, (a.batch + 31) / 32 * 32));
   const int sms = device_sm_count();
   const int ctas = int(std::min<long long>(sms > 0 ? sms : 148, std::max<long long>(1, ((long long)a.max_rows + threads - 1) / threads)));
-  page_update_kernel<<<ctas, threads, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(page_update_kernel, unsigned(ctas), threads, 0, st, 1, a);
 }
 
 }  // namespace kvq

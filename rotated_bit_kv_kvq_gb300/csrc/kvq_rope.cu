@@ -125,6 +125,7 @@ __device__ __forceinline__ void load_weights(const void* w, int dt, int ch, floa
 // so with many rows a warp takes a whole row, and with few a row's heads spread over 8 warps.
 template <int DT, int L, int NC, int W, int WPR>
 __global__ void __launch_bounds__(32 * W, W == 4 ? (NC == 1 ? 6 : 4) : 2) qk_norm_rope_kernel(RopeArgs a, kvq_rope_norm r) {
+  pdl_begin();
   constexpr int RPC = W / WPR, HW = 32 / L;  // rows of a CTA, heads of a warp
   constexpr int kAhead = DT == KVQ_F32 || NC > 1 ? 2 : 4;
   __shared__ __align__(16) float s_cos[RPC][kMaxPairs], s_sin[RPC][kMaxPairs];
@@ -293,11 +294,10 @@ cudaError_t launch_dt(const RopeArgs& a, const kvq_rope_norm& r, cudaStream_t st
   // 4 warps 6.0 us, 8 warps 4.5 us).
   auto go = [&](auto w8, auto w4, auto w2, auto w1) {
     const long long n = a.n_rows, m = sms > 0 ? sms : 148;
-    if (n <= 2 * m) w8<<<unsigned(n), 256, 0, st>>>(a, r);
-    else if (n <= 6 * m) w4<<<unsigned(n), 128, 0, st>>>(a, r);
-    else if (n <= 12 * m) w2<<<unsigned((n + 1) / 2), 128, 0, st>>>(a, r);
-    else w1<<<unsigned((n + 3) / 4), 128, 0, st>>>(a, r);
-    return cudaGetLastError();
+    if (n <= 2 * m) return launch_dependent(w8, unsigned(n), 256, 0, st, 1, a, r);
+    if (n <= 6 * m) return launch_dependent(w4, unsigned(n), 128, 0, st, 1, a, r);
+    if (n <= 12 * m) return launch_dependent(w2, unsigned((n + 1) / 2), 128, 0, st, 1, a, r);
+    return launch_dependent(w1, unsigned((n + 3) / 4), 128, 0, st, 1, a, r);
   };
 #define KVQ_ROPE(L, NC) \
   go(qk_norm_rope_kernel<DT, L, NC, 8, 8>, qk_norm_rope_kernel<DT, L, NC, 4, 4>, \

@@ -347,6 +347,7 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
   constexpr int WT = 128, kWarps = kW<D>;  // (tail rows of 2 D bytes are whole 128-byte columns)
   static_assert(box_w(2 * D) == WT && kTailRows == 8, "tail rows' swizzle");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
+  pdl_begin();
   const kvq_cache& c = a.c;
   const int S = int(cg::this_cluster().num_blocks()), rank = int(cg::this_cluster().block_rank());
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -847,18 +848,7 @@ cudaError_t run_sparse(SpArgs& a, cudaStream_t st) {
   if (lim)
     for (int k = 2; k <= kMaxCluster && (long long)k * kWarps <= tiles; ++k)
       if (lim->clusters[k] >= rows) S = k;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(rows * S));
-  cfg.blockDim = dim3(32 * kWarps);
-  cfg.dynamicSmemBytes = bytes;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = S;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, a, mk, mv, mkt, mvt);
+  return launch_dependent(kern, unsigned(rows * S), 32 * kWarps, bytes, st, S, a, mk, mv, mkt, mvt);
 }
 
 }  // namespace

@@ -164,8 +164,8 @@ __global__ void __launch_bounds__(D) index_update_kernel(kvq_cache c, kvq_block_
 // shared memory as order-preserving integers; there the n_select-th largest is found by
 // histograms of ever finer bins and the blocks at or above it are written in order.
 //
-// Bound by latency: 32 x 8 rows of up to 128 blocks 6.0 us (2.0 of them the launch); 4 rows of
-// 16384 blocks 17.6 us, of which scoring takes about 5 and the one CTA that selects 8.  Tried for
+// Bound by latency: 32 x 8 rows of up to 128 blocks 5.6 us; 4 rows of
+// 16384 blocks 17.1 us, of which scoring takes about 5 and the one CTA that selects 8.  Tried for
 // those and not kept: fp16 mma over the codes as subnormals (19.0 us: int8 mma is slow here, but
 // that wants more registers than 1024 threads have), a histogram over equal steps of the score
 // with a list of the one bin's keys (18.0), clusters of 16 (17.9).

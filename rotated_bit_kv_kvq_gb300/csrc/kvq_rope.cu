@@ -10,9 +10,9 @@
 // of a turn, pos * F modulo 2^64 its position (the overflow is whole turns), of which the
 // upper 32 bits feed sincospi.  No fp64, and as exact at position 2^30 as at 1.
 //
-// Bound by memory with many rows: 8192 rows of 48 heads of 128 in bf16, 201 MB in 38.9 us,
+// Bound by memory with many rows: 8192 rows of 48 heads of 128 in bf16, 201 MB in 38.7 us,
 // 5.2 TB/s (78% of the card's measured copy rate); by the chain position - angle - factors -
-// store with few: 4 rows of 32 heads of 256 4.5 us.
+// store with few: 4 rows of 32 heads of 256 4.3 us.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -124,10 +124,10 @@ __device__ __forceinline__ void load_weights(const void* w, int dt, int ch, floa
 // The channels' factors (norm weight times cosine or sine) are worked out once per warp and row,
 // so with many rows a warp takes a whole row, and with few a row's heads spread over 8 warps.
 template <int DT, int L, int NC, int W, int WPR>
-__global__ void __launch_bounds__(32 * W, W == 4 ? (NC == 1 ? 6 : 4) : 2) qk_norm_rope_kernel(RopeArgs a, kvq_rope_norm r) {
+__global__ void __launch_bounds__(32 * W, W == 4 ? (NC == 1 ? (WPR == 4 ? 8 : 6) : 4) : 2) qk_norm_rope_kernel(RopeArgs a, kvq_rope_norm r) {
   pdl_begin();
   constexpr int RPC = W / WPR, HW = 32 / L;  // rows of a CTA, heads of a warp
-  constexpr int kAhead = DT == KVQ_F32 || NC > 1 ? 2 : 4;
+  constexpr int kAhead = DT == KVQ_F32 || NC > 1 || WPR == 4 ? 2 : 4;
   __shared__ __align__(16) float s_cos[RPC][kMaxPairs], s_sin[RPC][kMaxPairs];
   const int lane = threadIdx.x & 31, sub = lane / L, l = lane % L;
   const int rc = (threadIdx.x >> 5) / WPR, warp = (threadIdx.x >> 5) % WPR, rt = warp * 32 + lane;  // row of the CTA, place in it
@@ -288,14 +288,13 @@ cudaError_t launch_dt(const RopeArgs& a, const kvq_rope_norm& r, cudaStream_t st
   const int n = a.head_dim / 8;
   const int sms = device_sm_count();
   // As many warps per row as one wave holds: the factors of a row are worked out in each of its
-  // warps, and a second wave costs a whole one (1001 rows of 48 heads of 128: 4 warps a row
-  // 8.6 us, 2
-  // 7.6 us; 8192 rows: 4 warps 52.6 us, 1 warp 38.8 us; 4 rows of 32 heads of 256:
-  // 4 warps 6.0 us, 8 warps 4.5 us).
+  // warps, and a second wave costs a whole one.  1001 rows of 48 heads of 128: 4 warps a row 7.3 us
+  // (8 CTAs an SM; 9 us with 6 of them, two waves), 2 warps 9.1, 1 warp 10.0; 8192 rows: 4 warps
+  // 52.6 us, 1 warp 38.7; 4 rows of 32 heads of 256: 4 warps 6.0 us, 8 warps 4.3.
   auto go = [&](auto w8, auto w4, auto w2, auto w1) {
     const long long n = a.n_rows, m = sms > 0 ? sms : 148;
     if (n <= 2 * m) return launch_dependent(w8, unsigned(n), 256, 0, st, 1, a, r);
-    if (n <= 6 * m) return launch_dependent(w4, unsigned(n), 128, 0, st, 1, a, r);
+    if (n <= 8 * m) return launch_dependent(w4, unsigned(n), 128, 0, st, 1, a, r);
     if (n <= 12 * m) return launch_dependent(w2, unsigned((n + 1) / 2), 128, 0, st, 1, a, r);
     return launch_dependent(w1, unsigned((n + 3) / 4), 128, 0, st, 1, a, r);
   };

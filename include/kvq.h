@@ -421,7 +421,7 @@ typedef struct kvq_page_pool {
  *              in order; the first that finds too few free pages (those free
  *              before the call: released ones can be had from the next call
  *              on) or too few rows gets nothing, as do all after it that need
- *              any (a page, or a row), and KVQ_DEV_ERR_NO_ROOM is set.
+ *              what ran out, and KVQ_DEV_ERR_NO_ROOM is set.
  *   c->page_table  is written at the new pages of granted tokens: pages
  *              ceil(seq_len / page_tokens) on, in ring order.  Nothing else in
  *              it changes; a released row keeps its entries, which mean nothing

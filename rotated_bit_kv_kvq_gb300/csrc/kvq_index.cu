@@ -164,15 +164,18 @@ __global__ void __launch_bounds__(D) index_update_kernel(kvq_cache c, kvq_block_
 // shared memory as order-preserving integers; there the n_select-th largest is found by
 // histograms of ever finer bins and the blocks at or above it are written in order.
 //
-// Bound by latency: 32 x 8 rows of up to 128 blocks 5.6 us; 4 rows of
-// 16384 blocks 17.1 us, of which scoring takes about 5 and the one CTA that selects 8.  Tried for
-// those and not kept: fp16 mma over the codes as subnormals (19.0 us: int8 mma is slow here, but
-// that wants more registers than 1024 threads have), a histogram over equal steps of the score
-// with a list of the one bin's keys (18.0), clusters of 16 (17.9).
+// Bound by latency: 32 x 8 rows of up to 128 blocks 5.5 us; 4 rows of 16384 blocks 15.4 us, of
+// which scoring takes about 5 and the one CTA that selects 6.  Tried for those and not kept: every
+// CTA of the cluster keeping its own keys and searching with all the others' histograms (20.4 us:
+// five cluster barriers and reads of all histograms by all), fp16 mma over the codes as subnormals
+// (1.5 us slower: int8 mma is slow here, but that wants more registers than 1024 threads have), a
+// histogram over equal steps of the score with a list of the one bin's keys (0.5 slower), clusters of
+// 16 (0.4 slower).
 // ---------------------------------------------------------------------------
 constexpr int kBins = 2048;
 constexpr int kMaxSelCluster = 8;
 constexpr int kFewBlocks = 256;  // up to these a thread ranks each block
+constexpr int kSmallIndex = 2048;  // up to these CTAs of 256 threads
 
 // D = A (16x32 int8, row) * B (32x8 int8, col) + C, int32
 __device__ __forceinline__ void mma16832_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -311,10 +314,13 @@ __global__ void __launch_bounds__(kThreads) select_kernel(SelArgs a) {
         const uint32_t u = __float_as_uint(sc);
         uint32_t key = (u >> 31) ? ~u : (u | 0x80000000u);
         if (sc != sc) key = 0;
-        if (r < a.n_first || r >= nb - a.n_last) key = 0xFFFFFFFFu;
-        keys[r] = key;
-        lo = min(lo, key);
-        hi = max(hi, key);
+        // (blocks taken in any case lie above every score, outside the range that is searched)
+        const bool forced = r < a.n_first || r >= nb - a.n_last;
+        keys[r] = forced ? 0xFFFFFFFFu : key;
+        if (!forced) {
+          lo = min(lo, key);
+          hi = max(hi, key);
+        }
       }
     }
   }
@@ -363,9 +369,10 @@ __global__ void __launch_bounds__(kThreads) select_kernel(SelArgs a) {
   }
   // ---- the n_select-th largest key: bins of 2^sh keys over [lo, hi], then the same in the
   // bin that holds it, until a bin is one key wide or taken whole
-  int need = a.n_select;   // keys to take from [lo, hi]; all above hi are taken
+  int need = a.n_select - a.n_first - a.n_last;  // keys to take from [lo, hi]; all above hi are taken
   bool ties = false;
-  for (;;) {
+  if (need == 0) lo = 0xFFFFFFFFu;
+  while (need) {
     const uint32_t range = hi - lo;
     const int sh = range < kBins ? 0 : 32 - __clz(range) - 11;
     for (int i = tid; i < kBins; i += kThreads) s_hist[i] = 0;
@@ -405,28 +412,57 @@ __global__ void __launch_bounds__(kThreads) select_kernel(SelArgs a) {
     if (sh == 0) { ties = true; break; }
   }
   // ---- the blocks above, and of those equal the first `need`, in order: a warp takes a run of
-  // blocks, 32 at a time
+  // blocks, 32 at a time, and its lane i keeps the i-th (and 32 + i-th) 32 blocks' bits
+  constexpr int kWords = ((kThreads == 1024 ? kMaxIndexBlocks : kSmallIndex) / kW + 1023) / 1024;
   const int per = ((nb + kW - 1) / kW + 31) / 32 * 32, i0 = warp * per, i1 = min(nb, i0 + per);
-  int gt = 0, eq = 0;
-  for (int i = i0; i < i1; i += 32) {
-    const uint32_t k = i + lane < i1 ? s_key[i + lane] : 0u;
-    const bool in = i + lane < i1 && k >= lo, tie = in && ties && k == lo;
-    eq += __popc(__ballot_sync(0xffffffffu, tie));
-    gt += __popc(__ballot_sync(0xffffffffu, in && !tie));
+  unsigned mg[kWords], mt[kWords];
+#pragma unroll
+  for (int w = 0; w < kWords; ++w) mg[w] = mt[w] = 0u;
+#pragma unroll
+  for (int w = 0; w < kWords; ++w) {
+    const int j0 = i0 + 1024 * w;
+#pragma unroll 4
+    for (int it = 0; it < 32; ++it) {
+      if (j0 + 32 * it >= i1) break;
+      const int i = j0 + 32 * it + lane;
+      const uint32_t k = i < i1 ? s_key[i] : 0u;
+      const bool in = i < i1 && k >= lo;
+      const unsigned m = __ballot_sync(0xffffffffu, in);
+      if (lane == it) mg[w] = m;
+      if (ties) {
+        const unsigned t = __ballot_sync(0xffffffffu, in && k == lo);
+        if (lane == it) mt[w] = t;
+      }
+    }
+  }
+  int bg[kWords], be[kWords], gt = 0, eq = 0;  // taken and equal blocks of the warp before lane's word w
+#pragma unroll
+  for (int w = 0; w < kWords; ++w) {
+    mg[w] &= ~mt[w];
+    int g1 = __popc(mg[w]), e1 = __popc(mt[w]);
+    bg[w] = gt - g1;
+    be[w] = eq - e1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, g1, o), z = __shfl_up_sync(0xffffffffu, e1, o);
+      if (lane >= o) { g1 += y; e1 += z; }
+    }
+    bg[w] += g1;
+    be[w] += e1;
+    gt += __shfl_sync(0xffffffffu, g1, 31);
+    eq += __shfl_sync(0xffffffffu, e1, 31);
   }
   if (lane == 0) { s_warp[0][warp] = gt; s_warp[1][warp] = eq; }
   __syncthreads();
-  int bg = int(__reduce_add_sync(0xffffffffu, lane < warp ? unsigned(s_warp[0][lane]) : 0u));
-  int be = int(__reduce_add_sync(0xffffffffu, lane < warp ? unsigned(s_warp[1][lane]) : 0u));
-  const unsigned below = (1u << lane) - 1u;
-  for (int i = i0; i < i1; i += 32) {
-    const uint32_t k = i + lane < i1 ? s_key[i + lane] : 0u;
-    const bool in = i + lane < i1 && k >= lo, tie = in && ties && k == lo;
-    const unsigned mt = __ballot_sync(0xffffffffu, tie), mg = __ballot_sync(0xffffffffu, in && !tie);
-    const int e = be + __popc(mt & below), at = bg + __popc(mg & below) + min(e, need);
-    if (in && (!tie || e < need)) sel[at] = i + lane;
-    be += __popc(mt);
-    bg += __popc(mg);
+  const int wg = int(__reduce_add_sync(0xffffffffu, lane < warp ? unsigned(s_warp[0][lane]) : 0u));
+  const int we = int(__reduce_add_sync(0xffffffffu, lane < warp ? unsigned(s_warp[1][lane]) : 0u));
+#pragma unroll
+  for (int w = 0; w < kWords; ++w) {
+    const int e0 = we + be[w];
+    unsigned m = mt[w];
+    for (int t = __popc(m) - max(need - e0, 0); t > 0; --t) m &= ~(0x80000000u >> __clz(m));  // the last ties stay out
+    int at = wg + bg[w] + min(e0, need);
+    for (m |= mg[w]; m; m &= m - 1) sel[at++] = i0 + 1024 * w + 32 * lane + __ffs(m) - 1;
   }
 }
 
@@ -446,7 +482,7 @@ cudaError_t select_t(const SelArgs& a, int batch, cudaStream_t st) {
 template <int D>
 cudaError_t select_d(const SelArgs& a, int batch, cudaStream_t st) {
   // few blocks: barriers of few warps
-  return a.nblk <= 2048 ? select_t<D, kFewBlocks>(a, batch, st) : select_t<D, 1024>(a, batch, st);
+  return a.nblk <= kSmallIndex ? select_t<D, kFewBlocks>(a, batch, st) : select_t<D, 1024>(a, batch, st);
 }
 
 }  // namespace

@@ -95,7 +95,8 @@ def test_index_of_zero_keys_and_of_a_bad_page():
     (64, 1, 1, 1, 0, 0, "f32", True), (64, 1, 9, 1, 1, 0, "f32", True), (64, 3, 40, 7, 1, 1, "bf16", True),
     (128, 4, 128, 32, 1, 1, "bf16", True), (128, 8, 100, 99, 2, 3, "f16", True), (192, 9, 77, 20, 0, 5, "f32", True),
     (256, 6, 1000, 64, 1, 1, "bf16", True), (320, 12, 33, 16, 1, 1, "bf16", True), (128, 16, 3000, 500, 4, 4, "f32", False),
-    (64, 128, 50, 10, 1, 1, "bf16", True), (128, 1, 49152, 700, 1, 1, "bf16", True), (64, 2, 20000, 19999, 1, 1, "f32", True)])
+    (64, 128, 50, 10, 1, 1, "bf16", True), (128, 1, 49152, 700, 1, 1, "bf16", True), (64, 2, 20000, 19999, 1, 1, "f32", True),
+    (128, 5, 400, 30, 1, 1, "bf16", True), (64, 8, 2100, 1049, 600, 449, "f32", True), (320, 7, 4097, 33, 0, 0, "f16", True)])
 def test_selection(d, g, nblk, nsel, first, last, dt, rot):
     torch = require_gpu()
     from rotated_bit_kv_kvq_gb300 import kvq

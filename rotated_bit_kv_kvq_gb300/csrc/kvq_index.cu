@@ -17,7 +17,7 @@ namespace {
 namespace cg = cooperative_groups;
 
 // ---------------------------------------------------------------------------
-// Index update: one CTA per (block, KV head, sequence), one warp per 32-channel
+// Index update: a CTA per (block, KV head, sequence) or for several blocks, one warp per 32-channel
 // quantization block.  Lane (j, s) of a warp adds the tokens j, j + 8, ... of its
 // eight channels: q8_0 channels 8s .. 8s+7 (eight bytes of a row), the nibble formats
 // 4s .. 4s+3 and 16+4s .. (four bytes).  Token order within a partial sum, then the
@@ -26,9 +26,9 @@ namespace cg = cooperative_groups;
 // fused multiply-add rounds as the sum of the two does.
 //
 // A byte becomes a float by a byte permute into 2^23's significand and one subtraction, two at a
-// time; the loads of a warp's 64 tokens are all in flight at once.  4 x 4 x 65536 tokens of
-// head_dim 256 in q8_0, 289 MB in 64 us, 4.5 TB/s (68% of the card's measured copy rate): bound
-// by the instructions per byte (issue slots 70% busy) as much as by memory.
+// time; the loads of a warp's 64 tokens are all in flight at once, and those of the next tokens while
+// a block is finished.  4 x 4 x 65536 tokens of head_dim 256 in q8_0, 289 MB in 51.9 us, 5.6 TB/s (84%
+// of the card's measured copy rate); one block a launch and sequence 2.1 us.
 // ---------------------------------------------------------------------------
 // four bytes as exact floats, less `off`: a byte in the low bits of 2^23's significand
 __device__ __forceinline__ void bytes_f32(uint32_t w, float off, float2& a, float2& b) {
@@ -87,74 +87,110 @@ __device__ __forceinline__ void add_token(const Token<KT>& t, int s, float2 (&ac
   }
 }
 
+struct IndexArgs {
+  kvq_cache c;
+  kvq_block_index x;
+  int n_last, nblk, pages_per_seq;
+  DivU32 by_block, by_page;
+};
+
 template <int KT, int D>
-__global__ void __launch_bounds__(D) index_update_kernel(kvq_cache c, kvq_block_index x, int n_last, int nblk) {
+__global__ void __launch_bounds__(D) index_update_kernel(IndexArgs a) {
   pdl_begin();
-  __shared__ uint32_t s_max[10];
-  constexpr int nw = D / 32, d = D;
+  __shared__ uint32_t s_max[2][10];
+  constexpr int nw = D / 32;
+  const kvq_cache& c = a.c;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int h = blockIdx.y, b = blockIdx.z, bt = x.block_tokens;
+  const int h = blockIdx.y, b = blockIdx.z, bt = a.x.block_tokens;
   const int n = min(max(c.seq_len[b], 0), c.max_ctx);
-  const long long j0 = n_last ? max(0, n - n_last) / bt : 0;
-  const long long blk = j0 + blockIdx.x;
-  if (blk * bt >= n) return;
-  const RowMap rm = row_map(c);
-  const int t0 = int(blk * bt), cnt = min(bt, n - t0);
+  const int nb = int(div_u32(uint32_t(n + bt - 1), a.by_block));
+  const int bh = b * c.n_kv_heads + h;
   const int j = lane >> 2, s = lane & 3;
-  float2 acc[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) acc[i] = make_float2(0.0f, 0.0f);
+  int blk = (a.n_last ? int(div_u32(uint32_t(max(0, n - a.n_last)), a.by_block)) : 0) + int(blockIdx.x);
+  if (blk >= nb) return;
   bool bad = false;
-  for (int u = 0; u < cnt; u += 64) {  // 64 positions lie in one page
-    const long long row0 = body_row(rm, b, h, t0 + u);
-    if (row0 < 0) { bad = true; continue; }
-    const long long row = row0 + j;
-    const int m = min(64, cnt - u);
-    Token<KT> t[8];  // (every load before the first use)
-    if (m == 64) {
+  // 64 positions (they lie in one page) from t0 of a block's m that are left
+  Token<KT> t[8];
+  bool have;
+  auto load = [&](int t0, int m) {
+    long long row = (long long)bh * c.max_ctx + t0;
+    have = true;
+    if (c.page_tokens) {
+      const int i = int(div_u32(uint32_t(t0), a.by_page)), pg = c.page_table[(long long)b * a.pages_per_seq + i];
+      have = pg >= 0 && pg < c.n_pages;
+      row = ((long long)pg * c.n_kv_heads + h) * c.page_tokens + t0 - i * c.page_tokens;
+      if (!have) { bad = true; return; }
+    }
+    row += j;
+    if (m >= 64) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) t[i] = load_token<KT, D>(c, row + 8 * i, warp, s);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) add_token<KT>(t[i], s, acc);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (8 * i + j < m) t[i] = load_token<KT, D>(c, row + 8 * i, warp, s);
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (8 * i + j < m) add_token<KT>(t[i], s, acc);
     }
+  };
+  float2 acc[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i] = make_float2(0.0f, 0.0f);
+  int u = 0, buf = 0;
+  load(blk * bt, n - blk * bt);
+  for (;;) {
+    const int t0 = blk * bt, cnt = min(bt, n - t0), m = cnt - u;
+    if (have) {
+      if (m >= 64) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) add_token<KT>(t[i], s, acc);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (8 * i + j < m) add_token<KT>(t[i], s, acc);
+      }
+    }
+    // the next 64 tokens are on their way while this block is finished
+    const bool last = m <= 64;
+    const int next = blk + (last ? int(gridDim.x) : 0);
+    const bool more = next < nb;
+    u = last ? 0 : u + 64;
+    if (more) load(next * bt + u, min(bt, n - next * bt) - u);
+    if (!last) continue;
+    // the partial sums in pairs (j, j ^ 1), (j, j ^ 2), (j, j ^ 4), each lane keeping half of its
+    // channels at every step: lane (j, s) ends with channel e of the eight
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i & 1 ? acc[i / 2].y : acc[i / 2].x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int step = 0; step < 3; ++step) {
+      const int half = 4 >> step;
+      const bool up = (j >> step) & 1;
+#pragma unroll
+      for (int i = 0; i < half; ++i) {
+        const float give = up ? v[i] : v[i + half], keep = up ? v[i + half] : v[i];
+        v[i] = __fadd_rn(keep, __shfl_xor_sync(0xffffffffu, give, 4 << step));
+      }
+    }
+    const int e = 4 * (j & 1) + (j & 2) + (j >> 2);
+    // (a product with the power of two 1 / count is the quotient)
+    const float mean = (cnt & (cnt - 1)) == 0 ? __fmul_rn(v[0], __uint_as_float(uint32_t(127 - (31 - __clz(cnt))) << 23))
+                                              : __fdiv_rn(v[0], float(cnt));
+    uint32_t mx = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(mean)));
+    if (lane == 0) s_max[buf][warp] = mx;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < nw; ++w) mx = max(mx, s_max[buf][w]);
+    buf ^= 1;
+    const float scale = __fdiv_rn(__uint_as_float(mx), 127.0f);
+    const long long at = (long long)bh * a.nblk + blk;
+    if (threadIdx.x == 0) a.x.scales[at] = scale;
+    const int ch = KT == KVQ_TYPE_Q8_0 ? 8 * s + e : e < 4 ? 4 * s + e : 12 + 4 * s + e;
+    a.x.codes[at * D + 32 * warp + ch] = int8_t(scale > 0.0f ? __float2int_rn(__fdiv_rn(mean, scale)) : 0);
+    if (!more) break;
+    blk = next;
   }
   if (bad && threadIdx.x == 0) atomicOr(c.status, KVQ_DEV_ERR_PAGE);
-  // the partial sums in pairs (j, j ^ 1), (j, j ^ 2), (j, j ^ 4), each lane keeping half of its
-  // channels at every step: lane (j, s) ends with channel e of the eight
-  float v[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = i & 1 ? acc[i / 2].y : acc[i / 2].x;
-#pragma unroll
-  for (int step = 0; step < 3; ++step) {
-    const int half = 4 >> step;
-    const bool up = (j >> step) & 1;
-#pragma unroll
-    for (int i = 0; i < half; ++i) {
-      const float give = up ? v[i] : v[i + half], keep = up ? v[i + half] : v[i];
-      v[i] = __fadd_rn(keep, __shfl_xor_sync(0xffffffffu, give, 4 << step));
-    }
-  }
-  const int e = 4 * (j & 1) + (j & 2) + (j >> 2);
-  // (a product with the power of two 1 / count is the quotient)
-  const float mean = (cnt & (cnt - 1)) == 0 ? __fmul_rn(v[0], __uint_as_float(uint32_t(127 - (31 - __clz(cnt))) << 23))
-                                            : __fdiv_rn(v[0], float(cnt));
-  uint32_t mx = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(mean)));
-  if (lane == 0) s_max[warp] = mx;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < nw; ++w) mx = max(mx, s_max[w]);
-  const float scale = __fdiv_rn(__uint_as_float(mx), 127.0f);
-  const long long at = ((long long)b * c.n_kv_heads + h) * nblk + blk;
-  if (threadIdx.x == 0) x.scales[at] = scale;
-  const int ch = KT == KVQ_TYPE_Q8_0 ? 8 * s + e : e < 4 ? 4 * s + e : 12 + 4 * s + e;
-  x.codes[at * d + 32 * warp + ch] = int8_t(scale > 0.0f ? __float2int_rn(__fdiv_rn(mean, scale)) : 0);
 }
 
 // ---------------------------------------------------------------------------
@@ -492,8 +528,16 @@ cudaError_t launch_block_index_update(const kvq_cache& c, const kvq_block_index&
   const int nblk = int((c.max_ctx + (long long)bt - 1) / bt);
   // blocks that can hold any of the last n_last tokens
   const int nx = n_last ? int(std::min<long long>(nblk, ((long long)n_last + bt - 2) / bt + 1)) : nblk;
-  const dim3 grid(nx, c.n_kv_heads, c.batch);
-#define KVQ_INDEX(KT, D) return launch_dependent(index_update_kernel<KT, D>, grid, D, 0, st, 1, c, x, n_last, nblk)
+  // Where the device is full many times over a CTA takes three blocks, so that the loads of one run
+  // while another is finished: 16384 blocks of head_dim 256 51.9 us (2: 52.4, 4: 52.4, 8: 53.5, 16:
+  // 55.8, 1: 56.4).  Few blocks have a CTA each.
+  const long long all = (long long)nx * c.n_kv_heads * c.batch;
+  const int sms = device_sm_count();
+  const int per = all > 32LL * (sms > 0 ? sms : 148) ? 3 : 1;
+  const dim3 grid((nx + per - 1) / per, c.n_kv_heads, c.batch);
+  const IndexArgs a{c, x, n_last, nblk, c.page_tokens ? c.max_ctx / c.page_tokens : 0, make_divu32(uint32_t(bt)),
+                    make_divu32(uint32_t(std::max(1, c.page_tokens)))};
+#define KVQ_INDEX(KT, D) return launch_dependent(index_update_kernel<KT, D>, grid, D, 0, st, 1, a)
 #define KVQ_INDEX_KT(KT)                        \
   case KT:                                      \
     if (c.head_dim == 64) KVQ_INDEX(KT, 64);    \

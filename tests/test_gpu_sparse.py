@@ -77,6 +77,37 @@ def test_index_codes(kt, d, bt, page):
     assert kvq.kvq_sync_status(gc.desc)[0] == 0
 
 
+def test_index_of_many_blocks():
+    """More blocks than CTAs run at once: a CTA takes several, one of them in a page outside the pool."""
+    torch = require_gpu()
+    from rotated_bit_kv_kvq_gb300 import kvq
+    rng = np.random.default_rng(29)
+    lens = [0, 1, 64, 200, 4096, 4095, 65, 1000, 2049, 4000]
+    gc, oc = _pair(torch, kvq, rng, 10, 8, 64, 4096, 24, "q5_1", "q4_0", lens, 64)
+    x = kvq.BlockIndex(gc.desc, 64)
+    x.codes.fill_(3)
+    x.scales.fill_(3)
+    kvq.kvq_block_index_update(gc.desc, x)
+    assert kvq.kvq_sync_status(gc.desc)[0] == 0
+    codes, scales = so.block_index(oc, 64)
+
+    def check():
+        got = x.codes.cpu().numpy(), x.scales.cpu().numpy()
+        for b, n in enumerate(lens):
+            have = -(-n // 64)
+            assert np.array_equal(got[0][b, :, :have], codes[b, :, :have]) and np.array_equal(got[1][b, :, :have], scales[b, :, :have])
+            assert (got[0][b, :, have:] == 3).all() and (got[1][b, :, have:] == 3).all()
+    check()
+    gc.page_table.view(10, 64)[4, 20] = 1 << 20
+    x.codes.fill_(3)
+    x.scales.fill_(3)
+    kvq.kvq_block_index_update(gc.desc, x)
+    assert kvq.kvq_sync_status(gc.desc) == (kvq.KVQ_ERR_DEVICE_RANGE, kvq.KVQ_DEV_ERR_PAGE)
+    codes[4, :, 20] = 0
+    scales[4, :, 20] = 0
+    check()
+
+
 def test_index_of_zero_keys_and_of_a_bad_page():
     torch = require_gpu()
     from rotated_bit_kv_kvq_gb300 import kvq

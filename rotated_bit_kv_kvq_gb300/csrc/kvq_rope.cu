@@ -10,8 +10,8 @@
 // of a turn, pos * F modulo 2^64 its position (the overflow is whole turns), of which the
 // upper 32 bits feed sincospi.  No fp64, and as exact at position 2^30 as at 1.
 //
-// Bound by memory with many rows: 8192 rows of 48 heads of 128 in bf16, 201 MB in 38.7 us,
-// 5.2 TB/s (78% of the card's measured copy rate); by the chain position - angle - factors -
+// Bound by memory with many rows: 8192 rows of 48 heads of 128 in bf16, 201 MB in 36.7 us,
+// 5.5 TB/s (82% of the card's measured copy rate); by the chain position - angle - factors -
 // store with few: 4 rows of 32 heads of 256 4.3 us.
 
 #include <cuda_bf16.h>
@@ -166,7 +166,16 @@ __global__ void __launch_bounds__(32 * W, W == 4 ? (NC == 1 ? (WPR == 4 ? 8 : 6)
   if (a.in[2] && live) {  // values: one run of n_kv_heads * head_dim elements
     const int n8 = a.n_kv_heads * d / 8;
     const long long from = row * a.stride[2], to = (long long)dst * a.n_kv_heads * d;
-    for (int i = rt; i < n8; i += 32 * WPR) store8<DT>(a.out[2], to + 8 * i, load8<DT>(a.in[2], from + 8 * i));
+    constexpr int kCopy = 4;  // loads in flight
+    for (int i0 = rt; i0 < n8; i0 += 32 * WPR * kCopy) {
+      Raw8<DT> x[kCopy];
+#pragma unroll
+      for (int u = 0; u < kCopy; ++u)
+        if (i0 + 32 * WPR * u < n8) x[u] = load8<DT>(a.in[2], from + 8 * (i0 + 32 * WPR * u));
+#pragma unroll
+      for (int u = 0; u < kCopy; ++u)
+        if (i0 + 32 * WPR * u < n8) store8<DT>(a.out[2], to + 8 * (i0 + 32 * WPR * u), x[u]);
+    }
   }
   for (int i = rt; i < half; i += 32 * WPR) {
     const unsigned long long t = (unsigned long long)(long long)pos * turns64(r.inv_freq[i]);
@@ -290,7 +299,7 @@ cudaError_t launch_dt(const RopeArgs& a, const kvq_rope_norm& r, cudaStream_t st
   // As many warps per row as one wave holds: the factors of a row are worked out in each of its
   // warps, and a second wave costs a whole one.  1001 rows of 48 heads of 128: 4 warps a row 7.3 us
   // (8 CTAs an SM; 9 us with 6 of them, two waves), 2 warps 9.1, 1 warp 10.0; 8192 rows: 4 warps
-  // 52.6 us, 1 warp 38.7; 4 rows of 32 heads of 256: 4 warps 6.0 us, 8 warps 4.3.
+  // 52.6 us, 1 warp 36.7; 4 rows of 32 heads of 256: 4 warps 6.0 us, 8 warps 4.3.
   auto go = [&](auto w8, auto w4, auto w2, auto w1) {
     const long long n = a.n_rows, m = sms > 0 ? sms : 148;
     if (n <= 2 * m) return launch_dependent(w8, unsigned(n), 256, 0, st, 1, a, r);

@@ -42,7 +42,7 @@ constexpr int kMaxStages = 4;
 
 // Weights P = 2^(score - lim + kHead), lim a reference kLazyMax above the largest score at its last
 // move, are at most 2^kHead: P times a V scale, split in two fp16 parts, keeps an absolute error of
-// 2^-25 (fp16's smallest step), so the weights have to be large.  2^7: the tail takes P times 2^8.
+// 2^-25 (fp16's smallest step), so the weights have to be large.
 // Scales from kBigScale on (codes of q8_0 go in divided by 16, their scales times 16) would overflow:
 // a warp that meets one takes P down to 1 from there on.
 constexpr float kHead = 7.0f;
@@ -332,12 +332,36 @@ __device__ __forceinline__ void body_values(uint32_t st, const SpStage& L, int r
   }
 }
 
-// a bf16 pair times 2^-8 (exact) as an fp16 pair
-__device__ __forceinline__ uint32_t bf16x2_scaled(uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(b), "r"(0x3B803B80u));
-  return pack_h2(__uint_as_float(r << 16), __uint_as_float(r & 0xFFFF0000u));
+// Tail rows go into the mma as they are stored, exact at every size.  Keys in tf32, whose significand
+// holds fp16's 11 bits of a query part and bf16's 8: D = A (16x8, row) * B (8x8, col) + C
+__device__ __forceinline__ void mma1688_tf32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                             uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// Values in bf16, the weights as three bf16 parts (24 bits).
+__device__ __forceinline__ void mma16816_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_bf2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// a, b less their rounding to bf16, which is returned
+__device__ __forceinline__ uint32_t take_bf2(float& a, float& b) {
+  const uint32_t r = pack_bf2(a, b);
+  a -= __uint_as_float(r << 16);
+  b -= __uint_as_float(r & 0xFFFF0000u);
+  return r;
+}
+// the halves of an fp16 pair as fp32 bits
+__device__ __forceinline__ uint32_t h_lo_f32(uint32_t h) { return __float_as_uint(__low2float(u32_as_h2(h))); }
+__device__ __forceinline__ uint32_t h_hi_f32(uint32_t h) { return __float_as_uint(__high2float(u32_as_h2(h))); }
 
 template <int D>
 __global__ void __launch_bounds__(32 * kW<D>, kSpCtas<D>)
@@ -493,7 +517,7 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
     }
     mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
     // a power of two that brings the largest value into [2^10, 2^11)
-    const int e = min(max(137 - int(__float_as_uint(mx) >> 23), -100), 100);
+    const int e = min(137 - int(__float_as_uint(mx) >> 23), 126);
     const float up = __uint_as_float(uint32_t(127 + e) << 23);
 #pragma unroll
     for (int j = 0; j < NB; ++j) sq[hh * D + fwht_channel<D, G>(lane, j)] = v[j] * up;
@@ -534,7 +558,7 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
     }
   }
   __syncthreads();
-  const float f_body = s_f[g], f_tail = f_body * 256.0f;  // (tail rows go in times 2^-8)
+  const float f = s_f[g];
 
   // ---- main loop
   const uint32_t wst_s = smem_u32(wst), qf_s = smem_u32(qf), qsum_s = smem_u32(qsum);
@@ -561,7 +585,6 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
     float sc[HB][2][2];
 #pragma unroll
     for (int hh = 0; hh < HB; ++hh) sc[hh][0][0] = sc[hh][0][1] = sc[hh][1][0] = sc[hh][1][1] = 0.0f;
-    float f = f_body;
     if (job.y > 0) {
 #define KVQ_SCORES(KT) \
   case KT: body_scores<D, KT>(st, a.s, qf_s, qsum_s, lane, sc); break;
@@ -574,7 +597,6 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
       }
 #undef KVQ_SCORES
     } else {
-      f = f_tail;
       float cc[4] = {0.f, 0.f, 0.f, 0.f};
       // token g, bytes 8tig .. of half block 0; half block j lies 32 bytes further, its 16-byte chunks swizzled
       const uint32_t k0 = st + g * WT + (((tig >> 1) ^ g) << 4) + (tig & 1) * 8;
@@ -582,8 +604,9 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
       for (int j = 0; j < 2 * NB; ++j) {
         const uint2 x = lds64((k0 ^ ((2 * (j & 3)) << 4)) + (j >> 2) * (kTailRows * WT));
         const uint4 q = lds128(qf_s + lane * 16 + j * 512);
-        const uint32_t qa[4] = {q.x, q.y, q.z, q.w};
-        mma16816(cc, qa, bf16x2_scaled(__byte_perm(x.x, x.y, 0x5410)), bf16x2_scaled(__byte_perm(x.x, x.y, 0x7632)));
+        // channels 4tig, 4tig + 2 as inner indices tig, tig + 4, then 4tig + 1, 4tig + 3
+        mma1688_tf32(cc, h_lo_f32(q.x), h_lo_f32(q.y), h_hi_f32(q.x), h_hi_f32(q.y), x.x << 16, x.y << 16);
+        mma1688_tf32(cc, h_lo_f32(q.z), h_lo_f32(q.w), h_hi_f32(q.z), h_hi_f32(q.w), x.x & 0xFFFF0000u, x.y & 0xFFFF0000u);
       }
       sc[0][0][0] = cc[0] + cc[2];
       sc[0][0][1] = cc[1] + cc[3];
@@ -658,8 +681,8 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
       }
 #undef KVQ_VALUES
     } else {
-      uint32_t bh_, bl_;
-      split_h2(p[0][0][0] * 256.0f, p[0][0][1] * 256.0f, bh_, bl_);
+      float r0 = p[0][0][0], r1 = p[0][0][1];
+      const uint32_t p1 = take_bf2(r0, r1), p2 = take_bf2(r0, r1), p3 = pack_bf2(r0, r1);
       // tokens 2tig and 2tig + 1, channels 2g, 2g + 1; 16 channels further 32 bytes, swizzled.  Rows past the
       // end hold anything: masked
       const uint32_t m0 = 2 * tig < cnt ? 0xFFFFFFFFu : 0u, m1 = 2 * tig + 1 < cnt ? 0xFFFFFFFFu : 0u;
@@ -669,10 +692,10 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
       for (int j = 0; j < 2 * NB; ++j) {
         const uint32_t w0 = lds32((v0 ^ ((2 * (j & 3)) << 4)) + (j >> 2) * (kTailRows * WT)) & m0;
         const uint32_t w1 = lds32((v1 ^ ((2 * (j & 3)) << 4)) + (j >> 2) * (kTailRows * WT)) & m1;
-        const uint32_t av[4] = {bf16x2_scaled(__byte_perm(w0, w1, 0x5410)),
-                                bf16x2_scaled(__byte_perm(w0, w1, 0x7632)), 0u, 0u};
-        mma16816(acc[j / 2][j % 2], av, bh_, 0u);
-        mma16816(acc[j / 2][j % 2], av, bl_, 0u);
+        // the eight tokens stand twice in the inner index: with the first two parts, then with the third
+        const uint32_t a0 = __byte_perm(w0, w1, 0x5410), a1 = __byte_perm(w0, w1, 0x7632);
+        mma16816_bf16(acc[j / 2][j % 2], a0, a1, a0, a1, p1, p2);
+        mma16816_bf16(acc[j / 2][j % 2], a0, a1, 0u, 0u, p3, 0u);
       }
     }
     __syncwarp();

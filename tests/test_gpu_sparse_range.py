@@ -1,0 +1,55 @@
+"""Sparse decode over the whole range of stored values, against the float64 oracle, on the GPU:
+the relative L2 error alone, as an absolute bar says nothing about small values.
+
+Bound.  The scores below are sums of products whose magnitudes add up to at most 2^4 in base 2
+(order-1 scores of normal data); the query in two 11-bit parts and the sums on the tensor cores
+hold them to 2^-20 of that, so the weights to 2^-16 of themselves, the exponential's 2^-22 beside it;
+the weights' parts, their products with the scales and the sums of the output add 2^-20 of the
+largest terms.  Outputs of a few dozen tokens' average: together below 2^-15 of the output's norm."""
+
+import numpy as np
+import pytest
+
+from kvq_testlib import append_both, require_gpu, to_dev
+from oracle import kvq_oracle as ko
+from oracle import step_oracle as so
+
+pytestmark = pytest.mark.gpu
+
+TYPES = ["q4_0", "q5_0", "q8_0", "q4_1", "q5_1"]
+BOUND = 2.0 ** -15
+
+
+def _caches(kvq, d, ctx, T, kt, vt, k, v, torch, flags=None):
+    flags = kvq.KVQ_ROT_AUTO if flags is None else flags
+    gc = kvq.KVCache(1, k.shape[2], d, ctx, T, kt, vt, flags=flags)
+    oc = ko.OracleCache(1, k.shape[2], d, ctx, T, kt, vt, not flags & kvq.KVQ_ROT_K_OFF, not flags & kvq.KVQ_ROT_V_OFF)
+    append_both(gc, oc, k, v, torch=torch)
+    return gc, oc
+
+
+def _sparse(kvq, torch, gc, q, sel, bt=64):
+    out = torch.full(q.shape, 9.0, device="cuda")
+    kvq.kvq_sparse_decode_attention(gc.desc, to_dev(q, "f32", torch), torch.tensor(sel, dtype=torch.int32, device="cuda"), out, bt)
+    assert kvq.kvq_sync_status(gc.desc)[0] == 0
+    return out.cpu().numpy().astype(np.float64)
+
+
+def _rel(got, ref):
+    assert np.all(np.isfinite(got))
+    return np.linalg.norm(got - ref) / np.linalg.norm(ref)
+
+
+@pytest.mark.parametrize("d", [64, 128, 192, 256, 320])
+@pytest.mark.parametrize("ks,vs", [(1.0, 1e-2), (1.0, 1e-3), (1.0, 1e-4), (1.0, 1e-5), (1e-2, 1.0), (1e-4, 1.0), (1e-5, 1e-5),
+                                   (1.0, 1e-30), (1e-12, 1.0), (1e6, 1e7), (1e10, 1e20)])
+def test_tail_values_of_every_size(d, ks, vs):
+    """A sequence no longer than the tail: keys and values are the stored bf16 numbers, whatever their size."""
+    torch = require_gpu()
+    from rotated_bit_kv_kvq_gb300 import kvq
+    rng = np.random.default_rng(41)
+    k, v = rng.standard_normal((2, 1, 61, 2, d))
+    gc, oc = _caches(kvq, d, 128, 64, "q8_0", "q4_0", (ks * k).astype(np.float32), (vs * v).astype(np.float32), torch)
+    q = (rng.standard_normal((1, 6, d)) / ks).astype(np.float32)
+    got = _sparse(kvq, torch, gc, q, [[[0], [0]]])
+    assert _rel(got, so.sparse_decode(oc, q, np.array([[[0], [0]]]), 64)) <= BOUND

@@ -131,6 +131,14 @@ struct LdRow {
   }
 };
 
+// D = A (16x8, row) * B (8x8, col) + C in tf32: 11 bits of an fp32 operand, its whole range
+__device__ __forceinline__ void mma1688_tf32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                             uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
 // Scores of a body tile (st, qf, qsum: shared addresses of its stage, the query fragments and block sums): S[hh][t][e] of tokens 16hh + 8t + 2tig + e and head g.
 template <int D, int KT>
 __device__ __forceinline__ void body_scores(uint32_t st, const SpStage& L, uint32_t qf, uint32_t qsum, int lane,
@@ -211,10 +219,10 @@ __device__ __forceinline__ void body_scores(uint32_t st, const SpStage& L, uint3
   }
 }
 
-__device__ __forceinline__ uint32_t hadd2_bits(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
+// x as tf32 parts: its upper 11 bits, and what they leave
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+  hi = __float_as_uint(x) & 0xFFFFE000u;
+  lo = __float_as_uint(x - __uint_as_float(hi));
 }
 
 // bytes I0, I1 of offset-binary codes as the fp16 pair code / 16 (exact: 1152 / 16 = 72)
@@ -224,11 +232,11 @@ __device__ __forceinline__ uint32_t i8_sixteenth(uint32_t r) {
 }
 
 // acc += codes_V^T . (P * scale) of the 16 body rows from row0: rows 2g (acc .. [0], [1]) and 2g + 1 of each
-// 16 channels, columns heads 2tig, 2tig + 1; dmin += the blocks' minima . P (rows blocks g, g + 8).
-// cnt: the tile's tokens; P comes times 16 where the codes are divided by 16 (q8_0).
+// 16 channels, columns heads 2tig, 2tig + 1; dmin += the blocks' minima . P (rows blocks g, g + 8; see below).
+// cnt: the tile's tokens; ph, pl: P times 16 where the codes are divided by 16 (q8_0); p: P of tokens 8t + 2tig + e.
 template <int D, int VT>
 __device__ __forceinline__ void body_values(uint32_t st, const SpStage& L, int row0, const uint32_t (&ph)[2],
-                                            const uint32_t (&pl)[2], int cnt, int lane,
+                                            const uint32_t (&pl)[2], const float (&p)[2][2], int cnt, int lane,
                                             float (&acc)[D / 32][2][4], float (&dmin)[4]) {
   constexpr int NB = D / 32, RB = kRows<D>, ROW = VT == KVQ_TYPE_Q8_0 ? D : D / 2, W = box_w(ROW);
   constexpr bool V1 = type_has_min(VT), V5 = type_has_qh(VT);
@@ -263,30 +271,32 @@ __device__ __forceinline__ void body_values(uint32_t st, const SpStage& L, int r
     mma16816(acc[blk][1], a1, l0, l1);
   };
   if constexpr (V1) {
-    // blocks' minima + centre * scale at tokens i, i + 1 of the lane's four, as fp16 high and low parts: the
-    // product with the centre, a power of two, is exact, and so is the remainder of the sum
-    constexpr uint32_t C2 = (code_centre(VT) == 16 ? 0x4C00u : 0x4800u) * 0x10001u;
+    // minimum + centre * scale of block blk at token i of the lane's four, in fp32 (fp16 may overflow), as tf32 high and
+    // low parts.  Up to 8 blocks their low parts take the rows g + 8; the merge adds them.  16 x 8 rows of 2048 tokens,
+    // head_dim 128, q4_1: 29.2 us, 28.8 with the sum in fp16.
     auto minimum = [&](int blk, int i, uint32_t& hi, uint32_t& lo) {
-      const int bb = blk < NB ? blk : NB - 1;
-      uint32_t w0 = lds32(vd + (8 * (i >> 1) * NB + bb) * 4);
-      uint32_t w1 = lds32(vd + ((8 * (i >> 1) + 1) * NB + bb) * 4);
-      if (partial) { w0 = ok(i) ? w0 : 0u; w1 = ok(i + 1) ? w1 : 0u; }
-      const uint32_t m = __byte_perm(w0, w1, 0x7632), p = hmul2_bits(__byte_perm(w0, w1, 0x5410), C2);
-      hi = hadd2_bits(p, m);
-      const uint32_t mm = hsub2_bits(hi, p);  // the part of m in the sum
-      lo = hadd2_bits(hsub2_bits(p, hsub2_bits(hi, mm)), hsub2_bits(m, mm));
-      if (blk >= NB) hi = lo = 0u;
+      uint32_t w = lds32(vd + ((i & 1) + 8 * (i >> 1)) * HP + (NB % 8 == 0 || blk < NB ? blk : NB - 1) * 4);
+      if (partial) w = ok(i) ? w : 0u;
+      const float2 f = __half22float2(u32_as_h2(w));
+      split_tf32(fmaf(f.x, float(code_centre(VT)), f.y), hi, lo);
     };
-    uint32_t ah[4] = {0, 0, 0, 0}, al[4] = {0, 0, 0, 0};
-    minimum(g, 0, ah[0], al[0]);
-    minimum(g, 2, ah[2], al[2]);
-    if constexpr (NB > 8) {
-      minimum(g + 8, 0, ah[1], al[1]);
-      minimum(g + 8, 2, ah[3], al[3]);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {  // tokens 8t + 2tig, + 1 as inner indices tig, tig + 4
+      uint32_t a[4], c[4], bh[2], bl[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if constexpr (NB <= 8) {
+          minimum(g, 2 * t + e, a[2 * e], a[2 * e + 1]);
+        } else {
+          minimum(g, 2 * t + e, a[2 * e], c[2 * e]);
+          minimum(g + 8, 2 * t + e, a[2 * e + 1], c[2 * e + 1]);
+        }
+        split_tf32(p[t][e], bh[e], bl[e]);
+      }
+      mma1688_tf32(dmin, a[0], a[1], a[2], a[3], bh[0], bh[1]);
+      mma1688_tf32(dmin, a[0], a[1], a[2], a[3], bl[0], bl[1]);
+      if constexpr (NB > 8) mma1688_tf32(dmin, c[0], c[1], c[2], c[3], bh[0], bh[1]);
     }
-    mma16816(dmin, ah, ph[0], ph[1]);
-    mma16816(dmin, ah, pl[0], pl[1]);
-    mma16816(dmin, al, ph[0], ph[1]);
   }
   constexpr uint32_t OFF = (0x6400u + uint32_t(code_centre(VT))) * 0x10001u, OFF16 = neg_off_x16_bits(code_centre(VT));
   const uint32_t v0 = uint32_t(8 * ((g & 3) >> 1) + 2 * (g & 1) - 4) & 31u, v1 = (v0 + 1) & 31u;
@@ -332,15 +342,8 @@ __device__ __forceinline__ void body_values(uint32_t st, const SpStage& L, int r
   }
 }
 
-// Tail rows go into the mma as they are stored, exact at every size.  Keys in tf32, whose significand
-// holds fp16's 11 bits of a query part and bf16's 8: D = A (16x8, row) * B (8x8, col) + C
-__device__ __forceinline__ void mma1688_tf32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                             uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-// Values in bf16, the weights as three bf16 parts (24 bits).
+// Tail rows go into the mma as they are stored, exact at every size: keys in tf32 (fp16's 11 bits of a query
+// part and bf16's 8 fit its significand), values in bf16, the weights as three bf16 parts (24 bits).
 __device__ __forceinline__ void mma16816_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                               uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -669,7 +672,7 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
         for (int t = 0; t < 2; ++t) split_h2(p[hh][t][0] * vs, p[hh][t][1] * vs, ph[hh][t], pl[hh][t]);
 #define KVQ_VALUES(VT)                                                                                               \
   case VT:                                                                                                           \
-    _Pragma("unroll") for (int hh = 0; hh < HB; ++hh) body_values<D, VT>(st, a.s, 16 * hh, ph[hh], pl[hh], cnt, lane, acc, \
+    _Pragma("unroll") for (int hh = 0; hh < HB; ++hh) body_values<D, VT>(st, a.s, 16 * hh, ph[hh], pl[hh], p[hh], cnt, lane, acc, \
                                                                           dmin);                                    \
     break;
       switch (c.v_type) {
@@ -726,6 +729,10 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
       *reinterpret_cast<float2*>(o + D) = make_float2(acc[blk][j][1], acc[blk][j][3]);
     }
   if (type_has_min(c.v_type)) {
+    if constexpr (NB <= 8) {  // high and low parts
+      dmin[0] += dmin[2];
+      dmin[1] += dmin[3];
+    }
     __syncwarp();
 #pragma unroll
     for (int half = 0; half < 2; ++half) {

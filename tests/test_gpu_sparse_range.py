@@ -53,3 +53,21 @@ def test_tail_values_of_every_size(d, ks, vs):
     q = (rng.standard_normal((1, 6, d)) / ks).astype(np.float32)
     got = _sparse(kvq, torch, gc, q, [[[0], [0]]])
     assert _rel(got, so.sparse_decode(oc, q, np.array([[[0], [0]]]), 64)) <= BOUND
+
+
+@pytest.mark.parametrize("T", [0, 40])
+@pytest.mark.parametrize("vt,d,lo,hi", [("q5_1", 128, -64000, 64000), ("q4_1", 128, -64000, 64000), ("q4_1", 64, 5e4, 9e4),
+                                        ("q5_1", 320, 5e4, 9e4), ("q5_1", 192, -65000, -60000), ("q4_1", 256, -1e3, 2e5)])
+def test_large_minima_and_scales(vt, d, lo, hi, T):
+    """A block's minimum plus a multiple of its scale passes fp16's largest number; its values are finite all the same."""
+    torch = require_gpu()
+    from rotated_bit_kv_kvq_gb300 import kvq
+    rng = np.random.default_rng(42)
+    n = 500
+    k = rng.standard_normal((1, n, 2, d)).astype(np.float32)
+    v = rng.uniform(lo, hi, (1, n, 2, d)).astype(np.float32)
+    gc, oc = _caches(kvq, d, 512, T, "q8_0", vt, k, v, torch, flags=kvq.KVQ_ROT_AUTO | kvq.KVQ_ROT_V_OFF)
+    q = rng.standard_normal((1, 6, d)).astype(np.float32)
+    sel = [[[0, 7, 3, 4, 1], [6, 5, -1, 2, 7]]]
+    got = _sparse(kvq, torch, gc, q, sel)
+    assert _rel(got, so.sparse_decode(oc, q, np.array(sel), 64)) <= BOUND

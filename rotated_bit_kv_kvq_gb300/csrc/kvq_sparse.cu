@@ -630,11 +630,12 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
     }
 #pragma unroll
     for (int i = 0; i < 4 * HB; ++i) mx = fmaxf(mx, sc[i >> 2][(i >> 1) & 1][i & 1]);
-    // The rescale runs only when a score passes the reference, or when a tile's scales ask for smaller weights.
+    // The rescale runs only when a score passes the reference, or when the scales of a tile's tokens ask for smaller
+    // weights (rows past its end hold anything).
     bool down = false;
     if (job.y > 0 && head != 0.0f) {
       uint32_t mxs = 0;
-      for (int i = lane; i < RB * a.s.vh / 4; i += 32) mxs = __vmaxu2(mxs, lds32(st + a.s.vd + 4 * i) & hmask);
+      for (int i = lane; i < cnt * a.s.vh / 4; i += 32) mxs = __vmaxu2(mxs, lds32(st + a.s.vd + 4 * i) & hmask);
       down = __any_sync(0xffffffffu, (mxs & 0xFFFFu) >= big || (mxs >> 16) >= big);
     }
     if (__any_sync(0xffffffffu, mx > lim) || down) {

@@ -71,3 +71,28 @@ def test_large_minima_and_scales(vt, d, lo, hi, T):
     sel = [[[0, 7, 3, 4, 1], [6, 5, -1, 2, 7]]]
     got = _sparse(kvq, torch, gc, q, sel)
     assert _rel(got, so.sparse_decode(oc, q, np.array(sel), 64)) <= BOUND
+
+
+@pytest.mark.parametrize("page", [0, 64])
+@pytest.mark.parametrize("vt", TYPES)
+def test_bits_do_not_depend_on_rows_past_the_end(vt, page):
+    """Rows at or past a sequence's end, and body rows that the tail replaces, hold anything: the result is the same bits."""
+    torch = require_gpu()
+    from rotated_bit_kv_kvq_gb300 import kvq
+    rng = np.random.default_rng(43)
+    H, d, ctx, T, n = 2, 128, 256, 20, 149
+    table = torch.tensor([2, 0, 3, 1], dtype=torch.int32)
+    paged = dict(page_tokens=page, n_pages=4, page_table=table) if page else {}
+    gc = kvq.KVCache(1, H, d, ctx, T, vt, vt, **paged)
+    k, v = (to_dev(rng.standard_normal((1, n, H, d)), "f32", torch) for _ in range(2))
+    kvq.kvq_rotate_quantize_append(gc.desc, k, v)
+    q = rng.standard_normal((1, 2 * H, d)).astype(np.float32)
+    sel = [[[0, 1, 2], [2, 1, 0]]]
+    want = _sparse(kvq, torch, gc, q, sel)
+    dead = [gc.desc.max_ctx * h + p if not page else (table[p // page].item() * H + h) * page + p % page
+            for h in range(H) for p in range(n - T, ctx)]
+    dead = torch.tensor(dead, device="cuda")
+    for word in (0x7FFF, 0x7BFF, -1):  # NaN, fp16's largest number, NaN with the sign
+        for name in ("k_qs", "v_qs", "k_d", "v_d"):
+            gc.plane(name).view(torch.int16).view(H * ctx, -1)[dead] = word
+        assert np.array_equal(_sparse(kvq, torch, gc, q, sel), want), (vt, word)

@@ -512,9 +512,9 @@ KVQ_API kvq_status kvq_select_blocks(const kvq_cache* c, const kvq_block_index* 
  * that only read a cache may run at the same time.  The first call for a
  * head_dim asks the device for its limits; make it before a stream capture.
  * Body planes of 2^31 rows or more (and as many tail rows) give
- * KVQ_ERR_UNSUPPORTED.  The arithmetic keeps fp32's precision, for body values
- * (rotated) below 5e5 in magnitude and tail rows of any size: those enter the
- * products as they are stored.
+ * KVQ_ERR_UNSUPPORTED.  The arithmetic keeps fp32's precision relative to the
+ * largest values of a row's tokens, over all that the body formats hold; tail rows
+ * enter the products as they are stored, values up to 1e20.
  */
 KVQ_API kvq_status kvq_sparse_decode_attention(const kvq_cache* c, const void* q, int32_t q_dtype, int32_t n_q_heads,
                                                float scale, int32_t block_tokens, const int32_t* sel,

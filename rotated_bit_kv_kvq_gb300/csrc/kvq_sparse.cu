@@ -40,13 +40,16 @@ namespace cg = cooperative_groups;
 constexpr int kTailRows = 8;   // tokens of a tail tile
 constexpr int kMaxStages = 4;
 
-// Weights P = 2^(score - lim + kHead), lim a reference kLazyMax above the largest score at its last
-// move, are at most 2^kHead: P times a V scale, split in two fp16 parts, keeps an absolute error of
-// 2^-25 (fp16's smallest step), so the weights have to be large.
-// Scales from kBigScale on (codes of q8_0 go in divided by 16, their scales times 16) would overflow:
-// a warp that meets one takes P down to 1 from there on.
-constexpr float kHead = 7.0f;
-__device__ __forceinline__ uint32_t big_scale(int vt) { return vt == KVQ_TYPE_Q8_0 ? 0x5000u : 0x6000u; }  // fp16 32, 512
+// Weights P = 2^(score - lim + head), lim a reference kLazyMax above the largest score at its last move, are at
+// most 2^head.  P times a V scale goes in as two fp16 parts, with an absolute error of 2^-25 (fp16's smallest
+// step): head is what brings the product with the largest scale met so far to 2^14 .. 2^15, so that small
+// values keep their bits and large ones stay finite.  A warp begins with kHeadMax and lowers head, with its sums,
+// where a tile's scale reaches 2^(16 - head).  P itself is at most 2^15 in fp16: for a larger head (scales
+// below 2^-10 only, so that others go without) the missing power of two 2^up goes to the tile's scales, in place.
+// For q8_0 P goes in times 16 and its codes divided by 16 (with their range the product would lose 4 bits).
+constexpr int kHeadMax = 30;
+__device__ __forceinline__ int head_shift(int vt) { return vt == KVQ_TYPE_Q8_0 ? 4 : 0; }
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(uint32_t(127 + e) << 23); }
 
 template <int D> constexpr int kRows = D <= 128 ? 32 : 16;               // tokens of a body tile
 template <int D> constexpr int kW = D <= 128 ? 8 : D <= 256 ? 6 : 8;      // warps of a CTA
@@ -78,6 +81,7 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(a));
   return r;
 }
+__device__ __forceinline__ void sts32(uint32_t a, uint32_t v) { asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory"); }
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
   uint2 r;
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
@@ -233,11 +237,12 @@ __device__ __forceinline__ uint32_t i8_sixteenth(uint32_t r) {
 
 // acc += codes_V^T . (P * scale) of the 16 body rows from row0: rows 2g (acc .. [0], [1]) and 2g + 1 of each
 // 16 channels, columns heads 2tig, 2tig + 1; dmin += the blocks' minima . P (rows blocks g, g + 8; see below).
-// cnt: the tile's tokens; ph, pl: P times 16 where the codes are divided by 16 (q8_0); p: P of tokens 8t + 2tig + e.
+// cnt: the tile's tokens; ph, pl: P for scales in units of `unit`, times 16 where the codes are divided by 16
+// (q8_0); p: P of tokens 8t + 2tig + e.
 template <int D, int VT>
 __device__ __forceinline__ void body_values(uint32_t st, const SpStage& L, int row0, const uint32_t (&ph)[2],
-                                            const uint32_t (&pl)[2], const float (&p)[2][2], int cnt, int lane,
-                                            float (&acc)[D / 32][2][4], float (&dmin)[4]) {
+                                            const uint32_t (&pl)[2], const float (&p)[2][2], float unit, int cnt,
+                                            int lane, float (&acc)[D / 32][2][4], float (&dmin)[4]) {
   constexpr int NB = D / 32, RB = kRows<D>, ROW = VT == KVQ_TYPE_Q8_0 ? D : D / 2, W = box_w(ROW);
   constexpr bool V1 = type_has_min(VT), V5 = type_has_qh(VT);
   constexpr int VHH = V1 ? 2 : 1;
@@ -273,12 +278,13 @@ __device__ __forceinline__ void body_values(uint32_t st, const SpStage& L, int r
   if constexpr (V1) {
     // minimum + centre * scale of block blk at token i of the lane's four, in fp32 (fp16 may overflow), as tf32 high and
     // low parts.  Up to 8 blocks their low parts take the rows g + 8; the merge adds them.  16 x 8 rows of 2048 tokens,
-    // head_dim 128, q4_1: 29.2 us, 28.8 with the sum in fp16.
+    // head_dim 128, q4_1: 29.9 us, 28.8 with the sum in fp16.
+    const float centre = float(code_centre(VT)) * unit;
     auto minimum = [&](int blk, int i, uint32_t& hi, uint32_t& lo) {
       uint32_t w = lds32(vd + ((i & 1) + 8 * (i >> 1)) * HP + (NB % 8 == 0 || blk < NB ? blk : NB - 1) * 4);
       if (partial) w = ok(i) ? w : 0u;
       const float2 f = __half22float2(u32_as_h2(w));
-      split_tf32(fmaf(f.x, float(code_centre(VT)), f.y), hi, lo);
+      split_tf32(fmaf(f.x, centre, f.y), hi, lo);
     };
 #pragma unroll
     for (int t = 0; t < 2; ++t) {  // tokens 8t + 2tig, + 1 as inner indices tig, tig + 4
@@ -573,9 +579,12 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
 #pragma unroll
       for (int r = 0; r < 4; ++r) acc[i][j][r] = 0.0f;
   float dmin[4] = {0.f, 0.f, 0.f, 0.f};
-  float lim = -INFINITY, l = 0.0f, head = kHead;
-  const float vs = c.v_type == KVQ_TYPE_Q8_0 ? 16.0f : 1.0f;
-  const uint32_t hmask = type_has_min(c.v_type) ? 0x00007FFFu : 0x7FFF7FFFu, big = big_scale(c.v_type);
+  float lim = -INFINITY, l = 0.0f;
+  const int hs = head_shift(c.v_type);
+  float head = float(kHeadMax - hs);
+  int up = kHeadMax - 15;
+  uint32_t big = uint32_t(31 - kHeadMax) << 10;  // 2^(16 - hs - head) in fp16; infinity with the smallest head
+  const uint32_t hmask = type_has_min(c.v_type) ? 0x00007FFFu : 0x7FFF7FFFu;
   bool timed_out = false;
   int k = 0;
   for (; k < issued; ++k) {
@@ -633,15 +642,25 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
     // The rescale runs only when a score passes the reference, or when the scales of a tile's tokens ask for smaller
     // weights (rows past its end hold anything).
     bool down = false;
-    if (job.y > 0 && head != 0.0f) {
-      uint32_t mxs = 0;
+    uint32_t mxs = 0;  // largest scales of the lane's headers, fp16 bits in each half
+    if (job.y > 0) {
+#pragma unroll 1  // (a warp has few tiles: code that is fetched once counts; unrolled the call takes 5% longer)
       for (int i = lane; i < cnt * a.s.vh / 4; i += 32) mxs = __vmaxu2(mxs, lds32(st + a.s.vd + 4 * i) & hmask);
       down = __any_sync(0xffffffffu, (mxs & 0xFFFFu) >= big || (mxs >> 16) >= big);
     }
     if (__any_sync(0xffffffffu, mx > lim) || down) {
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const float nl = mx > lim ? mx + kLazyMax : lim, nh = down ? 0.0f : head;
+      float nh = head;
+      if (down) {  // the largest scale lies in [2^(e - 15), 2^(e - 14)): weights up to 2^(29 - e), half of what has room
+        const int e = int(__reduce_max_sync(0xffffffffu, max(mxs & 0xFFFFu, mxs >> 16)) >> 10);
+        int t = max(29 - e, 0);
+        if (e >= 5) t = min(t, 15);
+        big = uint32_t(31 - t) << 10;
+        up = max(t - 15, 0);
+        nh = float(t - hs);
+      }
+      const float nl = mx > lim ? mx + kLazyMax : lim;
       const float r = lim == -INFINITY ? 0.0f : fast_exp2((lim - nl) + (nh - head));
       l *= r;
       lim = nl;
@@ -667,14 +686,21 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
     // ---- P.V
     if (job.y > 0) {
       uint32_t ph[HB][2], pl[HB][2];
+      const float vs = pow2(hs - up);
+      if (up) {  // (P times 2^-up is what fits; other lanes' headers are read after the warp's barrier)
+        const uint32_t m = uint32_t(15 + up) << 10, m2 = type_has_min(c.v_type) ? 0x3C000000u | m : m * 0x10001u;
+#pragma unroll 1
+        for (int i = lane; i < cnt * a.s.vh / 4; i += 32) sts32(st + a.s.vd + 4 * i, hmul2_bits(lds32(st + a.s.vd + 4 * i), m2));
+        __syncwarp();
+      }
 #pragma unroll
       for (int hh = 0; hh < HB; ++hh)
 #pragma unroll
         for (int t = 0; t < 2; ++t) split_h2(p[hh][t][0] * vs, p[hh][t][1] * vs, ph[hh][t], pl[hh][t]);
 #define KVQ_VALUES(VT)                                                                                               \
   case VT:                                                                                                           \
-    _Pragma("unroll") for (int hh = 0; hh < HB; ++hh) body_values<D, VT>(st, a.s, 16 * hh, ph[hh], pl[hh], p[hh], cnt, lane, acc, \
-                                                                          dmin);                                    \
+    _Pragma("unroll") for (int hh = 0; hh < HB; ++hh) body_values<D, VT>(st, a.s, 16 * hh, ph[hh], pl[hh], p[hh], pow2(-up), cnt, lane, \
+                                                                          acc, dmin);                                    \
     break;
       switch (c.v_type) {
         KVQ_VALUES(KVQ_TYPE_Q4_0)

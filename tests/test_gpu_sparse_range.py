@@ -96,3 +96,25 @@ def test_bits_do_not_depend_on_rows_past_the_end(vt, page):
         for name in ("k_qs", "v_qs", "k_d", "v_d"):
             gc.plane(name).view(torch.int16).view(H * ctx, -1)[dead] = word
         assert np.array_equal(_sparse(kvq, torch, gc, q, sel), want), (vt, word)
+
+
+@pytest.mark.parametrize("vt,d,T,scales", [(t, d, T, s) for t, d in zip(TYPES, (64, 128, 192, 256, 320)) for T in (0, 30)
+                                           for s in ((1e-3,) * 8, (1e-4,) * 8, (1e-5,) * 8, (1e-4, 1e-3, 1e-2, 0.1, 1, 10, 1e2, 1e3),
+                                                     (1e5,) * 8, (1e4, 1, 1e-2, 1e-4, 1e-5, 1e-5, 1e-5, 1e-5))])
+def test_body_values_of_every_size(vt, d, T, scales):
+    """Values from fp16's smallest scales to its largest, the same in all blocks, growing and falling along them."""
+    torch = require_gpu()
+    from rotated_bit_kv_kvq_gb300 import kvq
+    rng = np.random.default_rng(44)
+    k, v = rng.standard_normal((2, 1, 512, 2, d)).astype(np.float32)
+    v *= np.repeat(np.float32(scales), 64)[None, :, None, None]
+    gc, oc = _caches(kvq, d, 512, T, "q8_0", vt, k, v, torch)
+    q = rng.standard_normal((1, 6, d)).astype(np.float32)
+    sel = [[[0, 1, 2, 3, 4, 5, 6, 7], [7, 5, 3, -1, 2, 0, -1, 1]]]
+    got, ref = _sparse(kvq, torch, gc, q, sel), so.sparse_decode(oc, q, np.array(sel), 64)
+    if scales[0] == 1e5 and vt in ("q4_1", "q5_1"):
+        # a block's minimum is stored in fp16, down to -65504: of 32 normal values of spread 1e5 one lies below in
+        # all but 0.744^32 of the blocks, so the cache holds -inf and every output is a sum with it
+        assert not np.isfinite(ref).any() and not np.isfinite(got).any()
+        return
+    assert _rel(got, ref) <= BOUND

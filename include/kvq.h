@@ -489,10 +489,12 @@ KVQ_API kvq_status kvq_block_index_update(const kvq_cache* c, const kvq_block_in
  * Of the other blocks those with the highest score are taken, on equal scores
  * the lower ones: the query is rotated like the keys (channels paired at
  * distance 1, 2, 4, ..., then times fp32(1/sqrt(G))), coded in 8 bits (scale sq =
- * max |q'| / 127, code = q' / sq to the nearest, half to even), and score = max
- * over the group's heads of fp32(fp32(dot * sq) * scale), dot the integer product
- * of the codes.  Eight bits for the query as for the means: the score only ranks
- * blocks, and integers make the ranking the same wherever it is computed.  A NaN
+ * max |q'| / 127, code = q' / sq to the nearest, half to even), and score =
+ * fp32(scale * max over the group's heads of fp32(dot * sq)), dot the integer
+ * product of the codes.  Eight bits for the query as for the means: the score only
+ * ranks blocks, and integers make the ranking the same wherever it is computed.
+ * A head whose rotated query holds an infinity or NaN has NaN for dot * sq, which is
+ * below every number in the maximum; a block with nothing but NaN, or with a NaN
  * score ranks last.  Requires n_select in [1, 49152], nblk <= 49152 (take larger
  * blocks for a longer max_ctx) and 4 nblk + (head_dim + 20) * (query heads per KV
  * head, rounded up to 8) <= 216 KB, else KVQ_ERR_UNSUPPORTED.

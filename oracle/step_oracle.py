@@ -122,19 +122,19 @@ def coded_query(q, rot):
             step *= 2
         x = x * np.float32(1 / math.sqrt(g))
     scale = np.abs(x).max() / np.float32(127)
-    if scale == 0:
-        return np.zeros(len(x), np.int64), np.float32(0)
+    if scale == 0 or not np.isfinite(scale):
+        return np.zeros(len(x), np.int64), scale
     return np.rint(x / scale).astype(np.int64), scale
 
 
 def block_scores(q, codes, scales, rot):
     """q [group][d], codes [nblk][d] int8, scales [nblk]: one float32 score per block."""
-    best = np.full(len(codes), -np.inf, np.float32)
+    best = np.full(len(codes), np.nan, np.float32)
     for head in q:
         code, sq = coded_query(head, rot)
         dot = codes.astype(np.int64) @ code
-        best = np.maximum(best, (dot.astype(np.float32) * sq) * scales)
-    return best
+        best = np.fmax(best, dot.astype(np.float32) * sq)  # (a NaN head is left out)
+    return best * scales
 
 
 def select_blocks(q, codes, scales, seq_len, block_tokens, n_first, n_last, n_select, rot):
@@ -148,7 +148,7 @@ def select_blocks(q, codes, scales, seq_len, block_tokens, n_first, n_last, n_se
             s = block_scores(q[b, h * G:(h + 1) * G], codes[b, h, :have], scales[b, h, :have], rot).astype(np.float64)
             always = [j for j in range(have) if j < n_first or j >= have - n_last]
             s[always] = np.inf
-            take = sorted(sorted(range(have), key=lambda j: (-s[j], j))[:n_select])
+            take = sorted(sorted(range(have), key=lambda j: (np.isnan(s[j]), -s[j], j))[:n_select])
             sel[b, h, :len(take)] = take
     return sel
 

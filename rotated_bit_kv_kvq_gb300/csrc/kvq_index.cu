@@ -299,11 +299,11 @@ __global__ void __launch_bounds__(kThreads) select_kernel(SelArgs a) {
 #pragma unroll
       for (int e = 0; e < E; ++e) v[e] = __fmul_rn(v[e], inv_sqrt_group<G>());
     }
-    float mx = 0.0f;
+    uint32_t mx = 0;  // (as integers: a NaN is above every number, and makes the head's scores NaN)
 #pragma unroll
-    for (int e = 0; e < E; ++e) mx = fmaxf(mx, fabsf(v[e]));
-    mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
-    const float sq = __fdiv_rn(mx, 127.0f);
+    for (int e = 0; e < E; ++e) mx = max(mx, __float_as_uint(fabsf(v[e])));
+    mx = __reduce_max_sync(0xffffffffu, mx);
+    const float sq = __fdiv_rn(__uint_as_float(mx), 127.0f);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const int code = sq > 0.0f ? __float2int_rn(__fdiv_rn(v[e], sq)) : 0;
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(SelArgs a) {
   // order of their own that is the query's too
   uint32_t lo = 0xFFFFFFFFu, hi = 0;
   for (; r0 < nb; r0 += step) {
-    float ma = -INFINITY, mb = -INFINITY;
+    float ma = __uint_as_float(0x7FFFFFFFu), mb = ma;  // NaN: fmaxf keeps it only where every head's score is NaN
     for (int h0 = 0; h0 < a.group; h0 += 8) {
       int acc[4] = {0, 0, 0, 0};
 #pragma unroll

@@ -3,13 +3,16 @@
 ``ensure_built()`` compiles every ``csrc/*.cu`` translation unit in parallel
 with nvcc for ``sm_103a`` and links ``_build/libkvq.so`` when any source or
 header is newer than the library.  No other architecture is built.
-``ensure_binding()`` compiles ``csrc/kvq_torch.cpp`` (host code, for the torch
-that is installed) to the extension module ``_build/_kvq_torch.so`` beside it.
+``ensure_binding()`` compiles ``csrc/kvq_torch.cpp`` (host code) to an extension
+module beside it, whose name holds the torch and the Python it was compiled for.
+Processes that build at once wait for one another.
 """
 
 from __future__ import annotations
 
 import concurrent.futures as cf
+import contextlib
+import fcntl
 import glob
 import os
 import shutil
@@ -21,7 +24,6 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libkvq.so")
-BINDING = os.path.join(BUILD, "_kvq_torch.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -64,19 +66,30 @@ def _compile(src: str, verbose_ptxas: bool) -> str:
     return obj
 
 
+@contextlib.contextmanager
+def _building():
+    """One process at a time: the objects and the outputs have fixed names."""
+    os.makedirs(BUILD, exist_ok=True)
+    with open(os.path.join(BUILD, ".lock"), "w") as f:
+        fcntl.flock(f, fcntl.LOCK_EX)  # (let go of when the file is closed)
+        yield
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     """Compile and link the library; returns its path."""
     if not force and not is_stale():
         return LIB
-    os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
-        objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), _sources()))
-    tmp = LIB + ".tmp"
-    r = subprocess.run([nvcc(), *ARCH, "-shared", "-Xlinker", "-soname=libkvq.so", "-o", tmp, *objs],
-                       capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stderr}")
-    os.replace(tmp, LIB)
+    with _building():
+        if not force and not is_stale():  # built while this process waited
+            return LIB
+        with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
+            objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), _sources()))
+        tmp = LIB + ".tmp"
+        r = subprocess.run([nvcc(), *ARCH, "-shared", "-Xlinker", "-soname=libkvq.so", "-o", tmp, *objs],
+                           capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed:\n{r.stderr}")
+        os.replace(tmp, LIB)
     return LIB
 
 
@@ -88,11 +101,24 @@ def _binding_sources():
     return [os.path.join(CSRC, "kvq_torch.cpp"), os.path.join(INCLUDE, "kvq.h"), os.path.abspath(__file__)]
 
 
+def binding_path() -> str:
+    """The extension module for this torch and this Python: neither's interface is stable across versions."""
+    import sysconfig
+
+    import torch
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    return os.path.join(BUILD, f"_kvq_torch-torch{torch.__version__}-cxx11abi{abi}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
+def _binding_is_stale(path: str) -> bool:
+    return not os.path.exists(path) or any(os.path.getmtime(p) > os.path.getmtime(path) for p in _binding_sources())
+
+
 def ensure_binding() -> str:
     """Compile the extension module if a source of it is newer; returns its path.  It finds libkvq.so beside itself."""
-    lib = ensure_built()
-    if os.path.exists(BINDING) and all(os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in _binding_sources()):
-        return BINDING
+    lib, path = ensure_built(), binding_path()
+    if not _binding_is_stale(path):
+        return path
     import sysconfig
 
     import torch
@@ -100,16 +126,19 @@ def ensure_binding() -> str:
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     inc = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(root, "include"),
            os.path.join(root, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include")]
-    tmp = BINDING + ".tmp"
+    tmp = path + ".tmp"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{p}" for p in inc),
            _binding_sources()[0], "-o", tmp, lib, f"-L{os.path.join(root, 'lib')}", "-ltorch_python", "-ltorch_cpu", "-lc10",
            "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{os.path.join(root, 'lib')}"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"{cmd[0]} failed for kvq_torch.cpp:\n{r.stderr}")
-    os.replace(tmp, BINDING)
-    return BINDING
+    with _building():
+        if not _binding_is_stale(path):  # built while this process waited
+            return path
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"{cmd[0]} failed for kvq_torch.cpp:\n{r.stderr}")
+        os.replace(tmp, path)
+    return path
 
 
 if __name__ == "__main__":

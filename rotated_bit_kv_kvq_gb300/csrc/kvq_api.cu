@@ -301,7 +301,7 @@ kvq_status kvq_qk_norm_rope(const kvq_cache* c, const kvq_rope_norm* r, int32_t 
   if (!aligned16(r->q_weight) || !aligned16(r->k_weight) || !aligned4(r->inv_freq)) return KVQ_ERR_INVALID_ARG;
   if (!valid_dtype(dtype) || n_q_heads <= 0 || n_q_heads > (1 << 20)) return KVQ_ERR_INVALID_ARG;
   if (n_rows < 0 || n_dst_rows < 0 || (!dst_row && n_dst_rows < n_rows)) return KVQ_ERR_INVALID_ARG;
-  if (!v != !v_out) return KVQ_ERR_INVALID_ARG;
+  if (n_rows > 0 && !v != !v_out) return KVQ_ERR_INVALID_ARG;  // (an input without rows may have no address)
   const int es = dtype == KVQ_F32 ? 4 : 2;
   const void* in[] = {q, k, v};
   void* out[] = {q_out, k_out, v_out};

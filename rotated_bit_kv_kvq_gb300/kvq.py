@@ -275,6 +275,15 @@ def _expect_plan(what: str, dtypes, *tensors):
                              f"{tuple(t.shape)} of {t.dtype} on {t.device}")
 
 
+def _on_current_device(what: str, device: int):
+    """The memory of a plan, pool or index lies where the call runs: on the current device."""
+    if device >= 0:
+        import torch
+        if device == torch.cuda.current_device():
+            return
+    raise ValueError(f"{what}: made on {'the CPU' if device < 0 else f'CUDA device {device}'}, not on the current CUDA device")
+
+
 class RopeNorm:
     """The plan of kvq_qk_norm_rope: inv_freq fp32 [rot_dim / 2] (None: no rotation), weights [head_dim] or None."""
 
@@ -287,6 +296,7 @@ class RopeNorm:
             raise ValueError("RopeNorm: the weights are vectors of one type and size")
         self.inv_freq, self.q_weight, self.k_weight = inv_freq, q_weight, k_weight  # kept alive
         self.weight_dim = weights[0].numel() if weights else 0
+        self.device = next((t.get_device() for t in (inv_freq, *weights) if t is not None), None)
         self.desc = kvq_rope_norm()
         self.desc.rot_dim = 0 if inv_freq is None else 2 * inv_freq.numel()
         self.desc.interleaved = 1 if interleaved else 0
@@ -299,6 +309,8 @@ class RopeNorm:
 def kvq_qk_norm_rope(cache: kvq_cache, rope: RopeNorm, q, k, v, pos, q_out, k_out, v_out, dst_row=None, stream=None):
     """Rows q [n][heads * d] or [n][heads][d] (any row stride, e.g. parts of one projection), k and v (or None) the same
     with the KV heads; pos int32 [n], dst_row int32 [n] or None.  Outputs [..][heads][d], contiguous, of the same rows."""
+    if rope.device is not None:
+        _on_current_device("RopeNorm", rope.device)
     _check((_native or native()).qk_norm_rope(cache, rope.desc, rope.weight_dim, q, k, v, pos, q_out, k_out, v_out, dst_row,
                                               stream), "kvq_qk_norm_rope")
 
@@ -318,6 +330,7 @@ class PagePool:
         ids = torch.tensor(ids, dtype=torch.int32)
         self.ring[:len(ids)] = ids.to(device)
         self.state = torch.tensor([0, len(ids)], dtype=torch.int32, device=device)
+        self.device = self.ring.get_device()
         self.desc = kvq_page_pool(self.ring.data_ptr(), self.state.data_ptr(), self.state.data_ptr())
 
 
@@ -326,7 +339,10 @@ def kvq_page_update(cache: kvq_cache, pool, n_new, n_new_max: int, granted, row_
     """pool: PagePool or kvq_page_pool; n_new, granted, seq_len_out int32 [batch]; the row maps int32 [max_rows]."""
     pages = 0x7fffffff  # a descriptor of the caller's own: its sizes are theirs
     if isinstance(pool, PagePool):
+        _on_current_device("PagePool", pool.device)
         pool, pages = pool.desc, pool.pages
+    elif not isinstance(pool, kvq_page_pool):
+        raise ValueError("kvq_page_update: pool is a PagePool or a kvq_page_pool")
     _check((_native or native()).page_update(cache, pool, pages, n_new, n_new_max, granted, row_pos, row_dst, row_slot,
                                              seq_len_out, stream), "kvq_page_update")
 
@@ -342,12 +358,16 @@ class BlockIndex:
         self.sizes = (cache.batch, cache.n_kv_heads, cache.max_ctx, cache.head_dim)
         self.codes = torch.zeros(cache.batch, cache.n_kv_heads, nblk, cache.head_dim, dtype=torch.int8, device=device)
         self.scales = torch.zeros(cache.batch, cache.n_kv_heads, nblk, dtype=torch.float32, device=device)
+        self.device = self.codes.get_device()
         self.desc = kvq_block_index(block_tokens, self.codes.data_ptr(), self.scales.data_ptr())
 
 
 def _index_desc(cache, index):
-    if not isinstance(index, BlockIndex):
+    if isinstance(index, kvq_block_index):
         return index
+    if not isinstance(index, BlockIndex):
+        raise ValueError("index is a BlockIndex or a kvq_block_index")
+    _on_current_device("BlockIndex", index.device)
     if index.sizes != (cache.batch, cache.n_kv_heads, cache.max_ctx, cache.head_dim):
         raise ValueError("BlockIndex: made for a cache of other sizes")
     return index.desc

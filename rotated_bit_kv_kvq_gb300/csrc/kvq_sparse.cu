@@ -40,15 +40,14 @@ namespace cg = cooperative_groups;
 constexpr int kTailRows = 8;   // tokens of a tail tile
 constexpr int kMaxStages = 4;
 
-// Weights P = 2^(score - lim + head), lim a reference kLazyMax above the largest score at its last move, are at
-// most 2^head.  P times a V scale goes in as two fp16 parts, with an absolute error of 2^-25 (fp16's smallest
-// step): head is what brings the product with the largest scale met so far to 2^14 .. 2^15, so that small
-// values keep their bits and large ones stay finite.  A warp begins with kHeadMax and lowers head, with its sums,
-// where a tile's scale reaches 2^(16 - head).  P itself is at most 2^15 in fp16: for a larger head (scales
+// Weights p = 2^(score - lim), lim a reference kLazyMax above the largest score at its last move, are at most 1.
+// p times a V scale goes in as two fp16 parts, with an absolute error of 2^-25 (fp16's smallest step), so it is
+// taken times 2^top: top is what brings the product with the largest scale met so far to 2^14 .. 2^15, so that
+// small values keep their bits and large ones stay finite.  A warp begins with kTopMax and lowers top, with its
+// sums, where a tile's scale reaches 2^(16 - top).  p 2^top is at most 2^15 in fp16: where top is larger (scales
 // below 2^-10 only, so that others go without) the missing power of two 2^up goes to the tile's scales, in place.
-// For q8_0 P goes in times 16 and its codes divided by 16 (with their range the product would lose 4 bits).
-constexpr int kHeadMax = 30;
-__device__ __forceinline__ int head_shift(int vt) { return vt == KVQ_TYPE_Q8_0 ? 4 : 0; }
+// q8_0 codes go in divided by 16, 2^4 of top (with their range the product would lose 4 bits).
+constexpr int kTopMax = 30;
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(uint32_t(127 + e) << 23); }
 
 template <int D> constexpr int kRows = D <= 128 ? 32 : 16;               // tokens of a body tile
@@ -237,12 +236,11 @@ __device__ __forceinline__ uint32_t i8_sixteenth(uint32_t r) {
 
 // acc += codes_V^T . (P * scale) of the 16 body rows from row0: rows 2g (acc .. [0], [1]) and 2g + 1 of each
 // 16 channels, columns heads 2tig, 2tig + 1; dmin += the blocks' minima . P (rows blocks g, g + 8; see below).
-// cnt: the tile's tokens; ph, pl: P for scales in units of `unit`, times 16 where the codes are divided by 16
-// (q8_0); p: P of tokens 8t + 2tig + e.
+// cnt: the tile's tokens; ph, pl: P for scales in units of `unit`; p, times ps: P of tokens 8t + 2tig + e.
 template <int D, int VT>
 __device__ __forceinline__ void body_values(uint32_t st, const SpStage& L, int row0, const uint32_t (&ph)[2],
-                                            const uint32_t (&pl)[2], const float (&p)[2][2], float unit, int cnt,
-                                            int lane, float (&acc)[D / 32][2][4], float (&dmin)[4]) {
+                                            const uint32_t (&pl)[2], const float (&p)[2][2], float ps, float unit,
+                                            int cnt, int lane, float (&acc)[D / 32][2][4], float (&dmin)[4]) {
   constexpr int NB = D / 32, RB = kRows<D>, ROW = VT == KVQ_TYPE_Q8_0 ? D : D / 2, W = box_w(ROW);
   constexpr bool V1 = type_has_min(VT), V5 = type_has_qh(VT);
   constexpr int VHH = V1 ? 2 : 1;
@@ -278,7 +276,7 @@ __device__ __forceinline__ void body_values(uint32_t st, const SpStage& L, int r
   if constexpr (V1) {
     // minimum + centre * scale of block blk at token i of the lane's four, in fp32 (fp16 may overflow), as tf32 high and
     // low parts.  Up to 8 blocks their low parts take the rows g + 8; the merge adds them.  16 x 8 rows of 2048 tokens,
-    // head_dim 128, q4_1: 29.9 us, 28.8 with the sum in fp16.
+    // head_dim 128, q4_1: 29.6 us, 28.8 with the sum in fp16.
     const float centre = float(code_centre(VT)) * unit;
     auto minimum = [&](int blk, int i, uint32_t& hi, uint32_t& lo) {
       uint32_t w = lds32(vd + ((i & 1) + 8 * (i >> 1)) * HP + (NB % 8 == 0 || blk < NB ? blk : NB - 1) * 4);
@@ -297,7 +295,7 @@ __device__ __forceinline__ void body_values(uint32_t st, const SpStage& L, int r
           minimum(g, 2 * t + e, a[2 * e], c[2 * e]);
           minimum(g + 8, 2 * t + e, a[2 * e + 1], c[2 * e + 1]);
         }
-        split_tf32(p[t][e], bh[e], bl[e]);
+        split_tf32(p[t][e] * ps, bh[e], bl[e]);
       }
       mma1688_tf32(dmin, a[0], a[1], a[2], a[3], bh[0], bh[1]);
       mma1688_tf32(dmin, a[0], a[1], a[2], a[3], bl[0], bl[1]);
@@ -580,10 +578,8 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
       for (int r = 0; r < 4; ++r) acc[i][j][r] = 0.0f;
   float dmin[4] = {0.f, 0.f, 0.f, 0.f};
   float lim = -INFINITY, l = 0.0f;
-  const int hs = head_shift(c.v_type);
-  float head = float(kHeadMax - hs);
-  int up = kHeadMax - 15;
-  uint32_t big = uint32_t(31 - kHeadMax) << 10;  // 2^(16 - hs - head) in fp16; infinity with the smallest head
+  const int cs = c.v_type == KVQ_TYPE_Q8_0 ? 4 : 0;  // what of top the codes take
+  int top = kTopMax;
   const uint32_t hmask = type_has_min(c.v_type) ? 0x00007FFFu : 0x7FFF7FFFu;
   bool timed_out = false;
   int k = 0;
@@ -646,25 +642,24 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
     if (job.y > 0) {
 #pragma unroll 1  // (a warp has few tiles: code that is fetched once counts; unrolled the call takes 5% longer)
       for (int i = lane; i < cnt * a.s.vh / 4; i += 32) mxs = __vmaxu2(mxs, lds32(st + a.s.vd + 4 * i) & hmask);
+      const uint32_t big = uint32_t(31 - top) << 10;  // 2^(16 - top) in fp16; infinity with top 0
       down = __any_sync(0xffffffffu, (mxs & 0xFFFFu) >= big || (mxs >> 16) >= big);
     }
     if (__any_sync(0xffffffffu, mx > lim) || down) {
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      float nh = head;
-      if (down) {  // the largest scale lies in [2^(e - 15), 2^(e - 14)): weights up to 2^(29 - e), half of what has room
+      int nt = top;
+      if (down) {  // the largest scale lies in [2^(e - 15), 2^(e - 14)): half of what has room
         const int e = int(__reduce_max_sync(0xffffffffu, max(mxs & 0xFFFFu, mxs >> 16)) >> 10);
-        int t = max(29 - e, 0);
-        if (e >= 5) t = min(t, 15);
-        big = uint32_t(31 - t) << 10;
-        up = max(t - 15, 0);
-        nh = float(t - hs);
+        nt = max(29 - e, 0);
+        if (e >= 5) nt = min(nt, 15);
       }
       const float nl = mx > lim ? mx + kLazyMax : lim;
-      const float r = lim == -INFINITY ? 0.0f : fast_exp2((lim - nl) + (nh - head));
+      float r = lim == -INFINITY ? 0.0f : fast_exp2(lim - nl);
       l *= r;
+      r *= pow2(nt - top);
       lim = nl;
-      head = nh;
+      top = nt;
       const float r0 = __shfl_sync(0xffffffffu, r, 8 * tig), r1 = __shfl_sync(0xffffffffu, r, 8 * tig + 4);
 #pragma unroll
       for (int i = 0; i < NB; ++i)
@@ -672,7 +667,7 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
         for (int j = 0; j < 2; ++j) { acc[i][j][0] *= r0; acc[i][j][1] *= r1; acc[i][j][2] *= r0; acc[i][j][3] *= r1; }
       dmin[0] *= r0; dmin[1] *= r1; dmin[2] *= r0; dmin[3] *= r1;
     }
-    const float ms = lim == -INFINITY ? 0.0f : lim - head;
+    const float ms = lim == -INFINITY ? 0.0f : lim;
     float p[HB][2][2];
 #pragma unroll
     for (int hh = 0; hh < HB; ++hh)
@@ -686,8 +681,9 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
     // ---- P.V
     if (job.y > 0) {
       uint32_t ph[HB][2], pl[HB][2];
-      const float vs = pow2(hs - up);
-      if (up) {  // (P times 2^-up is what fits; other lanes' headers are read after the warp's barrier)
+      const int up = max(top - 15, 0);
+      const float vs = pow2(top - up);
+      if (up) {  // (other lanes' headers are read after the warp's barrier)
         const uint32_t m = uint32_t(15 + up) << 10, m2 = type_has_min(c.v_type) ? 0x3C000000u | m : m * 0x10001u;
 #pragma unroll 1
         for (int i = lane; i < cnt * a.s.vh / 4; i += 32) sts32(st + a.s.vd + 4 * i, hmul2_bits(lds32(st + a.s.vd + 4 * i), m2));
@@ -699,7 +695,7 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
         for (int t = 0; t < 2; ++t) split_h2(p[hh][t][0] * vs, p[hh][t][1] * vs, ph[hh][t], pl[hh][t]);
 #define KVQ_VALUES(VT)                                                                                               \
   case VT:                                                                                                           \
-    _Pragma("unroll") for (int hh = 0; hh < HB; ++hh) body_values<D, VT>(st, a.s, 16 * hh, ph[hh], pl[hh], p[hh], pow2(-up), cnt, lane, \
+    _Pragma("unroll") for (int hh = 0; hh < HB; ++hh) body_values<D, VT>(st, a.s, 16 * hh, ph[hh], pl[hh], p[hh], pow2(top), pow2(-up), cnt, lane, \
                                                                           acc, dmin);                                    \
     break;
       switch (c.v_type) {
@@ -711,7 +707,8 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
       }
 #undef KVQ_VALUES
     } else {
-      float r0 = p[0][0][0], r1 = p[0][0][1];
+      const float ps = pow2(top - cs);
+      float r0 = p[0][0][0] * ps, r1 = p[0][0][1] * ps;
       const uint32_t p1 = take_bf2(r0, r1), p2 = take_bf2(r0, r1), p3 = pack_bf2(r0, r1);
       // tokens 2tig and 2tig + 1, channels 2g, 2g + 1; 16 channels further 32 bytes, swizzled.  Rows past the
       // end hold anything: masked
@@ -742,9 +739,18 @@ sparse_kernel(SpArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_co
   l += __shfl_xor_sync(0xffffffffu, l, 1);
   l += __shfl_xor_sync(0xffffffffu, l, 2);
   if (tig == 0) {
-    s_m[warp * kMaxHeads + g] = lim == -INFINITY ? -INFINITY : lim - head;
+    s_m[warp * kMaxHeads + g] = lim;
     s_l[warp * kMaxHeads + g] = l;
   }
+  const float unscale = pow2(cs - top);
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[i][j][r] *= unscale;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) dmin[r] *= unscale;
   __syncthreads();  // the stages are free
   float* macc = reinterpret_cast<float*>(smem);  // [kWarps][8][D]
 #pragma unroll

@@ -34,10 +34,13 @@ inline long long body_row_count(const kvq_cache& c) {
                        : (long long)c.batch * c.n_kv_heads * c.max_ctx;
 }
 
+// The tables below may throw (no memory for an entry), which a C entry point must not: their
+// users return an error, or do without the table.
+
 // Raises a kernel's dynamic shared-memory limit once per device (again only for
 // a larger size), so that steady-state calls make no attribute call and can be
 // captured into a CUDA graph.
-inline cudaError_t ensure_dynamic_smem(const void* kernel, int bytes) {
+inline cudaError_t ensure_dynamic_smem(const void* kernel, int bytes) try {
   constexpr int kMaxDevices = 64;
   static std::mutex mu;
   static std::unordered_map<const void*, int[kMaxDevices]> done;
@@ -51,10 +54,12 @@ inline cudaError_t ensure_dynamic_smem(const void* kernel, int bytes) {
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess) have = bytes;
   return e;
+} catch (...) {
+  return cudaErrorMemoryAllocation;
 }
 
 // Allows a kernel clusters of more than 8 CTAs, once per device.
-inline cudaError_t allow_large_clusters(const void* kernel) {
+inline cudaError_t allow_large_clusters(const void* kernel) try {
   constexpr int kMaxDevices = 64;
   static std::mutex mu;
   static std::unordered_map<const void*, bool[kMaxDevices]> done;
@@ -66,6 +71,8 @@ inline cudaError_t allow_large_clusters(const void* kernel) {
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess && dev >= 0 && dev < kMaxDevices) done[kernel][dev] = true;
   return e;
+} catch (...) {
+  return cudaErrorMemoryAllocation;
 }
 
 // Launches a kernel as a programmatic dependent of what runs before it on the stream, in clusters
@@ -93,12 +100,12 @@ inline cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads
 
 // How many clusters of k CTAs of a kernel the device runs at once (a cluster stays within a
 // group of SMs, and the groups differ in size), for k = 2 .. kMaxCluster; asked once per kernel,
-// shared-memory size and device.  NULL when the query fails.
+// shared-memory size and device.  NULL when the query fails or there is no memory for the answer.
 constexpr int kMaxCluster = 16;
 struct ClusterLimits {
   int clusters[kMaxCluster + 1];
 };
-inline const ClusterLimits* cluster_limits(const void* kernel, int threads, int smem) {
+inline const ClusterLimits* cluster_limits(const void* kernel, int threads, int smem) try {
   static std::mutex mu;
   static std::map<std::tuple<const void*, int, int>, ClusterLimits> known;  // (a map's values never move)
   int dev = 0;
@@ -125,6 +132,8 @@ inline const ClusterLimits* cluster_limits(const void* kernel, int threads, int 
     }
   }
   return &known.emplace(key, lim).first->second;
+} catch (...) {
+  return nullptr;
 }
 
 // Launchers (arguments already validated by the API layer).

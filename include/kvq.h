@@ -259,6 +259,10 @@ KVQ_API size_t kvq_decode_workspace_bytes(const kvq_cache* c, int32_t n_q_heads)
  * when V rotation is on.  A sequence with n == 0 yields zeros.
  * n_q_heads must be a multiple of n_kv_heads.  workspace: device memory of at
  * least kvq_decode_workspace_bytes(c, n_q_heads) bytes, 16-byte aligned.
+ * The products' operands are fp16 parts with absolute steps: tail rows below 2^-6 in
+ * magnitude enter as multiples of 2^-16, and a weight (at most 1) times a body block's
+ * scale is held to 2^-25.  Values that are all far below 1e-2 lose relative precision
+ * by that; kvq_sparse_decode_attention over every block keeps it.
  */
 KVQ_API kvq_status kvq_decode_attention(const kvq_cache* c, const void* q, int32_t q_dtype,
                                 int32_t n_q_heads, float scale, void* out, int32_t out_dtype,
@@ -386,10 +390,10 @@ typedef struct kvq_rope_norm {
  * Per head: y = x * 1/sqrt(mean(x^2) + eps) * weight (queries and keys with a
  * weight only), then every pair (a, b) of the rotated channels becomes (a cos t
  * - b sin t, a sin t + b cos t), t = pos * inv_freq[pair]; values are copied.
- * All of it in fp32 -- the angle modulo one turn is exact to 2^-31 turns at
- * every position, for |inv_freq| <= 1 (to 2^(k - 31) up to 2^k) -- and rounded
- * once, to nearest even.  Rows of the outputs that no
- * row goes to keep what they held.  An output may be its own input (same
+ * All of it in fp32 -- the angle modulo one turn is taken in 64-bit integers and
+ * rounded to fp32 once: it is within 2^-26 turns at every position, for |inv_freq|
+ * <= 1 (2^-26 + 2^(k - 31) up to 2^k) -- and rounded once, to nearest even.  Rows of
+ * the outputs that no row goes to keep what they held.  An output may be its own input (same
  * pointer, stride heads * head_dim, dst_row NULL); no other overlap is allowed.
  * n_rows 0 is a no-op.  Of the cache only head_dim, n_kv_heads and status are
  * used; head_dim: every multiple of 32 up to 512.
@@ -435,7 +439,8 @@ typedef struct kvq_page_pool {
  *   seq_len_out  device int32 [batch] or NULL: the lengths with released
  *              sequences at 0 (may be c->seq_len itself, which is what a
  *              serving loop wants).  Granted tokens are not added: the append
- *              does that.
+ *              does that, and it has to run before the next call, which counts a
+ *              sequence's pages by its length.
  * A state outside its ranges sets KVQ_DEV_ERR_PAGE; nothing is granted or
  * released then, and `next` gets the state as it was.  Free and released pages
  * that together pass n_pages set it too, and the released ones are lost, as does
@@ -469,7 +474,7 @@ typedef struct kvq_block_index {
  * For a block's tokens below seq_len[b], x_t = the dequantized rotated key of
  * the body (which holds every token, those of the bf16 tail too): mean m = (sum
  * of x_t) / count, scale = max |m| / 127, code = m / scale rounded to the nearest,
- * half to even (all codes 0 with a scale of 0), in fp32 with this order of
+ * half to even (all codes 0 with a scale of 0, infinity or NaN), in fp32 with this order of
  * sums, so that the codes are the same wherever they are computed: token t of the
  * block is added to partial sum t % 8 in token order; then s0+s1, s2+s3, s4+s5,
  * s6+s7; (s0+s1)+(s2+s3), ...; the last two.  Blocks that hold no token keep what
@@ -512,7 +517,8 @@ KVQ_API kvq_status kvq_select_blocks(const kvq_cache* c, const kvq_block_index* 
  *             or paged, positions of the last tail_len tokens from the bf16 tail)
  * A (sequence, KV head) with no listed token yields zeros.  No workspace: calls
  * that only read a cache may run at the same time.  The first call for a
- * head_dim asks the device for its limits; make it before a stream capture.
+ * head_dim, format pair and tail (on or off) asks the device for its limits; make it
+ * before a stream capture.
  * Body planes of 2^31 rows or more (and as many tail rows) give
  * KVQ_ERR_UNSUPPORTED.  The arithmetic keeps fp32's precision relative to the
  * largest values of a row's tokens, over all that the body formats hold; tail rows

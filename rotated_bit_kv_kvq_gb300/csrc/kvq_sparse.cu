@@ -19,11 +19,12 @@
 // some times larger than their result, and fp32 outputs were 1.4e-6 off instead of 1.5e-7.  The
 // scale + minimum formats are centred too: code - c with the minimum + c * scale.
 //
-// Bound by the instruction stream: about 650 warp instructions per 16 tokens of head_dim 128 in
-// q5_0 (the 5-bit codes' conversion takes 250 of them).  32 sequences x 8 KV heads x up to 2048
-// tokens, q5_0 / q5_0: 53.0 us (92 MB: 13.8 us at the card's measured copy rate); 4 x 4 x 8192 tokens
-// of head_dim 256, q8_0 / q4_0, paged: 37.6 us (55 MB, 8.2 us), where the chain of 8 warps an
-// SM and a call's fixed part (first tiles 5 us, merge 4 us) weigh; the smallest call 6.0 us.
+// Bound by the instruction stream, about 630 warp instructions per 16 tokens of head_dim 128 in
+// q5_0 (the 5-bit codes' conversion takes 250 of them), and with many rows by their division: a row
+// is one CTA then, so that some SMs have two and others one, and short rows leave theirs early.  32
+// sequences x 8 KV heads x up to 2048 tokens, q5_0 / q5_0: 52.0 us (92 MB: 13.8 us at the card's measured
+// copy rate); 4 x 4 x 8192 tokens of head_dim 256, q8_0 / q4_0, paged: 37.5 us (55 MB, 8.2 us), where the
+// chain of 8 warps an SM and a call's fixed part (first tiles 5 us, merge 4 us) weigh; the smallest call 6.1 us.
 
 #include <cooperative_groups.h>
 #include <string.h>

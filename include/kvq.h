@@ -259,10 +259,11 @@ KVQ_API size_t kvq_decode_workspace_bytes(const kvq_cache* c, int32_t n_q_heads)
  * when V rotation is on.  A sequence with n == 0 yields zeros.
  * n_q_heads must be a multiple of n_kv_heads.  workspace: device memory of at
  * least kvq_decode_workspace_bytes(c, n_q_heads) bytes, 16-byte aligned.
- * The products' operands are fp16 parts with absolute steps: tail rows below 2^-6 in
- * magnitude enter as multiples of 2^-16, and a weight (at most 1) times a body block's
- * scale is held to 2^-25.  Values that are all far below 1e-2 lose relative precision
- * by that; kvq_sparse_decode_attention over every block keeps it.
+ * The products' operands are fp16 parts with absolute steps: the scaled query, and a
+ * weight (at most 1) times a body block's scale, are held to 2^-25, and tail rows below
+ * 2^-6 in magnitude enter as multiples of 2^-16.  Values that are all far below 1e-2
+ * lose relative precision by that (kvq_prefill_attention holds keys and values to 2^-17);
+ * kvq_sparse_decode_attention over every block keeps it.
  */
 KVQ_API kvq_status kvq_decode_attention(const kvq_cache* c, const void* q, int32_t q_dtype,
                                 int32_t n_q_heads, float scale, void* out, int32_t out_dtype,

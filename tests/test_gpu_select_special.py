@@ -58,3 +58,29 @@ def test_scores_that_are_not_numbers(kind, rot, nblk):
         assert got == list(range(nsel - 1)) + [nblk - 1]
     elif kind in ("nan scales", "inf scales of zero codes"):
         assert got[-20:] == list(range(nblk - 20, nblk))
+
+
+@pytest.mark.parametrize("kt", ["q4_0", "q5_0", "q8_0", "q4_1", "q5_1"])
+def test_blocks_of_keys_that_are_not_numbers(kt):
+    """A key scale that is infinite or NaN: its block's codes are zeros, its scale is no finite number, it ranks last."""
+    torch = require_gpu()
+    from rotated_bit_kv_kvq_gb300 import kvq
+    d, nblk = 64, 12
+    gc = kvq.KVCache(1, 1, d, nblk * 64, 0, kt, "q4_0")
+    gen = torch.Generator(device="cuda").manual_seed(52)
+    k = torch.randn(1, nblk * 64, 1, d, device="cuda", generator=gen)
+    kvq.kvq_rotate_quantize_append(gc.desc, k, k)
+    x = kvq.BlockIndex(gc.desc, 64)
+    kvq.kvq_block_index_update(gc.desc, x)
+    before = x.codes.clone(), x.scales.clone()
+    heads = gc.plane("k_d").view(torch.int16).view(nblk * 64, -1)
+    heads[3 * 64 + 5, 0] = 0x7C00   # infinity
+    heads[7 * 64 + 60, 0] = 0x7E00  # NaN
+    kvq.kvq_block_index_update(gc.desc, x)
+    bad = torch.tensor([3, 7], device="cuda")
+    good = torch.tensor([j for j in range(nblk) if j not in (3, 7)], device="cuda")
+    assert not x.codes[0, 0, bad].any() and not torch.isfinite(x.scales[0, 0, bad]).any()
+    assert torch.equal(x.codes[0, 0, good], before[0][0, 0, good]) and torch.equal(x.scales[0, 0, good], before[1][0, 0, good])
+    sel = torch.empty(1, 1, nblk - 2, dtype=torch.int32, device="cuda")
+    kvq.kvq_select_blocks(gc.desc, x, torch.randn(1, 2, d, device="cuda", generator=gen), sel, n_first=0, n_last=0)
+    assert sel[0, 0].tolist() == good.tolist()

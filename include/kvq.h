@@ -118,7 +118,8 @@ typedef int32_t kvq_status;
 #define KVQ_DEV_ERR_PAGE          8u  /* a page_table entry lies outside [0, n_pages) (paged layout)        */
 #define KVQ_DEV_ERR_OUTLIER      16u  /* an outlier_idx row is not strictly increasing inside [0, head_dim) */
 #define KVQ_DEV_ERR_NO_ROOM      32u  /* kvq_page_update: no free page or no row left for a sequence's tokens */
-#define KVQ_DEV_ERR_ROW          64u  /* kvq_qk_norm_rope: dst_row at or past n_dst_rows                       */
+#define KVQ_DEV_ERR_ROW          64u  /* kvq_qk_norm_rope: dst_row at or past n_dst_rows; kvq_chunk_attention: row_start */
+#define KVQ_DEV_ERR_FORK        128u  /* kvq_page_fork: a fork's sequences or its number of tokens               */
 
 /*
  * The cache descriptor.  Body planes hold the packed payload of every block:
@@ -453,6 +454,127 @@ typedef struct kvq_page_pool {
 KVQ_API kvq_status kvq_page_update(const kvq_cache* c, const kvq_page_pool* pool, const int32_t* n_new,
                                    int32_t n_new_max, int32_t* granted, int32_t max_rows, int32_t* row_pos,
                                    int32_t* row_dst, int32_t* row_slot, int32_t* seq_len_out, void* stream);
+
+/*
+ * Pages that several sequences hold: a sequence begins with the tokens of another
+ * one (kvq_page_fork), gives its pages back (kvq_page_free), and the pages in use
+ * move together (kvq_page_compact).  Library addition beside kvq_page_update, for
+ * samples, beams and requests with a prompt in common.  Only full pages are shared:
+ * a sequence appends to pages that it holds alone.
+ */
+typedef struct kvq_page_share {
+  const int32_t* count;  /* device [n_pages]: of each page, the sequences that hold it beyond the first */
+  int32_t* next;         /* device [n_pages]: the counts after the call (may be `count` itself)        */
+} kvq_page_share;
+/*
+ * All counts are 0 at first, and those of the pages that kvq_page_update hands out
+ * are.  A sequence that holds a shared page is released by kvq_page_free, not by
+ * KVQ_PAGE_RELEASE.  All three calls require the paged layout; their pool is that
+ * of kvq_page_update, and next may be its state itself.  Calls that touch the same
+ * pool, counts or table must be ordered on one stream.  No array may overlap
+ * another but as said.
+ *
+ * Sequence dst[i] begins with the first n tokens of sequence src[i], for each i.
+ *   src, dst   device int32 [n_forks]
+ *   n_tokens   device int32 [n_forks] or NULL: how many (NULL: all of them)
+ *   granted    device int32 [n_forks]: the tokens that dst[i] now has, or -1
+ *   seq_len_out  device int32 [batch]: the lengths after the call (may be
+ *              c->seq_len itself)
+ * The n / page_tokens full pages are shared: their table entries copied, their
+ * counts raised by one.  A last page that is not full is copied, with all that it
+ * holds, to the next free page of the ring; forks take theirs in order, and those
+ * that find none get -1 and set KVQ_DEV_ERR_NO_ROOM.  The bf16 tail rows of
+ * positions [n - tail_len, n) are copied; where the source's tail holds later
+ * positions already (n below its length), a row is the stored value of the body
+ * (code * d, plus the minimum, in fp32) rounded to bf16.  A sequence outside the
+ * batch, dst[i] == src[i], a dst that has tokens or is named twice (all its forks),
+ * and n outside [0, seq_len] give -1 and set KVQ_DEV_ERR_FORK.  Lengths are those
+ * before the call.  A page id outside the pool sets KVQ_DEV_ERR_PAGE, as does a
+ * state outside its ranges (all forks get -1 then).  With outlier channels
+ * tail_len must be 0 (else KVQ_ERR_UNSUPPORTED).  n_forks 0 is refused with
+ * seq_len_out or counts elsewhere, else a no-op.
+ */
+KVQ_API kvq_status kvq_page_fork(const kvq_cache* c, const kvq_page_pool* pool, const kvq_page_share* share,
+                                 const int32_t* src, const int32_t* dst, const int32_t* n_tokens, int32_t n_forks,
+                                 int32_t* granted, int32_t* seq_len_out, void* stream);
+/*
+ * Sequences give their pages back.
+ *   release    device int32 [batch]: not 0 for those that do
+ *   seq_len_out  device int32 [batch] or NULL: the lengths with released
+ *              sequences at 0 (may be c->seq_len itself)
+ * Each of a released sequence's pages loses one holder; those that lose their last
+ * one go into the ring behind the free ones, in ascending order, with a count of 0.
+ * A released row of the table keeps its entries, which mean nothing.  A page that is
+ * given back more often than it is held, more pages than the ring has room for (the
+ * rest is lost) and a page id outside the pool set KVQ_DEV_ERR_PAGE, as does a state
+ * outside its ranges (nothing is released then); a length outside [0, max_ctx]
+ * sets KVQ_DEV_ERR_APPEND_RANGE and that sequence keeps what it has.
+ */
+KVQ_API kvq_status kvq_page_free(const kvq_cache* c, const kvq_page_pool* pool, const kvq_page_share* share,
+                                 const int32_t* release, int32_t* seq_len_out, void* stream);
+/*
+ * Moves pages so that those in use have the lowest ids: of the pages in use (in a
+ * sequence's table, below its length) and the free ones (in the ring), together
+ * the lowest as many as are in use.  Pages that are neither stay where they are.
+ *   table_out  device int32 [batch][max_ctx / page_tokens]: the table afterwards
+ *              (may be c->page_table itself); entries past a sequence's pages as before
+ *   ring_out   device int32 [n_pages] (may be pool->ring): the free pages in
+ *              ascending order, then -1; the state after the call is (0, their number)
+ *   page_map   device int32 [n_pages] or NULL: where each page is afterwards (itself
+ *              where it did not move), for tables of the caller's own
+ *   share      NULL where no page is shared
+ * The i-th page that moves, in ascending order, goes to the i-th free place; its
+ * count goes with it.  The planes' rows of the places it leaves keep what they
+ * held.  A page both in use and free, one twice in the ring, a page id outside the
+ * pool, a length outside [0, max_ctx] or a state outside its ranges set
+ * KVQ_DEV_ERR_PAGE, and nothing moves.  workspace: device memory, 16-byte aligned.
+ */
+KVQ_API size_t kvq_page_compact_workspace_bytes(const kvq_cache* c);
+KVQ_API kvq_status kvq_page_compact(const kvq_cache* c, const kvq_page_pool* pool, const kvq_page_share* share,
+                                    int32_t* table_out, int32_t* ring_out, int32_t* page_map, void* workspace,
+                                    size_t ws_bytes, void* stream);
+
+/*
+ * Attention of packed rows of new tokens over the cache, after their keys and values
+ * have been appended: any number of rows per sequence, from none (a sequence that
+ * rests) and one (a decode step) to a whole prompt.  Library addition beside
+ * kvq_decode_attention and kvq_prefill_attention: every head_dim of the decode
+ * (64, 128, 192, 256, 320), every K / V format pair, contiguous or paged, no staging
+ * of the cache, and scores that are capped, biased or masked:
+ */
+typedef struct kvq_score_mod {
+  float softcap;              /* > 0: s becomes softcap * tanh(s / softcap); 0: it stays (>= 0, finite)    */
+  const float* slopes;        /* device fp32 [n_q_heads] or NULL: then s -= slopes[head] * |position - t| */
+  const int32_t* first_key;   /* device int32 [n_rows] or NULL: row r sees no key t < first_key[r] (a
+                                 document's beginning, for example)                                       */
+  const int32_t* prefix_len;  /* device int32 [batch] or NULL: keys t < prefix_len[b] are seen by every row
+                                 of sequence b, earlier and later ones alike                              */
+} kvq_score_mod;
+/*
+ *   q          device [n_rows][n_q_heads][head_dim] of q_dtype (unrotated)
+ *   row_start  device int32 [batch + 1]: rows row_start[b] .. row_start[b + 1] - 1 are
+ *              the last tokens of sequence b, in order: with m of them, row i has
+ *              position seq_len[b] - m + i.  Not ascending, or outside [0, n_rows]:
+ *              KVQ_DEV_ERR_ROW is set and nothing is written.  More rows than the
+ *              sequence has tokens: KVQ_DEV_ERR_PREFILL_RANGE, and those with a
+ *              negative position are zeros.
+ *   mod        host struct or NULL: no cap, bias or further mask
+ *   scale      softmax scale, before cap and bias; 0 means 1/sqrt(head_dim)
+ *   out        device [n_rows][n_q_heads][head_dim] of out_dtype (original basis).
+ *              Rows before row_start[0] and from row_start[batch] on keep what they held.
+ * A row at position p sees the keys t < seq_len[b] with t >= first_key and t <= p or t <
+ * prefix_len; one that sees none is zeros.  Body / tail selection, rotation and
+ * query heads are as in kvq_decode_attention.  A key whose stored key or value holds
+ * an infinity or NaN makes NaN of the rows that see it, and does not touch others.
+ * workspace: device memory, 16-byte aligned, kvq_chunk_workspace_bytes bytes, not
+ * shared with a call that runs at the same time.  n_rows 0 is a no-op.  n_rows *
+ * n_q_heads must stay below 2^31, body planes and tails below 2^31 rows, and there
+ * are no outlier channels, else KVQ_ERR_UNSUPPORTED.
+ */
+KVQ_API size_t kvq_chunk_workspace_bytes(const kvq_cache* c, int32_t n_q_heads, int32_t n_rows);
+KVQ_API kvq_status kvq_chunk_attention(const kvq_cache* c, const kvq_score_mod* mod, const void* q, int32_t q_dtype,
+                                       int32_t n_q_heads, int32_t n_rows, const int32_t* row_start, float scale, void* out,
+                                       int32_t out_dtype, void* workspace, size_t ws_bytes, void* stream);
 
 /*
  * Sparse attention over blocks of a sequence: an index holds the mean key of

@@ -114,6 +114,33 @@ kvq_status check_index(const kvq_cache* c, const kvq_block_index* x) {
   return sparse_supported(c) ? KVQ_OK : KVQ_ERR_UNSUPPORTED;
 }
 
+// What the calls on shared pages have in common: the descriptor's sizes, table and pool (planes: those that move too).
+kvq_status check_share(const kvq_cache* c, const kvq_page_pool* pool, const kvq_page_share* share, bool planes) {
+  if (!shape_ok(c) || !pool || !c->page_tokens) return KVQ_ERR_INVALID_ARG;
+  if (planes) {
+    const kvq_status s = check_cache(c);
+    if (s != KVQ_OK) return s;
+  }
+  if (!c->seq_len || !c->status || !c->page_table || !aligned16(c->seq_len) || !aligned16(c->status) ||
+      !aligned4(c->page_table))
+    return KVQ_ERR_INVALID_ARG;
+  const void* must[] = {pool->ring, pool->state, pool->next};
+  for (const void* p : must)
+    if (!p || !aligned4(p)) return KVQ_ERR_INVALID_ARG;
+  if (share && (!share->count || !share->next || !aligned4(share->count) || !aligned4(share->next))) return KVQ_ERR_INVALID_ARG;
+  return KVQ_OK;
+}
+size_t compact_workspace(const kvq_cache* c) { return (size_t(c->n_pages) * 4 + 1) * sizeof(int32_t); }
+
+bool chunk_shape_ok(const kvq_cache* c, int n_q_heads, int n_rows) {
+  return n_q_heads > 0 && n_q_heads % c->n_kv_heads == 0 && n_rows >= 0;
+}
+// the decode's head dims without outlier channels; rows of planes and of work are 32-bit numbers
+bool chunk_supported(const kvq_cache* c, int n_q_heads, int n_rows) {
+  return sparse_supported(c) && kvq::body_row_count(*c) <= 0x7fffffffLL &&
+         (long long)c->batch * c->n_kv_heads * c->tail_len <= 0x7fffffffLL && (long long)n_rows * n_q_heads <= 0x7fffffffLL;
+}
+
 kvq_status from_cuda(cudaError_t e) { return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA; }
 
 int sm_count() { return kvq::device_sm_count(); }
@@ -348,6 +375,79 @@ kvq_status kvq_page_update(const kvq_cache* c, const kvq_page_pool* pool, const 
   a.n_new = n_new; a.n_new_max = n_new_max; a.max_rows = max_rows;
   a.granted = granted; a.row_pos = row_pos; a.row_dst = row_dst; a.row_slot = row_slot; a.seq_len_out = seq_len_out;
   return from_cuda(kvq::launch_page_update(a, static_cast<cudaStream_t>(stream)));
+}
+
+kvq_status kvq_page_fork(const kvq_cache* c, const kvq_page_pool* pool, const kvq_page_share* share, const int32_t* src,
+                         const int32_t* dst, const int32_t* n_tokens, int32_t n_forks, int32_t* granted,
+                         int32_t* seq_len_out, void* stream) {
+  const kvq_status s = check_share(c, pool, share, true);
+  if (s != KVQ_OK) return s;
+  if (!share || n_forks < 0 || !seq_len_out || !aligned4(seq_len_out)) return KVQ_ERR_INVALID_ARG;
+  if (n_forks == 0) {  // nothing to do, unless results go elsewhere
+    const bool in_place = pool->next == pool->state && share->next == share->count && seq_len_out == c->seq_len;
+    return in_place ? KVQ_OK : KVQ_ERR_INVALID_ARG;
+  }
+  if (!src || !dst || !granted || !aligned4(src) || !aligned4(dst) || !aligned4(n_tokens) || !aligned4(granted))
+    return KVQ_ERR_INVALID_ARG;
+  if (c->n_outlier && c->tail_len) return KVQ_ERR_UNSUPPORTED;
+  kvq::ForkArgs f{};
+  f.src = src; f.dst = dst; f.n_tokens = n_tokens; f.n_forks = n_forks; f.granted = granted; f.seq_len_out = seq_len_out;
+  return from_cuda(kvq::launch_page_fork(*c, *pool, *share, f, static_cast<cudaStream_t>(stream)));
+}
+
+kvq_status kvq_page_free(const kvq_cache* c, const kvq_page_pool* pool, const kvq_page_share* share, const int32_t* release,
+                         int32_t* seq_len_out, void* stream) {
+  const kvq_status s = check_share(c, pool, share, false);
+  if (s != KVQ_OK) return s;
+  if (!share || !release || !aligned4(release) || !aligned4(seq_len_out)) return KVQ_ERR_INVALID_ARG;
+  return from_cuda(kvq::launch_page_free(*c, *pool, *share, release, seq_len_out, static_cast<cudaStream_t>(stream)));
+}
+
+size_t kvq_page_compact_workspace_bytes(const kvq_cache* c) {
+  return shape_ok(c) && c->page_tokens ? compact_workspace(c) : 0;
+}
+
+kvq_status kvq_page_compact(const kvq_cache* c, const kvq_page_pool* pool, const kvq_page_share* share, int32_t* table_out,
+                            int32_t* ring_out, int32_t* page_map, void* workspace, size_t ws_bytes, void* stream) {
+  const kvq_status s = check_share(c, pool, share, true);
+  if (s != KVQ_OK) return s;
+  if (!table_out || !ring_out || !aligned4(table_out) || !aligned4(ring_out) || !aligned4(page_map)) return KVQ_ERR_INVALID_ARG;
+  if (!workspace || !aligned16(workspace) || ws_bytes < compact_workspace(c)) return KVQ_ERR_WORKSPACE;
+  int32_t* w = static_cast<int32_t*>(workspace);
+  const size_t n = size_t(c->n_pages);
+  kvq::CompactArgs m{};
+  m.table_out = table_out; m.ring_out = ring_out;
+  m.moves = w; m.mark = w + 1 + 2 * n; m.map = page_map ? page_map : w + 1 + 3 * n;
+  return from_cuda(kvq::launch_page_compact(*c, *pool, share, m, static_cast<cudaStream_t>(stream)));
+}
+
+size_t kvq_chunk_workspace_bytes(const kvq_cache* c, int32_t n_q_heads, int32_t n_rows) {
+  if (!shape_ok(c) || !chunk_shape_ok(c, n_q_heads, n_rows) || !chunk_supported(c, n_q_heads, n_rows)) return 0;
+  return kvq::chunk_workspace_bytes(*c, n_q_heads, n_rows);
+}
+
+kvq_status kvq_chunk_attention(const kvq_cache* c, const kvq_score_mod* mod, const void* q, int32_t q_dtype,
+                               int32_t n_q_heads, int32_t n_rows, const int32_t* row_start, float scale, void* out,
+                               int32_t out_dtype, void* workspace, size_t ws_bytes, void* stream) {
+  kvq_status s = check_cache(c);
+  if (s != KVQ_OK) return s;
+  kvq::Rot r{};
+  if ((s = resolve(c, &r)) != KVQ_OK) return s;
+  if (!valid_dtype(q_dtype) || !valid_dtype(out_dtype) || !chunk_shape_ok(c, n_q_heads, n_rows)) return KVQ_ERR_INVALID_ARG;
+  if (!(scale >= 0.0f) || scale > 1e30f) return KVQ_ERR_INVALID_ARG;
+  if (mod && (!(mod->softcap >= 0.0f) || mod->softcap > 1e30f || !aligned4(mod->slopes) || !aligned4(mod->first_key) ||
+              !aligned4(mod->prefix_len)))
+    return KVQ_ERR_INVALID_ARG;
+  if (!chunk_supported(c, n_q_heads, n_rows)) return KVQ_ERR_UNSUPPORTED;
+  if (n_rows == 0) return KVQ_OK;
+  if (!q || !out || !aligned16(q) || !aligned16(out) || !row_start || !aligned4(row_start)) return KVQ_ERR_INVALID_ARG;
+  if (!workspace || !aligned16(workspace) || ws_bytes < kvq::chunk_workspace_bytes(*c, n_q_heads, n_rows))
+    return KVQ_ERR_WORKSPACE;
+  kvq::ChunkCall a{};
+  a.mod = mod; a.q = q; a.q_dtype = q_dtype; a.n_q_heads = n_q_heads; a.n_rows = n_rows; a.row_start = row_start;
+  a.scale = scale == 0.0f ? 1.0f / sqrtf(float(c->head_dim)) : scale;
+  a.out = out; a.out_dtype = out_dtype;
+  return from_cuda(kvq::launch_chunk(*c, r, a, workspace, static_cast<cudaStream_t>(stream)));
 }
 
 kvq_status kvq_block_index_update(const kvq_cache* c, const kvq_block_index* x, int32_t n_last, void* stream) {

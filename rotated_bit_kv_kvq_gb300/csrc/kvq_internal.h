@@ -247,6 +247,52 @@ struct PageArgs {
 };
 cudaError_t launch_page_update(PageArgs a, cudaStream_t st);
 
+// Shared pages (kvq_page_fork, kvq_page_free, kvq_page_compact).
+constexpr int kMaxPlanes = 7;
+struct ShareArgs {
+  const int32_t* seq_len;
+  uint32_t* status;
+  int32_t* table;
+  int batch, max_ctx, page_tokens, n_pages;
+  kvq_page_pool pool;
+  kvq_page_share share;                // (NULL pointers: no counts)
+  int n_planes, page_units;            // the planes of the body, and the units of a page's copy over all of them
+  uint8_t* plane[kMaxPlanes];
+  long long page_bytes[kMaxPlanes];
+  int units[kMaxPlanes];
+};
+struct ForkArgs {
+  kvq_cache c;                         // set at the launch, as what follows `seq_len_out`
+  const int32_t *src, *dst, *n_tokens;  // n_tokens may be NULL
+  int n_forks;
+  int32_t *granted, *seq_len_out;
+  int units, tail_rows, tail_pieces;   // units of a fork, tail rows of a unit, units of a (side, KV head)
+  DivU32 by_row;                       // 16-byte pieces of a tail row
+};
+struct CompactArgs {
+  int32_t *table_out, *ring_out, *map;
+  int32_t *mark, *moves;               // [n_pages], [1 + 2 n_pages]
+};
+cudaError_t launch_page_fork(const kvq_cache& c, const kvq_page_pool& pool, const kvq_page_share& share, ForkArgs f,
+                             cudaStream_t st);
+cudaError_t launch_page_free(const kvq_cache& c, const kvq_page_pool& pool, const kvq_page_share& share, const int32_t* release,
+                             int32_t* seq_len_out, cudaStream_t st);
+cudaError_t launch_page_compact(const kvq_cache& c, const kvq_page_pool& pool, const kvq_page_share* share, CompactArgs m,
+                                cudaStream_t st);
+
+// Attention of packed rows of new tokens (kvq_chunk_attention).
+struct ChunkCall {
+  const kvq_score_mod* mod;            // may be NULL
+  const void* q;
+  int q_dtype, n_q_heads, n_rows;
+  const int32_t* row_start;
+  float scale;
+  void* out;
+  int out_dtype;
+};
+size_t chunk_workspace_bytes(const kvq_cache& c, int n_q_heads, int n_rows);
+cudaError_t launch_chunk(const kvq_cache& c, Rot rot, const ChunkCall& a, void* ws, cudaStream_t st);
+
 // Block index and sparse decode (the decode's head dims, no outlier channels).
 constexpr int kMaxIndexBlocks = 49152;  // keys of a row in shared memory: 192 KB
 cudaError_t launch_block_index_update(const kvq_cache& c, const kvq_block_index& x, int n_last, cudaStream_t st);

@@ -1,0 +1,522 @@
+// Pages that several sequences hold (kvq_page_fork, kvq_page_free, kvq_page_compact).
+//
+// A page's count is the number of sequences that hold it beyond the first, so that pages handed out by kvq_page_update have
+// a count of 0 without knowing of it.  Only full pages are shared: a sequence appends to pages that it holds alone.
+//
+// All three are bound by what they move (fork and compact: page and tail bytes, read and written once) or by the latency of
+// their launches and scans (free).  Results do not depend on the order of atomics: counts are sums, and pages freed in one
+// call go into the ring in ascending order, from a scan over the counts.
+
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "kvq_device.cuh"
+#include "kvq_internal.h"
+#include "kvq_rows.cuh"
+
+namespace kvq {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kPlanThreads = 1024;
+constexpr int kCopyThreads = 256;
+constexpr int kCopyCtas = 4;             // of an SM
+constexpr int kCopyBytes = 16 * 1024;    // of a unit: four 16-byte loads a thread, in flight together
+constexpr int kMaxForkBatch = 65536;     // bits of a sequence bitmap in shared memory
+
+__device__ __forceinline__ bool pool_ok(int head, int count, int n_pages) {
+  return head >= 0 && head < n_pages && count >= 0 && count <= n_pages;
+}
+__device__ __forceinline__ int held_pages(int len, const ShareArgs& a) {  // 0 for a length out of range
+  return len >= 0 && len <= a.max_ctx ? int((uint32_t(len) + uint32_t(a.page_tokens) - 1) / uint32_t(a.page_tokens)) : 0;
+}
+
+// Inclusive sums over a block of kPlanThreads; s: 32 ints.  Returns this thread's, and the block's in total.
+__device__ __forceinline__ int block_sums(int v, int* s, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  __syncthreads();  // (the sums before are read)
+  if (lane == 31) s[warp] = v;
+  __syncthreads();
+  int w = s[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += u;
+  }
+  total = __shfl_sync(0xffffffffu, w, 31);
+  const int before = __shfl_sync(0xffffffffu, w, warp == 0 ? 0 : warp - 1);
+  return v + (warp == 0 ? 0 : before);
+}
+
+// `bytes` (a multiple of 16) by the threads of a CTA, both sides 16-byte aligned
+__device__ __forceinline__ void copy_unit(uint8_t* dst, const uint8_t* src, int bytes) {
+  const uint4* s = reinterpret_cast<const uint4*>(src);
+  uint4* d = reinterpret_cast<uint4*>(dst);
+  const int n = bytes / 16;
+  for (int i = threadIdx.x; i < n; i += 4 * kCopyThreads) {
+    uint4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (i + k * kCopyThreads < n) v[k] = s[i + k * kCopyThreads];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (i + k * kCopyThreads < n) d[i + k * kCopyThreads] = v[k];
+  }
+}
+// unit u of a page's copy: the planes' pieces one after another
+__device__ __forceinline__ void copy_page_unit(const ShareArgs& a, int u, int to, int from) {
+  for (int p = 0; p < a.n_planes; ++p) {
+    if (u < a.units[p]) {
+      const long long at = (long long)u * kCopyBytes;
+      const int n = int(min((long long)kCopyBytes, a.page_bytes[p] - at));
+      copy_unit(a.plane[p] + to * a.page_bytes[p] + at, a.plane[p] + from * a.page_bytes[p] + at, n);
+      return;
+    }
+    u -= a.units[p];
+  }
+}
+
+// ---- fork ------------------------------------------------------------------------------------------
+
+// CTA 0: which forks are valid, the pages they get, the pool's state.  The others: counts and lengths where the results go
+// elsewhere.
+__global__ void __launch_bounds__(kPlanThreads, 1) fork_plan_kernel(ShareArgs a, ForkArgs f) {
+  pdl_begin();
+  const int tid = threadIdx.x;
+  if (blockIdx.x > 0) {
+    const long long i0 = (long long)(blockIdx.x - 1) * kPlanThreads + tid, step = (long long)(gridDim.x - 1) * kPlanThreads;
+    if (a.share.next != a.share.count)
+      for (long long i = i0; i < a.n_pages; i += step) a.share.next[i] = a.share.count[i];
+    if (f.seq_len_out != a.seq_len)
+      for (long long i = i0; i < a.batch; i += step) f.seq_len_out[i] = a.seq_len[i];
+    return;
+  }
+  __shared__ int s_sum[32];
+  __shared__ uint32_t s_once[kMaxForkBatch / 32], s_twice[kMaxForkBatch / 32];
+  const int P = a.page_tokens, per_seq = a.max_ctx / P;
+  const int head = a.pool.state[0], count = a.pool.state[1];
+  const bool pool = pool_ok(head, count, a.n_pages);
+  for (int i = tid; i < (a.batch + 31) / 32; i += kPlanThreads) s_once[i] = s_twice[i] = 0u;
+  __syncthreads();
+  for (int i = tid; i < f.n_forks; i += kPlanThreads) {
+    const int d = f.dst[i];
+    if (d < 0 || d >= a.batch) continue;
+    const uint32_t bit = 1u << (d & 31);
+    if (atomicOr(&s_once[d >> 5], bit) & bit) atomicOr(&s_twice[d >> 5], bit);
+  }
+  __syncthreads();
+  uint32_t err = pool ? 0u : KVQ_DEV_ERR_PAGE;
+  int taken = 0;
+  for (int i0 = 0; i0 < f.n_forks; i0 += kPlanThreads) {
+    const int i = i0 + tid;
+    int n = -1, dst = 0;
+    if (i < f.n_forks) {
+      const int src = f.src[i];
+      dst = f.dst[i];
+      bool ok = src >= 0 && src < a.batch && dst >= 0 && dst < a.batch && src != dst;
+      if (ok) {
+        const int len = a.seq_len[src], want = f.n_tokens ? f.n_tokens[i] : len;
+        ok = len >= 0 && len <= a.max_ctx && want >= 0 && want <= len && a.seq_len[dst] == 0 &&
+             !(s_twice[dst >> 5] >> (dst & 31) & 1u);
+        if (ok) n = want;
+      }
+      if (!ok) err |= KVQ_DEV_ERR_FORK;
+    }
+    const int need = n > 0 && n % P ? 1 : 0;
+    int total;
+    const int at = taken + block_sums(need, s_sum, total) - need;
+    if (i < f.n_forks) {
+      int got = pool ? n : -1;
+      if (pool && need) {
+        if (at < count) {
+          int r = head + at;
+          if (r >= a.n_pages) r -= a.n_pages;
+          const int pg = a.pool.ring[r];
+          if (pg >= 0 && pg < a.n_pages) {
+            a.table[(long long)dst * per_seq + n / P] = pg;
+          } else {  // a ring gone wrong
+            err |= KVQ_DEV_ERR_PAGE;
+            got = -1;
+          }
+        } else {
+          err |= KVQ_DEV_ERR_NO_ROOM;
+          got = -1;
+        }
+      }
+      f.granted[i] = got;
+    }
+    taken += total;
+  }
+  if (err) atomicOr(a.status, err);
+  if (tid == 0) {
+    const int popped = pool ? min(taken, count) : 0;
+    int h = head;
+    if (pool && (h += popped) >= a.n_pages) h -= a.n_pages;
+    a.pool.next[0] = h;
+    a.pool.next[1] = count - popped;
+  }
+}
+
+// Units of a fork: its table row and length, the pieces of the page that is copied, the pieces of its tail.
+__global__ void __launch_bounds__(kCopyThreads, kCopyCtas) fork_copy_kernel(ShareArgs a, ForkArgs f) {
+  pdl_begin();
+  const int P = a.page_tokens, per_seq = a.max_ctx / P, tid = threadIdx.x;
+  const kvq_cache& c = f.c;
+  const int T = c.tail_len, D = c.head_dim, H = c.n_kv_heads;
+  for (long long w = blockIdx.x; w < (long long)f.n_forks * f.units; w += gridDim.x) {
+    // units of a kind lie together: all table rows, then all pages, then all tails
+    const int u = int(w / f.n_forks), i = int(w - (long long)u * f.n_forks);
+    const int n = f.granted[i];
+    if (n < 0) continue;
+    const int src = f.src[i], dst = f.dst[i];
+    const int32_t* from = a.table + (long long)src * per_seq;
+    if (u == 0) {
+      if (tid == 0) f.seq_len_out[dst] = n;
+      for (int j = tid; j < n / P; j += kCopyThreads) {
+        const int pg = from[j];
+        a.table[(long long)dst * per_seq + j] = pg;
+        if (pg >= 0 && pg < a.n_pages) atomicAdd(&a.share.next[pg], 1);
+        else atomicOr(a.status, KVQ_DEV_ERR_PAGE);
+      }
+    } else if (u <= a.page_units) {
+      if (n % P == 0) continue;
+      const int old = from[n / P], pg = a.table[(long long)dst * per_seq + n / P];
+      if (old >= 0 && old < a.n_pages) copy_page_unit(a, u - 1, pg, old);
+      else if (tid == 0) atomicOr(a.status, KVQ_DEV_ERR_PAGE);
+    } else if (n > 0) {
+      // tail slots s0 .. of (side, KV head): slot s holds the position p = s (mod T) of the last T
+      int v = u - 1 - a.page_units;
+      const int piece = v % f.tail_pieces, h = (v /= f.tail_pieces) % H;
+      const bool k = v / H == 0;
+      const int s0 = piece * f.tail_rows, rows = min(f.tail_rows, T - s0), r0 = n % T, first = a.seq_len[src] - T;
+      uint8_t* plane = static_cast<uint8_t*>(k ? c.k_tail : c.v_tail);
+      const uint8_t* in = plane + ((long long)src * H + h) * T * (2 * D);
+      uint8_t* out = plane + ((long long)dst * H + h) * T * (2 * D);
+      const BodySide side = body_side(c, k);
+      const int per_row = D / 8;
+      const int chunks = rows * per_row;
+      auto position = [&](int s) { return n - r0 + s - (s < r0 ? 0 : T); };
+      for (int j0 = tid; j0 < chunks; j0 += 4 * kCopyThreads) {
+        uint4 x[4];
+        long long at[4];
+        int p[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int j = j0 + q * kCopyThreads;
+          const int r = int(div_u32(uint32_t(j), f.by_row)), s = s0 + r;
+          p[q] = j < chunks ? position(s) : -1;
+          at[q] = ((long long)s * per_row + j - r * per_row) * 16;
+          x[q] = p[q] >= 0 && p[q] >= first ? *reinterpret_cast<const uint4*>(in + at[q]) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (p[q] < 0) continue;
+          if (p[q] < first) {  // the source's tail has moved on: the stored values, rounded to bf16
+            const long long row = body_row(row_map(c), src, h, p[q]);
+            if (row < 0) {
+              atomicOr(a.status, KVQ_DEV_ERR_PAGE);
+              continue;
+            }
+            float y[8];
+            body_values8(side, D, row, int(at[q] / 16 % per_row), y);
+            uint32_t wds[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const __nv_bfloat162 b2 = __floats2bfloat162_rn(y[2 * e], y[2 * e + 1]);
+              wds[e] = *reinterpret_cast<const uint32_t*>(&b2);
+            }
+            x[q] = make_uint4(wds[0], wds[1], wds[2], wds[3]);
+          }
+          *reinterpret_cast<uint4*>(out + at[q]) = x[q];
+        }
+      }
+    }
+  }
+}
+
+// ---- free ------------------------------------------------------------------------------------------
+
+// One cluster.  Every released table entry takes one from its page's count; pages that come below 0 are free and go, in
+// ascending order, behind the ring's.
+__global__ void __launch_bounds__(kPlanThreads, 1) free_kernel(ShareArgs a, const int32_t* release, int32_t* seq_len_out) {
+  pdl_begin();
+  cg::cluster_group cl = cg::this_cluster();
+  __shared__ int s_sum[32];
+  __shared__ int s_total;
+  const int S = int(cl.num_blocks()), rank = int(cl.block_rank()), tid = threadIdx.x, lane = tid & 31;
+  const int nt = S * kPlanThreads, gt = rank * kPlanThreads + tid, per_seq = a.max_ctx / a.page_tokens;
+  const int head = a.pool.state[0], count = a.pool.state[1];
+  const bool pool = pool_ok(head, count, a.n_pages);
+  uint32_t err = pool ? 0u : KVQ_DEV_ERR_PAGE;
+  if (a.share.next != a.share.count) {
+    for (long long i = gt; i < a.n_pages; i += nt) a.share.next[i] = a.share.count[i];
+    cl.sync();
+  }
+  if (pool)
+    for (int b = gt >> 5; b < a.batch; b += nt >> 5) {  // a warp a sequence
+      if (release[b] == 0) continue;
+      const int len = a.seq_len[b], held = held_pages(len, a);
+      if (len < 0 || len > a.max_ctx) err |= KVQ_DEV_ERR_APPEND_RANGE;
+      for (int j = lane; j < held; j += 32) {
+        const int pg = a.table[(long long)b * per_seq + j];
+        if (pg >= 0 && pg < a.n_pages) atomicSub(&a.share.next[pg], 1);
+        else err |= KVQ_DEV_ERR_PAGE;
+      }
+    }
+  __threadfence();
+  cl.sync();
+  const int chunk = int(((long long)a.n_pages + S - 1) / S), p0 = int(min((long long)a.n_pages, (long long)rank * chunk)),
+            p1 = int(min((long long)a.n_pages, (long long)p0 + chunk));
+  int mine = 0;
+  for (int p = p0 + tid; p < p1; p += kPlanThreads) mine += __ldcg(&a.share.next[p]) < 0;
+  int total;
+  block_sums(mine, s_sum, total);
+  if (tid == 0) s_total = total;
+  cl.sync();
+  int before = 0, all = 0;
+  for (int r = 0; r < S; ++r) {
+    const int t = *cl.map_shared_rank(&s_total, r);
+    if (r < rank) before += t;
+    all += t;
+  }
+  const int room = a.n_pages - count;  // (a bad state: nothing is free below)
+  for (int q = p0; pool && q < p1; q += kPlanThreads) {
+    const int p = q + tid, v = p < p1 ? __ldcg(&a.share.next[p]) : 0;
+    const int at = before + block_sums(v < 0, s_sum, total) - (v < 0);
+    if (v < 0) {
+      if (v < -1) err |= KVQ_DEV_ERR_PAGE;  // given back more often than it was held
+      a.share.next[p] = 0;
+      if (at < room) {
+        long long i = (long long)head + count + at;
+        while (i >= a.n_pages) i -= a.n_pages;
+        a.pool.ring[i] = p;
+      }
+    }
+    before += total;
+  }
+  if (pool && all > room) err |= KVQ_DEV_ERR_PAGE;
+  if (err) atomicOr(a.status, err);
+  if (seq_len_out)
+    for (int b = gt; b < a.batch; b += nt) {
+      const int len = a.seq_len[b];
+      seq_len_out[b] = pool && release[b] != 0 && len >= 0 && len <= a.max_ctx ? 0 : len;
+    }
+  cl.sync();  // every CTA has read the state, and the others' sums
+  if (rank == 0 && tid == 0) {
+    a.pool.next[0] = head;
+    a.pool.next[1] = pool ? count + min(all, room) : count;
+  }
+}
+
+// ---- compact ---------------------------------------------------------------------------------------
+
+// One cluster.  Marks pages as free (in the ring) or live (in a sequence's table); of the n live ones those that are not
+// among the n lowest marked pages move, the i-th to the i-th free page among these.  moves: [0] their number, then the
+// sources and the destinations.
+__global__ void __launch_bounds__(kPlanThreads, 1) compact_plan_kernel(ShareArgs a, CompactArgs m) {
+  pdl_begin();
+  cg::cluster_group cl = cg::this_cluster();
+  __shared__ int s_sum[32];
+  __shared__ int s_live, s_hand, s_low, s_bad;
+  const int S = int(cl.num_blocks()), rank = int(cl.block_rank()), tid = threadIdx.x, lane = tid & 31;
+  const int nt = S * kPlanThreads, gt = rank * kPlanThreads + tid, per_seq = a.max_ctx / a.page_tokens;
+  const int head = a.pool.state[0], count = a.pool.state[1];
+  const bool pool = pool_ok(head, count, a.n_pages);
+  if (tid == 0) s_bad = pool ? 0 : 1;
+  for (long long i = gt; i < a.n_pages; i += nt) {
+    m.mark[i] = 0;
+    m.map[i] = int(i);
+    if (a.share.next && a.share.next != a.share.count) a.share.next[i] = a.share.count[i];
+  }
+  __threadfence();
+  cl.sync();
+  bool bad = false;
+  if (pool) {
+    for (int b = gt >> 5; b < a.batch; b += nt >> 5) {
+      const int len = a.seq_len[b], held = held_pages(len, a);
+      bad |= len < 0 || len > a.max_ctx;
+      for (int j = lane; j < held; j += 32) {
+        const int pg = a.table[(long long)b * per_seq + j];
+        if (pg >= 0 && pg < a.n_pages) bad |= (atomicOr(&m.mark[pg], 2) & 1) != 0;
+        else bad = true;
+      }
+    }
+    for (int i = gt; i < count; i += nt) {
+      long long r = (long long)head + i;
+      if (r >= a.n_pages) r -= a.n_pages;
+      const int pg = a.pool.ring[r];
+      if (pg >= 0 && pg < a.n_pages) bad |= atomicOr(&m.mark[pg], 1) != 0;  // (twice in the ring, or also in a table)
+      else bad = true;
+    }
+  }
+  if (bad) s_bad = 1;
+  __threadfence();
+  cl.sync();
+  const int chunk = int(((long long)a.n_pages + S - 1) / S), p0 = int(min((long long)a.n_pages, (long long)rank * chunk)),
+            p1 = int(min((long long)a.n_pages, (long long)p0 + chunk));
+  int live = 0, hand = 0, total;
+  for (int p = p0 + tid; p < p1; p += kPlanThreads) {
+    const int k = __ldcg(&m.mark[p]);
+    live += (k & 2) != 0;
+    hand += k != 0;
+  }
+  block_sums(live, s_sum, total);
+  if (tid == 0) s_live = total;
+  block_sums(hand, s_sum, total);
+  if (tid == 0) s_hand = total;
+  cl.sync();
+  int n_live = 0, n_hand = 0, live0 = 0, hand0 = 0;
+  bool any_bad = false;
+  for (int r = 0; r < S; ++r) {
+    const int l = *cl.map_shared_rank(&s_live, r), h = *cl.map_shared_rank(&s_hand, r);
+    any_bad |= *cl.map_shared_rank(&s_bad, r) != 0;
+    if (r < rank) { live0 += l; hand0 += h; }
+    n_live += l;
+    n_hand += h;
+  }
+  // live pages among the n_live lowest
+  int low = 0;
+  for (int q = p0, h0 = hand0; q < p1; q += kPlanThreads) {
+    const int p = q + tid, k = p < p1 ? __ldcg(&m.mark[p]) : 0;
+    const int at = h0 + block_sums(k != 0, s_sum, total) - (k != 0);
+    low += (k & 2) && at < n_live;
+    h0 += total;
+  }
+  block_sums(low, s_sum, total);
+  if (tid == 0) s_low = total;
+  cl.sync();
+  int n_low = 0;
+  for (int r = 0; r < S; ++r) n_low += *cl.map_shared_rank(&s_low, r);
+  const int n_moves = any_bad ? 0 : n_live - n_low;
+  int32_t *from = m.moves + 1, *to = from + a.n_pages;
+  if (!any_bad) {
+    int free0 = hand0 - live0;
+    for (int q = p0; q < p1; q += kPlanThreads) {
+      const int p = q + tid, k = p < p1 ? __ldcg(&m.mark[p]) : 0;
+      const int isl = (k & 2) != 0, isf = k == 1;
+      const int al = live0 + block_sums(isl, s_sum, total) - isl;
+      live0 += total;
+      const int af = free0 + block_sums(isf, s_sum, total) - isf;
+      free0 += total;
+      if (k && al + af < n_live) {
+        if (isf) to[af] = p;
+      } else if (k) {
+        if (isl) from[al - n_low] = p;
+        m.ring_out[al + af - n_live] = p;
+      }
+    }
+    for (int i = n_hand - n_live + gt; i < a.n_pages; i += nt) m.ring_out[i] = -1;
+  } else if (m.ring_out != a.pool.ring) {
+    for (int i = gt; i < a.n_pages; i += nt) m.ring_out[i] = a.pool.ring[i];
+  }
+  __threadfence();
+  cl.sync();
+  for (int i = gt; i < n_moves; i += nt) {
+    const int f = __ldcg(&from[i]), t = __ldcg(&to[i]);
+    m.map[f] = t;
+    if (a.share.next) {
+      a.share.next[t] = a.share.count[f];
+      a.share.next[f] = 0;
+    }
+  }
+  if (rank == 0 && tid == 0) {
+    if (any_bad) atomicOr(a.status, KVQ_DEV_ERR_PAGE);
+    m.moves[0] = n_moves;
+    a.pool.next[0] = any_bad ? head : 0;
+    a.pool.next[1] = any_bad ? count : n_hand - n_live;
+  }
+  cl.sync();  // no CTA leaves while another reads its sums
+}
+
+__global__ void __launch_bounds__(kCopyThreads, kCopyCtas) compact_copy_kernel(ShareArgs a, CompactArgs m) {
+  pdl_begin();
+  const int n = m.moves[0], per_seq = a.max_ctx / a.page_tokens;
+  const int32_t *from = m.moves + 1, *to = from + a.n_pages;
+  const long long work = (long long)n * a.page_units;
+  for (long long w = blockIdx.x; w < work; w += gridDim.x) {
+    const int i = int(w / a.page_units);
+    copy_page_unit(a, int(w - (long long)i * a.page_units), to[i], from[i]);
+  }
+  const long long entries = (long long)a.batch * per_seq;
+  for (long long e = (long long)blockIdx.x * kCopyThreads + threadIdx.x; e < entries; e += (long long)gridDim.x * kCopyThreads) {
+    const int b = int(e / per_seq), pg = a.table[e];
+    const bool used = int(e - (long long)b * per_seq) < held_pages(a.seq_len[b], a);
+    const int out = used && pg >= 0 && pg < a.n_pages ? m.map[pg] : pg;
+    if (m.table_out != a.table || out != pg) m.table_out[e] = out;
+  }
+}
+
+ShareArgs share_args(const kvq_cache& c, const kvq_page_pool& pool, const kvq_page_share* share) {
+  ShareArgs a{};
+  a.seq_len = c.seq_len; a.status = c.status;
+  a.table = const_cast<int32_t*>(c.page_table);
+  a.batch = c.batch; a.max_ctx = c.max_ctx; a.page_tokens = c.page_tokens; a.n_pages = c.n_pages;
+  a.pool = pool;
+  if (share) a.share = *share;
+  const long long rows = (long long)c.n_kv_heads * c.page_tokens, nb = c.head_dim / 32;
+  auto plane = [&](void* p, long long bytes) {
+    if (!p) return;
+    a.plane[a.n_planes] = static_cast<uint8_t*>(p);
+    a.page_bytes[a.n_planes] = bytes;
+    a.units[a.n_planes] = int((bytes + kCopyBytes - 1) / kCopyBytes);
+    a.page_units += a.units[a.n_planes++];
+  };
+  plane(c.k_qs, rows * (long long)qs_row_bytes_host(c.k_type, c.head_dim));
+  plane(c.v_qs, rows * (long long)qs_row_bytes_host(c.v_type, c.head_dim));
+  plane(c.k_d, rows * nb * (type_has_min(c.k_type) ? 4 : 2));
+  plane(c.v_d, rows * nb * (type_has_min(c.v_type) ? 4 : 2));
+  plane(c.k_qh, rows * nb * 4);
+  plane(c.v_qh, rows * nb * 4);
+  plane(c.outl, rows / 16 * kOutlTile);
+  return a;
+}
+int sms() {
+  const int n = device_sm_count();
+  return n > 0 ? n : 148;
+}
+// a cluster of eight where there is work for it: a page a thread, or a table's pages a warp
+int plan_ctas(const kvq_cache& c) { return c.n_pages > 4 * kPlanThreads || c.batch > 64 ? 8 : 1; }
+
+}  // namespace
+
+cudaError_t launch_page_fork(const kvq_cache& c, const kvq_page_pool& pool, const kvq_page_share& share, ForkArgs f,
+                             cudaStream_t st) {
+  ShareArgs a = share_args(c, pool, &share);
+  f.c = c;
+  f.tail_rows = std::max(1, kCopyBytes / (2 * c.head_dim));
+  f.tail_pieces = (c.tail_len + f.tail_rows - 1) / f.tail_rows;
+  f.by_row = make_divu32(uint32_t(c.head_dim / 8));
+  f.units = 1 + a.page_units + 2 * c.n_kv_heads * f.tail_pieces;
+  const bool elsewhere = share.next != share.count || f.seq_len_out != c.seq_len;
+  const int more = elsewhere ? int(std::min<long long>(sms(), ((long long)std::max(c.n_pages, c.batch) + kPlanThreads - 1) / kPlanThreads)) : 0;
+  cudaError_t e = launch_dependent(fork_plan_kernel, unsigned(1 + more), kPlanThreads, 0, st, 1, a, f);
+  if (e != cudaSuccess) return e;
+  const long long work = (long long)f.n_forks * f.units;
+  return launch_dependent(fork_copy_kernel, unsigned(std::min<long long>(work, (long long)sms() * kCopyCtas)), kCopyThreads, 0, st, 1, a, f);
+}
+
+cudaError_t launch_page_free(const kvq_cache& c, const kvq_page_pool& pool, const kvq_page_share& share, const int32_t* release,
+                             int32_t* seq_len_out, cudaStream_t st) {
+  const int S = plan_ctas(c);
+  return launch_dependent(free_kernel, unsigned(S), kPlanThreads, 0, st, S, share_args(c, pool, &share), release, seq_len_out);
+}
+
+cudaError_t launch_page_compact(const kvq_cache& c, const kvq_page_pool& pool, const kvq_page_share* share, CompactArgs m,
+                                cudaStream_t st) {
+  const ShareArgs a = share_args(c, pool, share);
+  const int S = plan_ctas(c);
+  cudaError_t e = launch_dependent(compact_plan_kernel, unsigned(S), kPlanThreads, 0, st, S, a, m);
+  if (e != cudaSuccess) return e;
+  const long long work = std::max((long long)c.n_pages * a.page_units, ((long long)c.batch * (c.max_ctx / c.page_tokens) + kCopyThreads - 1) / kCopyThreads);
+  return launch_dependent(compact_copy_kernel, unsigned(std::min<long long>(work, (long long)sms() * kCopyCtas)), kCopyThreads, 0, st, 1, a, m);
+}
+
+}  // namespace kvq

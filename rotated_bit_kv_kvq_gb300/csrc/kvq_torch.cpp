@@ -26,7 +26,8 @@ template <class T>
 struct Struct {
   Py_buffer view{};
   bool held = false;
-  Struct(PyObject* o, const char* what) {
+  Struct(PyObject* o, const char* what, bool given = true) {
+    if (!given) return;
     if (PyObject_GetBuffer(o, &view, PyBUF_SIMPLE) != 0) {
       PyErr_Clear();
       throw std::invalid_argument(std::string(what) + ": not a descriptor");
@@ -269,9 +270,116 @@ PyObject* sparse_decode_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+int32_t* int_out(const char* what, const Tensor* t, int dev, Shape shape) {
+  return static_cast<int32_t*>(ints(what, t, dev, shape));
+}
+// pages of a pool or of counts (what they were made for) against the cache's
+void for_pages(const char* what, PyObject* pages, const kvq_cache* c) {
+  if (integer(pages) < c->n_pages) throw std::invalid_argument(std::string(what) + ": the pool or the counts were made for fewer pages");
+}
+
+// (cache, pool, share, pages, src, dst, granted, n_tokens, seq_len_out, stream)
+PyObject* page_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 10, [&]() -> kvq_status {
+    static const char* const me = "kvq_page_fork";
+    const Struct<kvq_cache> c(a[0], me);
+    const Struct<kvq_page_pool> pool(a[1], me);
+    const Struct<kvq_page_share> share(a[2], me);
+    for_pages(me, a[3], c.get());
+    const Tensor &src = *tensor(a[4], me), &dst = *tensor(a[5], me), &granted = *tensor(a[6], me);
+    const Tensor *count = tensor(a[7], me, true), *after = tensor(a[8], me, true);
+    const int dev = c10::cuda::current_device();
+    const int64_t forks = src.numel();
+    if (forks > INT32_MAX) throw std::invalid_argument("kvq_page_fork: too many forks");
+    const int32_t* s = int_out("kvq_page_fork: src", &src, dev, {forks});
+    const int32_t* d = int_out("kvq_page_fork: dst", &dst, dev, {forks});
+    int32_t* g = int_out("kvq_page_fork: granted", &granted, dev, {forks});
+    const int32_t* k = int_out("kvq_page_fork: n_tokens", count, dev, {forks});
+    int32_t* l = after ? int_out("kvq_page_fork: seq_len_out", after, dev, {c->batch}) : c->seq_len;
+    void* st = stream_of(a[9]);
+    KVQ_LAUNCH(kvq_page_fork(c.get(), pool.get(), share.get(), s, d, k, int32_t(forks), g, l, st));
+  });
+}
+
+// (cache, pool, share, pages, release, seq_len_out, stream)
+PyObject* page_free(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 7, [&]() -> kvq_status {
+    static const char* const me = "kvq_page_free";
+    const Struct<kvq_cache> c(a[0], me);
+    const Struct<kvq_page_pool> pool(a[1], me);
+    const Struct<kvq_page_share> share(a[2], me);
+    for_pages(me, a[3], c.get());
+    const Tensor& release = *tensor(a[4], me);
+    const Tensor* after = tensor(a[5], me, true);
+    const int dev = c10::cuda::current_device();
+    const int32_t* r = int_out("kvq_page_free: release", &release, dev, {c->batch});
+    int32_t* l = after ? int_out("kvq_page_free: seq_len_out", after, dev, {c->batch}) : c->seq_len;
+    void* st = stream_of(a[6]);
+    KVQ_LAUNCH(kvq_page_free(c.get(), pool.get(), share.get(), r, l, st));
+  });
+}
+
+// (cache, pool, share or None, pages, table_out or None, ring_out or None, workspace, page_map or None, stream)
+PyObject* page_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 9, [&]() -> kvq_status {
+    static const char* const me = "kvq_page_compact";
+    const Struct<kvq_cache> c(a[0], me);
+    const Struct<kvq_page_pool> pool(a[1], me);
+    const bool counts = a[2] != Py_None;
+    const Struct<kvq_page_share> share(counts ? a[2] : a[1], me, counts);
+    for_pages(me, a[3], c.get());
+    const Tensor *table = tensor(a[4], me, true), *ring = tensor(a[5], me, true), *map = tensor(a[7], me, true);
+    const Tensor& ws = *tensor(a[6], me);
+    const int dev = c10::cuda::current_device();
+    const int64_t per = c->page_tokens > 0 ? c->max_ctx / c->page_tokens : 0;
+    int32_t* t = table ? int_out("kvq_page_compact: table_out", table, dev, {c->batch, per}) : const_cast<int32_t*>(c->page_table);
+    int32_t* r = ring ? int_out("kvq_page_compact: ring_out", ring, dev, {c->n_pages}) : pool->ring;
+    int32_t* m = int_out("kvq_page_compact: page_map", map, dev, {c->n_pages});
+    void* w = plain("kvq_page_compact: workspace", ws, dev);
+    const size_t bytes = size_t(ws.numel()) * ws.element_size();
+    void* st = stream_of(a[8]);
+    KVQ_LAUNCH(kvq_page_compact(c.get(), pool.get(), counts ? share.get() : nullptr, t, r, m, w, bytes, st));
+  });
+}
+
+// (cache, mod or None, slopes, first_key, prefix_len, q, row_start, out, workspace, scale, stream); the three tensors are mod's, or None
+PyObject* chunk_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 11, [&]() -> kvq_status {
+    static const char* const me = "kvq_chunk_attention";
+    const Struct<kvq_cache> c(a[0], me);
+    const bool mods = a[1] != Py_None;
+    const Struct<kvq_score_mod> mod(mods ? a[1] : a[0], me, mods);
+    const Tensor *slopes = tensor(a[2], me, true), *first = tensor(a[3], me, true), *prefix = tensor(a[4], me, true);
+    const Tensor &q = *tensor(a[5], me), &start = *tensor(a[6], me), &out = *tensor(a[7], me), &ws = *tensor(a[8], me);
+    const double scale = PyFloat_AsDouble(a[9]);
+    if (scale == -1.0 && PyErr_Occurred()) {
+      PyErr_Clear();
+      throw std::invalid_argument("kvq_chunk_attention: scale is a number");
+    }
+    const int dev = c10::cuda::current_device();
+    const int64_t rows = q.dim() == 3 ? q.size(0) : 0, hq = q.dim() == 3 ? q.size(1) : 0;
+    const int id = floats("kvq_chunk_attention: q", q, {rows, hq, c->head_dim});
+    const int od = floats("kvq_chunk_attention: out", out, {rows, hq, c->head_dim});
+    const int32_t* s = int_out("kvq_chunk_attention: row_start", &start, dev, {int64_t(c->batch) + 1});
+    if (slopes && slopes->sizes() != at::IntArrayRef({hq})) refuse("kvq_chunk_attention: slopes", *slopes, "a value per query head");
+    if (slopes) plain("kvq_chunk_attention: slopes", *slopes, dev);
+    int_out("kvq_chunk_attention: first_key", first, dev, {rows});
+    int_out("kvq_chunk_attention: prefix_len", prefix, dev, {c->batch});
+    const void* qp = plain("kvq_chunk_attention: q", q, dev);
+    void* op = plain("kvq_chunk_attention: out", out, dev);
+    void* w = plain("kvq_chunk_attention: workspace", ws, dev);
+    if (rows > INT32_MAX || hq > INT32_MAX) throw std::invalid_argument("kvq_chunk_attention: sizes do not fit 32 bits");
+    const size_t bytes = size_t(ws.numel()) * ws.element_size();
+    void* st = stream_of(a[10]);
+    KVQ_LAUNCH(kvq_chunk_attention(c.get(), mods ? mod.get() : nullptr, qp, id, int32_t(hq), int32_t(rows), s, float(scale), op,
+                                   od, w, bytes, st));
+  });
+}
+
 #define KVQ_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {KVQ_METHOD(qk_norm_rope), KVQ_METHOD(page_update), KVQ_METHOD(block_index_update),
-                         KVQ_METHOD(select_blocks), KVQ_METHOD(sparse_decode_attention), {nullptr, nullptr, 0, nullptr}};
+                         KVQ_METHOD(select_blocks), KVQ_METHOD(sparse_decode_attention), KVQ_METHOD(page_fork),
+                         KVQ_METHOD(page_free), KVQ_METHOD(page_compact), KVQ_METHOD(chunk_attention), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kvq_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

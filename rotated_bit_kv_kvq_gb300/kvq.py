@@ -36,7 +36,7 @@ KVQ_INPUT_PREROTATED = 1
 KVQ_NUM_PLANES = 12
 KVQ_DEV_ERR_APPEND_RANGE, KVQ_DEV_ERR_PREFILL_RANGE, KVQ_DEV_ERR_TIMEOUT, KVQ_DEV_ERR_PAGE = 1, 2, 4, 8
 KVQ_DEV_ERR_OUTLIER = 16
-KVQ_DEV_ERR_NO_ROOM, KVQ_DEV_ERR_ROW = 32, 64
+KVQ_DEV_ERR_NO_ROOM, KVQ_DEV_ERR_ROW, KVQ_DEV_ERR_FORK = 32, 64, 128
 KVQ_PAGE_RELEASE = -1
 
 
@@ -65,6 +65,15 @@ class kvq_rope_norm(ctypes.Structure):
 
 class kvq_page_pool(ctypes.Structure):
     _fields_ = [("ring", ctypes.c_void_p), ("state", ctypes.c_void_p), ("next", ctypes.c_void_p)]
+
+
+class kvq_page_share(ctypes.Structure):
+    _fields_ = [("count", ctypes.c_void_p), ("next", ctypes.c_void_p)]
+
+
+class kvq_score_mod(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p), ("first_key", ctypes.c_void_p),
+                ("prefix_len", ctypes.c_void_p)]
 
 
 class kvq_block_index(ctypes.Structure):
@@ -106,6 +115,20 @@ SIGNATURES = {
     "kvq_page_update": (ctypes.c_int32, [_P, ctypes.POINTER(kvq_page_pool), ctypes.c_void_p, ctypes.c_int32,
                                          ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
                                          ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "kvq_page_fork": (ctypes.c_int32, [_P, ctypes.POINTER(kvq_page_pool), ctypes.POINTER(kvq_page_share), ctypes.c_void_p,
+                                       ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                                       ctypes.c_void_p, ctypes.c_void_p]),
+    "kvq_page_free": (ctypes.c_int32, [_P, ctypes.POINTER(kvq_page_pool), ctypes.POINTER(kvq_page_share), ctypes.c_void_p,
+                                       ctypes.c_void_p, ctypes.c_void_p]),
+    "kvq_page_compact_workspace_bytes": (ctypes.c_size_t, [_P]),
+    "kvq_page_compact": (ctypes.c_int32, [_P, ctypes.POINTER(kvq_page_pool), ctypes.POINTER(kvq_page_share),
+                                          ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                          ctypes.c_size_t, ctypes.c_void_p]),
+    "kvq_chunk_workspace_bytes": (ctypes.c_size_t, [_P, ctypes.c_int32, ctypes.c_int32]),
+    "kvq_chunk_attention": (ctypes.c_int32, [_P, ctypes.POINTER(kvq_score_mod), ctypes.c_void_p, ctypes.c_int32,
+                                             ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p, ctypes.c_float,
+                                             ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t,
+                                             ctypes.c_void_p]),
     "kvq_block_index_update": (ctypes.c_int32, [_P, ctypes.POINTER(kvq_block_index), ctypes.c_int32,
                                                 ctypes.c_void_p]),
     "kvq_select_blocks": (ctypes.c_int32, [_P, ctypes.POINTER(kvq_block_index), ctypes.c_void_p, ctypes.c_int32,
@@ -345,6 +368,84 @@ def kvq_page_update(cache: kvq_cache, pool, n_new, n_new_max: int, granted, row_
         raise ValueError("kvq_page_update: pool is a PagePool or a kvq_page_pool")
     _check((_native or native()).page_update(cache, pool, pages, n_new, n_new_max, granted, row_pos, row_dst, row_slot,
                                              seq_len_out, stream), "kvq_page_update")
+
+
+class PageShare:
+    """How many sequences hold each page of a cache beyond the first: none at first."""
+
+    def __init__(self, cache: kvq_cache, device="cuda"):
+        import torch
+        self.pages = cache.n_pages
+        self.count = torch.zeros(max(self.pages, 1), dtype=torch.int32, device=device)
+        self.device = self.count.get_device()
+        self.desc = kvq_page_share(self.count.data_ptr(), self.count.data_ptr())
+
+
+def _pages_of(what: str, pool, share):
+    """Descriptors of a pool and counts, and the pages that both were made for."""
+    pages = 0x7fffffff  # descriptors of the caller's own: their sizes are theirs
+    for x, kind, own in ((pool, PagePool, kvq_page_pool), (share, PageShare, kvq_page_share)):
+        if isinstance(x, kind):
+            _on_current_device(kind.__name__, x.device)
+            pages = min(pages, x.pages)
+        elif not isinstance(x, own) and x is not None:
+            raise ValueError(f"{what}: expected a {kind.__name__} or a {own.__name__}")
+    return getattr(pool, "desc", pool), getattr(share, "desc", share), pages
+
+
+def kvq_page_fork(cache: kvq_cache, pool, share, src, dst, granted, n_tokens=None, seq_len_out=None, stream=None):
+    """pool: PagePool or kvq_page_pool, share: PageShare or kvq_page_share; src, dst, granted, n_tokens int32 [n_forks];
+    seq_len_out int32 [batch] (None: the cache's own lengths)."""
+    pool, share, pages = _pages_of("kvq_page_fork", pool, share)
+    _check((_native or native()).page_fork(cache, pool, share, pages, src, dst, granted, n_tokens, seq_len_out, stream),
+           "kvq_page_fork")
+
+
+def kvq_page_free(cache: kvq_cache, pool, share, release, seq_len_out=None, stream=None):
+    """release int32 [batch]: not 0 for the sequences that give their pages back; seq_len_out int32 [batch] (None: the
+    cache's own lengths)."""
+    pool, share, pages = _pages_of("kvq_page_free", pool, share)
+    _check((_native or native()).page_free(cache, pool, share, pages, release, seq_len_out, stream), "kvq_page_free")
+
+
+def kvq_page_compact_workspace_bytes(cache: kvq_cache) -> int:
+    return lib().kvq_page_compact_workspace_bytes(ctypes.byref(cache))
+
+
+def kvq_page_compact(cache: kvq_cache, pool, share, table_out, ring_out, workspace, page_map=None, stream=None):
+    """share None: no page is shared; table_out int32 [batch][pages of a sequence] and ring_out int32 [n_pages] (None: in
+    place); page_map int32 [n_pages] or None."""
+    pool, share, pages = _pages_of("kvq_page_compact", pool, share)
+    _check((_native or native()).page_compact(cache, pool, share, pages, table_out, ring_out, workspace, page_map, stream),
+           "kvq_page_compact")
+
+
+class ScoreMod:
+    """What kvq_chunk_attention does to scores: softcap (0: none), slopes fp32 [n_q_heads], first_key int32 [n_rows],
+    prefix_len int32 [batch], or None."""
+
+    def __init__(self, softcap=0.0, slopes=None, first_key=None, prefix_len=None):
+        import torch
+        _expect_plan("ScoreMod", (torch.float32,), slopes)
+        _expect_plan("ScoreMod", (torch.int32,), first_key, prefix_len)
+        self.slopes, self.first_key, self.prefix_len = slopes, first_key, prefix_len  # kept alive
+        self.desc = kvq_score_mod(softcap, _ptr(slopes), _ptr(first_key), _ptr(prefix_len))
+
+
+def kvq_chunk_workspace_bytes(cache: kvq_cache, n_q_heads: int, n_rows: int) -> int:
+    return lib().kvq_chunk_workspace_bytes(ctypes.byref(cache), n_q_heads, n_rows)
+
+
+def kvq_chunk_attention(cache: kvq_cache, q, row_start, out, workspace, mod=None, scale: float = 0.0, stream=None):
+    """q, out [n_rows][n_q_heads][head_dim]; row_start int32 [batch + 1]; mod: ScoreMod, kvq_score_mod or None."""
+    if isinstance(mod, ScoreMod):
+        given = (mod.desc, mod.slopes, mod.first_key, mod.prefix_len)
+    elif mod is None or isinstance(mod, kvq_score_mod):
+        given = (mod, None, None, None)
+    else:
+        raise ValueError("kvq_chunk_attention: mod is a ScoreMod or a kvq_score_mod")
+    _check((_native or native()).chunk_attention(cache, *given, q, row_start, out, workspace, scale, stream),
+           "kvq_chunk_attention")
 
 
 class BlockIndex:

@@ -133,13 +133,19 @@ def forked_tail(oc, which, src, dst, n):
 
 
 def chunk(keys, values, rot_k, rot_v, q, row_start, seq_len, n_kv_heads, scale, softcap=0.0, slopes=None, first_key=None,
-          prefix_len=None):
+          prefix_len=None, rounding=None):
     """keys, values(b, h): rotated rows [n][d] in float64; q [rows][heads][d].  Zeros where no key is seen; rows that belong
-    to no sequence are NaN here (nothing is written there)."""
+    to no sequence are NaN here (nothing is written there).
+
+    rounding e: also how far the result may be off where rotated queries, keys, values and weights are each rounded by at
+    most e of themselves.  A score is off by at most D = ((1 + e)^2 - 1) scale sum |q_i k_i| (the cap has a slope of at most
+    1, the bias is exact), its weight by a factor within exp(+-D), a normalised one within exp(+-2D); with the weight's and
+    the value's rounding a channel of the rotated result is off by at most (exp(2D) (1 + e)^2 - 1) sum p |v|, and the
+    rotation back sums these over 1 / sqrt(G) of a group's channels."""
     q = np.asarray(q, dtype=np.float64)
     rows, heads, d = q.shape
     G = heads // n_kv_heads
-    out = np.full(q.shape, np.nan)
+    out, off = np.full(q.shape, np.nan), np.zeros(q.shape)
     qr = ko.rotate(q) if rot_k else q
     for b in range(len(seq_len)):
         n, r0, r1 = int(seq_len[b]), int(row_start[b]), int(row_start[b + 1])
@@ -166,4 +172,12 @@ def chunk(keys, values, rot_k, rot_v, q, row_start, seq_len, n_kv_heads, scale, 
                 w = np.exp(s - s.max(-1, keepdims=True))
                 y = (w / w.sum(-1, keepdims=True)) @ V[seen]
                 out[r, h * G:(h + 1) * G] = ko.rotate(y) if rot_v else y
-    return out
+                if rounding:
+                    e = rounding
+                    D = ((1 + e) ** 2 - 1) * scale * (np.abs(qr[r, h * G:(h + 1) * G]) @ np.abs(K[seen]).T).max(-1, keepdims=True)
+                    z = (np.exp(2 * D) * (1 + e) ** 2 - 1) * ((w / w.sum(-1, keepdims=True)) @ np.abs(V[seen]))
+                    if rot_v:
+                        g = ko.rotation_group(d)
+                        z = np.repeat(z.reshape(G, d // g, g).sum(-1) / np.sqrt(g), g, -1).reshape(G, d)
+                    off[r, h * G:(h + 1) * G] = z
+    return (out, off) if rounding else out

@@ -457,11 +457,33 @@ cudaError_t by_dim(int d, F&& f) {
   }
 }
 
-// Sizes of a call, and where its parts lie in the workspace; returns the bytes.
-size_t layout(ChunkArgs& a, char* ws) {
+ChunkTiles tc_tiles_of(int d, int parts) {
+  switch (d) {
+    case 64: return chunk_tc_tiles_d64(parts);
+    case 128: return chunk_tc_tiles_d128(parts);
+    case 192: return chunk_tc_tiles_d192(parts);
+    case 256: return chunk_tc_tiles_d256(parts);
+    case 320: return chunk_tc_tiles_d320(parts);
+    default: return ChunkTiles{0, 0, 0};
+  }
+}
+cudaError_t launch_tc_of(ChunkArgs& a, int parts, cudaStream_t st) {
+  switch (a.c.head_dim) {
+    case 64: return launch_chunk_tc_d64(a, parts, st);
+    case 128: return launch_chunk_tc_d128(a, parts, st);
+    case 192: return launch_chunk_tc_d192(a, parts, st);
+    case 256: return launch_chunk_tc_d256(a, parts, st);
+    case 320: return launch_chunk_tc_d320(a, parts, st);
+    default: return cudaErrorInvalidValue;
+  }
+}
+// fp16 parts of the operands: one is an eighth of a bf16 output's step, two are below fp16's and at fp32's
+int parts_of(int out_dtype) { return out_dtype == KVQ_BF16 ? 1 : 2; }
+
+// Sizes of a call with `t`'s items, and where its parts lie in the workspace; returns the bytes.
+size_t layout(ChunkArgs& a, const ChunkTiles& t, char* ws) {
   const kvq_cache& c = a.c;
-  a.m = c.head_dim <= 192 ? 128 : 64;
-  a.tile = a.tail_tile = kSt;
+  a.m = t.m; a.tile = t.tile; a.tail_tile = t.tail_tile;
   const int sms = device_sm_count();
   a.ctas = sms > 0 ? sms : 148;
   const long long items = chunk_max_items(c, (long long)a.n_rows * a.group, a.m);
@@ -478,6 +500,7 @@ size_t layout(ChunkArgs& a, char* ws) {
   a.part = reinterpret_cast<float*>(take(size_t(2 * a.ctas) * a.m * c.head_dim * sizeof(float)));
   return at;
 }
+ChunkTiles simple_tiles(int d) { return ChunkTiles{d <= 192 ? 128 : 64, kSt, kSt}; }
 
 ChunkArgs chunk_args(const kvq_cache& c, int n_q_heads, int n_rows) {
   ChunkArgs a{};
@@ -490,12 +513,14 @@ ChunkArgs chunk_args(const kvq_cache& c, int n_q_heads, int n_rows) {
 
 size_t chunk_workspace_bytes(const kvq_cache& c, int n_q_heads, int n_rows) {
   ChunkArgs a = chunk_args(c, n_q_heads, n_rows);
-  return layout(a, nullptr);
+  return std::max(layout(a, tc_tiles_of(c.head_dim, 1), nullptr), layout(a, simple_tiles(c.head_dim), nullptr));
 }
 
 cudaError_t launch_chunk(const kvq_cache& c, Rot rot, const ChunkCall& call, void* ws, cudaStream_t st) {
   ChunkArgs a = chunk_args(c, call.n_q_heads, call.n_rows);
-  layout(a, static_cast<char*>(ws));
+  const int parts = parts_of(call.out_dtype);
+  const ChunkTiles t = tc_tiles_of(c.head_dim, parts);
+  layout(a, t.m ? t : simple_tiles(c.head_dim), static_cast<char*>(ws));
   if (call.mod) a.mod = *call.mod;
   a.q = call.q; a.out = call.out; a.row_start = call.row_start;
   a.q_dtype = call.q_dtype; a.out_dtype = call.out_dtype; a.scale = call.scale;
@@ -506,7 +531,7 @@ cudaError_t launch_chunk(const kvq_cache& c, Rot rot, const ChunkCall& call, voi
   a.pages_per_seq = c.page_tokens ? c.max_ctx / c.page_tokens : 0;
   cudaError_t e = launch_dependent(chunk_plan_kernel, 1u, kPlanThreads, 0, st, 1, a);
   if (e != cudaSuccess) return e;
-  e = by_dim(c.head_dim, [&](auto d) { return run_simple<decltype(d)::value>(a, st); });
+  e = t.m ? launch_tc_of(a, parts, st) : by_dim(c.head_dim, [&](auto d) { return run_simple<decltype(d)::value>(a, st); });
   if (e != cudaSuccess) return e;
   return by_dim(c.head_dim, [&](auto d) {
     return launch_dependent(chunk_merge_kernel<decltype(d)::value>, dim3(unsigned(a.ctas), unsigned(a.m / (2 * kMergeRows))),

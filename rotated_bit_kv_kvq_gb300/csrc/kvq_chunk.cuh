@@ -55,6 +55,21 @@ struct ChunkArgs {
   float2* part_ml;        // [2 * ctas][m]: their reference (log2) and sum of weights
 };
 
+// What a kernel's items and tiles are: rows, keys, tail rows (m 0: there is no such kernel).
+struct ChunkTiles {
+  int m, tile, tail_tile;
+};
+// The kernels on tcgen05, with operands in one or two fp16 parts; one translation unit per head_dim.
+#define KVQ_CHUNK_TC(D)                      \
+  ChunkTiles chunk_tc_tiles_d##D(int parts); \
+  cudaError_t launch_chunk_tc_d##D(ChunkArgs& a, int parts, cudaStream_t st);
+KVQ_CHUNK_TC(64)
+KVQ_CHUNK_TC(128)
+KVQ_CHUNK_TC(192)
+KVQ_CHUNK_TC(256)
+KVQ_CHUNK_TC(320)
+#undef KVQ_CHUNK_TC
+
 inline long long chunk_max_items(const kvq_cache& c, long long work_rows, int m) { return work_rows / m + c.batch; }
 
 // One tile of an item: first position, keys, body or tail.

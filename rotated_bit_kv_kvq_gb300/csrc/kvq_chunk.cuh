@@ -110,7 +110,7 @@ __device__ __forceinline__ ChunkSpan chunk_span(const ChunkArgs& a, int b, int n
 struct ChunkWalk {
   long long x, end;       // place in the stream
   int kvh, item;
-  __device__ __noinline__ void begin(const ChunkArgs& a, const ChunkHeader& h, int piece) {
+  __device__ __forceinline__ void begin(const ChunkArgs& a, const ChunkHeader& h, int piece) {
     const long long all = h.total * a.c.n_kv_heads;
     x = min(all, piece * h.piece);
     end = min(all, x + h.piece);
@@ -126,7 +126,7 @@ struct ChunkWalk {
     item = lo;
   }
   // The next segment with tiles, or an item without any whose place is here; false: none left.
-  __device__ __noinline__ bool next(const ChunkArgs& a, const ChunkHeader& h, ChunkItem& it, int& head, int& j0, int& j1) {
+  __device__ __forceinline__ bool next(const ChunkArgs& a, const ChunkHeader& h, ChunkItem& it, int& head, int& j0, int& j1) {
     while (x < end) {
       if (item == h.items) { item = 0; ++kvh; }
       it = a.items[item];

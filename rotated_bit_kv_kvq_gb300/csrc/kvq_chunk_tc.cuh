@@ -5,8 +5,8 @@
 //   scout         a warp: a landed tile's scales, and its keys that are not finite
 //   converters    eight warps: a tile to fp16 operands, keys and values in the same layout (rows of 64 channels, 128-byte
 //                 swizzle), which is K-major for Q K^T and, read along N, V for P V: nothing is transposed
-//   S issuer      a thread: S = Q K^T, Q in TMEM (shared memory at head_dim 320)
-//   P V issuer    a thread: O += P V, P in TMEM
+//   S issuer      a warp: S = Q K^T, Q in TMEM (shared memory at head_dim 320)
+//   P V issuer    a warp: O += P V, P in TMEM
 //   softmax       one or two groups of four warps, a row per thread.  Two groups (small heads) take every other tile, each
 //                 with its own running maximum, sum and accumulator, and are joined at the item's end: two chains of
 //                 score -> weight -> product in flight, without a word between them.
@@ -39,6 +39,7 @@ namespace {
 constexpr long long kTcWait = 2000000000LL;  // ~1 s per wait
 constexpr float kTcLazy = 7.0f;              // log2: weights stay below 2^(8 + 7)
 constexpr int kTcMaxStages = 8;
+constexpr int kTcMaxSlots = 4;
 constexpr int kTcMeta = 16;                  // (a tile's is read before the ring has come round and two more tiles are done)
 constexpr int kTcConv = 8;                   // converter warps
 
@@ -57,7 +58,9 @@ struct TC {
   static_assert((OVER ? scol + 2 * TK : pcol + 2 * pw) <= 512, "TMEM columns");
   // shared memory
   static constexpr int part = D * TK * 2, slot = PARTS * part;  // a tile's operand
-  static constexpr int off_q = 0, off_k = QSMEM ? PARTS * D * 256 : 0, off_v = off_k + 2 * slot, off_ring = off_v + 2 * slot;
+  // slots of each side: conversion may run that far ahead of the products (as many as leave room for a ring of three stages)
+  static constexpr int NS = slot <= 8192 ? 4 : slot <= 24576 && D < 320 ? 3 : 2;
+  static constexpr int off_q = 0, off_k = QSMEM ? PARTS * D * 256 : 0, off_v = off_k + NS * slot, off_ring = off_v + NS * slot;
   static constexpr int N1 = D > 256 ? 192 : D, N2 = D - N1;     // P V as one or two instructions
 };
 
@@ -74,7 +77,7 @@ struct __align__(16) TcMeta {
 
 struct TcSync {
   uint64_t rfull[kTcMaxStages], mfull[kTcMaxStages], rempty[kTcMaxStages];
-  uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], sfree[2], pfull[2], odone[2], qready, fin[2];
+  uint64_t kfull[kTcMaxSlots], kempty[kTcMaxSlots], vfull[kTcMaxSlots], vempty[kTcMaxSlots], sfull[2], sfree[2], pfull[2], odone[2], qready, fin[2];
   int4 job[kTcMaxStages];  // first position, keys (-1: the end), tail slot or -1, first tile of a segment
   TcMeta meta[kTcMeta];
   float rowmax[2][128];
@@ -86,9 +89,20 @@ struct TcSync {
 // Bounded wait; false once any wait of the CTA has given up.  (Code that seldom runs is kept out of line throughout: an SM's
 // instruction cache holds 32 KB, and the roles' loops have to fit it together: while they did not, every tile took 19 KB from
 // the cache that 18 SMs share, and a call 2.5 times as long.)
+// (without a time hint: 7% shorter calls than with one of 20 us)
+__device__ __forceinline__ bool tc_try(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+  return ok != 0;
+}
 __device__ __noinline__ bool tc_wait_long(uint64_t* bar, uint32_t parity, TcSync* sy, uint32_t* status) {
   const long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity, 20000u)) {
+#pragma unroll 1
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)  // (an attempt returns after some hundred cycles)
+      if (tc_try(bar, parity)) return true;
     if (*reinterpret_cast<volatile int*>(&sy->abort)) return false;
     if (clock64() - t0 > kTcWait) {
       *reinterpret_cast<volatile int*>(&sy->abort) = 1;
@@ -96,10 +110,9 @@ __device__ __noinline__ bool tc_wait_long(uint64_t* bar, uint32_t parity, TcSync
       return false;
     }
   }
-  return true;
 }
 __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, TcSync* sy, uint32_t* status) {
-  return mbar_try_wait(bar, parity) || tc_wait_long(bar, parity, sy, status);
+  return tc_try(bar, parity) || tc_wait_long(bar, parity, sy, status);
 }
 
 __device__ __forceinline__ float tc_pow2(int e) {  // clamped to normal numbers
@@ -353,7 +366,11 @@ __device__ __forceinline__ int tc_body_scale(int qt, uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint32_t tc_header_max(uint32_t hdr, int words, int lane) {
   uint32_t mx = 0;
 #pragma unroll 1
-  for (int i = lane; i < words; i += 32) mx = __vmaxu2(mx, tc_lds32(hdr + 4 * i) & 0x7FFF7FFFu);
+  for (int i = lane; i < words / 4; i += 32) {
+    const uint4 q = tc_lds128(hdr + 16 * i);
+    mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(q.x & 0x7FFF7FFFu, q.y & 0x7FFF7FFFu), __vmaxu2(q.z & 0x7FFF7FFFu, q.w & 0x7FFF7FFFu)));
+  }
+  if (lane < (words & 3)) mx = __vmaxu2(mx, tc_lds32(hdr + 4 * (words / 4 * 4 + lane)) & 0x7FFF7FFFu);
   return mx;
 }
 __device__ __noinline__ uint32_t tc_header_max_finite(uint32_t hdr, int words, int lane) {
@@ -469,11 +486,10 @@ __device__ void tc_convert(const ChunkArgs& a, const TcStage& L, uint32_t sb, Tc
   using C = TC<D, PARTS>;
   constexpr int TK = C::TK, NB = C::NB, U = (TK + 31) / 32 * NB;  // units of a side
   uint32_t* status = a.c.status;
-  int r = 0;
-  uint32_t phase = 0;
+  int r = 0, b = 0;
+  uint32_t phase = 0, turn = 1;  // parities of the ring's round and of the slots' round before
+#pragma unroll 1
   for (int ct = 0;; ++ct) {
-    const int b = ct & 1;
-    const uint32_t u = uint32_t(ct) >> 1;
     if (!tc_wait(&sy->rfull[r], phase, sy, status) || !tc_wait(&sy->mfull[r], phase, sy, status)) return;
     const uint4 mt = tc_lds128(smem_u32(&sy->meta[ct % kTcMeta]));
     const int cnt = int(mt.y);
@@ -482,7 +498,7 @@ __device__ void tc_convert(const ChunkArgs& a, const TcStage& L, uint32_t sb, Tc
     const uint32_t st = sb + C::off_ring + r * L.bytes;
 #pragma unroll 1
     for (int side = 0; side < 2; ++side) {
-      if (u > 0 && !tc_wait(side ? &sy->vempty[b] : &sy->kempty[b], (u - 1) & 1, sy, status)) return;
+      if (ct >= C::NS && !tc_wait(side ? &sy->vempty[b] : &sy->kempty[b], turn, sy, status)) return;
       TcSide x;
       x.is_k = side == 0;
       x.type = side ? a.c.v_type : a.c.k_type;
@@ -505,6 +521,7 @@ __device__ void tc_convert(const ChunkArgs& a, const TcStage& L, uint32_t sb, Tc
       }
     }
     if (++r == L.stages) { r = 0; phase ^= 1; }
+    if (++b == C::NS) { b = 0; turn ^= 1; }
   }
 }
 
@@ -600,6 +617,14 @@ __device__ void tc_produce(const ChunkArgs& a, const TcStage& L, const ChunkHead
 
 // ---- issuers ---------------------------------------------------------------------------------------
 
+// A segment's number of tiles, the same in every lane for the compiler too; -1: none left.
+__device__ __forceinline__ int tc_next_tiles(ChunkWalk& walk, const ChunkArgs& a, const ChunkHeader& h) {
+  ChunkItem it;
+  int kvh, j0 = 0, j1 = 0;
+  const bool more = walk.next(a, h, it, kvh, j0, j1);
+  return __shfl_sync(0xffffffffu, more ? j1 - j0 : -1, 0);
+}
+
 template <int D, int PARTS>
 __device__ void tc_issue_s(const ChunkArgs& a, const ChunkHeader& h, uint32_t sb, uint32_t tmem, TcSync* sy) {
   using C = TC<D, PARTS>;
@@ -607,28 +632,30 @@ __device__ void tc_issue_s(const ChunkArgs& a, const ChunkHeader& h, uint32_t sb
   const uint64_t dk = tc::sdesc_sw128(sb + C::off_k), dq = tc::sdesc_sw128(sb + C::off_q);
   ChunkWalk walk;
   walk.begin(a, h, blockIdx.x);
-  ChunkItem it;
-  int kvh, j0, j1, ct = 0, seg = 0;
-  bool ok = true;
-  while (ok && walk.next(a, h, it, kvh, j0, j1)) {
-    if (j1 == j0) continue;
-    ok = tc_wait(&sy->qready, seg++ & 1, sy, a.c.status);
-    for (int j = j0; ok && j < j1; ++j, ++ct) {
+  int ct = 0, seg = 0, s = 0;
+  uint32_t phase = 0;
+  // (no loop ends on what a wait returns: the compiler has to see that all lanes go the same way)
+#pragma unroll 1
+  for (int nt; (nt = tc_next_tiles(walk, a, h)) >= 0;) {
+    if (nt == 0) continue;
+    tc_wait(&sy->qready, seg++ & 1, sy, a.c.status);
+#pragma unroll 1
+    for (int k = 0; k < nt; ++k, ++ct) {
       const int b = ct & 1;
       const uint32_t u = uint32_t(ct) >> 1;
-      ok = tc_wait(&sy->kfull[b], u & 1, sy, a.c.status) &&
-           (u == 0 || tc_wait(C::OVER ? &sy->odone[b] : &sy->sfree[b], (u - 1) & 1, sy, a.c.status));
-      if (!ok) break;
+      const bool ok = tc_wait(&sy->kfull[s], phase, sy, a.c.status) &&
+                      (u == 0 || tc_wait(C::OVER ? &sy->odone[b] : &sy->sfree[b], (u - 1) & 1, sy, a.c.status));
+      if (!__all_sync(0xffffffffu, ok)) continue;
       tc::fence_after_sync();
-      const uint64_t kb = dk + ((b * C::slot) >> 4);
+      const uint64_t kb = dk + ((s * C::slot) >> 4);
       const uint32_t d = tmem + C::scol + b * C::TK;
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
         const uint32_t ko = ((ks / 4) * (C::TK * 128) + (ks % 4) * 32) >> 4;
         const uint32_t qo = ((ks / 4) * (128 * 128) + (ks % 4) * 32) >> 4;
         auto mma = [&](int qp, int kp, uint32_t acc) {
-          if constexpr (C::QSMEM) tc::mma_f16(d, dq + qo + ((qp * D * 256) >> 4), kb + ko + ((kp * C::part) >> 4), idesc, acc);
-          else tc::mma_f16_ts(d, tmem + C::qcol + qp * (D / 2) + ks * 8, kb + ko + ((kp * C::part) >> 4), idesc, acc);
+          if constexpr (C::QSMEM) tc::mma_f16_warp(d, dq + qo + ((qp * D * 256) >> 4), kb + ko + ((kp * C::part) >> 4), idesc, acc);
+          else tc::mma_f16_ts_warp(d, tmem + C::qcol + qp * (D / 2) + ks * 8, kb + ko + ((kp * C::part) >> 4), idesc, acc);
         };
         mma(0, 0, ks > 0 ? 1u : 0u);
         if constexpr (PARTS == 2) {
@@ -636,11 +663,13 @@ __device__ void tc_issue_s(const ChunkArgs& a, const ChunkHeader& h, uint32_t sb
           mma(1, 0, 1u);
         }
       }
-      tc::commit(&sy->sfull[b]);
-      tc::commit(&sy->kempty[b]);
+      tc::commit_warp(&sy->sfull[b]);
+      tc::commit_warp(&sy->kempty[s]);
+      phase ^= s == C::NS - 1;
+      s = s == C::NS - 1 ? 0 : s + 1;
     }
   }
-  tc::commit(&sy->fin[0]);
+  tc::commit_warp(&sy->fin[0]);
 }
 
 template <int D, int PARTS>
@@ -651,26 +680,27 @@ __device__ void tc_issue_pv(const ChunkArgs& a, const ChunkHeader& h, uint32_t s
   const uint64_t dv = tc::sdesc_sw128_mn(sb + C::off_v, C::TK * 128);
   ChunkWalk walk;
   walk.begin(a, h, blockIdx.x);
-  ChunkItem it;
-  int kvh, j0, j1, ct = 0;
-  bool ok = true;
-  while (ok && walk.next(a, h, it, kvh, j0, j1)) {
-    for (int j = j0; ok && j < j1; ++j, ++ct) {
+  int ct = 0, s = 0;
+  uint32_t phase = 0;
+#pragma unroll 1
+  for (int nt; (nt = tc_next_tiles(walk, a, h)) >= 0;) {
+#pragma unroll 1
+    for (int k = 0; k < nt; ++k, ++ct) {
       const int b = ct & 1;
       const uint32_t u = uint32_t(ct) >> 1;
-      ok = tc_wait(&sy->pfull[b], u & 1, sy, a.c.status) && tc_wait(&sy->vfull[b], u & 1, sy, a.c.status);
-      if (!ok) break;
+      const bool ok = tc_wait(&sy->pfull[b], u & 1, sy, a.c.status) && tc_wait(&sy->vfull[s], phase, sy, a.c.status);
+      if (!__all_sync(0xffffffffu, ok)) continue;
       tc::fence_after_sync();
-      const uint64_t vb = dv + ((b * C::slot) >> 4);
+      const uint64_t vb = dv + ((s * C::slot) >> 4);
       const uint32_t o = tmem + C::ocol + (C::NG == 2 ? b * D : 0), p = tmem + C::pcol + b * C::pstep;
-      const uint32_t first = j - j0 < C::NG ? 0u : 1u;  // the group's first tile of the segment begins a new sum
+      const uint32_t first = k < C::NG ? 0u : 1u;  // the group's first tile of the segment begins a new sum
 #pragma unroll
       for (int ks = 0; ks < C::TK / 16; ++ks) {
         auto mma = [&](int pp, int vp, uint32_t acc) {
           const uint64_t v = vb + ((vp * C::part + ks * 2048) >> 4);
-          tc::mma_f16_ts(o, p + pp * (C::TK / 2) + ks * 8, v, idesc1, acc);
+          tc::mma_f16_ts_warp(o, p + pp * (C::TK / 2) + ks * 8, v, idesc1, acc);
           if constexpr (C::N2 > 0)
-            tc::mma_f16_ts(o + C::N1, p + pp * (C::TK / 2) + ks * 8, v + (((C::N1 / 64) * C::TK * 128) >> 4), idesc2, acc);
+            tc::mma_f16_ts_warp(o + C::N1, p + pp * (C::TK / 2) + ks * 8, v + (((C::N1 / 64) * C::TK * 128) >> 4), idesc2, acc);
         };
         mma(0, 0, ks > 0 ? 1u : first);
         if constexpr (PARTS == 2) {
@@ -678,11 +708,13 @@ __device__ void tc_issue_pv(const ChunkArgs& a, const ChunkHeader& h, uint32_t s
           mma(1, 0, 1u);
         }
       }
-      tc::commit(&sy->odone[b]);
-      tc::commit(&sy->vempty[b]);
+      tc::commit_warp(&sy->odone[b]);
+      tc::commit_warp(&sy->vempty[s]);
+      phase ^= s == C::NS - 1;
+      s = s == C::NS - 1 ? 0 : s + 1;
     }
   }
-  tc::commit(&sy->fin[1]);
+  tc::commit_warp(&sy->fin[1]);
 }
 
 // ---- softmax ---------------------------------------------------------------------------------------
@@ -873,16 +905,15 @@ __device__ void tc_softmax(const ChunkArgs& a, const ChunkHeader& h, uint8_t* sm
         const int lo = span.lo - t0, hi = min(span.hi - t0, cnt);
         const bool changed = mods || __any_sync(0xffffffffu, lo > 0 || hi < TK);
         if (bad0 | bad1) nan |= tc_sees(bad0, bad1, lo, hi);
-        // pass 1, 32 columns at a time: the maximum; scores that are capped, biased or masked go back to TMEM, times f
+        // scores that are capped, biased or masked: 32 columns at a time, back to TMEM, times f
         const uint32_t sc0 = lanes + C::scol + b * TK;
-        float mt2 = -INFINITY;
+        if (changed) {
 #pragma unroll 1
-        for (int c0 = 0; c0 < TK; c0 += 32) {
-          float sv[32];
-          tc::ld_x16(sc0 + c0, *reinterpret_cast<float(*)[16]>(&sv[0]));
-          tc::ld_x16(sc0 + c0 + 16, *reinterpret_cast<float(*)[16]>(&sv[16]));
-          tc::wait_ld();
-          if (changed) {
+          for (int c0 = 0; c0 < TK; c0 += 32) {
+            float sv[32];
+            tc::ld_x16(sc0 + c0, *reinterpret_cast<float(*)[16]>(&sv[0]));
+            tc::ld_x16(sc0 + c0 + 16, *reinterpret_cast<float(*)[16]>(&sv[16]));
+            tc::wait_ld();
             if (a.mod.softcap > 0.0f) {
               const float fi = f * icap;
 #pragma unroll
@@ -907,16 +938,22 @@ __device__ void tc_softmax(const ChunkArgs& a, const ChunkHeader& h, uint8_t* sm
             tc::st_x16(sc0 + c0, *reinterpret_cast<float(*)[16]>(&sv[0]));
             tc::st_x16(sc0 + c0 + 16, *reinterpret_cast<float(*)[16]>(&sv[16]));
           }
-          float mx[4] = {sv[0], sv[1], sv[2], sv[3]};
-#pragma unroll
-          for (int c = 4; c < 32; ++c) mx[c & 3] = fmaxf(mx[c & 3], sv[c]);
-          mt2 = fmaxf(mt2, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-        }
-        if (changed) {
           tc::wait_st();
           f = 1.0f;
         }
-        mt2 *= f;
+        float sv[TK];
+#pragma unroll
+        for (int c = 0; c < TK; c += 16) tc::ld_x16(sc0 + c, *reinterpret_cast<float(*)[16]>(&sv[c]));
+        tc::wait_ld();
+        if (!C::OVER) {
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sy->sfree[b]);
+        }
+        float mx[4] = {sv[0], sv[1], sv[2], sv[3]};
+#pragma unroll
+        for (int c = 4; c < TK; ++c) mx[c & 3] = fmaxf(mx[c & 3], sv[c]);
+        const float mt2 = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f;
         float alpha = 1.0f;
         bool move = mt2 > m_used + kTcLazy || (m_used == -INFINITY && mt2 > -INFINITY);
         if (move) {
@@ -949,34 +986,26 @@ __device__ void tc_softmax(const ChunkArgs& a, const ChunkHeader& h, uint8_t* sm
               tc::st_x16(o + c, t);
             }
           }
-          // pass 2: the weights.  (P over S: columns c0 / 2 .. of P lie before those still to be read)
+          // the weights
           const uint32_t p = lanes + C::pcol + b * C::pstep;
-#pragma unroll 1
+          float ls[2] = {0.0f, 0.0f};
+#pragma unroll
           for (int c0 = 0; c0 < TK; c0 += 32) {
-            float sv[32];
-            tc::ld_x16(sc0 + c0, *reinterpret_cast<float(*)[16]>(&sv[0]));
-            tc::ld_x16(sc0 + c0 + 16, *reinterpret_cast<float(*)[16]>(&sv[16]));
-            tc::wait_ld();
-            float ls[2] = {0.0f, 0.0f};
             uint32_t ph[16], pl[PARTS == 2 ? 16 : 1];
 #pragma unroll
             for (int c = 0; c < 32; c += 2) {
-              const float e0 = ex2_approx(fmaf(sv[c], f, -mb)), e1 = ex2_approx(fmaf(sv[c + 1], f, -mb));
+              const float e0 = ex2_approx(fmaf(sv[c0 + c], f, -mb)), e1 = ex2_approx(fmaf(sv[c0 + c + 1], f, -mb));
               ls[0] += e0;
               ls[1] += e1;
               if constexpr (PARTS == 2) split_h2(e0, e1, ph[c / 2], pl[c / 2]);
               else ph[c / 2] = pack_h2(e0, e1);
             }
-            l += ls[0] + ls[1];
             tc::st_x16(p + c0 / 2, *reinterpret_cast<float(*)[16]>(&ph[0]));
             if constexpr (PARTS == 2) tc::st_x16(p + TK / 2 + c0 / 2, *reinterpret_cast<float(*)[16]>(&pl[0]));
           }
+          l += ls[0] + ls[1];
           tc::wait_st();
           tc::fence_before_sync();
-          if (!C::OVER) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sy->sfree[b]);
-          }
         }
       } else {  // no rows: in step with the others all the same, or its arrivals would count for their next tile
         __syncwarp();
@@ -1121,9 +1150,11 @@ chunk_tc_kernel(ChunkArgs a, TcStage L, const __grid_constant__ CUtensorMap tmK,
       mbar_init(&sy->mfull[i], 1);
       mbar_init(&sy->rempty[i], kTcConv);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < C::NS; ++i) {
       mbar_init(&sy->kfull[i], kTcConv); mbar_init(&sy->kempty[i], 1);
       mbar_init(&sy->vfull[i], kTcConv); mbar_init(&sy->vempty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&sy->sfull[i], 1); mbar_init(&sy->sfree[i], 4);
       mbar_init(&sy->pfull[i], 4); mbar_init(&sy->odone[i], 1);
       mbar_init(&sy->fin[i], 1);
@@ -1137,7 +1168,10 @@ chunk_tc_kernel(ChunkArgs a, TcStage L, const __grid_constant__ CUtensorMap tmK,
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = sy->tmem;
+  // (Addresses of TMEM go through uniform registers.  Where the compiler cannot tell that one, or the way to it, is the same in
+  // every lane, each tcgen05 instruction becomes a loop of 30: so the walks are inlined, not on the stack, and no loop around
+  // one ends on what a wait returns.)
+  const uint32_t tmem = __shfl_sync(0xffffffffu, sy->tmem, 0);
   constexpr int W0 = C::kSoft / 32;
   if (warp < W0) {
     tc_softmax<D, PARTS>(a, h, sm, tmem, sy, warp, lane);
@@ -1147,9 +1181,10 @@ chunk_tc_kernel(ChunkArgs a, TcStage L, const __grid_constant__ CUtensorMap tmK,
     tc_scout<D, PARTS>(a, L, smem_u32(sm) + C::off_ring, sy, lane);
   } else if (warp == W0 + kTcConv) {
     tc_produce<D, PARTS>(a, L, h, sm, sy, lane, &tmK, &tmV, &tmKt, &tmVt);
-  } else if (lane == 0) {
-    if (warp == W0 + kTcConv + 1) tc_issue_s<D, PARTS>(a, h, smem_u32(sm), tmem, sy);
-    else tc_issue_pv<D, PARTS>(a, h, smem_u32(sm), tmem, sy);
+  } else if (warp == W0 + kTcConv + 1) {
+    tc_issue_s<D, PARTS>(a, h, smem_u32(sm), tmem, sy);
+  } else {
+    tc_issue_pv<D, PARTS>(a, h, smem_u32(sm), tmem, sy);
   }
   __syncwarp();
   tc::fence_before_sync();

@@ -513,7 +513,12 @@ ChunkArgs chunk_args(const kvq_cache& c, int n_q_heads, int n_rows) {
 
 size_t chunk_workspace_bytes(const kvq_cache& c, int n_q_heads, int n_rows) {
   ChunkArgs a = chunk_args(c, n_q_heads, n_rows);
-  return std::max(layout(a, tc_tiles_of(c.head_dim, 1), nullptr), layout(a, simple_tiles(c.head_dim), nullptr));
+  size_t most = layout(a, simple_tiles(c.head_dim), nullptr);  // (any output type)
+  for (int parts = 1; parts <= 2; ++parts) {
+    const ChunkTiles t = tc_tiles_of(c.head_dim, parts);
+    if (t.m) most = std::max(most, layout(a, t, nullptr));
+  }
+  return most;
 }
 
 cudaError_t launch_chunk(const kvq_cache& c, Rot rot, const ChunkCall& call, void* ws, cudaStream_t st) {

@@ -1,15 +1,16 @@
 // Attention of packed rows of new tokens on tcgen05 (kvq_chunk_attention), included by one translation unit per head_dim.
 //
-// A CTA walks its piece of the plan's stream (kvq_chunk.cuh).  An item's 128 rows are the lanes of TMEM.  Roles:
+// A CTA walks its piece of the plan's stream (kvq_chunk.cuh).  128 rows are the lanes of TMEM.  Roles:
 //   producer      a warp: tiles of packed codes, headers and high bits (or bf16 tail rows) by TMA into a ring
 //   scout         a warp: a landed tile's scales, and its keys that are not finite
 //   converters    eight warps: a tile to fp16 operands, keys and values in the same layout (rows of 64 channels, 128-byte
 //                 swizzle), which is K-major for Q K^T and, read along N, V for P V: nothing is transposed
 //   S issuer      a warp: S = Q K^T, Q in TMEM (shared memory at head_dim 320)
 //   P V issuer    a warp: O += P V, P in TMEM
-//   softmax       one or two groups of four warps, a row per thread.  Two groups (small heads) take every other tile, each
-//                 with its own running maximum, sum and accumulator, and are joined at the item's end: two chains of
-//                 score -> weight -> product in flight, without a word between them.
+//   softmax       one or two groups of four warps, a row per thread.  Two groups (small heads) each have a running maximum, sum
+//                 and accumulator of their own: two chains of score -> weight -> product in flight, without a word between
+//                 them.  Of an item of more than 128 rows they take 128 each, so that a tile is converted once for both; of
+//                 a smaller one every other tile, and are joined at the item's end.
 //
 // PARTS 1 (bf16 outputs): queries, keys, values and weights rounded once to fp16, 2^-11, an eighth of the output's step;
 // PARTS 2 (fp16 and fp32): two fp16 parts each and three products, 22 bits.  Sums and softmax statistics are fp32.
@@ -41,7 +42,7 @@ constexpr float kTcLazy = 7.0f;              // log2: weights stay below 2^(8 + 
 constexpr int kTcMaxStages = 8;
 constexpr int kTcMaxSlots = 4;
 constexpr int kTcMeta = 16;                  // (a tile's is read before the ring has come round and two more tiles are done)
-constexpr int kTcConv = 8;                   // converter warps
+constexpr int kTcConv = 8;                   // converter warps, the first half for keys, the others for values
 
 template <int D, int PARTS>
 struct TC {
@@ -49,11 +50,12 @@ struct TC {
   static constexpr int TK = D == 320 ? 32 : 64;                // keys of a tile
   static constexpr int TT = D <= 128 ? 32 : 16;                // tail rows of a tile
   static constexpr bool QSMEM = D == 320;                      // (TMEM: O takes 320 columns)
-  static constexpr bool OVER = D == 256;                       // P over S (TMEM again)
+  static constexpr bool OVER = D == 256 || (D == 128 && PARTS == 1);  // P over S (TMEM again)
+  static constexpr int M = NG * 128;                           // rows of an item
   static constexpr int G = (D & (D - 1)) == 0 ? D : 64, GC = G / 32, NB = D / 32;
   static constexpr int kSoft = NG * 128, kThreads = kSoft + (kTcConv + 4) * 32;
   // TMEM columns
-  static constexpr int qcol = 0, ocol = QSMEM ? 0 : PARTS * D / 2, scol = ocol + NG * D;
+  static constexpr int qw = QSMEM ? 0 : PARTS * D / 2, ocol = NG * qw, scol = ocol + NG * D;  // (queries from column 0 on)
   static constexpr int pw = PARTS * TK / 2, pcol = OVER ? scol : scol + 2 * TK, pstep = OVER ? TK : pw;
   static_assert((OVER ? scol + 2 * TK : pcol + 2 * pw) <= 512, "TMEM columns");
   // shared memory
@@ -484,8 +486,13 @@ __device__ void tc_scout(const ChunkArgs& a, const TcStage& L, uint32_t ring, Tc
 template <int D, int PARTS>
 __device__ void tc_convert(const ChunkArgs& a, const TcStage& L, uint32_t sb, TcSync* sy, int warp, int lane) {
   using C = TC<D, PARTS>;
-  constexpr int TK = C::TK, NB = C::NB, U = (TK + 31) / 32 * NB;  // units of a side
+  constexpr int TK = C::TK, NB = C::NB, U = (TK + 31) / 32 * NB, W = kTcConv / 2;  // units of a tile, warps of a side
   uint32_t* status = a.c.status;
+  const int side = warp / W;
+  uint64_t *empty = side ? sy->vempty : sy->kempty, *full = side ? sy->vfull : sy->kfull;
+  TcSide x;
+  x.is_k = side == 0;
+  x.type = side ? a.c.v_type : a.c.k_type;
   int r = 0, b = 0;
   uint32_t phase = 0, turn = 1;  // parities of the ring's round and of the slots' round before
 #pragma unroll 1
@@ -496,29 +503,23 @@ __device__ void tc_convert(const ChunkArgs& a, const TcStage& L, uint32_t sb, Tc
     if (cnt < 0) return;
     const bool tail = int(tc_lds32(smem_u32(&sy->job[r].z))) >= 0;
     const uint32_t st = sb + C::off_ring + r * L.bytes;
+    if (ct >= C::NS && !tc_wait(&empty[b], turn, sy, status)) return;
+    x.scale = int(side ? mt.w : mt.z);
+    x.codes = st + (side ? (tail ? L.vt : L.v) : 0);
+    x.hdr = st + (side ? L.vd : L.kd);
+    x.qh = st + (side ? L.vqh : L.kqh);
+    x.dst = sb + (side ? C::off_v : C::off_k) + b * C::slot;
 #pragma unroll 1
-    for (int side = 0; side < 2; ++side) {
-      if (ct >= C::NS && !tc_wait(side ? &sy->vempty[b] : &sy->kempty[b], turn, sy, status)) return;
-      TcSide x;
-      x.is_k = side == 0;
-      x.type = side ? a.c.v_type : a.c.k_type;
-      x.scale = int(side ? mt.w : mt.z);
-      x.codes = st + (side ? (tail ? L.vt : L.v) : 0);
-      x.hdr = st + (side ? L.vd : L.kd);
-      x.qh = st + (side ? L.vqh : L.kqh);
-      x.dst = sb + (side ? C::off_v : C::off_k) + b * C::slot;
-#pragma unroll 1
-      for (int i = (warp + (side ? U : 0)) % kTcConv; i < U; i += kTcConv) {  // (with few units the sides take other warps)
-        const int h = i / NB, blk = i - h * NB, key = 32 * h + lane;
-        if (!tail) tc_body_unit<D, PARTS>(x, key, blk, key < cnt);
-        else if (side == 1 || h == 0) tc_tail_unit<D, PARTS>(x, key, blk, key < cnt);  // (scores past the end are masked)
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(side ? &sy->vfull[b] : &sy->kfull[b]);
-        if (side) mbar_arrive(&sy->rempty[r]);
-      }
+    for (int i = warp % W; i < U; i += W) {
+      const int h = i / NB, blk = i - h * NB, key = 32 * h + lane;
+      if (!tail) tc_body_unit<D, PARTS>(x, key, blk, key < cnt);
+      else if (side == 1 || h == 0) tc_tail_unit<D, PARTS>(x, key, blk, key < cnt);  // (scores past the end are masked)
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(&full[b]);
+      mbar_arrive(&sy->rempty[r]);
     }
     if (++r == L.stages) { r = 0; phase ^= 1; }
     if (++b == C::NS) { b = 0; turn ^= 1; }
@@ -617,12 +618,23 @@ __device__ void tc_produce(const ChunkArgs& a, const TcStage& L, const ChunkHead
 
 // ---- issuers ---------------------------------------------------------------------------------------
 
-// A segment's number of tiles, the same in every lane for the compiler too; -1: none left.
-__device__ __forceinline__ int tc_next_tiles(ChunkWalk& walk, const ChunkArgs& a, const ChunkHeader& h) {
+// Score buffers (with their weights): a group's own with two groups, two in turn with one.  Barriers of a buffer count its uses.
+// Of a segment's tile k (tile ct of the CTA) the buffers are `first`, and the other one too where the groups share the tile.
+template <int NG>
+struct TcUse {
+  bool both;
+  uint32_t used[2];
+  __device__ __forceinline__ int first(int k, int ct) const { return NG == 1 ? ct & 1 : both ? 0 : k & 1; }
+  __device__ __forceinline__ int count() const { return NG == 2 && both ? 2 : 1; }
+};
+
+// The next segment's number of tiles (-1: none left), and whether its rows are more than a group's.
+__device__ __forceinline__ int tc_next_tiles(ChunkWalk& walk, const ChunkArgs& a, const ChunkHeader& h, bool& both) {
   ChunkItem it;
   int kvh, j0 = 0, j1 = 0;
   const bool more = walk.next(a, h, it, kvh, j0, j1);
-  return __shfl_sync(0xffffffffu, more ? j1 - j0 : -1, 0);
+  both = more && it.rows > 128;
+  return more ? j1 - j0 : -1;
 }
 
 template <int D, int PARTS>
@@ -632,38 +644,42 @@ __device__ void tc_issue_s(const ChunkArgs& a, const ChunkHeader& h, uint32_t sb
   const uint64_t dk = tc::sdesc_sw128(sb + C::off_k), dq = tc::sdesc_sw128(sb + C::off_q);
   ChunkWalk walk;
   walk.begin(a, h, blockIdx.x);
+  TcUse<C::NG> use{false, {0, 0}};
   int ct = 0, seg = 0, s = 0;
   uint32_t phase = 0;
   // (no loop ends on what a wait returns: the compiler has to see that all lanes go the same way)
 #pragma unroll 1
-  for (int nt; (nt = tc_next_tiles(walk, a, h)) >= 0;) {
+  for (int nt; (nt = tc_next_tiles(walk, a, h, use.both)) >= 0;) {
     if (nt == 0) continue;
     tc_wait(&sy->qready, seg++ & 1, sy, a.c.status);
 #pragma unroll 1
     for (int k = 0; k < nt; ++k, ++ct) {
-      const int b = ct & 1;
-      const uint32_t u = uint32_t(ct) >> 1;
-      const bool ok = tc_wait(&sy->kfull[s], phase, sy, a.c.status) &&
-                      (u == 0 || tc_wait(C::OVER ? &sy->odone[b] : &sy->sfree[b], (u - 1) & 1, sy, a.c.status));
-      if (!__all_sync(0xffffffffu, ok)) continue;
-      tc::fence_after_sync();
+      const bool have = tc_wait(&sy->kfull[s], phase, sy, a.c.status);
       const uint64_t kb = dk + ((s * C::slot) >> 4);
-      const uint32_t d = tmem + C::scol + b * C::TK;
+#pragma unroll 1
+      for (int i = 0; i < use.count(); ++i) {
+        const int b = use.first(k, ct) + i;
+        const uint32_t u = b ? use.used[1]++ : use.used[0]++;
+        const bool ok = have && (u == 0 || tc_wait(C::OVER ? &sy->odone[b] : &sy->sfree[b], (u - 1) & 1, sy, a.c.status));
+        if (!__all_sync(0xffffffffu, ok)) continue;
+        tc::fence_after_sync();
+        const uint32_t d = tmem + C::scol + b * C::TK, q = tmem + (use.both ? b * C::qw : 0);
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        const uint32_t ko = ((ks / 4) * (C::TK * 128) + (ks % 4) * 32) >> 4;
-        const uint32_t qo = ((ks / 4) * (128 * 128) + (ks % 4) * 32) >> 4;
-        auto mma = [&](int qp, int kp, uint32_t acc) {
-          if constexpr (C::QSMEM) tc::mma_f16_warp(d, dq + qo + ((qp * D * 256) >> 4), kb + ko + ((kp * C::part) >> 4), idesc, acc);
-          else tc::mma_f16_ts_warp(d, tmem + C::qcol + qp * (D / 2) + ks * 8, kb + ko + ((kp * C::part) >> 4), idesc, acc);
-        };
-        mma(0, 0, ks > 0 ? 1u : 0u);
-        if constexpr (PARTS == 2) {
-          mma(0, 1, 1u);
-          mma(1, 0, 1u);
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t ko = ((ks / 4) * (C::TK * 128) + (ks % 4) * 32) >> 4;
+          const uint32_t qo = ((ks / 4) * (128 * 128) + (ks % 4) * 32) >> 4;
+          auto mma = [&](int qp, int kp, uint32_t acc) {
+            if constexpr (C::QSMEM) tc::mma_f16_warp(d, dq + qo + ((qp * D * 256) >> 4), kb + ko + ((kp * C::part) >> 4), idesc, acc);
+            else tc::mma_f16_ts_warp(d, q + qp * (D / 2) + ks * 8, kb + ko + ((kp * C::part) >> 4), idesc, acc);
+          };
+          mma(0, 0, ks > 0 ? 1u : 0u);
+          if constexpr (PARTS == 2) {
+            mma(0, 1, 1u);
+            mma(1, 0, 1u);
+          }
         }
+        tc::commit_warp(&sy->sfull[b]);
       }
-      tc::commit_warp(&sy->sfull[b]);
       tc::commit_warp(&sy->kempty[s]);
       phase ^= s == C::NS - 1;
       s = s == C::NS - 1 ? 0 : s + 1;
@@ -680,35 +696,40 @@ __device__ void tc_issue_pv(const ChunkArgs& a, const ChunkHeader& h, uint32_t s
   const uint64_t dv = tc::sdesc_sw128_mn(sb + C::off_v, C::TK * 128);
   ChunkWalk walk;
   walk.begin(a, h, blockIdx.x);
+  TcUse<C::NG> use{false, {0, 0}};
   int ct = 0, s = 0;
   uint32_t phase = 0;
 #pragma unroll 1
-  for (int nt; (nt = tc_next_tiles(walk, a, h)) >= 0;) {
+  for (int nt; (nt = tc_next_tiles(walk, a, h, use.both)) >= 0;) {
 #pragma unroll 1
     for (int k = 0; k < nt; ++k, ++ct) {
-      const int b = ct & 1;
-      const uint32_t u = uint32_t(ct) >> 1;
-      const bool ok = tc_wait(&sy->pfull[b], u & 1, sy, a.c.status) && tc_wait(&sy->vfull[s], phase, sy, a.c.status);
-      if (!__all_sync(0xffffffffu, ok)) continue;
-      tc::fence_after_sync();
+      const bool have = tc_wait(&sy->vfull[s], phase, sy, a.c.status);
       const uint64_t vb = dv + ((s * C::slot) >> 4);
-      const uint32_t o = tmem + C::ocol + (C::NG == 2 ? b * D : 0), p = tmem + C::pcol + b * C::pstep;
-      const uint32_t first = k < C::NG ? 0u : 1u;  // the group's first tile of the segment begins a new sum
+      const uint32_t first = k < (C::NG == 2 && !use.both ? 2 : 1) ? 0u : 1u;  // a group's first tile begins a new sum
+#pragma unroll 1
+      for (int i = 0; i < use.count(); ++i) {
+        const int b = use.first(k, ct) + i;
+        const uint32_t u = b ? use.used[1]++ : use.used[0]++;
+        const bool ok = have && tc_wait(&sy->pfull[b], u & 1, sy, a.c.status);
+        if (!__all_sync(0xffffffffu, ok)) continue;
+        tc::fence_after_sync();
+        const uint32_t o = tmem + C::ocol + (C::NG == 2 ? b * D : 0), p = tmem + C::pcol + b * C::pstep;
 #pragma unroll
-      for (int ks = 0; ks < C::TK / 16; ++ks) {
-        auto mma = [&](int pp, int vp, uint32_t acc) {
-          const uint64_t v = vb + ((vp * C::part + ks * 2048) >> 4);
-          tc::mma_f16_ts_warp(o, p + pp * (C::TK / 2) + ks * 8, v, idesc1, acc);
-          if constexpr (C::N2 > 0)
-            tc::mma_f16_ts_warp(o + C::N1, p + pp * (C::TK / 2) + ks * 8, v + (((C::N1 / 64) * C::TK * 128) >> 4), idesc2, acc);
-        };
-        mma(0, 0, ks > 0 ? 1u : first);
-        if constexpr (PARTS == 2) {
-          mma(0, 1, 1u);
-          mma(1, 0, 1u);
+        for (int ks = 0; ks < C::TK / 16; ++ks) {
+          auto mma = [&](int pp, int vp, uint32_t acc) {
+            const uint64_t v = vb + ((vp * C::part + ks * 2048) >> 4);
+            tc::mma_f16_ts_warp(o, p + pp * (C::TK / 2) + ks * 8, v, idesc1, acc);
+            if constexpr (C::N2 > 0)
+              tc::mma_f16_ts_warp(o + C::N1, p + pp * (C::TK / 2) + ks * 8, v + (((C::N1 / 64) * C::TK * 128) >> 4), idesc2, acc);
+          };
+          mma(0, 0, ks > 0 ? 1u : first);
+          if constexpr (PARTS == 2) {
+            mma(0, 1, 1u);
+            mma(1, 0, 1u);
+          }
         }
+        tc::commit_warp(&sy->odone[b]);
       }
-      tc::commit_warp(&sy->odone[b]);
       tc::commit_warp(&sy->vempty[s]);
       phase ^= s == C::NS - 1;
       s = s == C::NS - 1 ? 0 : s + 1;
@@ -759,7 +780,8 @@ __device__ void tc_softmax(const ChunkArgs& a, const ChunkHeader& h, uint8_t* sm
   using C = TC<D, PARTS>;
   constexpr int TK = C::TK, NG = C::NG;
   uint32_t* status = a.c.status;
-  const int grp = NG == 2 ? warp / 4 : 0, row = (warp & 3) * 32 + lane;
+  const int grp = NG == 2 ? warp / 4 : 0, line = (warp & 3) * 32 + lane;
+  uint32_t used0 = 0, used1 = 0;  // uses of the buffers (with two groups: of the group's own, in used0)
   const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16);
   auto all = [&]() {  // the softmax warps, TMEM contents included
     tc::fence_before_sync();
@@ -775,7 +797,9 @@ __device__ void tc_softmax(const ChunkArgs& a, const ChunkHeader& h, uint8_t* sm
   while (walk.next(a, h, it, kvh, j0, j1)) {
     const int row0 = a.row_start[it.b], m = a.row_start[it.b + 1] - row0, n = min(max(a.c.seq_len[it.b], 0), a.c.max_ctx);
     const int nk = it.n_body + it.n_tail, nt = j1 - j0;
-    const bool whole = nt == nk, have = row < it.rows, busy = (warp & 3) * 32 < it.rows;  // busy: the warp has rows
+    const bool both = NG == 2 && it.rows > 128;  // the groups have different rows
+    const int row = both ? grp * 128 + line : line, c0 = both ? 0 : grp, cstep = both ? 1 : NG;  // the row's item; its chunks
+    const bool whole = nt == nk, have = row < it.rows, busy = (both ? grp * 128 : 0) + (warp & 3) * 32 < it.rows;  // busy: the warp has rows
     const int w = have ? it.r0 + row : it.r0, tok = int(div_u32(uint32_t(w), a.by_group)), hh = w - tok * a.group;
     const size_t base = ((size_t)(row0 + tok) * a.n_q_heads + kvh * a.group + hh) * D;
     ChunkSpan span{0, 0, 0};
@@ -785,11 +809,11 @@ __device__ void tc_softmax(const ChunkArgs& a, const ChunkHeader& h, uint8_t* sm
       if (have) span = chunk_span(a, it.b, n, row0, m, tok);
       if (a.mod.slopes && have) slope2 = a.mod.slopes[kvh * a.group + hh] * kChunkLog2e;
       // ---- queries: 32 channels at a time to TMEM (where O will be), rotated there, scaled, to their operand's place
-      const uint32_t tmp = lanes + C::ocol;
+      const uint32_t tmp = lanes + C::ocol + (both ? grp * D : 0);
       float top = 0.0f;
       if (busy) {
 #pragma unroll 1
-        for (int c = grp; c < C::NB; c += NG) {
+        for (int c = c0; c < C::NB; c += cstep) {
           float v[32];
           if (a.q_dtype == KVQ_F32) {
             const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + base + c * 32);
@@ -829,7 +853,7 @@ __device__ void tc_softmax(const ChunkArgs& a, const ChunkHeader& h, uint8_t* sm
         all();
         if (busy) {
 #pragma unroll 1
-          for (int s = grp; s < 4 * (D / C::G); s += NG) {  // 8 of the 32 channels, of all chunks of a rotation group
+          for (int s = c0; s < 4 * (D / C::G); s += cstep) {  // 8 of the 32 channels, of all chunks of a rotation group
             const uint32_t at = tmp + (s / 4) * C::G + (s % 4) * 8;
             float v[C::GC][8];
 #pragma unroll
@@ -846,15 +870,16 @@ __device__ void tc_softmax(const ChunkArgs& a, const ChunkHeader& h, uint8_t* sm
           tc::wait_st();
         }
       }
-      if constexpr (NG == 2) sy->rowmax[grp][row] = top;
+      if constexpr (NG == 2) sy->rowmax[grp][line] = top;
       all();
-      if constexpr (NG == 2) top = fmaxf(top, sy->rowmax[1 - grp][row]);
+      if constexpr (NG == 2)
+        if (!both) top = fmaxf(top, sy->rowmax[1 - grp][line]);
       const float sc = a.scale * kChunkLog2e * (a.rot_k ? inv_sqrt_group<C::G>() : 1.0f);
       qs = min(11 - tc_exp(top * sc), 126);  // the largest below 2^11
       const float qf = tc_pow2(qs);
       if (busy) {
 #pragma unroll 1
-        for (int c = grp; c < C::NB; c += NG) {
+        for (int c = c0; c < C::NB; c += cstep) {
           float v[32];
           tc::ld_x16(tmp + c * 32, *reinterpret_cast<float(*)[16]>(&v[0]));
           tc::ld_x16(tmp + c * 32 + 16, *reinterpret_cast<float(*)[16]>(&v[16]));
@@ -872,10 +897,11 @@ __device__ void tc_softmax(const ChunkArgs& a, const ChunkHeader& h, uint8_t* sm
             const uint32_t at = smem_u32(sm) + C::off_q + (c / 2) * (128 * 128);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              tc_sts128(at + tc::sw128_chunk(row, (c & 1) * 4 + i), *reinterpret_cast<uint32_t(*)[4]>(&hi[4 * i]));
+              tc_sts128(at + tc::sw128_chunk(line, (c & 1) * 4 + i), *reinterpret_cast<uint32_t(*)[4]>(&hi[4 * i]));
           } else {
-            tc::st_x16(lanes + C::qcol + c * 16, *reinterpret_cast<float(*)[16]>(&hi[0]));
-            if constexpr (PARTS == 2) tc::st_x16(lanes + C::qcol + D / 2 + c * 16, *reinterpret_cast<float(*)[16]>(&lo[0]));
+            const uint32_t qc = lanes + (both ? grp * C::qw : 0) + c * 16;
+            tc::st_x16(qc, *reinterpret_cast<float(*)[16]>(&hi[0]));
+            if constexpr (PARTS == 2) tc::st_x16(qc + D / 2, *reinterpret_cast<float(*)[16]>(&lo[0]));
           }
         }
         tc::wait_st();
@@ -888,12 +914,12 @@ __device__ void tc_softmax(const ChunkArgs& a, const ChunkHeader& h, uint8_t* sm
 
     // ---- tiles
     float m_used = -INFINITY, l = 0.0f;
-    int vs = 0, mine = 0, last = -1;  // the group's tiles so far, the last one's number
+    int vs = 0, mine = 0;  // the group's tiles so far
     bool nan = false;
     for (int k = 0; k < nt; ++k, ++ct) {
-      const int b = ct & 1;
-      const uint32_t u = uint32_t(ct) >> 1;
-      if (NG == 2 && b != grp) continue;
+      if (NG == 2 && !both && (k & 1) != grp) continue;
+      const int b = NG == 2 ? grp : ct & 1;
+      const uint32_t u = NG == 2 || b == 0 ? used0++ : used1++;
       bool ok = tc_wait(&sy->sfull[b], u & 1, sy, status);
       ok = __all_sync(0xffffffffu, ok);
       if (ok && busy) {
@@ -970,7 +996,7 @@ __device__ void tc_softmax(const ChunkArgs& a, const ChunkHeader& h, uint8_t* sm
         // the weights' place is free once the product that read it is done; to rescale O, the group's last product has to be
         if (u > 0) ok = tc_wait(&sy->odone[b], (u - 1) & 1, sy, status);
         const bool resc = mine > 0 && __any_sync(0xffffffffu, move);
-        if (NG == 1 && resc) ok = tc_wait(&sy->odone[b ^ 1], ((uint32_t(ct) - 1) >> 1) & 1, sy, status) && ok;
+        if (NG == 1 && resc) ok = tc_wait(&sy->odone[b ^ 1], ((b ? used0 : used1) - 1) & 1, sy, status) && ok;
         ok = __all_sync(0xffffffffu, ok);
         if (ok) {
           tc::fence_after_sync();
@@ -1015,18 +1041,20 @@ __device__ void tc_softmax(const ChunkArgs& a, const ChunkHeader& h, uint8_t* sm
       __syncwarp();
       if (lane == 0) mbar_arrive(&sy->pfull[b]);
       ++mine;
-      last = ct;
     }
 
     // ---- the rows' results
     bool ok = true;
-    if (last >= 0) ok = tc_wait(&sy->odone[last & 1], (uint32_t(last) >> 1) & 1, sy, status);
+    if (mine > 0) {  // the group's last product
+      const int b = NG == 2 ? grp : (ct - 1) & 1;
+      ok = tc_wait(&sy->odone[b], ((NG == 2 || b == 0 ? used0 : used1) - 1) & 1, sy, status);
+    }
     float M = m_used, f[2] = {1.0f, 0.0f};
     bool read[2] = {mine > 0, false};
-    if constexpr (NG == 2) {
-      sy->join[grp][row] = make_float4(mine > 0 ? m_used : -INFINITY, l, tc_pow2(-vs), nan || mine == 0 ? (nan ? 1.0f : 2.0f) : 0.0f);
+    if (NG == 2 && !both) {
+      sy->join[grp][line] = make_float4(mine > 0 ? m_used : -INFINITY, l, tc_pow2(-vs), nan || mine == 0 ? (nan ? 1.0f : 2.0f) : 0.0f);
       all();
-      const float4 x0 = sy->join[0][row], x1 = sy->join[1][row];
+      const float4 x0 = sy->join[0][line], x1 = sy->join[1][line];
       M = fmaxf(x0.x, x1.x);
       f[0] = x0.x == -INFINITY ? 0.0f : ex2_approx(x0.x - M);
       f[1] = x1.x == -INFINITY ? 0.0f : ex2_approx(x1.x - M);
@@ -1042,15 +1070,16 @@ __device__ void tc_softmax(const ChunkArgs& a, const ChunkHeader& h, uint8_t* sm
     }
     if (nan) l = NAN;
     ok = __all_sync(0xffffffffu, ok);
-    const size_t slot = (size_t)(2 * blockIdx.x + (j0 == 0 ? 1 : 0)) * 128 + row;
+    const size_t slot = (size_t)(2 * blockIdx.x + (j0 == 0 ? 1 : 0)) * C::M + row;
     if (whole) {
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       f[0] *= inv;
       f[1] *= inv;
-    } else if (have && grp == 0) {
+    } else if (have && (both || grp == 0)) {
       a.part_ml[slot] = make_float2(M == -INFINITY && nan ? 0.0f : M, l);
     }
     const bool any0 = __any_sync(0xffffffffu, read[0]) && ok, any1 = NG == 2 && __any_sync(0xffffffffu, read[1]) && ok;
+    const uint32_t own = lanes + C::ocol + (both ? grp * D : 0);
     // 32 channels of O, joined, in natural order
     auto chunk = [&](int c, float (&v)[32]) {
 #pragma unroll
@@ -1059,8 +1088,8 @@ __device__ void tc_softmax(const ChunkArgs& a, const ChunkHeader& h, uint8_t* sm
       for (int g = 0; g < NG; ++g) {
         if (!(g ? any1 : any0)) continue;
         float t[32];
-        tc::ld_x16(lanes + C::ocol + g * D + c * 32, *reinterpret_cast<float(*)[16]>(&t[0]));
-        tc::ld_x16(lanes + C::ocol + g * D + c * 32 + 16, *reinterpret_cast<float(*)[16]>(&t[16]));
+        tc::ld_x16(own + g * D + c * 32, *reinterpret_cast<float(*)[16]>(&t[0]));
+        tc::ld_x16(own + g * D + c * 32 + 16, *reinterpret_cast<float(*)[16]>(&t[16]));
         tc::wait_ld();
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -1086,13 +1115,13 @@ __device__ void tc_softmax(const ChunkArgs& a, const ChunkHeader& h, uint8_t* sm
     const bool turn = whole && a.rot_v;
     if (busy) {
 #pragma unroll 1
-      for (int c = grp; c < C::NB; c += NG) {
+      for (int c = c0; c < C::NB; c += cstep) {
         float v[32];
         chunk(c, v);
         if (turn) {
           tc_fwht32(v);
-          tc::st_x16(lanes + C::ocol + c * 32, *reinterpret_cast<float(*)[16]>(&v[0]));
-          tc::st_x16(lanes + C::ocol + c * 32 + 16, *reinterpret_cast<float(*)[16]>(&v[16]));
+          tc::st_x16(own + c * 32, *reinterpret_cast<float(*)[16]>(&v[0]));
+          tc::st_x16(own + c * 32 + 16, *reinterpret_cast<float(*)[16]>(&v[16]));
         } else if (have && whole) {
 #pragma unroll
           for (int e = 0; e < 32; e += 8) store8(c * 32 + e, v + e);
@@ -1108,11 +1137,11 @@ __device__ void tc_softmax(const ChunkArgs& a, const ChunkHeader& h, uint8_t* sm
       all();
       if (busy) {
 #pragma unroll 1
-        for (int s = grp; s < 4 * (D / C::G); s += NG) {
+        for (int s = c0; s < 4 * (D / C::G); s += cstep) {
           const int at = (s / 4) * C::G + (s % 4) * 8;
           float v[C::GC][8];
 #pragma unroll
-          for (int k = 0; k < C::GC; ++k) tc::ld_x8(lanes + C::ocol + at + k * 32, v[k]);
+          for (int k = 0; k < C::GC; ++k) tc::ld_x8(own + at + k * 32, v[k]);
           tc::wait_ld();
           tc_fwht_chunks<C::GC>(v);
 #pragma unroll
@@ -1151,8 +1180,8 @@ chunk_tc_kernel(ChunkArgs a, TcStage L, const __grid_constant__ CUtensorMap tmK,
       mbar_init(&sy->rempty[i], kTcConv);
     }
     for (int i = 0; i < C::NS; ++i) {
-      mbar_init(&sy->kfull[i], kTcConv); mbar_init(&sy->kempty[i], 1);
-      mbar_init(&sy->vfull[i], kTcConv); mbar_init(&sy->vempty[i], 1);
+      mbar_init(&sy->kfull[i], kTcConv / 2); mbar_init(&sy->kempty[i], 1);
+      mbar_init(&sy->vfull[i], kTcConv / 2); mbar_init(&sy->vempty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sy->sfull[i], 1); mbar_init(&sy->sfree[i], 4);
@@ -1244,7 +1273,8 @@ cudaError_t run_chunk_tc(ChunkArgs& a, cudaStream_t st) {
 constexpr int tc_max_parts(int d) { return d <= 128 ? 2 : 1; }  // (two parts of wider operands do not fit)
 template <int D>
 ChunkTiles tc_tiles(int parts) {
-  return parts <= tc_max_parts(D) ? ChunkTiles{128, TC<D, 1>::TK, TC<D, 1>::TT} : ChunkTiles{0, 0, 0};
+  if (parts > tc_max_parts(D)) return ChunkTiles{0, 0, 0};
+  return ChunkTiles{parts == 1 ? TC<D, 1>::M : TC<D, tc_max_parts(D)>::M, TC<D, 1>::TK, TC<D, 1>::TT};
 }
 template <int D>
 cudaError_t launch_tc(ChunkArgs& a, int parts, cudaStream_t st) {

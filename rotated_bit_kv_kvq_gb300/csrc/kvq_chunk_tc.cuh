@@ -48,7 +48,7 @@ template <int D, int PARTS>
 struct TC {
   static constexpr int NG = D <= 64 * (3 - PARTS) ? 2 : 1;     // groups of softmax warps, each with an O of its own
   static constexpr int TK = D == 320 ? 32 : 64;                // keys of a tile
-  static constexpr int TT = D <= 128 ? 32 : 16;                // tail rows of a tile
+  static constexpr int TT = D <= 128 ? 64 : D == 192 || D == 256 ? 32 : 16;  // tail rows of a tile
   static constexpr bool QSMEM = D == 320;                      // (TMEM: O takes 320 columns)
   static constexpr bool OVER = D == 256 || (D == 128 && PARTS == 1);  // P over S (TMEM again)
   static constexpr int M = NG * 128;                           // rows of an item
@@ -513,7 +513,7 @@ __device__ void tc_convert(const ChunkArgs& a, const TcStage& L, uint32_t sb, Tc
     for (int i = warp % W; i < U; i += W) {
       const int h = i / NB, blk = i - h * NB, key = 32 * h + lane;
       if (!tail) tc_body_unit<D, PARTS>(x, key, blk, key < cnt);
-      else if (side == 1 || h == 0) tc_tail_unit<D, PARTS>(x, key, blk, key < cnt);  // (scores past the end are masked)
+      else if (side == 1 || 32 * h < cnt) tc_tail_unit<D, PARTS>(x, key, blk, key < cnt);  // (scores past the end are masked)
     }
     fence_proxy_async_smem();
     __syncwarp();
@@ -579,7 +579,8 @@ __device__ void tc_produce(const ChunkArgs& a, const TcStage& L, const ChunkHead
       if (!more) {
         job.y = -1;
       } else if (jb + lane < j1) {
-        const ChunkTile t = chunk_tile(a, it, n, jb + lane);
+        // from the last keys to the first: with a bias by distance the largest score comes first, and O is not rescaled
+        const ChunkTile t = chunk_tile(a, it, n, j1 - 1 - (jb + lane - j0));
         job = make_int4(t.t0, t.cnt, -1, jb + lane == j0);
         if (t.tail) {
           job.z = t.t0 - int(div_u32(uint32_t(t.t0), a.by_tail)) * T;
@@ -931,55 +932,52 @@ __device__ void tc_softmax(const ChunkArgs& a, const ChunkHeader& h, uint8_t* sm
         const int lo = span.lo - t0, hi = min(span.hi - t0, cnt);
         const bool changed = mods || __any_sync(0xffffffffu, lo > 0 || hi < TK);
         if (bad0 | bad1) nan |= tc_sees(bad0, bad1, lo, hi);
-        // scores that are capped, biased or masked: 32 columns at a time, back to TMEM, times f
+        // scores that are capped, biased or masked: 16 columns at a time, back to TMEM, times f
         const uint32_t sc0 = lanes + C::scol + b * TK;
         if (changed) {
 #pragma unroll 1
-          for (int c0 = 0; c0 < TK; c0 += 32) {
-            float sv[32];
-            tc::ld_x16(sc0 + c0, *reinterpret_cast<float(*)[16]>(&sv[0]));
-            tc::ld_x16(sc0 + c0 + 16, *reinterpret_cast<float(*)[16]>(&sv[16]));
+          for (int c0 = 0; c0 < TK; c0 += 16) {
+            float sv[16];
+            tc::ld_x16(sc0 + c0, sv);
             tc::wait_ld();
             if (a.mod.softcap > 0.0f) {
               const float fi = f * icap;
 #pragma unroll
-              for (int c = 0; c < 32; ++c) {
+              for (int c = 0; c < 16; ++c) {
                 float r;
                 asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + ex2_approx(sv[c] * fi)));
                 sv[c] = fmaf(-2.0f * cap2, r, cap2);
               }
             } else {
 #pragma unroll
-              for (int c = 0; c < 32; ++c) sv[c] *= f;
+              for (int c = 0; c < 16; ++c) sv[c] *= f;
             }
             if (a.mod.slopes) {
               const float d0 = float(t0 + c0 - span.pos);
 #pragma unroll
-              for (int c = 0; c < 32; ++c) sv[c] = fmaf(-slope2, fabsf(d0 + float(c)), sv[c]);
+              for (int c = 0; c < 16; ++c) sv[c] = fmaf(-slope2, fabsf(d0 + float(c)), sv[c]);
             }
-            const int l32 = lo - c0, h32 = hi - c0;
+            // (columns c0 + c from lo on, below hi)
+            const uint32_t room = uint32_t(max(hi - lo, 0)), from = uint32_t(c0 - lo);
 #pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (c < l32 || c >= h32) sv[c] = -INFINITY;
-            tc::st_x16(sc0 + c0, *reinterpret_cast<float(*)[16]>(&sv[0]));
-            tc::st_x16(sc0 + c0 + 16, *reinterpret_cast<float(*)[16]>(&sv[16]));
+            for (int c = 0; c < 16; ++c)
+              if (from + c >= room) sv[c] = -INFINITY;
+            tc::st_x16(sc0 + c0, sv);
           }
           tc::wait_st();
           f = 1.0f;
         }
-        float sv[TK];
+        float mt2;
+        {
+          float sv[TK];
 #pragma unroll
-        for (int c = 0; c < TK; c += 16) tc::ld_x16(sc0 + c, *reinterpret_cast<float(*)[16]>(&sv[c]));
-        tc::wait_ld();
-        if (!C::OVER) {
-          tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sy->sfree[b]);
+          for (int c = 0; c < TK; c += 16) tc::ld_x16(sc0 + c, *reinterpret_cast<float(*)[16]>(&sv[c]));
+          tc::wait_ld();
+          float mx[4] = {sv[0], sv[1], sv[2], sv[3]};
+#pragma unroll
+          for (int c = 4; c < TK; ++c) mx[c & 3] = fmaxf(mx[c & 3], sv[c]);
+          mt2 = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f;
         }
-        float mx[4] = {sv[0], sv[1], sv[2], sv[3]};
-#pragma unroll
-        for (int c = 4; c < TK; ++c) mx[c & 3] = fmaxf(mx[c & 3], sv[c]);
-        const float mt2 = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f;
         float alpha = 1.0f;
         bool move = mt2 > m_used + kTcLazy || (m_used == -INFINITY && mt2 > -INFINITY);
         if (move) {
@@ -1012,26 +1010,32 @@ __device__ void tc_softmax(const ChunkArgs& a, const ChunkHeader& h, uint8_t* sm
               tc::st_x16(o + c, t);
             }
           }
-          // the weights
+          // the weights, 16 columns at a time.  (P over S: it lies before the scores still to be read)
           const uint32_t p = lanes + C::pcol + b * C::pstep;
           float ls[2] = {0.0f, 0.0f};
+#pragma unroll 1
+          for (int c0 = 0; c0 < TK; c0 += 16) {
+            float sv[16], ph[8], pl[PARTS == 2 ? 8 : 1];
+            tc::ld_x16(sc0 + c0, sv);
+            tc::wait_ld();
 #pragma unroll
-          for (int c0 = 0; c0 < TK; c0 += 32) {
-            uint32_t ph[16], pl[PARTS == 2 ? 16 : 1];
-#pragma unroll
-            for (int c = 0; c < 32; c += 2) {
-              const float e0 = ex2_approx(fmaf(sv[c0 + c], f, -mb)), e1 = ex2_approx(fmaf(sv[c0 + c + 1], f, -mb));
+            for (int c = 0; c < 16; c += 2) {
+              const float e0 = ex2_approx(fmaf(sv[c], f, -mb)), e1 = ex2_approx(fmaf(sv[c + 1], f, -mb));
               ls[0] += e0;
               ls[1] += e1;
-              if constexpr (PARTS == 2) split_h2(e0, e1, ph[c / 2], pl[c / 2]);
-              else ph[c / 2] = pack_h2(e0, e1);
+              if constexpr (PARTS == 2) split_h2(e0, e1, reinterpret_cast<uint32_t&>(ph[c / 2]), reinterpret_cast<uint32_t&>(pl[c / 2]));
+              else ph[c / 2] = __uint_as_float(pack_h2(e0, e1));
             }
-            tc::st_x16(p + c0 / 2, *reinterpret_cast<float(*)[16]>(&ph[0]));
-            if constexpr (PARTS == 2) tc::st_x16(p + TK / 2 + c0 / 2, *reinterpret_cast<float(*)[16]>(&pl[0]));
+            tc::st_x8(p + c0 / 2, ph);
+            if constexpr (PARTS == 2) tc::st_x8(p + TK / 2 + c0 / 2, pl);
           }
           l += ls[0] + ls[1];
           tc::wait_st();
           tc::fence_before_sync();
+          if (!C::OVER) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sy->sfree[b]);
+          }
         }
       } else {  // no rows: in step with the others all the same, or its arrivals would count for their next tile
         __syncwarp();

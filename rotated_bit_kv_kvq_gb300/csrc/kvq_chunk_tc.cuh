@@ -48,21 +48,23 @@ template <int D, int PARTS>
 struct TC {
   static constexpr int NG = D <= 64 * (3 - PARTS) ? 2 : 1;     // groups of softmax warps, each with an O of its own
   static constexpr int TK = D == 320 ? 32 : 64;                // keys of a tile
-  static constexpr int TT = D <= 128 ? 64 : D == 192 || D == 256 ? 32 : 16;  // tail rows of a tile
-  static constexpr bool QSMEM = D == 320;                      // (TMEM: O takes 320 columns)
-  static constexpr bool OVER = D == 256 || (D == 128 && PARTS == 1);  // P over S (TMEM again)
+  static constexpr int TT = D == 64 ? 64 : D <= 256 ? 32 : 16;  // tail rows of a tile
+  static constexpr int SB = NG == 2 && PARTS == 2 ? 1 : 2;     // score buffers of a group: with two, S of the next tile is ready
+  static constexpr bool QSMEM = D == 320 || (D == 128 && PARTS == 1);  // (TMEM has no room for the queries)
+  static constexpr bool OVER = D == 256 || (NG == 2 && SB == 2);  // P over S (TMEM again)
   static constexpr int M = NG * 128;                           // rows of an item
   static constexpr int G = (D & (D - 1)) == 0 ? D : 64, GC = G / 32, NB = D / 32;
   static constexpr int kSoft = NG * 128, kThreads = kSoft + (kTcConv + 4) * 32;
   // TMEM columns
   static constexpr int qw = QSMEM ? 0 : PARTS * D / 2, ocol = NG * qw, scol = ocol + NG * D;  // (queries from column 0 on)
-  static constexpr int pw = PARTS * TK / 2, pcol = OVER ? scol : scol + 2 * TK, pstep = OVER ? TK : pw;
-  static_assert((OVER ? scol + 2 * TK : pcol + 2 * pw) <= 512, "TMEM columns");
+  static constexpr int pw = PARTS * TK / 2, pcol = OVER ? scol : scol + NG * SB * TK, pstep = OVER ? TK : pw;
+  static_assert(pcol + NG * SB * pstep <= 512, "TMEM columns");
+  static_assert(!OVER || PARTS == 1, "a second part of P would lie over scores not read yet");
   // shared memory
   static constexpr int part = D * TK * 2, slot = PARTS * part;  // a tile's operand
   // slots of each side: conversion may run that far ahead of the products (as many as leave room for a ring of three stages)
-  static constexpr int NS = slot <= 8192 ? 4 : slot <= 24576 && D < 320 ? 3 : 2;
-  static constexpr int off_q = 0, off_k = QSMEM ? PARTS * D * 256 : 0, off_v = off_k + NS * slot, off_ring = off_v + NS * slot;
+  static constexpr int NS = slot <= 8192 ? 4 : D == 192 ? 3 : 2;
+  static constexpr int off_q = 0, off_k = QSMEM ? NG * PARTS * D * 256 : 0, off_v = off_k + NS * slot, off_ring = off_v + NS * slot;
   static constexpr int N1 = D > 256 ? 192 : D, N2 = D - N1;     // P V as one or two instructions
 };
 
@@ -79,7 +81,7 @@ struct __align__(16) TcMeta {
 
 struct TcSync {
   uint64_t rfull[kTcMaxStages], mfull[kTcMaxStages], rempty[kTcMaxStages];
-  uint64_t kfull[kTcMaxSlots], kempty[kTcMaxSlots], vfull[kTcMaxSlots], vempty[kTcMaxSlots], sfull[2], sfree[2], pfull[2], odone[2], qready, fin[2];
+  uint64_t kfull[kTcMaxSlots], kempty[kTcMaxSlots], vfull[kTcMaxSlots], vempty[kTcMaxSlots], sfull[4], sfree[4], pfull[4], odone[4], qready, fin[2];
   int4 job[kTcMaxStages];  // first position, keys (-1: the end), tail slot or -1, first tile of a segment
   TcMeta meta[kTcMeta];
   float rowmax[2][128];
@@ -619,22 +621,19 @@ __device__ void tc_produce(const ChunkArgs& a, const TcStage& L, const ChunkHead
 
 // ---- issuers ---------------------------------------------------------------------------------------
 
-// Score buffers (with their weights): a group's own with two groups, two in turn with one.  Barriers of a buffer count its uses.
-// Of a segment's tile k (tile ct of the CTA) the buffers are `first`, and the other one too where the groups share the tile.
-template <int NG>
-struct TcUse {
-  bool both;
-  uint32_t used[2];
-  __device__ __forceinline__ int first(int k, int ct) const { return NG == 1 ? ct & 1 : both ? 0 : k & 1; }
-  __device__ __forceinline__ int count() const { return NG == 2 && both ? 2 : 1; }
-};
+// Which of its score buffers (with their weights) a group's n-th tile uses, and the parity of that use.
+template <class C>
+__device__ __forceinline__ int tc_buffer(int g, uint32_t n) { return C::SB == 2 ? 2 * g + int(n & 1) : g; }
+template <class C>
+__device__ __forceinline__ uint32_t tc_turn(uint32_t n) { return (C::SB == 2 ? n >> 1 : n) & 1; }
 
-// The next segment's number of tiles (-1: none left), and whether its rows are more than a group's.
+// The next segment's number of tiles (-1: none left), and whether its rows are more than a group's (C2: there are two groups).
+template <bool C2>
 __device__ __forceinline__ int tc_next_tiles(ChunkWalk& walk, const ChunkArgs& a, const ChunkHeader& h, bool& both) {
   ChunkItem it;
   int kvh, j0 = 0, j1 = 0;
   const bool more = walk.next(a, h, it, kvh, j0, j1);
-  both = more && it.rows > 128;
+  both = C2 && more && it.rows > 128;
   return more ? j1 - j0 : -1;
 }
 
@@ -645,32 +644,34 @@ __device__ void tc_issue_s(const ChunkArgs& a, const ChunkHeader& h, uint32_t sb
   const uint64_t dk = tc::sdesc_sw128(sb + C::off_k), dq = tc::sdesc_sw128(sb + C::off_q);
   ChunkWalk walk;
   walk.begin(a, h, blockIdx.x);
-  TcUse<C::NG> use{false, {0, 0}};
-  int ct = 0, seg = 0, s = 0;
-  uint32_t phase = 0;
+  bool both;
+  int seg = 0, s = 0;
+  uint32_t phase = 0, n0 = 0, n1 = 0;  // the groups' tiles
   // (no loop ends on what a wait returns: the compiler has to see that all lanes go the same way)
 #pragma unroll 1
-  for (int nt; (nt = tc_next_tiles(walk, a, h, use.both)) >= 0;) {
+  for (int nt; (nt = tc_next_tiles<C::NG == 2>(walk, a, h, both)) >= 0;) {
     if (nt == 0) continue;
     tc_wait(&sy->qready, seg++ & 1, sy, a.c.status);
 #pragma unroll 1
-    for (int k = 0; k < nt; ++k, ++ct) {
+    for (int k = 0; k < nt; ++k) {
       const bool have = tc_wait(&sy->kfull[s], phase, sy, a.c.status);
       const uint64_t kb = dk + ((s * C::slot) >> 4);
 #pragma unroll 1
-      for (int i = 0; i < use.count(); ++i) {
-        const int b = use.first(k, ct) + i;
-        const uint32_t u = b ? use.used[1]++ : use.used[0]++;
-        const bool ok = have && (u == 0 || tc_wait(C::OVER ? &sy->odone[b] : &sy->sfree[b], (u - 1) & 1, sy, a.c.status));
+      for (int i = 0; i < (both ? 2 : 1); ++i) {
+        const int g = C::NG == 1 ? 0 : both ? i : k & 1;
+        const uint32_t n = g ? n1++ : n0++;
+        const int b = tc_buffer<C>(g, n);
+        const bool ok = have && (n < C::SB || tc_wait(C::OVER ? &sy->odone[b] : &sy->sfree[b], tc_turn<C>(n) ^ 1, sy, a.c.status));
         if (!__all_sync(0xffffffffu, ok)) continue;
         tc::fence_after_sync();
-        const uint32_t d = tmem + C::scol + b * C::TK, q = tmem + (use.both ? b * C::qw : 0);
+        const uint32_t d = tmem + C::scol + b * C::TK, q = tmem + (both ? g * C::qw : 0);
+        const uint64_t qd = dq + (both ? (g * PARTS * D * 256) >> 4 : 0);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           const uint32_t ko = ((ks / 4) * (C::TK * 128) + (ks % 4) * 32) >> 4;
           const uint32_t qo = ((ks / 4) * (128 * 128) + (ks % 4) * 32) >> 4;
           auto mma = [&](int qp, int kp, uint32_t acc) {
-            if constexpr (C::QSMEM) tc::mma_f16_warp(d, dq + qo + ((qp * D * 256) >> 4), kb + ko + ((kp * C::part) >> 4), idesc, acc);
+            if constexpr (C::QSMEM) tc::mma_f16_warp(d, qd + qo + ((qp * D * 256) >> 4), kb + ko + ((kp * C::part) >> 4), idesc, acc);
             else tc::mma_f16_ts_warp(d, q + qp * (D / 2) + ks * 8, kb + ko + ((kp * C::part) >> 4), idesc, acc);
           };
           mma(0, 0, ks > 0 ? 1u : 0u);
@@ -697,24 +698,25 @@ __device__ void tc_issue_pv(const ChunkArgs& a, const ChunkHeader& h, uint32_t s
   const uint64_t dv = tc::sdesc_sw128_mn(sb + C::off_v, C::TK * 128);
   ChunkWalk walk;
   walk.begin(a, h, blockIdx.x);
-  TcUse<C::NG> use{false, {0, 0}};
-  int ct = 0, s = 0;
-  uint32_t phase = 0;
+  bool both;
+  int s = 0;
+  uint32_t phase = 0, n0 = 0, n1 = 0;
 #pragma unroll 1
-  for (int nt; (nt = tc_next_tiles(walk, a, h, use.both)) >= 0;) {
+  for (int nt; (nt = tc_next_tiles<C::NG == 2>(walk, a, h, both)) >= 0;) {
 #pragma unroll 1
-    for (int k = 0; k < nt; ++k, ++ct) {
+    for (int k = 0; k < nt; ++k) {
       const bool have = tc_wait(&sy->vfull[s], phase, sy, a.c.status);
       const uint64_t vb = dv + ((s * C::slot) >> 4);
-      const uint32_t first = k < (C::NG == 2 && !use.both ? 2 : 1) ? 0u : 1u;  // a group's first tile begins a new sum
+      const uint32_t first = k < (C::NG == 2 && !both ? 2 : 1) ? 0u : 1u;  // a group's first tile begins a new sum
 #pragma unroll 1
-      for (int i = 0; i < use.count(); ++i) {
-        const int b = use.first(k, ct) + i;
-        const uint32_t u = b ? use.used[1]++ : use.used[0]++;
-        const bool ok = have && tc_wait(&sy->pfull[b], u & 1, sy, a.c.status);
+      for (int i = 0; i < (both ? 2 : 1); ++i) {
+        const int g = C::NG == 1 ? 0 : both ? i : k & 1;
+        const uint32_t n = g ? n1++ : n0++;
+        const int b = tc_buffer<C>(g, n);
+        const bool ok = have && tc_wait(&sy->pfull[b], tc_turn<C>(n), sy, a.c.status);
         if (!__all_sync(0xffffffffu, ok)) continue;
         tc::fence_after_sync();
-        const uint32_t o = tmem + C::ocol + (C::NG == 2 ? b * D : 0), p = tmem + C::pcol + b * C::pstep;
+        const uint32_t o = tmem + C::ocol + g * D, p = tmem + C::pcol + b * C::pstep;
 #pragma unroll
         for (int ks = 0; ks < C::TK / 16; ++ks) {
           auto mma = [&](int pp, int vp, uint32_t acc) {
@@ -782,7 +784,7 @@ __device__ void tc_softmax(const ChunkArgs& a, const ChunkHeader& h, uint8_t* sm
   constexpr int TK = C::TK, NG = C::NG;
   uint32_t* status = a.c.status;
   const int grp = NG == 2 ? warp / 4 : 0, line = (warp & 3) * 32 + lane;
-  uint32_t used0 = 0, used1 = 0;  // uses of the buffers (with two groups: of the group's own, in used0)
+  uint32_t used = 0;  // the group's tiles
   const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16);
   auto all = [&]() {  // the softmax warps, TMEM contents included
     tc::fence_before_sync();
@@ -895,10 +897,13 @@ __device__ void tc_softmax(const ChunkArgs& a, const ChunkHeader& h, uint8_t* sm
               else hi[2 * i + e] = pack_h2(x, y);
             }
           if constexpr (C::QSMEM) {
-            const uint32_t at = smem_u32(sm) + C::off_q + (c / 2) * (128 * 128);
+            const uint32_t at = smem_u32(sm) + C::off_q + (both ? grp * PARTS * D * 256 : 0) + (c / 2) * (128 * 128);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i) {
               tc_sts128(at + tc::sw128_chunk(line, (c & 1) * 4 + i), *reinterpret_cast<uint32_t(*)[4]>(&hi[4 * i]));
+              if constexpr (PARTS == 2)
+                tc_sts128(at + D * 256 + tc::sw128_chunk(line, (c & 1) * 4 + i), *reinterpret_cast<uint32_t(*)[4]>(&lo[4 * i]));
+            }
           } else {
             const uint32_t qc = lanes + (both ? grp * C::qw : 0) + c * 16;
             tc::st_x16(qc, *reinterpret_cast<float(*)[16]>(&hi[0]));
@@ -919,9 +924,9 @@ __device__ void tc_softmax(const ChunkArgs& a, const ChunkHeader& h, uint8_t* sm
     bool nan = false;
     for (int k = 0; k < nt; ++k, ++ct) {
       if (NG == 2 && !both && (k & 1) != grp) continue;
-      const int b = NG == 2 ? grp : ct & 1;
-      const uint32_t u = NG == 2 || b == 0 ? used0++ : used1++;
-      bool ok = tc_wait(&sy->sfull[b], u & 1, sy, status);
+      const uint32_t n = used++;
+      const int b = tc_buffer<C>(grp, n);
+      bool ok = tc_wait(&sy->sfull[b], tc_turn<C>(n), sy, status);
       ok = __all_sync(0xffffffffu, ok);
       if (ok && busy) {
         tc::fence_after_sync();
@@ -992,9 +997,9 @@ __device__ void tc_softmax(const ChunkArgs& a, const ChunkHeader& h, uint8_t* sm
         vs = nvs;
         const float mb = m_used == -INFINITY ? 0.0f : m_used - 8.0f;
         // the weights' place is free once the product that read it is done; to rescale O, the group's last product has to be
-        if (u > 0) ok = tc_wait(&sy->odone[b], (u - 1) & 1, sy, status);
+        if (n >= C::SB) ok = tc_wait(&sy->odone[b], tc_turn<C>(n) ^ 1, sy, status);
         const bool resc = mine > 0 && __any_sync(0xffffffffu, move);
-        if (NG == 1 && resc) ok = tc_wait(&sy->odone[b ^ 1], ((b ? used0 : used1) - 1) & 1, sy, status) && ok;
+        if (C::SB == 2 && resc) ok = tc_wait(&sy->odone[tc_buffer<C>(grp, n - 1)], tc_turn<C>(n - 1), sy, status) && ok;
         ok = __all_sync(0xffffffffu, ok);
         if (ok) {
           tc::fence_after_sync();
@@ -1040,7 +1045,7 @@ __device__ void tc_softmax(const ChunkArgs& a, const ChunkHeader& h, uint8_t* sm
       } else {  // no rows: in step with the others all the same, or its arrivals would count for their next tile
         __syncwarp();
         if (!C::OVER && lane == 0) mbar_arrive(&sy->sfree[b]);
-        if (u > 0) tc_wait(&sy->odone[b], (u - 1) & 1, sy, status);
+        if (n >= C::SB) tc_wait(&sy->odone[b], tc_turn<C>(n) ^ 1, sy, status);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sy->pfull[b]);
@@ -1049,10 +1054,7 @@ __device__ void tc_softmax(const ChunkArgs& a, const ChunkHeader& h, uint8_t* sm
 
     // ---- the rows' results
     bool ok = true;
-    if (mine > 0) {  // the group's last product
-      const int b = NG == 2 ? grp : (ct - 1) & 1;
-      ok = tc_wait(&sy->odone[b], ((NG == 2 || b == 0 ? used0 : used1) - 1) & 1, sy, status);
-    }
+    if (mine > 0) ok = tc_wait(&sy->odone[tc_buffer<C>(grp, used - 1)], tc_turn<C>(used - 1), sy, status);  // the last product
     float M = m_used, f[2] = {1.0f, 0.0f};
     bool read[2] = {mine > 0, false};
     if (NG == 2 && !both) {
@@ -1187,11 +1189,12 @@ chunk_tc_kernel(ChunkArgs a, TcStage L, const __grid_constant__ CUtensorMap tmK,
       mbar_init(&sy->kfull[i], kTcConv / 2); mbar_init(&sy->kempty[i], 1);
       mbar_init(&sy->vfull[i], kTcConv / 2); mbar_init(&sy->vempty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&sy->sfull[i], 1); mbar_init(&sy->sfree[i], 4);
       mbar_init(&sy->pfull[i], 4); mbar_init(&sy->odone[i], 1);
-      mbar_init(&sy->fin[i], 1);
     }
+    mbar_init(&sy->fin[0], 1);
+    mbar_init(&sy->fin[1], 1);
     mbar_init(&sy->qready, C::kSoft / 32);
     sy->abort = 0;
     fence_barrier_init();

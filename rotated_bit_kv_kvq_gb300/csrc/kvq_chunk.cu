@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kSthreads<D>, 1) chunk_simple_kernel(ChunkArgs
       for (int e = 0; e < 4; ++e) o[i][e] = 0.0f;
     bool nan[2] = {false, false};
     for (int j = j0; j < j1; ++j) {
-      const ChunkTile t = chunk_tile(a, it, n, j);
+      const ChunkTile t = chunk_tile<kSt, kSt>(a, it, n, j);
       __syncthreads();  // the tile before is done with
       if (tid < 2) s_bad[tid] = 0;
       __syncthreads();

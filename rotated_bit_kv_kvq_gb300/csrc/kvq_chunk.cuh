@@ -77,18 +77,18 @@ struct ChunkTile {
   int t0, cnt;
   bool tail;
 };
+template <int TILE, int TAIL>  // (= a.tile, a.tail_tile)
 __device__ __forceinline__ ChunkTile chunk_tile(const ChunkArgs& a, const ChunkItem& it, int n, int j) {
   const int T = a.c.tail_len, body_end = n - T;
   if (j < it.n_body) {
-    const int t0 = it.lo / a.tile * a.tile + j * a.tile;
-    return ChunkTile{t0, min(a.tile, min(it.hi, body_end) - t0), false};
+    const int t0 = (it.lo / TILE + j) * TILE;
+    return ChunkTile{t0, min(TILE, min(it.hi, body_end) - t0), false};
   }
   j -= it.n_body;
   const int ts = max(it.lo, body_end), slot = ts - int(div_u32(uint32_t(ts), a.by_tail)) * T;
-  const int first = min(T - slot, it.hi - ts), n1 = (first + a.tail_tile - 1) / a.tail_tile;  // up to where the ring wraps
-  if (j < n1) return ChunkTile{ts + j * a.tail_tile, min(a.tail_tile, first - j * a.tail_tile), true};
-  const int t0 = ts + first + (j - n1) * a.tail_tile;
-  return ChunkTile{t0, min(a.tail_tile, it.hi - t0), true};
+  const int first = min(T - slot, it.hi - ts), n1 = int(uint32_t(first + TAIL - 1) / TAIL);  // up to where the ring wraps
+  const int t0 = ts + (j < n1 ? j * TAIL : first + (j - n1) * TAIL), end = j < n1 ? ts + first : it.hi;
+  return ChunkTile{t0, min(TAIL, end - t0), true};
 }
 
 // The keys that a row sees: [lo, hi)

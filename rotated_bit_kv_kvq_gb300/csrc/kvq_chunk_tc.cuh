@@ -317,15 +317,15 @@ __device__ __forceinline__ void tc_body_unit(const TcSide& u, int key, int blk, 
 
 // The same of a tail tile (bf16 rows, 128-byte box columns of TT rows)
 template <int D, int PARTS>
-__device__ __noinline__ void tc_tail_unit(const TcSide& u, int key, int blk, bool ok) {
+__device__ __noinline__ void tc_tail_unit(uint32_t rows, uint32_t dst, int pow, int key, int blk, bool ok) {
   using C = TC<D, PARTS>;
-  const uint32_t row = u.dst + (blk / 2) * (C::TK * 128) + key * 128;
-  const float scale = tc_pow2(u.scale);
+  const uint32_t row = dst + (blk / 2) * (C::TK * 128) + key * 128;
+  const float scale = tc_pow2(pow);
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
     uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};
     if (ok) {
-      const uint4 v = tc_lds128(u.codes + swz_off<128>(key, 64 * blk + 16 * c, C::TT));
+      const uint4 v = tc_lds128(rows + swz_off<128>(key, 64 * blk + 16 * c, C::TT));
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -389,8 +389,8 @@ __device__ __noinline__ uint32_t tc_header_max_finite(uint32_t hdr, int words, i
   return mx;
 }
 template <int D, int TT>
-__device__ __noinline__ uint32_t tc_tail_max(uint32_t rows, int cnt, bool& odd, int lane) {
-  uint32_t mx = 0;
+__device__ __noinline__ uint32_t tc_tail_max(uint32_t rows, int cnt, int lane) {  // (bit 31: not all are finite)
+  uint32_t mx = 0, odd = 0;
 #pragma unroll 4
   for (int i = lane; i < cnt * (D / 8); i += 32) {
     const uint4 q = tc_lds128(rows + swz_off<128>(i / (D / 8), i % (D / 8) * 16, TT));
@@ -398,7 +398,7 @@ __device__ __noinline__ uint32_t tc_tail_max(uint32_t rows, int cnt, bool& odd, 
   }
   mx = __reduce_max_sync(0xffffffffu, max(mx & 0xFFFFu, mx >> 16));
   if (mx >= 0x7F80u) {
-    odd = true;
+    odd = 1u << 31;
     mx = 0;
 #pragma unroll 1
     for (int i = lane; i < cnt * D; i += 32) {
@@ -407,11 +407,11 @@ __device__ __noinline__ uint32_t tc_tail_max(uint32_t rows, int cnt, bool& odd, 
     }
     mx = __reduce_max_sync(0xffffffffu, mx);
   }
-  return mx;
+  return mx | odd;
 }
 // The keys of a tile that are not finite
 template <int D, int TK, int TT>
-__device__ __noinline__ uint2 tc_not_finite(const TcStage& L, uint32_t st, int cnt, bool tail, int lane) {
+__device__ __noinline__ uint2 tc_not_finite(uint32_t k, uint32_t v, int kh, int vh, int cnt, bool tail, int lane) {
   uint2 bad = make_uint2(0u, 0u);
 #pragma unroll 1
   for (int h = 0; h < (TK + 31) / 32; ++h) {
@@ -419,13 +419,13 @@ __device__ __noinline__ uint2 tc_not_finite(const TcStage& L, uint32_t st, int c
     bool is = false;
     if (key < cnt && !tail) {
 #pragma unroll 1
-      for (int i = 0; i < L.kh / 2; ++i) is |= (tc_lds16(st + L.kd + key * L.kh + 2 * i) & 0x7FFFu) >= 0x7C00u;
+      for (int i = 0; i < kh / 2; ++i) is |= (tc_lds16(k + key * kh + 2 * i) & 0x7FFFu) >= 0x7C00u;
 #pragma unroll 1
-      for (int i = 0; i < L.vh / 2; ++i) is |= (tc_lds16(st + L.vd + key * L.vh + 2 * i) & 0x7FFFu) >= 0x7C00u;
+      for (int i = 0; i < vh / 2; ++i) is |= (tc_lds16(v + key * vh + 2 * i) & 0x7FFFu) >= 0x7C00u;
     } else if (key < cnt) {
 #pragma unroll 1
       for (int i = 0; i < 2 * D; ++i) {
-        const uint32_t base = st + (i >= D ? L.vt : 0);
+        const uint32_t base = i >= D ? v : k;
         is |= (tc_lds16(base + swz_off<128>(key, (i % D) * 2, TT)) & 0x7FFFu) >= 0x7F80u;
       }
     }
@@ -448,35 +448,39 @@ __device__ void tc_scout(const ChunkArgs& a, const TcStage& L, uint32_t ring, Tc
     const int cnt = int(job.y);
     const uint32_t st = ring + r * L.bytes;
     const bool tail = int(job.z) >= 0;
-    int scale[2] = {120, 120};
+    int kscale = 120, vscale = 120;
     bool odd = false;
-    if (cnt > 0 && !tail) {
-      uint32_t k = tc_header_max(st + L.kd, cnt * L.kh / 4, lane), v = tc_header_max(st + L.vd, cnt * L.vh / 4, lane);
-      uint32_t k0 = __reduce_max_sync(0xffffffffu, k & 0xFFFFu), k1 = __reduce_max_sync(0xffffffffu, k >> 16);
-      uint32_t v0 = __reduce_max_sync(0xffffffffu, v & 0xFFFFu), v1 = __reduce_max_sync(0xffffffffu, v >> 16);
-      if (max(max(k0, k1), max(v0, v1)) >= 0x7C00u) {
-        odd = true;
-        k = tc_header_max_finite(st + L.kd, cnt * L.kh / 4, lane);
-        v = tc_header_max_finite(st + L.vd, cnt * L.vh / 4, lane);
-        k0 = __reduce_max_sync(0xffffffffu, k & 0xFFFFu); k1 = __reduce_max_sync(0xffffffffu, k >> 16);
-        v0 = __reduce_max_sync(0xffffffffu, v & 0xFFFFu); v1 = __reduce_max_sync(0xffffffffu, v >> 16);
-      }
-      scale[0] = tc_body_scale<PARTS>(a.c.k_type, k0, k1);
-      scale[1] = tc_body_scale<PARTS>(a.c.v_type, v0, v1);
-    } else if (cnt > 0) {
-#pragma unroll
+    if (cnt > 0) {
+#pragma unroll 1
       for (int side = 0; side < 2; ++side) {
-        const uint32_t mx = tc_tail_max<D, C::TT>(st + (side ? L.vt : 0), cnt, odd, lane);
-        if (mx) scale[side] = min(120, 15 - tc_exp(bf16_bits_to_f32(mx)));
+        int e = 120;
+        if (!tail) {
+          const uint32_t hdr = st + (side ? L.vd : L.kd);
+          const int words = cnt * (side ? L.vh : L.kh) / 4;
+          uint32_t m = tc_header_max(hdr, words, lane);
+          uint32_t m0 = __reduce_max_sync(0xffffffffu, m & 0xFFFFu), m1 = __reduce_max_sync(0xffffffffu, m >> 16);
+          if (max(m0, m1) >= 0x7C00u) {
+            odd = true;
+            m = tc_header_max_finite(hdr, words, lane);
+            m0 = __reduce_max_sync(0xffffffffu, m & 0xFFFFu);
+            m1 = __reduce_max_sync(0xffffffffu, m >> 16);
+          }
+          e = tc_body_scale<PARTS>(side ? a.c.v_type : a.c.k_type, m0, m1);
+        } else {
+          const uint32_t mx = tc_tail_max<D, C::TT>(st + (side ? L.vt : 0), cnt, lane);
+          odd |= mx >> 31 != 0;
+          if (mx << 1) e = min(120, 15 - tc_exp(bf16_bits_to_f32(mx & 0x7FFFu)));
+        }
+        if (side) vscale = e; else kscale = e;
       }
     }
     uint2 bad = make_uint2(0u, 0u);
-    if (odd) bad = tc_not_finite<D, C::TK, C::TT>(L, st, cnt, tail, lane);
+    if (odd) bad = tc_not_finite<D, C::TK, C::TT>(st + (tail ? 0 : L.kd), st + (tail ? L.vt : L.vd), L.kh, L.vh, cnt, tail, lane);
     // values: the smallest scale of the segment so far, with some room when it has to come down
-    if (job.w || vs > scale[1]) vs = scale[1] - 2;
+    if (job.w || vs > vscale) vs = vscale - 2;
     if (lane == 0) {
       volatile TcMeta* m = &sy->meta[ct % kTcMeta];
-      m->t0 = int(job.x); m->cnt = cnt; m->ks = scale[0]; m->vs = vs;
+      m->t0 = int(job.x); m->cnt = cnt; m->ks = kscale; m->vs = vs;
       m->bad[0] = bad.x; m->bad[1] = bad.y;
       mbar_arrive(&sy->mfull[r]);
     }
@@ -515,7 +519,7 @@ __device__ void tc_convert(const ChunkArgs& a, const TcStage& L, uint32_t sb, Tc
     for (int i = warp % W; i < U; i += W) {
       const int h = i / NB, blk = i - h * NB, key = 32 * h + lane;
       if (!tail) tc_body_unit<D, PARTS>(x, key, blk, key < cnt);
-      else if (side == 1 || 32 * h < cnt) tc_tail_unit<D, PARTS>(x, key, blk, key < cnt);  // (scores past the end are masked)
+      else if (side == 1 || 32 * h < cnt) tc_tail_unit<D, PARTS>(x.codes, x.dst, x.scale, key, blk, key < cnt);  // (scores past the end are masked)
     }
     fence_proxy_async_smem();
     __syncwarp();
@@ -582,7 +586,7 @@ __device__ void tc_produce(const ChunkArgs& a, const TcStage& L, const ChunkHead
         job.y = -1;
       } else if (jb + lane < j1) {
         // from the last keys to the first: with a bias by distance the largest score comes first, and O is not rescaled
-        const ChunkTile t = chunk_tile(a, it, n, j1 - 1 - (jb + lane - j0));
+        const ChunkTile t = chunk_tile<C::TK, C::TT>(a, it, n, j1 - 1 - (jb + lane - j0));
         job = make_int4(t.t0, t.cnt, -1, jb + lane == j0);
         if (t.tail) {
           job.z = t.t0 - int(div_u32(uint32_t(t.t0), a.by_tail)) * T;

@@ -40,6 +40,7 @@ namespace {
 constexpr long long kTcWait = 2000000000LL;  // ~1 s per wait
 constexpr float kTcLazy = 7.0f;              // log2: weights stay below 2^(8 + 7)
 constexpr int kTcMaxStages = 8;
+constexpr int kTcSyncBytes = 7168;           // of TcSync, in front of everything else in shared memory
 constexpr int kTcMaxSlots = 4;
 constexpr int kTcMeta = 16;                  // (a tile's is read before the ring has come round and two more tiles are done)
 constexpr int kTcConv = 8;                   // converter warps, the first half for keys, the others for values
@@ -64,7 +65,7 @@ struct TC {
   static constexpr int part = D * TK * 2, slot = PARTS * part;  // a tile's operand
   // slots of each side: conversion may run that far ahead of the products (as many as leave room for a ring of three stages)
   static constexpr int NS = slot <= 8192 ? 4 : D == 192 ? 3 : 2;
-  static constexpr int off_q = 0, off_k = QSMEM ? NG * PARTS * D * 256 : 0, off_v = off_k + NS * slot, off_ring = off_v + NS * slot;
+  static constexpr int off_q = kTcSyncBytes, off_k = off_q + (QSMEM ? NG * PARTS * D * 256 : 0), off_v = off_k + NS * slot, off_ring = off_v + NS * slot;
   static constexpr int N1 = D > 256 ? 192 : D, N2 = D - N1;     // P V as one or two instructions
 };
 
@@ -86,21 +87,29 @@ struct TcSync {
   TcMeta meta[kTcMeta];
   float rowmax[2][128];
   float4 join[2][128];     // a group's (reference, sum, value scale, NaN) of each row
+  uint32_t* status;
   uint32_t tmem;
   int abort;
 };
+static_assert(sizeof(TcSync) <= kTcSyncBytes && kTcSyncBytes % 1024 == 0, "shared memory");
+
+// Where TcSync lies: the first 1024-byte boundary of the dynamic shared memory.
+__device__ __forceinline__ TcSync* tc_sync() {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  return reinterpret_cast<TcSync*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+}
 
 // Bounded wait; false once any wait of the CTA has given up.  (Code that seldom runs is kept out of line throughout: an SM's
 // instruction cache holds 32 KB, and the roles' loops have to fit it together: while they did not, every tile took 19 KB from
 // the cache that 18 SMs share, and a call 2.5 times as long.)
-// (without a time hint: 7% shorter calls than with one of 20 us)
-__device__ __forceinline__ bool tc_try(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
+__device__ __forceinline__ bool tc_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;  // (without a time hint: 7% shorter calls than with one of 20 us)
   asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-               : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+               : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
   return ok != 0;
 }
-__device__ __noinline__ bool tc_wait_long(uint64_t* bar, uint32_t parity, TcSync* sy, uint32_t* status) {
+__device__ __noinline__ bool tc_wait_long(uint32_t bar, uint32_t parity) {
+  TcSync* sy = tc_sync();
   const long long t0 = clock64();
 #pragma unroll 1
   for (;;) {
@@ -110,13 +119,14 @@ __device__ __noinline__ bool tc_wait_long(uint64_t* bar, uint32_t parity, TcSync
     if (*reinterpret_cast<volatile int*>(&sy->abort)) return false;
     if (clock64() - t0 > kTcWait) {
       *reinterpret_cast<volatile int*>(&sy->abort) = 1;
-      atomicOr(status, KVQ_DEV_ERR_TIMEOUT);
+      atomicOr(sy->status, KVQ_DEV_ERR_TIMEOUT);
       return false;
     }
   }
 }
-__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, TcSync* sy, uint32_t* status) {
-  return tc_try(bar, parity) || tc_wait_long(bar, parity, sy, status);
+__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity) {
+  const uint32_t at = smem_u32(bar);
+  return tc_try(at, parity) || tc_wait_long(at, parity);
 }
 
 __device__ __forceinline__ float tc_pow2(int e) {  // clamped to normal numbers
@@ -443,7 +453,7 @@ __device__ void tc_scout(const ChunkArgs& a, const TcStage& L, uint32_t ring, Tc
   uint32_t phase = 0;
 #pragma unroll 1
   for (int ct = 0;; ++ct) {
-    if (!tc_wait(&sy->rfull[r], phase, sy, a.c.status)) return;
+    if (!tc_wait(&sy->rfull[r], phase)) return;
     const uint4 job = tc_lds128(smem_u32(&sy->job[r]));
     const int cnt = int(job.y);
     const uint32_t st = ring + r * L.bytes;
@@ -493,7 +503,6 @@ template <int D, int PARTS>
 __device__ void tc_convert(const ChunkArgs& a, const TcStage& L, uint32_t sb, TcSync* sy, int warp, int lane) {
   using C = TC<D, PARTS>;
   constexpr int TK = C::TK, NB = C::NB, U = (TK + 31) / 32 * NB, W = kTcConv / 2;  // units of a tile, warps of a side
-  uint32_t* status = a.c.status;
   const int side = warp / W;
   uint64_t *empty = side ? sy->vempty : sy->kempty, *full = side ? sy->vfull : sy->kfull;
   TcSide x;
@@ -503,13 +512,13 @@ __device__ void tc_convert(const ChunkArgs& a, const TcStage& L, uint32_t sb, Tc
   uint32_t phase = 0, turn = 1;  // parities of the ring's round and of the slots' round before
 #pragma unroll 1
   for (int ct = 0;; ++ct) {
-    if (!tc_wait(&sy->rfull[r], phase, sy, status) || !tc_wait(&sy->mfull[r], phase, sy, status)) return;
+    if (!tc_wait(&sy->rfull[r], phase) || !tc_wait(&sy->mfull[r], phase)) return;
     const uint4 mt = tc_lds128(smem_u32(&sy->meta[ct % kTcMeta]));
     const int cnt = int(mt.y);
     if (cnt < 0) return;
     const bool tail = int(tc_lds32(smem_u32(&sy->job[r].z))) >= 0;
     const uint32_t st = sb + C::off_ring + r * L.bytes;
-    if (ct >= C::NS && !tc_wait(&empty[b], turn, sy, status)) return;
+    if (ct >= C::NS && !tc_wait(&empty[b], turn)) return;
     x.scale = int(side ? mt.w : mt.z);
     x.codes = st + (side ? (tail ? L.vt : L.v) : 0);
     x.hdr = st + (side ? L.vd : L.kd);
@@ -546,7 +555,7 @@ __device__ void tc_produce(const ChunkArgs& a, const TcStage& L, const ChunkHead
   int r = 0;
   uint32_t phase = 1;  // (a ring's first round waits for nothing)
   auto put = [&](int4 job, int row) {  // one lane
-    if (ct >= L.stages && !tc_wait(&sy->rempty[r], phase, sy, c.status)) return false;
+    if (ct >= L.stages && !tc_wait(&sy->rempty[r], phase)) return false;
     volatile int4* j = reinterpret_cast<volatile int4*>(&sy->job[r]);
     j->x = job.x; j->y = job.y; j->z = job.z; j->w = job.w;
     uint8_t* st = sm + C::off_ring + r * L.bytes;
@@ -655,17 +664,17 @@ __device__ void tc_issue_s(const ChunkArgs& a, const ChunkHeader& h, uint32_t sb
 #pragma unroll 1
   for (int nt; (nt = tc_next_tiles<C::NG == 2>(walk, a, h, both)) >= 0;) {
     if (nt == 0) continue;
-    tc_wait(&sy->qready, seg++ & 1, sy, a.c.status);
+    tc_wait(&sy->qready, seg++ & 1);
 #pragma unroll 1
     for (int k = 0; k < nt; ++k) {
-      const bool have = tc_wait(&sy->kfull[s], phase, sy, a.c.status);
+      const bool have = tc_wait(&sy->kfull[s], phase);
       const uint64_t kb = dk + ((s * C::slot) >> 4);
 #pragma unroll 1
       for (int i = 0; i < (both ? 2 : 1); ++i) {
         const int g = C::NG == 1 ? 0 : both ? i : k & 1;
         const uint32_t n = g ? n1++ : n0++;
         const int b = tc_buffer<C>(g, n);
-        const bool ok = have && (n < C::SB || tc_wait(C::OVER ? &sy->odone[b] : &sy->sfree[b], tc_turn<C>(n) ^ 1, sy, a.c.status));
+        const bool ok = have && (n < C::SB || tc_wait(C::OVER ? &sy->odone[b] : &sy->sfree[b], tc_turn<C>(n) ^ 1));
         if (!__all_sync(0xffffffffu, ok)) continue;
         tc::fence_after_sync();
         const uint32_t d = tmem + C::scol + b * C::TK, q = tmem + (both ? g * C::qw : 0);
@@ -709,7 +718,7 @@ __device__ void tc_issue_pv(const ChunkArgs& a, const ChunkHeader& h, uint32_t s
   for (int nt; (nt = tc_next_tiles<C::NG == 2>(walk, a, h, both)) >= 0;) {
 #pragma unroll 1
     for (int k = 0; k < nt; ++k) {
-      const bool have = tc_wait(&sy->vfull[s], phase, sy, a.c.status);
+      const bool have = tc_wait(&sy->vfull[s], phase);
       const uint64_t vb = dv + ((s * C::slot) >> 4);
       const uint32_t first = k < (C::NG == 2 && !both ? 2 : 1) ? 0u : 1u;  // a group's first tile begins a new sum
 #pragma unroll 1
@@ -717,7 +726,7 @@ __device__ void tc_issue_pv(const ChunkArgs& a, const ChunkHeader& h, uint32_t s
         const int g = C::NG == 1 ? 0 : both ? i : k & 1;
         const uint32_t n = g ? n1++ : n0++;
         const int b = tc_buffer<C>(g, n);
-        const bool ok = have && tc_wait(&sy->pfull[b], tc_turn<C>(n), sy, a.c.status);
+        const bool ok = have && tc_wait(&sy->pfull[b], tc_turn<C>(n));
         if (!__all_sync(0xffffffffu, ok)) continue;
         tc::fence_after_sync();
         const uint32_t o = tmem + C::ocol + g * D, p = tmem + C::pcol + b * C::pstep;
@@ -809,7 +818,7 @@ __device__ void tc_softmax(const ChunkArgs& a, const ChunkHeader& h, uint8_t* sm
     const bool whole = nt == nk, have = row < it.rows, busy = (both ? grp * 128 : 0) + (warp & 3) * 32 < it.rows;  // busy: the warp has rows
     const int w = have ? it.r0 + row : it.r0, tok = int(div_u32(uint32_t(w), a.by_group)), hh = w - tok * a.group;
     const size_t base = ((size_t)(row0 + tok) * a.n_q_heads + kvh * a.group + hh) * D;
-    ChunkSpan span{0, 0, 0};
+    ChunkSpan span{0, 0x7fffffff, 0};  // (lanes without a row mask nothing)
     float slope2 = 0.0f;
     int qs = 0;
     if (nt > 0) {
@@ -930,7 +939,7 @@ __device__ void tc_softmax(const ChunkArgs& a, const ChunkHeader& h, uint8_t* sm
       if (NG == 2 && !both && (k & 1) != grp) continue;
       const uint32_t n = used++;
       const int b = tc_buffer<C>(grp, n);
-      bool ok = tc_wait(&sy->sfull[b], tc_turn<C>(n), sy, status);
+      bool ok = tc_wait(&sy->sfull[b], tc_turn<C>(n));
       ok = __all_sync(0xffffffffu, ok);
       if (ok && busy) {
         tc::fence_after_sync();
@@ -943,6 +952,7 @@ __device__ void tc_softmax(const ChunkArgs& a, const ChunkHeader& h, uint8_t* sm
         if (bad0 | bad1) nan |= tc_sees(bad0, bad1, lo, hi);
         // scores that are capped, biased or masked: 16 columns at a time, back to TMEM, times f
         const uint32_t sc0 = lanes + C::scol + b * TK;
+        float mt2 = -INFINITY;
         if (changed) {
 #pragma unroll 1
           for (int c0 = 0; c0 < TK; c0 += 16) {
@@ -972,12 +982,14 @@ __device__ void tc_softmax(const ChunkArgs& a, const ChunkHeader& h, uint8_t* sm
             for (int c = 0; c < 16; ++c)
               if (from + c >= room) sv[c] = -INFINITY;
             tc::st_x16(sc0 + c0, sv);
+            float mx[2] = {sv[0], sv[1]};
+#pragma unroll
+            for (int c = 2; c < 16; ++c) mx[c & 1] = fmaxf(mx[c & 1], sv[c]);
+            mt2 = fmaxf(mt2, fmaxf(mx[0], mx[1]));
           }
           tc::wait_st();
           f = 1.0f;
-        }
-        float mt2;
-        {
+        } else {
           float sv[TK];
 #pragma unroll
           for (int c = 0; c < TK; c += 16) tc::ld_x16(sc0 + c, *reinterpret_cast<float(*)[16]>(&sv[c]));
@@ -1001,9 +1013,9 @@ __device__ void tc_softmax(const ChunkArgs& a, const ChunkHeader& h, uint8_t* sm
         vs = nvs;
         const float mb = m_used == -INFINITY ? 0.0f : m_used - 8.0f;
         // the weights' place is free once the product that read it is done; to rescale O, the group's last product has to be
-        if (n >= C::SB) ok = tc_wait(&sy->odone[b], tc_turn<C>(n) ^ 1, sy, status);
+        if (n >= C::SB) ok = tc_wait(&sy->odone[b], tc_turn<C>(n) ^ 1);
         const bool resc = mine > 0 && __any_sync(0xffffffffu, move);
-        if (C::SB == 2 && resc) ok = tc_wait(&sy->odone[tc_buffer<C>(grp, n - 1)], tc_turn<C>(n - 1), sy, status) && ok;
+        if (C::SB == 2 && resc) ok = tc_wait(&sy->odone[tc_buffer<C>(grp, n - 1)], tc_turn<C>(n - 1)) && ok;
         ok = __all_sync(0xffffffffu, ok);
         if (ok) {
           tc::fence_after_sync();
@@ -1049,7 +1061,7 @@ __device__ void tc_softmax(const ChunkArgs& a, const ChunkHeader& h, uint8_t* sm
       } else {  // no rows: in step with the others all the same, or its arrivals would count for their next tile
         __syncwarp();
         if (!C::OVER && lane == 0) mbar_arrive(&sy->sfree[b]);
-        if (n >= C::SB) tc_wait(&sy->odone[b], tc_turn<C>(n) ^ 1, sy, status);
+        if (n >= C::SB) tc_wait(&sy->odone[b], tc_turn<C>(n) ^ 1);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sy->pfull[b]);
@@ -1058,7 +1070,7 @@ __device__ void tc_softmax(const ChunkArgs& a, const ChunkHeader& h, uint8_t* sm
 
     // ---- the rows' results
     bool ok = true;
-    if (mine > 0) ok = tc_wait(&sy->odone[tc_buffer<C>(grp, used - 1)], tc_turn<C>(used - 1), sy, status);  // the last product
+    if (mine > 0) ok = tc_wait(&sy->odone[tc_buffer<C>(grp, used - 1)], tc_turn<C>(used - 1));  // the last product
     float M = m_used, f[2] = {1.0f, 0.0f};
     bool read[2] = {mine > 0, false};
     if (NG == 2 && !both) {
@@ -1175,7 +1187,7 @@ chunk_tc_kernel(ChunkArgs a, TcStage L, const __grid_constant__ CUtensorMap tmK,
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   pdl_begin();
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  TcSync* sy = reinterpret_cast<TcSync*>(sm + C::off_ring + L.stages * L.bytes);
+  TcSync* sy = tc_sync();
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const ChunkHeader h = *a.head;
   if (!h.ok || int(blockIdx.x) >= h.pieces) return;  // (the whole CTA)
@@ -1201,6 +1213,7 @@ chunk_tc_kernel(ChunkArgs a, TcStage L, const __grid_constant__ CUtensorMap tmK,
     mbar_init(&sy->fin[1], 1);
     mbar_init(&sy->qready, C::kSoft / 32);
     sy->abort = 0;
+    sy->status = a.c.status;
     fence_barrier_init();
     prefetch_tmap(&tmK);
     prefetch_tmap(&tmV);
@@ -1257,11 +1270,11 @@ cudaError_t run_chunk_tc(ChunkArgs& a, cudaStream_t st) {
   s.tx = uint32_t(C::TK * (rowK + rowV + s.kh + s.vh) + kq + vq);
   s.vt = align_up(C::TT * 2 * D, 1024);
   s.bytes = align_up(std::max(s.vqh + vq, c.tail_len > 0 ? s.vt + C::TT * 2 * D : 0), 1024);
-  const int room = 232448 - 1024 - C::off_ring - int(sizeof(TcSync));
+  const int room = 232448 - 1024 - C::off_ring;
   s.stages = std::min(kTcMaxStages, room / s.bytes);
   if (s.stages < 1) return cudaErrorInvalidValue;
   // (more than half of an SM's, so that no two CTAs of one SM ask for all of TMEM)
-  const int bytes = std::max(120 * 1024, C::off_ring + s.stages * s.bytes + int(sizeof(TcSync)) + 1024);
+  const int bytes = std::max(120 * 1024, C::off_ring + s.stages * s.bytes + 1024);
 
   alignas(64) CUtensorMap mk, mv, mkt, mvt;
   memset(&mkt, 0, sizeof(mkt));

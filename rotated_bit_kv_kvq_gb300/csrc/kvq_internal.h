@@ -266,7 +266,8 @@ struct ForkArgs {
   const int32_t *src, *dst, *n_tokens;  // n_tokens may be NULL
   int n_forks;
   int32_t *granted, *seq_len_out;
-  int units, tail_rows, tail_pieces;   // units of a fork, tail rows of a unit, units of a (side, KV head)
+  int units, parts;                    // units of a fork's copy, and the CTAs that share them
+  int tail_rows, tail_pieces;          // tail rows of a unit, units of a (side, KV head)
   DivU32 by_row;                       // 16-byte pieces of a tail row
 };
 struct CompactArgs {

@@ -34,6 +34,9 @@ __device__ __forceinline__ int held_pages(int len, const ShareArgs& a) {  // 0 f
   return len >= 0 && len <= a.max_ctx ? int((uint32_t(len) + uint32_t(a.page_tokens) - 1) / uint32_t(a.page_tokens)) : 0;
 }
 
+// Pages that a plan's CTA scans at a time, four consecutive ones a thread
+constexpr int kScan = 4 * kPlanThreads;
+
 // Inclusive sums over a block of kPlanThreads; s: 32 ints.  Returns this thread's, and the block's in total.
 __device__ __forceinline__ int block_sums(int v, int* s, int& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -165,20 +168,21 @@ __global__ void __launch_bounds__(kPlanThreads, 1) fork_plan_kernel(ShareArgs a,
   }
 }
 
-// Units of a fork: its table row and length, the pieces of the page that is copied, the pieces of its tail.
+// Units of a fork: its table row and length, the pieces of the page that is copied, the pieces of its tail.  A CTA takes every
+// parts-th unit of a fork: one look at the fork's numbers for many units (a look a unit: 95 us for 64 forks with tails of 512
+// tokens, 2 MB each).
 __global__ void __launch_bounds__(kCopyThreads, kCopyCtas) fork_copy_kernel(ShareArgs a, ForkArgs f) {
   pdl_begin();
   const int P = a.page_tokens, per_seq = a.max_ctx / P, tid = threadIdx.x;
   const kvq_cache& c = f.c;
   const int T = c.tail_len, D = c.head_dim, H = c.n_kv_heads;
-  for (long long w = blockIdx.x; w < (long long)f.n_forks * f.units; w += gridDim.x) {
-    // units of a kind lie together: all table rows, then all pages, then all tails
-    const int u = int(w / f.n_forks), i = int(w - (long long)u * f.n_forks);
+  for (long long w = blockIdx.x; w < (long long)f.n_forks * f.parts; w += gridDim.x) {
+    const int i = int(w / f.parts), part = int(w - (long long)i * f.parts);
     const int n = f.granted[i];
     if (n < 0) continue;
     const int src = f.src[i], dst = f.dst[i];
     const int32_t* from = a.table + (long long)src * per_seq;
-    if (u == 0) {
+    if (part == 0) {
       if (tid == 0) f.seq_len_out[dst] = n;
       for (int j = tid; j < n / P; j += kCopyThreads) {
         const int pg = from[j];
@@ -186,57 +190,56 @@ __global__ void __launch_bounds__(kCopyThreads, kCopyCtas) fork_copy_kernel(Shar
         if (pg >= 0 && pg < a.n_pages) atomicAdd(&a.share.next[pg], 1);
         else atomicOr(a.status, KVQ_DEV_ERR_PAGE);
       }
-    } else if (u <= a.page_units) {
-      if (n % P == 0) continue;
-      const int old = from[n / P], pg = a.table[(long long)dst * per_seq + n / P];
-      if (old >= 0 && old < a.n_pages) copy_page_unit(a, u - 1, pg, old);
-      else if (tid == 0) atomicOr(a.status, KVQ_DEV_ERR_PAGE);
-    } else if (n > 0) {
+    }
+    if (n == 0) continue;
+    const int old = n % P ? from[n / P] : 0, fresh = n % P ? a.table[(long long)dst * per_seq + n / P] : 0;
+    const int first = a.seq_len[src] - T, r0 = T > 0 ? n % T : 0;
+    const bool page_ok = old >= 0 && old < a.n_pages;
+    if (!page_ok && part == 0 && tid == 0) atomicOr(a.status, KVQ_DEV_ERR_PAGE);
+    for (int u = part; u < f.units; u += f.parts) {
+      if (u < a.page_units) {
+        if (n % P && page_ok) copy_page_unit(a, u, fresh, old);
+        continue;
+      }
       // tail slots s0 .. of (side, KV head): slot s holds the position p = s (mod T) of the last T
-      int v = u - 1 - a.page_units;
+      int v = u - a.page_units;
       const int piece = v % f.tail_pieces, h = (v /= f.tail_pieces) % H;
       const bool k = v / H == 0;
-      const int s0 = piece * f.tail_rows, rows = min(f.tail_rows, T - s0), r0 = n % T, first = a.seq_len[src] - T;
+      const int s0 = piece * f.tail_rows, rows = min(f.tail_rows, T - s0);
       uint8_t* plane = static_cast<uint8_t*>(k ? c.k_tail : c.v_tail);
       const uint8_t* in = plane + ((long long)src * H + h) * T * (2 * D);
       uint8_t* out = plane + ((long long)dst * H + h) * T * (2 * D);
-      const BodySide side = body_side(c, k);
-      const int per_row = D / 8;
-      const int chunks = rows * per_row;
       auto position = [&](int s) { return n - r0 + s - (s < r0 ? 0 : T); };
-      for (int j0 = tid; j0 < chunks; j0 += 4 * kCopyThreads) {
-        uint4 x[4];
-        long long at[4];
-        int p[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int j = j0 + q * kCopyThreads;
-          const int r = int(div_u32(uint32_t(j), f.by_row)), s = s0 + r;
-          p[q] = j < chunks ? position(s) : -1;
-          at[q] = ((long long)s * per_row + j - r * per_row) * 16;
-          x[q] = p[q] >= 0 && p[q] >= first ? *reinterpret_cast<const uint4*>(in + at[q]) : make_uint4(0u, 0u, 0u, 0u);
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if (p[q] < 0) continue;
-          if (p[q] < first) {  // the source's tail has moved on: the stored values, rounded to bf16
-            const long long row = body_row(row_map(c), src, h, p[q]);
-            if (row < 0) {
-              atomicOr(a.status, KVQ_DEV_ERR_PAGE);
-              continue;
-            }
-            float y[8];
-            body_values8(side, D, row, int(at[q] / 16 % per_row), y);
-            uint32_t wds[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const __nv_bfloat162 b2 = __floats2bfloat162_rn(y[2 * e], y[2 * e + 1]);
-              wds[e] = *reinterpret_cast<const uint32_t*>(&b2);
-            }
-            x[q] = make_uint4(wds[0], wds[1], wds[2], wds[3]);
+      if (n >= T && n - T >= first) {  // every slot is copied as it is
+        copy_unit(out + (long long)s0 * 2 * D, in + (long long)s0 * 2 * D, rows * 2 * D);
+        continue;
+      }
+      const BodySide side = body_side(c, k);
+      const int per_row = D / 8, chunks = rows * per_row;
+      for (int j = tid; j < chunks; j += kCopyThreads) {
+        const int r = int(div_u32(uint32_t(j), f.by_row)), s = s0 + r, ch = j - r * per_row, p = position(s);
+        if (p < 0) continue;
+        const long long at = ((long long)s * per_row + ch) * 16;
+        uint4 x;
+        if (p >= first) {
+          x = *reinterpret_cast<const uint4*>(in + at);
+        } else {  // the source's tail has moved on: the stored values, rounded to bf16
+          const long long row = body_row(row_map(c), src, h, p);
+          if (row < 0) {
+            atomicOr(a.status, KVQ_DEV_ERR_PAGE);
+            continue;
           }
-          *reinterpret_cast<uint4*>(out + at[q]) = x[q];
+          float y[8];
+          body_values8(side, D, row, ch, y);
+          uint32_t wds[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 b2 = __floats2bfloat162_rn(y[2 * e], y[2 * e + 1]);
+            wds[e] = *reinterpret_cast<const uint32_t*>(&b2);
+          }
+          x = make_uint4(wds[0], wds[1], wds[2], wds[3]);
         }
+        *reinterpret_cast<uint4*>(out + at) = x;
       }
     }
   }
@@ -276,6 +279,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) free_kernel(ShareArgs a, cons
   const int chunk = int(((long long)a.n_pages + S - 1) / S), p0 = int(min((long long)a.n_pages, (long long)rank * chunk)),
             p1 = int(min((long long)a.n_pages, (long long)p0 + chunk));
   int mine = 0;
+#pragma unroll 4
   for (int p = p0 + tid; p < p1; p += kPlanThreads) mine += __ldcg(&a.share.next[p]) < 0;
   int total;
   block_sums(mine, s_sum, total);
@@ -288,17 +292,27 @@ __global__ void __launch_bounds__(kPlanThreads, 1) free_kernel(ShareArgs a, cons
     all += t;
   }
   const int room = a.n_pages - count;  // (a bad state: nothing is free below)
-  for (int q = p0; pool && q < p1; q += kPlanThreads) {
-    const int p = q + tid, v = p < p1 ? __ldcg(&a.share.next[p]) : 0;
-    const int at = before + block_sums(v < 0, s_sum, total) - (v < 0);
-    if (v < 0) {
-      if (v < -1) err |= KVQ_DEV_ERR_PAGE;  // given back more often than it was held
+  for (int q = p0; pool && q < p1; q += kScan) {
+    int v[4], free = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int p = q + 4 * tid + e;
+      v[e] = p < p1 ? __ldcg(&a.share.next[p]) : 0;
+      free += v[e] < 0;
+    }
+    int at = before + block_sums(free, s_sum, total) - free;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int p = q + 4 * tid + e;
+      if (v[e] >= 0) continue;
+      if (v[e] < -1) err |= KVQ_DEV_ERR_PAGE;  // given back more often than it was held
       a.share.next[p] = 0;
       if (at < room) {
         long long i = (long long)head + count + at;
         while (i >= a.n_pages) i -= a.n_pages;
         a.pool.ring[i] = p;
       }
+      ++at;
     }
     before += total;
   }
@@ -363,6 +377,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) compact_plan_kernel(ShareArgs
   const int chunk = int(((long long)a.n_pages + S - 1) / S), p0 = int(min((long long)a.n_pages, (long long)rank * chunk)),
             p1 = int(min((long long)a.n_pages, (long long)p0 + chunk));
   int live = 0, hand = 0, total;
+#pragma unroll 4
   for (int p = p0 + tid; p < p1; p += kPlanThreads) {
     const int k = __ldcg(&m.mark[p]);
     live += (k & 2) != 0;
@@ -383,11 +398,25 @@ __global__ void __launch_bounds__(kPlanThreads, 1) compact_plan_kernel(ShareArgs
     n_hand += h;
   }
   // live pages among the n_live lowest
+  auto marks = [&](int q, int (&k)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int p = q + 4 * tid + e;
+      k[e] = p < p1 ? __ldcg(&m.mark[p]) : 0;
+    }
+  };
   int low = 0;
-  for (int q = p0, h0 = hand0; q < p1; q += kPlanThreads) {
-    const int p = q + tid, k = p < p1 ? __ldcg(&m.mark[p]) : 0;
-    const int at = h0 + block_sums(k != 0, s_sum, total) - (k != 0);
-    low += (k & 2) && at < n_live;
+  for (int q = p0, h0 = hand0; q < p1; q += kScan) {
+    int k[4], n = 0;
+    marks(q, k);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) n += k[e] != 0;
+    int at = h0 + block_sums(n, s_sum, total) - n;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      low += (k[e] & 2) && at < n_live;
+      at += k[e] != 0;
+    }
     h0 += total;
   }
   block_sums(low, s_sum, total);
@@ -399,18 +428,29 @@ __global__ void __launch_bounds__(kPlanThreads, 1) compact_plan_kernel(ShareArgs
   int32_t *from = m.moves + 1, *to = from + a.n_pages;
   if (!any_bad) {
     int free0 = hand0 - live0;
-    for (int q = p0; q < p1; q += kPlanThreads) {
-      const int p = q + tid, k = p < p1 ? __ldcg(&m.mark[p]) : 0;
-      const int isl = (k & 2) != 0, isf = k == 1;
-      const int al = live0 + block_sums(isl, s_sum, total) - isl;
+    for (int q = p0; q < p1; q += kScan) {
+      int k[4], isl = 0, isf = 0;
+      marks(q, k);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        isl += (k[e] & 2) != 0;
+        isf += k[e] == 1;
+      }
+      int al = live0 + block_sums(isl, s_sum, total) - isl;
       live0 += total;
-      const int af = free0 + block_sums(isf, s_sum, total) - isf;
+      int af = free0 + block_sums(isf, s_sum, total) - isf;
       free0 += total;
-      if (k && al + af < n_live) {
-        if (isf) to[af] = p;
-      } else if (k) {
-        if (isl) from[al - n_low] = p;
-        m.ring_out[al + af - n_live] = p;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int p = q + 4 * tid + e;
+        if (k[e] && al + af < n_live) {
+          if (k[e] == 1) to[af] = p;
+        } else if (k[e]) {
+          if (k[e] & 2) from[al - n_low] = p;
+          m.ring_out[al + af - n_live] = p;
+        }
+        al += (k[e] & 2) != 0;
+        af += k[e] == 1;
       }
     }
     for (int i = n_hand - n_live + gt; i < a.n_pages; i += nt) m.ring_out[i] = -1;
@@ -441,9 +481,17 @@ __global__ void __launch_bounds__(kCopyThreads, kCopyCtas) compact_copy_kernel(S
   const int n = m.moves[0], per_seq = a.max_ctx / a.page_tokens;
   const int32_t *from = m.moves + 1, *to = from + a.n_pages;
   const long long work = (long long)n * a.page_units;
+  int i = int(blockIdx.x / a.page_units);
+  int t = blockIdx.x < work ? to[i] : 0, f = blockIdx.x < work ? from[i] : 0;
   for (long long w = blockIdx.x; w < work; w += gridDim.x) {
-    const int i = int(w / a.page_units);
-    copy_page_unit(a, int(w - (long long)i * a.page_units), to[i], from[i]);
+    const long long next = w + gridDim.x;
+    const int u = int(w - (long long)i * a.page_units), t0 = t, f0 = f;
+    i = int(next / a.page_units);
+    if (next < work) {  // (known when its turn comes)
+      t = to[i];
+      f = from[i];
+    }
+    copy_page_unit(a, u, t0, f0);
   }
   const long long entries = (long long)a.batch * per_seq;
   for (long long e = (long long)blockIdx.x * kCopyThreads + threadIdx.x; e < entries; e += (long long)gridDim.x * kCopyThreads) {
@@ -494,12 +542,13 @@ cudaError_t launch_page_fork(const kvq_cache& c, const kvq_page_pool& pool, cons
   f.tail_rows = std::max(1, kCopyBytes / (2 * c.head_dim));
   f.tail_pieces = (c.tail_len + f.tail_rows - 1) / f.tail_rows;
   f.by_row = make_divu32(uint32_t(c.head_dim / 8));
-  f.units = 1 + a.page_units + 2 * c.n_kv_heads * f.tail_pieces;
+  f.units = a.page_units + 2 * c.n_kv_heads * f.tail_pieces;
+  f.parts = int(std::max<long long>(1, std::min<long long>(f.units, 2LL * sms() * kCopyCtas / f.n_forks)));
   const bool elsewhere = share.next != share.count || f.seq_len_out != c.seq_len;
   const int more = elsewhere ? int(std::min<long long>(sms(), ((long long)std::max(c.n_pages, c.batch) + kPlanThreads - 1) / kPlanThreads)) : 0;
   cudaError_t e = launch_dependent(fork_plan_kernel, unsigned(1 + more), kPlanThreads, 0, st, 1, a, f);
   if (e != cudaSuccess) return e;
-  const long long work = (long long)f.n_forks * f.units;
+  const long long work = (long long)f.n_forks * f.parts;
   return launch_dependent(fork_copy_kernel, unsigned(std::min<long long>(work, (long long)sms() * kCopyCtas)), kCopyThreads, 0, st, 1, a, f);
 }
 

@@ -1,4 +1,4 @@
-// What the kernels of kvq_chunk_attention share: the plan of a call and the score of a (row, key).
+// What the kernels of kvq_chunk_attention share: the plan of a call.
 //
 // A row of work is a (token, query head of a KV head): the rows of a sequence, token by token and a token's heads together,
 // are cut into items of `m` rows.  An item's keys lie between the smallest first key and the largest end of its rows; they
@@ -55,7 +55,7 @@ struct ChunkArgs {
   float2* part_ml;        // [2 * ctas][m]: their reference (log2) and sum of weights
 };
 
-// What a kernel's items and tiles are: rows, keys, tail rows (m 0: there is no such kernel).
+// What a kernel's items and tiles are: rows, keys, tail rows.
 struct ChunkTiles {
   int m, tile, tail_tile;
 };
@@ -144,11 +144,5 @@ struct ChunkWalk {
     return false;
   }
 };
-
-// Scores: cap and bias, natural units (dist: |position - t|)
-__device__ __forceinline__ float soft_cap(float s, float cap, float two_log2e_over_cap) {
-  // cap tanh(s / cap) = cap - 2 cap / (e^(2 s / cap) + 1)
-  return fmaf(-2.0f * cap, __frcp_rn(1.0f + ex2_approx(s * two_log2e_over_cap)), cap);
-}
 
 }  // namespace kvq

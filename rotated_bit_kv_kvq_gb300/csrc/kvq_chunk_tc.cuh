@@ -48,12 +48,14 @@ constexpr int kTcConv = 8;                   // converter warps, the first half 
 template <int D, int PARTS>
 struct TC {
   static constexpr int NG = D <= 64 * (3 - PARTS) ? 2 : 1;     // groups of softmax warps, each with an O of its own
-  static constexpr int TK = D == 320 ? 32 : 64;                // keys of a tile
-  static constexpr int TT = D == 64 ? 64 : D <= 256 ? 32 : 16;  // tail rows of a tile
+  // keys of a tile, and tail rows of one (as many as shared memory has room for)
+  static constexpr int TK = PARTS == 1 ? (D == 320 ? 32 : 64) : D <= 128 ? 64 : D <= 256 ? 32 : 16;
+  static constexpr int TT = PARTS == 1 ? (D == 64 ? 64 : D <= 256 ? 32 : 16) : D == 64 ? 64 : D <= 192 ? 32 : D == 256 ? 16 : 8;
+  static_assert(TT <= TK, "");
   static constexpr int SB = NG == 2 && PARTS == 2 ? 1 : 2;     // score buffers of a group: with two, S of the next tile is ready
-  static constexpr bool QSMEM = D == 320 || (D == 128 && PARTS == 1);  // (TMEM has no room for the queries)
-  static constexpr bool OVER = D == 256 || (NG == 2 && SB == 2);  // P over S (TMEM again)
-  static constexpr int KH = TK / 32;                           // keys of a converting lane
+  static constexpr bool QSMEM = D == 320 || (D == 128 && PARTS == 1) || (D == 256 && PARTS == 2);  // (TMEM has no room for the queries)
+  static constexpr bool OVER = PARTS == 1 && (D == 256 || NG == 2);  // P over S (TMEM again)
+  static constexpr int KH = (TK + 31) / 32;                    // keys of a converting lane
   static constexpr int M = NG * 128;                           // rows of an item
   static constexpr int G = (D & (D - 1)) == 0 ? D : 64, GC = G / 32, NB = D / 32;
   static constexpr int kSoft = NG * 128, kThreads = kSoft + (kTcConv + 4) * 32;
@@ -65,7 +67,7 @@ struct TC {
   // shared memory
   static constexpr int part = D * TK * 2, slot = PARTS * part;  // a tile's operand
   // slots of each side: conversion may run that far ahead of the products (as many as leave room for a ring of three stages)
-  static constexpr int NS = slot <= 8192 ? 4 : D == 192 ? 3 : 2;
+  static constexpr int NS = slot <= 8192 ? 4 : D == 192 ? 3 : PARTS == 2 && D >= 256 ? 1 : 2;
   static constexpr int off_q = kTcSyncBytes, off_k = off_q + (QSMEM ? NG * PARTS * D * 256 : 0), off_v = off_k + NS * slot, off_ring = off_v + NS * slot;
   static constexpr int N1 = D > 256 ? 192 : D, N2 = D - N1;     // P V as one or two instructions
 };
@@ -327,6 +329,7 @@ __device__ __forceinline__ void tc_body_unit(const TcSide& u, int lane, int blk,
       fd = __half2float(__ushort_as_half(uint16_t(tc_lds16(u.hdr + (key * NB + blk) * 2))));
       fm = 0.0f;
     }
+    if (KH * 32 > TC<D, PARTS>::TK && key >= TC<D, PARTS>::TK) return;  // (half a warp's keys)
     if (key >= cnt || !(fabsf(fd) <= 65504.0f) || !(fabsf(fm) <= 65504.0f)) fd = fm = 0.0f;  // past the end, or noted as not finite
     fd *= sc;
     fm *= sc;
@@ -1339,17 +1342,13 @@ cudaError_t run_chunk_tc(ChunkArgs& a, cudaStream_t st) {
   return launch_dependent(kern, unsigned(a.ctas), C::kThreads, bytes, st, 1, a, s, mk, mv, mkt, mvt);
 }
 
-constexpr int tc_max_parts(int d) { return d <= 128 ? 2 : 1; }  // (two parts of wider operands do not fit)
 template <int D>
 ChunkTiles tc_tiles(int parts) {
-  if (parts > tc_max_parts(D)) return ChunkTiles{0, 0, 0};
-  return ChunkTiles{parts == 1 ? TC<D, 1>::M : TC<D, tc_max_parts(D)>::M, TC<D, 1>::TK, TC<D, 1>::TT};
+  return parts == 1 ? ChunkTiles{TC<D, 1>::M, TC<D, 1>::TK, TC<D, 1>::TT} : ChunkTiles{TC<D, 2>::M, TC<D, 2>::TK, TC<D, 2>::TT};
 }
 template <int D>
 cudaError_t launch_tc(ChunkArgs& a, int parts, cudaStream_t st) {
-  if constexpr (tc_max_parts(D) == 2)
-    if (parts == 2) return run_chunk_tc<D, 2>(a, st);
-  return parts == 1 ? run_chunk_tc<D, 1>(a, st) : cudaErrorInvalidValue;
+  return parts == 1 ? run_chunk_tc<D, 1>(a, st) : run_chunk_tc<D, 2>(a, st);
 }
 
 }  // namespace

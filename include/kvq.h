@@ -566,6 +566,11 @@ typedef struct kvq_score_mod {
  * prefix_len; one that sees none is zeros.  Body / tail selection, rotation and
  * query heads are as in kvq_decode_attention.  A key whose stored key or value holds
  * an infinity or NaN makes NaN of the rows that see it, and does not touch others.
+ * Precision: the products' operands are fp16, brought into its range by powers of two
+ * taken from the largest values; bf16 outputs take them rounded once (2^-11 of
+ * themselves), fp16 and fp32 outputs as two parts (22 bits).  Sums and softmax are fp32.
+ * The first call for a head_dim, output type and pair of formats asks the device for
+ * its limits; make it before a stream capture.
  * workspace: device memory, 16-byte aligned, kvq_chunk_workspace_bytes bytes, not
  * shared with a call that runs at the same time.  n_rows 0 is a no-op.  n_rows *
  * n_q_heads must stay below 2^31, body planes and tails below 2^31 rows, and there

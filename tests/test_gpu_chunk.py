@@ -256,7 +256,14 @@ def test_errors_on_the_device():
                 s = ko.rotate(qr[r, h].astype(np.float64)) @ K[t].T * 0.125
                 w = np.exp(s - s.max())
                 ref[r, h] = ko.rotate((w / w.sum()) @ V[t])
-        # (the bound of the whole is not the rest's; four times it is: the rest has more than a quarter of each row's weight)
+        # (The whole's bound is a sum over all keys of weight times |value| terms.  Without the page's keys each weight is the whole's over
+        # the rest's share of it, at least a quarter here: asserted below.  So is the bound, its sum only losing terms.)
+        for r in range(20):
+            t = np.arange(64 if r < 10 else 0, 181 + r)
+            for h in range(2):
+                s = ko.rotate(qr[r, h].astype(np.float64)) @ K[t].T * 0.125
+                w = np.exp(s - s.max())
+                assert w[(t < 64) | (t >= 128)].sum() >= 0.25 * w.sum()
         _close(got, (ref, 4 * whole[1]), od)
 
 

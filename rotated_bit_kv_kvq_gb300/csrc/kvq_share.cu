@@ -36,29 +36,27 @@ __device__ __forceinline__ int held_pages(int len, const ShareArgs& a) {  // 0 f
   return len >= 0 && len <= a.max_ctx ? int((uint32_t(len) + uint32_t(a.page_tokens) - 1) / uint32_t(a.page_tokens)) : 0;
 }
 
-// Pages that a plan's CTA scans at a time, four consecutive ones a thread
-constexpr int kScan = 4 * kPlanThreads;
-
-// Inclusive sums over a block of kPlanThreads; s: 32 ints.  Returns this thread's, and the block's in total.
-__device__ __forceinline__ int block_sums(int v, int* s, int& total) {
+// Inclusive sums over a block of kPlanThreads; s: 32 values.  Returns this thread's, and the block's in total.
+template <class T>
+__device__ __forceinline__ T block_sums(T v, T* s, T& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    const T u = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += u;
   }
   __syncthreads();  // (the sums before are read)
   if (lane == 31) s[warp] = v;
   __syncthreads();
-  int w = s[lane];
+  T w = s[lane];
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, w, o);
+    const T u = __shfl_up_sync(0xffffffffu, w, o);
     if (lane >= o) w += u;
   }
   total = __shfl_sync(0xffffffffu, w, 31);
-  const int before = __shfl_sync(0xffffffffu, w, warp == 0 ? 0 : warp - 1);
-  return v + (warp == 0 ? 0 : before);
+  const T before = __shfl_sync(0xffffffffu, w, warp == 0 ? 0 : warp - 1);
+  return v + (warp == 0 ? T(0) : before);
 }
 
 // `bytes` (a multiple of 16) by the threads of a CTA, both sides 16-byte aligned
@@ -180,9 +178,8 @@ __global__ void __launch_bounds__(kCopyThreads, kCopyCtas) fork_copy_kernel(Shar
   const int T = c.tail_len, D = c.head_dim, H = c.n_kv_heads;
   for (long long w = blockIdx.x; w < (long long)f.n_forks * f.parts; w += gridDim.x) {
     const int i = int(w / f.parts), part = int(w - (long long)i * f.parts);
-    const int n = f.granted[i];
+    const int n = f.granted[i], src = f.src[i], dst = f.dst[i];
     if (n < 0) continue;
-    const int src = f.src[i], dst = f.dst[i];
     const int32_t* from = a.table + (long long)src * per_seq;
     if (part == 0) {
       if (tid == 0) f.seq_len_out[dst] = n;
@@ -249,83 +246,92 @@ __global__ void __launch_bounds__(kCopyThreads, kCopyCtas) fork_copy_kernel(Shar
 
 // ---- free ------------------------------------------------------------------------------------------
 
-// One cluster.  Every released table entry takes one from its page's count; pages that come below 0 are free and go, in
-// ascending order, behind the ring's.
+// One cluster.  Every released table entry takes one from its page's count; the page of the entry that finds 0 there is free.
+// Free pages are bits in shared memory, a range of pages per CTA, and go, in ascending order, behind the ring's: a scan over
+// words of 32 pages instead of the pool's counts.  (A pool of more pages than there are bits: in several rounds over the tables.)
+constexpr int kFreeWords = 4096;
 __global__ void __launch_bounds__(kPlanThreads, 1) free_kernel(ShareArgs a, const int32_t* release, int32_t* seq_len_out) {
   pdl_begin();
   cg::cluster_group cl = cg::this_cluster();
-  __shared__ int s_sum[32];
+  __shared__ int s_sum[32], s_before[kPlanThreads];
+  __shared__ uint32_t s_bits[kFreeWords];
   __shared__ int s_total;
-  const int S = int(cl.num_blocks()), rank = int(cl.block_rank()), tid = threadIdx.x, lane = tid & 31;
+  const int S = int(cl.num_blocks()), rank = int(cl.block_rank()), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int nt = S * kPlanThreads, gt = rank * kPlanThreads + tid, per_seq = a.max_ctx / a.page_tokens;
   const int head = a.pool.state[0], count = a.pool.state[1];
   const bool pool = pool_ok(head, count, a.n_pages);
   uint32_t err = pool ? 0u : KVQ_DEV_ERR_PAGE;
-  if (a.share.next != a.share.count) {
+  const int words = min(kFreeWords, int(((long long)a.n_pages + 32 * S - 1) / (32 * S)));  // of a CTA
+  if (a.share.next != a.share.count)
     for (long long i = gt; i < a.n_pages; i += nt) a.share.next[i] = a.share.count[i];
-    cl.sync();
-  }
-  if (pool)
+  const int room = a.n_pages - count;  // (a bad state: nothing is free below)
+  int all = 0;
+  for (long long base = 0; pool && base < a.n_pages; base += (long long)S * words * 32) {
+    __syncthreads();  // (the round before has been read)
+    for (int w = tid; w < words; w += kPlanThreads) s_bits[w] = 0u;
+    cl.sync();  // (the counts are there, too)
     for (int b = gt >> 5; b < a.batch; b += nt >> 5) {  // a warp a sequence
-      if (release[b] == 0) continue;
-      const int len = a.seq_len[b], held = held_pages(len, a);
+      const int32_t* row = a.table + (long long)b * per_seq;
+      const int gone = release[b], len = a.seq_len[b];
+      int next = lane < per_seq ? row[lane] : 0;  // (loads that wait for nothing: each wait is most of a microsecond)
+      if (gone == 0) continue;
+      const int held = held_pages(len, a);
       if (len < 0 || len > a.max_ctx) err |= KVQ_DEV_ERR_APPEND_RANGE;
       for (int j = lane; j < held; j += 32) {
-        const int pg = a.table[(long long)b * per_seq + j];
-        if (pg >= 0 && pg < a.n_pages) atomicSub(&a.share.next[pg], 1);
-        else err |= KVQ_DEV_ERR_PAGE;
+        const int pg = next;
+        if (j + 32 < held) next = row[j + 32];
+        if (pg < 0 || pg >= a.n_pages) {
+          err |= KVQ_DEV_ERR_PAGE;
+          continue;
+        }
+        const long long at = pg - base;
+        if (at < 0 || at >= (long long)S * words * 32) continue;  // another round's
+        const int was = atomicSub(&a.share.next[pg], 1);
+        if (was > 0) continue;
+        if (was < 0) err |= KVQ_DEV_ERR_PAGE;  // given back more often than it was held
+        const int r = int(uint32_t(at >> 5) / uint32_t(words)), w = int(at >> 5) - r * words;
+        atomicOr(cl.map_shared_rank(s_bits, r) + w, 1u << (at & 31));
       }
     }
-  __threadfence();
-  cl.sync();
-  const int chunk = int(((long long)a.n_pages + S - 1) / S), p0 = int(min((long long)a.n_pages, (long long)rank * chunk)),
-            p1 = int(min((long long)a.n_pages, (long long)p0 + chunk));
-  int mine = 0;
-#pragma unroll 4
-  for (int p = p0 + tid; p < p1; p += kPlanThreads) mine += __ldcg(&a.share.next[p]) < 0;
-  int total;
-  block_sums(mine, s_sum, total);
-  if (tid == 0) s_total = total;
-  cl.sync();
-  int before = 0, all = 0;
-  for (int r = 0; r < S; ++r) {
-    const int t = *cl.map_shared_rank(&s_total, r);
-    if (r < rank) before += t;
-    all += t;
-  }
-  const int room = a.n_pages - count;  // (a bad state: nothing is free below)
-  for (int q = p0; pool && q < p1; q += kScan) {
-    int v[4], free = 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int p = q + 4 * tid + e;
-      v[e] = p < p1 ? __ldcg(&a.share.next[p]) : 0;
-      free += v[e] < 0;
+    cl.sync();
+    int mine = 0, total;
+    for (int w = tid; w < words; w += kPlanThreads) mine += __popc(s_bits[w]);
+    block_sums(mine, s_sum, total);
+    if (tid == 0) s_total = total;
+    cl.sync();
+    int before = all;
+    for (int r = 0; r < S; ++r) {
+      const int t = *cl.map_shared_rank(&s_total, r);
+      if (r < rank) before += t;
+      all += t;
     }
-    int at = before + block_sums(free, s_sum, total) - free;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int p = q + 4 * tid + e;
-      if (v[e] >= 0) continue;
-      if (v[e] < -1) err |= KVQ_DEV_ERR_PAGE;  // given back more often than it was held
-      a.share.next[p] = 0;
-      if (at < room) {
-        long long i = (long long)head + count + at;
-        while (i >= a.n_pages) i -= a.n_pages;
-        a.pool.ring[i] = p;
+    const long long p0 = base + (long long)rank * words * 32;
+    for (int q = 0; q < words; q += kPlanThreads) {
+      const int n = q + tid < words ? __popc(s_bits[q + tid]) : 0;
+      s_before[tid] = before + block_sums(n, s_sum, total) - n;
+      before += total;
+      __syncthreads();
+      for (int i = warp; i < kPlanThreads && q + i < words; i += 32) {  // a warp a word
+        const uint32_t bits = s_bits[q + i];
+        if (!(bits >> lane & 1u)) continue;
+        const int p = int(p0 + (q + i) * 32 + lane), at = s_before[i] + __popc(bits & ((1u << lane) - 1u));
+        a.share.next[p] = 0;
+        if (at < room) {
+          long long k = (long long)head + count + at;
+          while (k >= a.n_pages) k -= a.n_pages;
+          a.pool.ring[k] = p;
+        }
       }
-      ++at;
     }
-    before += total;
   }
   if (pool && all > room) err |= KVQ_DEV_ERR_PAGE;
   if (err) atomicOr(a.status, err);
+  cl.sync();  // every CTA has read the lengths, the state and the others' sums
   if (seq_len_out)
     for (int b = gt; b < a.batch; b += nt) {
       const int len = a.seq_len[b];
       seq_len_out[b] = pool && release[b] != 0 && len >= 0 && len <= a.max_ctx ? 0 : len;
     }
-  cl.sync();  // every CTA has read the state, and the others' sums
   if (rank == 0 && tid == 0) {
     a.pool.next[0] = head;
     a.pool.next[1] = pool ? count + min(all, room) : count;
@@ -334,132 +340,129 @@ __global__ void __launch_bounds__(kPlanThreads, 1) free_kernel(ShareArgs a, cons
 
 // ---- compact ---------------------------------------------------------------------------------------
 
-// One cluster.  Marks pages as free (in the ring) or live (in a sequence's table); of the n live ones those that are not
-// among the n lowest marked pages move, the i-th to the i-th free page among these.  moves: [0] their number, then the
-// sources and the destinations.
+// One cluster.  Pages that are live (in a sequence's table) or free (in the ring) are bits, a range of pages per CTA, in shared
+// memory, or in the workspace where they do not fit; of the n live ones those that are not among the n lowest marked pages
+// move, the i-th to the i-th free page among these.  moves: [0] their number, then the sources and the destinations.
+constexpr int kMarkWords = 2048;
+struct Marked {  // pages, live ones in the upper half, live and free ones in the lower
+  long long n;
+  __device__ __forceinline__ int live() const { return int(n >> 32); }
+  __device__ __forceinline__ int all() const { return int(n & 0xffffffffLL); }
+};
 __global__ void __launch_bounds__(kPlanThreads, 1) compact_plan_kernel(ShareArgs a, CompactArgs m) {
   pdl_begin();
   cg::cluster_group cl = cg::this_cluster();
-  __shared__ int s_sum[32];
-  __shared__ int s_live, s_hand, s_low, s_bad;
-  const int S = int(cl.num_blocks()), rank = int(cl.block_rank()), tid = threadIdx.x, lane = tid & 31;
+  __shared__ long long s_sum[32], s_before[kPlanThreads], s_total;
+  __shared__ uint32_t s_bits[2][kMarkWords];
+  __shared__ int s_low, s_bad;
+  const int S = int(cl.num_blocks()), rank = int(cl.block_rank()), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int nt = S * kPlanThreads, gt = rank * kPlanThreads + tid, per_seq = a.max_ctx / a.page_tokens;
   const int head = a.pool.state[0], count = a.pool.state[1];
   const bool pool = pool_ok(head, count, a.n_pages);
-  if (tid == 0) s_bad = pool ? 0 : 1;
+  const int words = int(((long long)a.n_pages + 32 * S - 1) / (32 * S));  // of a CTA
+  const bool here = words <= kMarkWords;
+  auto bits = [&](int r, int k) -> uint32_t* {  // CTA r's; k 0: free, 1: live
+    return here ? cl.map_shared_rank(&s_bits[k][0], r) : reinterpret_cast<uint32_t*>(m.mark) + ((long long)k * S + r) * words;
+  };
+  volatile uint32_t *fre = bits(rank, 0), *liv = bits(rank, 1);
+  if (tid == 0) {
+    s_bad = pool ? 0 : 1;
+    s_low = 0;
+  }
+  for (int w = tid; w < words; w += kPlanThreads) fre[w] = liv[w] = 0u;
   for (long long i = gt; i < a.n_pages; i += nt) {
-    m.mark[i] = 0;
     m.map[i] = int(i);
     if (a.share.next && a.share.next != a.share.count) a.share.next[i] = a.share.count[i];
   }
-  __threadfence();
   cl.sync();
   bool bad = false;
+  auto mark = [&](int pg, int k) {  // false: outside the pool, or marked before
+    if (pg < 0 || pg >= a.n_pages) return false;
+    const int r = int(uint32_t(pg >> 5) / uint32_t(words));
+    const uint32_t bit = 1u << (pg & 31);
+    return !(atomicOr(bits(r, k) + ((pg >> 5) - r * words), bit) & bit);
+  };
   if (pool) {
     for (int b = gt >> 5; b < a.batch; b += nt >> 5) {
-      const int len = a.seq_len[b], held = held_pages(len, a);
+      const int32_t* row = a.table + (long long)b * per_seq;
+      const int len = a.seq_len[b];
+      int next = lane < per_seq ? row[lane] : 0;  // (no wait for the length)
+      const int held = held_pages(len, a);
       bad |= len < 0 || len > a.max_ctx;
       for (int j = lane; j < held; j += 32) {
-        const int pg = a.table[(long long)b * per_seq + j];
-        if (pg >= 0 && pg < a.n_pages) bad |= (atomicOr(&m.mark[pg], 2) & 1) != 0;
-        else bad = true;
+        const int pg = next;
+        if (j + 32 < held) next = row[j + 32];
+        bad |= !mark(pg, 1) && (pg < 0 || pg >= a.n_pages);  // (several sequences may hold it)
       }
     }
-    for (int i = gt; i < count; i += nt) {
-      long long r = (long long)head + i;
-      if (r >= a.n_pages) r -= a.n_pages;
-      const int pg = a.pool.ring[r];
-      if (pg >= 0 && pg < a.n_pages) bad |= atomicOr(&m.mark[pg], 1) != 0;  // (twice in the ring, or also in a table)
-      else bad = true;
+    for (int i = gt; i < a.n_pages; i += nt) {  // (no wait for the state)
+      const int pg = a.pool.ring[i], at = i - head;
+      if ((at < 0 ? at + a.n_pages : at) < count) bad |= !mark(pg, 0);
     }
+  }
+  cl.sync();
+  long long mine = 0, total;
+  for (int w = tid; w < words; w += kPlanThreads) {
+    const uint32_t l = liv[w], f = fre[w];
+    bad |= (l & f) != 0u;
+    mine += ((long long)__popc(l) << 32) + __popc(l | f);
   }
   if (bad) s_bad = 1;
-  __threadfence();
+  block_sums(mine, s_sum, total);
+  if (tid == 0) s_total = total;
   cl.sync();
-  const int chunk = int(((long long)a.n_pages + S - 1) / S), p0 = int(min((long long)a.n_pages, (long long)rank * chunk)),
-            p1 = int(min((long long)a.n_pages, (long long)p0 + chunk));
-  int live = 0, hand = 0, total;
-#pragma unroll 4
-  for (int p = p0 + tid; p < p1; p += kPlanThreads) {
-    const int k = __ldcg(&m.mark[p]);
-    live += (k & 2) != 0;
-    hand += k != 0;
-  }
-  block_sums(live, s_sum, total);
-  if (tid == 0) s_live = total;
-  block_sums(hand, s_sum, total);
-  if (tid == 0) s_hand = total;
-  cl.sync();
-  int n_live = 0, n_hand = 0, live0 = 0, hand0 = 0;
+  Marked sum{0}, before{0};
   bool any_bad = false;
   for (int r = 0; r < S; ++r) {
-    const int l = *cl.map_shared_rank(&s_live, r), h = *cl.map_shared_rank(&s_hand, r);
+    const long long t = *cl.map_shared_rank(&s_total, r);
     any_bad |= *cl.map_shared_rank(&s_bad, r) != 0;
-    if (r < rank) { live0 += l; hand0 += h; }
-    n_live += l;
-    n_hand += h;
+    if (r < rank) before.n += t;
+    sum.n += t;
   }
-  // live pages among the n_live lowest
-  auto marks = [&](int q, int (&k)[4]) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int p = q + 4 * tid + e;
-      k[e] = p < p1 ? __ldcg(&m.mark[p]) : 0;
+  const int n_live = sum.live(), n_hand = sum.all();
+  // marked pages before each word of words q ..; returns those before this thread's
+  auto scan = [&](int q, Marked& at) {
+    const uint32_t l = q + tid < words ? liv[q + tid] : 0u, f = q + tid < words ? fre[q + tid] : 0u;
+    const long long n = ((long long)__popc(l) << 32) + __popc(l | f);
+    const Marked b{at.n + block_sums(n, s_sum, total) - n};
+    s_before[tid] = b.n;
+    at.n += total;
+    const int k = n_live - b.all();
+    if (k > 0 && k <= __popc(l | f)) {  // the n_live-th marked page is in this word: the live ones up to it
+      uint32_t rest = l | f;
+      for (int i = 0; i < k; ++i) rest &= rest - 1u;
+      const int low = b.live() + __popc(l & ~rest);
+      for (int r = 0; r < S; ++r) *cl.map_shared_rank(&s_low, r) = low;
     }
+    __syncthreads();
   };
-  int low = 0;
-  for (int q = p0, h0 = hand0; q < p1; q += kScan) {
-    int k[4], n = 0;
-    marks(q, k);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) n += k[e] != 0;
-    int at = h0 + block_sums(n, s_sum, total) - n;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      low += (k[e] & 2) && at < n_live;
-      at += k[e] != 0;
-    }
-    h0 += total;
-  }
-  block_sums(low, s_sum, total);
-  if (tid == 0) s_low = total;
+  Marked at = before;
+  for (int q = 0; q < words; q += kPlanThreads) scan(q, at);
   cl.sync();
-  int n_low = 0;
-  for (int r = 0; r < S; ++r) n_low += *cl.map_shared_rank(&s_low, r);
-  const int n_moves = any_bad ? 0 : n_live - n_low;
+  const int n_low = s_low, n_moves = any_bad ? 0 : n_live - n_low;
   int32_t *from = m.moves + 1, *to = from + a.n_pages;
   if (!any_bad) {
-    int free0 = hand0 - live0;
-    for (int q = p0; q < p1; q += kScan) {
-      int k[4], isl = 0, isf = 0;
-      marks(q, k);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        isl += (k[e] & 2) != 0;
-        isf += k[e] == 1;
-      }
-      int al = live0 + block_sums(isl, s_sum, total) - isl;
-      live0 += total;
-      int af = free0 + block_sums(isf, s_sum, total) - isf;
-      free0 += total;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int p = q + 4 * tid + e;
-        if (k[e] && al + af < n_live) {
-          if (k[e] == 1) to[af] = p;
-        } else if (k[e]) {
-          if (k[e] & 2) from[al - n_low] = p;
-          m.ring_out[al + af - n_live] = p;
+    at = before;
+    for (int q = 0; q < words; q += kPlanThreads) {
+      if (words > kPlanThreads) scan(q, at);  // (else as it was left)
+      for (int i = warp; i < kPlanThreads && q + i < words; i += 32) {  // a warp a word
+        const uint32_t l = liv[q + i], k = l | fre[q + i], below = (1u << lane) - 1u;
+        if (!(k >> lane & 1u)) continue;
+        const Marked b{s_before[i]};
+        const int p = int(((long long)rank * words + q + i) * 32 + lane), al = b.live() + __popc(l & below), ah = b.all() + __popc(k & below);
+        const bool is_live = l >> lane & 1u;
+        if (ah < n_live) {
+          if (!is_live) to[ah - al] = p;
+        } else {
+          if (is_live) from[al - n_low] = p;
+          m.ring_out[ah - n_live] = p;
         }
-        al += (k[e] & 2) != 0;
-        af += k[e] == 1;
       }
     }
     for (int i = n_hand - n_live + gt; i < a.n_pages; i += nt) m.ring_out[i] = -1;
   } else if (m.ring_out != a.pool.ring) {
     for (int i = gt; i < a.n_pages; i += nt) m.ring_out[i] = a.pool.ring[i];
   }
-  __threadfence();
   cl.sync();
   for (int i = gt; i < n_moves; i += nt) {
     const int f = __ldcg(&from[i]), t = __ldcg(&to[i]);
@@ -475,7 +478,6 @@ __global__ void __launch_bounds__(kPlanThreads, 1) compact_plan_kernel(ShareArgs
     a.pool.next[0] = any_bad ? head : 0;
     a.pool.next[1] = any_bad ? count : n_hand - n_live;
   }
-  cl.sync();  // no CTA leaves while another reads its sums
 }
 
 __global__ void __launch_bounds__(kCopyThreads, kCopyCtas) compact_copy_kernel(ShareArgs a, CompactArgs m) {
@@ -484,7 +486,7 @@ __global__ void __launch_bounds__(kCopyThreads, kCopyCtas) compact_copy_kernel(S
   const int32_t *from = m.moves + 1, *to = from + a.n_pages;
   const long long work = (long long)n * a.page_units;
   int i = int(blockIdx.x / a.page_units);
-  int t = blockIdx.x < work ? to[i] : 0, f = blockIdx.x < work ? from[i] : 0;
+  int t = i < a.n_pages ? to[i] : 0, f = i < a.n_pages ? from[i] : 0;  // (loaded beside their number; no move: not used)
   for (long long w = blockIdx.x; w < work; w += gridDim.x) {
     const long long next = w + gridDim.x;
     const int u = int(w - (long long)i * a.page_units), t0 = t, f0 = f;
@@ -496,9 +498,10 @@ __global__ void __launch_bounds__(kCopyThreads, kCopyCtas) compact_copy_kernel(S
     copy_page_unit(a, u, t0, f0);
   }
   const long long entries = (long long)a.batch * per_seq;
-  for (long long e = (long long)blockIdx.x * kCopyThreads + threadIdx.x; e < entries; e += (long long)gridDim.x * kCopyThreads) {
-    const int b = int(e / per_seq), pg = a.table[e];
-    const bool used = int(e - (long long)b * per_seq) < held_pages(a.seq_len[b], a);
+  // the table, by the last CTAs first: a few moves leave them free
+  for (long long e = (long long)(gridDim.x - 1 - blockIdx.x) * kCopyThreads + threadIdx.x; e < entries; e += (long long)gridDim.x * kCopyThreads) {
+    const int b = int(e / per_seq), pg = a.table[e], len = a.seq_len[b];
+    const bool used = int(e - (long long)b * per_seq) < held_pages(len, a);
     const int out = used && pg >= 0 && pg < a.n_pages ? m.map[pg] : pg;
     if (m.table_out != a.table || out != pg) m.table_out[e] = out;
   }

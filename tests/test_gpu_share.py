@@ -15,7 +15,8 @@ PLANES = ("k_qs", "k_qh", "k_d", "v_qs", "v_qh", "v_d", "outl")
 class _Shared:
     """A paged cache with a pool and counts, their arrays on the GPU and in numpy."""
 
-    def __init__(self, B, H, d, ctx, P, n_pages, T=0, kt="q4_0", vt="q4_0", seed=0, head=0, outliers=None):
+    def __init__(self, B, H, d, ctx, P, n_pages, T=0, kt="q4_0", vt="q4_0", seed=0, head=0, outliers=None, contents=True):
+        self.contents = contents
         self.torch = torch = require_gpu()
         from rotated_bit_kv_kvq_gb300 import kvq
         self.kvq, self.rng = kvq, np.random.default_rng(seed)
@@ -26,7 +27,7 @@ class _Shared:
         order = self.rng.permutation(n_pages)
         self.ring, self.state, self.count = np.roll(order, head), np.array([head, n_pages]), np.zeros(n_pages, np.int64)
         for name in PLANES:  # every page has contents of its own (finite headers)
-            if name in self.gc.planes:
+            if contents and name in self.gc.planes:
                 raw = self.rng.integers(0, 256, self.gc.planes[name].numel()).astype(np.uint8)
                 if name in ("k_d", "v_d"):
                     raw = (self.rng.standard_normal(len(raw) // 2) * 0.1).astype(np.float16).view(np.uint8)
@@ -55,7 +56,7 @@ class _Shared:
         p = lambda k: self.t[k].data_ptr()  # noqa: E731
         self.pool = self.kvq.kvq_page_pool(p("ring"), p("state"), p("state_out"))
         self.share = self.kvq.kvq_page_share(p("count"), p("count_out"))
-        self.before = {k: self.pages(k) for k in PLANES if k in self.gc.planes}
+        self.before = {k: self.pages(k) for k in PLANES if self.contents and k in self.gc.planes}
 
     def pages(self, name):
         return self.gc.planes[name].cpu().numpy().reshape(self.n_pages, -1).copy()
@@ -160,6 +161,22 @@ def test_large_pool_and_batch():
     s.free([b % 2 for b in range(1500)], in_place=False)
     s.compact(in_place=False)
     s.fork([0, 2, 4, 4], [1499, 1497, 1495, 1495], in_place=False)
+
+
+def test_a_pool_past_the_bits_in_shared_memory():
+    """1.1 million pages (2.5 GB): more than a cluster's shared memory has bits for, so that a release takes two rounds and a
+    compaction marks in its workspace.  What is in the pages is not compared: the copies are those of the other tests."""
+    s = _Shared(300, 1, 32, 1024, 64, 1100000, seed=9, head=1099000, contents=False)
+    for b in range(0, 300, 2):
+        s.give(b, int(s.rng.integers(1, 1025)))
+    s.fork(range(0, 100, 2), range(1, 100, 2))
+    assert (s.table > 8 * 4096 * 32).any()
+    s.free(s.rng.random(300) < 0.5, in_place=False)
+    s.free(s.rng.random(300) < 0.3)
+    assert s.compact(in_place=False)["moves"]
+    s.table[2][0] = s.ring[3]  # in use and free: nothing moves
+    s.lens[2] = max(s.lens[2], 1)
+    assert s.compact()["bits"] == sh.PAGE
 
 
 def test_nothing_left():

@@ -268,7 +268,7 @@ struct ForkArgs {
   int32_t *granted, *seq_len_out;
   int units, parts;                    // units of a fork's copy, and the CTAs that share them
   int tail_rows, tail_pieces;          // tail rows of a unit, units of a (side, KV head)
-  DivU32 by_row;                       // 16-byte pieces of a tail row
+  DivU32 by_row;                       // pieces of 16 channels of a tail row
 };
 struct CompactArgs {
   int32_t *table_out, *ring_out, *map;

@@ -18,30 +18,36 @@ __host__ __device__ inline BodySide body_side(const kvq_cache& c, bool k) {
                   static_cast<const uint32_t*>(k ? c.k_qh : c.v_qh), k ? c.k_type : c.v_type, k};
 }
 
-// Values of channels 8ch .. 8ch + 7 of a body row, in fp32: (code - offset) * d is exact, the minimum's sum rounded once.
-__device__ __forceinline__ void body_values8(const BodySide& s, int head_dim, long long row, int ch, float (&x)[8]) {
-  const int nb = head_dim / 32, blk = ch / 4, w = (ch * 8) % 32;
+// Values of channels 8u .. 8u + 7 and, 16 further, of the same 8 bytes of a 4-bit block's codes (u 0 or 1 within block blk), in
+// fp32: (code - offset) * d is exact, the minimum's sum rounded once.
+__device__ __forceinline__ void body_values16(const BodySide& s, int head_dim, long long row, int blk, int u, float (&x)[2][8]) {
+  const int nb = head_dim / 32;
   const bool has_min = type_has_min(s.type);
   const uint8_t* h = s.hd + (size_t(row) * nb + blk) * (has_min ? 4 : 2);
   const uint32_t hdr = has_min ? *reinterpret_cast<const uint32_t*>(h) : uint32_t(*reinterpret_cast<const uint16_t*>(h));
   const float d = __half2float(__ushort_as_half(uint16_t(hdr & 0xFFFFu)));
   if (s.type == KVQ_TYPE_Q8_0) {
-    const uint2 q = *reinterpret_cast<const uint2*>(s.qs + size_t(row) * head_dim + ch * 8);
+    const uint2* src = reinterpret_cast<const uint2*>(s.qs + size_t(row) * head_dim + blk * 32 + u * 8);
+    const uint2 q[2] = {src[0], src[2]};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = float(int(((e < 4 ? q.x : q.y) >> (8 * (e & 3))) & 0xFFu) - 128) * d;  // offset binary
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[k][e] = float(int(((e < 4 ? q[k].x : q[k].y) >> (8 * (e & 3))) & 0xFFu) - 128) * d;  // offset binary
     return;
   }
   const float lo = has_min ? __half2float(__ushort_as_half(uint16_t(hdr >> 16))) : 0.0f;
-  const uint2 q = *reinterpret_cast<const uint2*>(s.qs + size_t(row) * (head_dim / 2) + blk * 16 + (w & 15));
-  const uint32_t high = type_has_qh(s.type) ? qh_get(s.qh, s.is_k, size_t(row), nb, blk) >> w : 0u;
-  const int shift = w < 16 ? 0 : 4, off = type_code_offset(s.type);
+  const uint2 q = *reinterpret_cast<const uint2*>(s.qs + size_t(row) * (head_dim / 2) + blk * 16 + u * 8);
+  const uint32_t high = type_has_qh(s.type) ? qh_get(s.qh, s.is_k, size_t(row), nb, blk) >> (u * 8) : 0u;
+  const int off = type_code_offset(s.type);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const uint32_t byte = (e < 4 ? q.x : q.y) >> (8 * (e & 3));
-    const int code = int((byte >> shift) & 15u) | int(((high >> e) & 1u) << 4);
-    const float v = __fmul_rn(float(code - off), d);
-    x[e] = has_min ? __fadd_rn(v, lo) : v;
-  }
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t byte = (e < 4 ? q.x : q.y) >> (8 * (e & 3));
+      const int code = int((byte >> (4 * k)) & 15u) | int(((high >> (16 * k + e)) & 1u) << 4);
+      const float v = __fmul_rn(float(code - off), d);
+      x[k][e] = has_min ? __fadd_rn(v, lo) : v;
+    }
 }
 
 }  // namespace kvq

@@ -4,9 +4,9 @@
 // a count of 0 without knowing of it.  Only full pages are shared: a sequence appends to pages that it holds alone.
 //
 // All three are bound by what they move (fork and compact: page and tail bytes, read and written once) or by the latency of
-// their launches and scans (free).  Measured (GB300): 64 forks of 8 prompts, tails of 512 tokens, 162 MB: 71 us (2.3 TB/s; two
-// thirds is the decoding of tail rows that the source no longer has); half of a pool of 4096 pages moved, 234 MB: 59 us, 36 of
-// them the copy (6.5 TB/s); 256 of 512 sequences freed: 22 us.  Results do not depend on the order of atomics: counts are sums, and pages freed in one
+// their launches and scans (free).  Measured (GB300): 64 forks of 8 prompts, tails of 512 tokens, 162 MB: 50 us (3.3 TB/s; most of
+// it the decoding of tail rows that the source no longer has); half of a pool of 4096 pages moved, 234 MB: 52 us, 35 of
+// them the copy (6.7 TB/s); 256 of 512 sequences freed: 19 us.  Results do not depend on the order of atomics: counts are sums, and pages freed in one
 // call go into the ring in ascending order, from a scan over the counts.
 
 #include <cooperative_groups.h>
@@ -214,31 +214,37 @@ __global__ void __launch_bounds__(kCopyThreads, kCopyCtas) fork_copy_kernel(Shar
         continue;
       }
       const BodySide side = body_side(c, k);
-      const int per_row = D / 8, chunks = rows * per_row;
-      for (int j = tid; j < chunks; j += kCopyThreads) {
-        const int r = int(div_u32(uint32_t(j), f.by_row)), s = s0 + r, ch = j - r * per_row, p = position(s);
+      // 16 channels a thread, those of 8 bytes of a 4-bit block's codes (8 channels a thread: 70 us for 64 forks, tails of 512)
+      const int per_row = D / 16, pieces = rows * per_row;
+      for (int j = tid; j < pieces; j += kCopyThreads) {
+        const int r = int(div_u32(uint32_t(j), f.by_row)), s = s0 + r, blk = (j - r * per_row) / 2, u = j - r * per_row - 2 * blk, p = position(s);
         if (p < 0) continue;
-        const long long at = ((long long)s * per_row + ch) * 16;
-        uint4 x;
+        const long long at = ((long long)s * (D / 8) + blk * 4 + u) * 16;
+        uint4 x[2];
         if (p >= first) {
-          x = *reinterpret_cast<const uint4*>(in + at);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) x[k] = *reinterpret_cast<const uint4*>(in + at + 32 * k);
         } else {  // the source's tail has moved on: the stored values, rounded to bf16
           const long long row = body_row(row_map(c), src, h, p);
           if (row < 0) {
             atomicOr(a.status, KVQ_DEV_ERR_PAGE);
             continue;
           }
-          float y[8];
-          body_values8(side, D, row, ch, y);
-          uint32_t wds[4];
+          float y[2][8];
+          body_values16(side, D, row, blk, u, y);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const __nv_bfloat162 b2 = __floats2bfloat162_rn(y[2 * e], y[2 * e + 1]);
-            wds[e] = *reinterpret_cast<const uint32_t*>(&b2);
+          for (int k = 0; k < 2; ++k) {
+            uint32_t wds[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const __nv_bfloat162 b2 = __floats2bfloat162_rn(y[k][2 * e], y[k][2 * e + 1]);
+              wds[e] = *reinterpret_cast<const uint32_t*>(&b2);
+            }
+            x[k] = make_uint4(wds[0], wds[1], wds[2], wds[3]);
           }
-          x = make_uint4(wds[0], wds[1], wds[2], wds[3]);
         }
-        *reinterpret_cast<uint4*>(out + at) = x;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) *reinterpret_cast<uint4*>(out + at + 32 * k) = x[k];
       }
     }
   }
@@ -546,7 +552,7 @@ cudaError_t launch_page_fork(const kvq_cache& c, const kvq_page_pool& pool, cons
   f.c = c;
   f.tail_rows = std::max(1, kCopyBytes / (2 * c.head_dim));
   f.tail_pieces = (c.tail_len + f.tail_rows - 1) / f.tail_rows;
-  f.by_row = make_divu32(uint32_t(c.head_dim / 8));
+  f.by_row = make_divu32(uint32_t(c.head_dim / 16));
   f.units = a.page_units + 2 * c.n_kv_heads * f.tail_pieces;
   f.parts = int(std::max<long long>(1, std::min<long long>(f.units, 2LL * sms() * kCopyCtas / f.n_forks)));
   const bool elsewhere = share.next != share.count || f.seq_len_out != c.seq_len;

@@ -11,6 +11,7 @@ namespace kvq {
 namespace {
 
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanItems = 2048;  // whose beginnings are kept in shared memory: a search there, not in L2, once for all kernels (2 us each)
 
 // ---- plan --------------------------------------------------------------------------------------
 
@@ -38,7 +39,7 @@ __device__ __forceinline__ long long block_sums(long long v, long long* s, long 
 
 __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(ChunkArgs a) {
   pdl_begin();
-  __shared__ long long s_sum[32];
+  __shared__ long long s_sum[32], s_at[kPlanItems];
   __shared__ int s_bad;
   const int tid = threadIdx.x, B = a.c.batch;
   if (tid == 0) s_bad = 0;
@@ -117,13 +118,22 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(ChunkArgs a
     }
     it.at = length + block_sums(cost, s_sum, total) - cost;
     if (i < int(items)) a.items[i] = it;
+    if (i < min(int(items), kPlanItems)) s_at[i] = it.at;
     length += total;
   }
-  if (tid == 0) {
-    const long long all = length * a.c.n_kv_heads;
-    ChunkHeader h{length, max((long long)kChunkMinPiece, (all + a.ctas - 1) / a.ctas), int(items), 0, items > 0, 0};
-    h.pieces = int((all + h.piece - 1) / h.piece);
-    *a.head = h;
+  const long long all = length * a.c.n_kv_heads;
+  ChunkHeader h{length, max((long long)kChunkMinPiece, (all + a.ctas - 1) / a.ctas), int(items), 0, items > 0, 0};
+  h.pieces = int((all + h.piece - 1) / h.piece);
+  if (tid == 0) *a.head = h;
+  __syncthreads();
+  for (int c = tid; c < h.pieces; c += kPlanThreads) {
+    const long long z = c * h.piece % length;
+    int lo = 0, hi = int(items) - 1;  // the last item that begins at or before z
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if ((items <= kPlanItems ? s_at[mid] : a.items[mid].at) <= z) lo = mid; else hi = mid - 1;
+    }
+    a.first[c] = lo;
   }
 }
 
@@ -161,15 +171,9 @@ __global__ void __launch_bounds__(32 * kMergeRows) chunk_merge_kernel(ChunkArgs 
   const ChunkHeader h = *a.head;
   const int c = blockIdx.x;
   if (!h.ok || c + 1 >= h.pieces) return;
-  const long long cut = (c + 1) * h.piece, y = cut - 1;  // the last place of piece c
-  const int kvh = int(y / h.total);
-  const long long z = y - kvh * h.total;
-  int lo = 0, hi = h.items - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (a.items[mid].at <= z) lo = mid; else hi = mid - 1;
-  }
-  const ChunkItem it = a.items[lo];
+  const long long cut = (c + 1) * h.piece;  // where piece c + 1 begins: an item that begins there itself is not cut
+  const int kvh = int(cut / h.total);
+  const ChunkItem it = a.items[a.first[c + 1]];
   const int nk = it.n_body + it.n_tail;
   const long long first = kvh * h.total + it.at + kChunkGap, last = first + nk - 1;  // places of the first and last tile
   // cut for the first time here: the first tile lies in piece c, the last one behind it
@@ -256,6 +260,7 @@ size_t layout(ChunkArgs& a, const ChunkTiles& t, char* ws) {
   a.head = reinterpret_cast<ChunkHeader*>(take(sizeof(ChunkHeader)));
   a.tiles0 = reinterpret_cast<int32_t*>(take(size_t(c.batch + 1) * 4));
   a.items = reinterpret_cast<ChunkItem*>(take(size_t(items) * sizeof(ChunkItem)));
+  a.first = reinterpret_cast<int32_t*>(take(size_t(a.ctas) * sizeof(int32_t)));
   a.part_ml = reinterpret_cast<float2*>(take(size_t(2 * a.ctas) * a.m * sizeof(float2)));
   a.part = reinterpret_cast<float*>(take(size_t(2 * a.ctas) * a.m * c.head_dim * sizeof(float)));
   return at;

@@ -51,6 +51,7 @@ struct ChunkArgs {
   ChunkHeader* head;
   int32_t* tiles0;        // [batch + 1]: items before sequence b
   ChunkItem* items;
+  int32_t* first;         // [ctas]: the item in which a piece begins
   float* part;            // [2 * ctas][m][head_dim]: sums of weighted values, unnormalised
   float2* part_ml;        // [2 * ctas][m]: their reference (log2) and sum of weights
 };
@@ -117,13 +118,7 @@ struct ChunkWalk {
     if (!h.ok || piece >= h.pieces) end = x;
     if (x >= end) return;
     kvh = int(x / h.total);
-    const long long y = x - kvh * h.total;
-    int lo = 0, hi = h.items - 1;  // the last item that begins at or before y
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (a.items[mid].at <= y) lo = mid; else hi = mid - 1;
-    }
-    item = lo;
+    item = a.first[piece];
   }
   // The next segment with tiles, or an item without any whose place is here; false: none left.
   __device__ __forceinline__ bool next(const ChunkArgs& a, const ChunkHeader& h, ChunkItem& it, int& head, int& j0, int& j1) {

@@ -1239,12 +1239,10 @@ chunk_tc_kernel(ChunkArgs a, TcStage L, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmKt, const __grid_constant__ CUtensorMap tmVt) {
   using C = TC<D, PARTS>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  pdl_begin();
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   TcSync* sy = tc_sync();
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  const ChunkHeader h = *a.head;
-  if (!h.ok || int(blockIdx.x) >= h.pieces) return;  // (the whole CTA)
+  // while the plan is made: what needs none of it
   if (warp == 0) {
     tc::tmem_alloc(&sy->tmem, 512);
     tc::tmem_relinquish();
@@ -1279,6 +1277,12 @@ chunk_tc_kernel(ChunkArgs a, TcStage L, const __grid_constant__ CUtensorMap tmK,
   // every lane, each tcgen05 instruction becomes a loop of 30: so the walks are inlined, not on the stack, and no loop around
   // one ends on what a wait returns.)
   const uint32_t tmem = __shfl_sync(0xffffffffu, sy->tmem, 0);
+  pdl_begin();
+  const ChunkHeader h = *a.head;
+  if (!h.ok || int(blockIdx.x) >= h.pieces) {  // (the whole CTA)
+    if (warp == 0) tc::tmem_dealloc(tmem, 512);
+    return;
+  }
   constexpr int W0 = C::kSoft / 32;
   if (warp < W0) {
     tc_softmax<D, PARTS>(a, h, sm, tmem, sy, warp, lane);

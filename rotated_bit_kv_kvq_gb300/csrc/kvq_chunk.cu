@@ -185,22 +185,38 @@ __global__ void __launch_bounds__(32 * kMergeRows) chunk_merge_kernel(ChunkArgs 
     // the first piece's part lies in slot 2c + 1, those that begin inside the item in slots 2 (c + i)
     auto slot = [&](int i) { return i == 0 ? 2 * c + 1 : 2 * (c + i); };
     float M = -INFINITY, L = 0.0f, x[D / 32];
-    for (int i = lane; i < pieces; i += 32) {
-      const float2 ml = a.part_ml[(size_t)slot(i) * a.m + r];
-      if (!(ml.y == 0.0f)) M = fmaxf(M, ml.x);
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
 #pragma unroll
     for (int j = 0; j < D / 32; ++j) x[j] = 0.0f;
-    for (int i = 0; i < pieces; ++i) {
-      const float2 ml = a.part_ml[(size_t)slot(i) * a.m + r];
-      if (ml.y == 0.0f) continue;  // (saw no key; NaN goes on)
-      const float w = ex2_approx(ml.x - M);
-      L = fmaf(ml.y, w, L);
-      const float* p = a.part + ((size_t)slot(i) * a.m + r) * D;
+    for (int i = 0; i < pieces; i += 2) {  // (two pieces' loads in flight together; most items are cut once)
+      float2 ml[2];
+      float y[2][D / 32];
 #pragma unroll
-      for (int j = 0; j < D / 32; ++j) x[j] = fmaf(p[fwht_channel<D, G>(lane, j)], w, x[j]);
+      for (int k = 0; k < 2; ++k) {
+        ml[k] = make_float2(-INFINITY, 0.0f);
+        if (i + k >= pieces) continue;
+        const size_t at = (size_t)slot(i + k) * a.m + r;
+        ml[k] = a.part_ml[at];
+        const float* p = a.part + at * D;
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) y[k][j] = p[fwht_channel<D, G>(lane, j)];
+      }
+      float next = M;
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (!(ml[k].y == 0.0f)) next = fmaxf(next, ml[k].x);  // (0: saw no key, nothing was stored; NaN goes on)
+      const float f = M == -INFINITY ? 0.0f : ex2_approx(M - next);
+      M = next;
+      L *= f;
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) x[j] *= f;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        if (ml[k].y == 0.0f) continue;
+        const float w = ex2_approx(ml[k].x - M);
+        L = fmaf(ml[k].y, w, L);
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) x[j] = fmaf(y[k][j], w, x[j]);
+      }
     }
     const float inv = L == 0.0f ? 0.0f : 1.0f / L;
 #pragma unroll

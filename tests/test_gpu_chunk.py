@@ -146,6 +146,22 @@ def test_long_context_in_many_pieces(d, od):
         _check(torch, kvq, gc, oc, q, _starts(new), od, mod)
 
 
+@pytest.mark.parametrize("od", ["bf16", "f16"])
+def test_more_sequences_than_the_plan_keeps(od):
+    """2,500 sequences of up to 64 tokens, from none to three rows each: the plan's loops, and its search past shared memory."""
+    torch = require_gpu()
+    from rotated_bit_kv_kvq_gb300 import kvq
+    rng = np.random.default_rng(77)
+    lens = rng.integers(0, 65, 2500).tolist()
+    new = [int(min(n, rng.integers(0, 4))) for n in lens]
+    new[:2200] = [min(n, 1 + m) for n, m in zip(lens[:2200], new[:2200])]
+    gc, oc = _cache(torch, kvq, rng, 2500, 2, 64, 64, 16, "q8_0", "q5_0", lens)
+    start = _starts(new)
+    assert sum(m > 0 for m in new) > 2048
+    q = 0.7 * rng.standard_normal((start[-1], 4, 64)).astype(np.float32)
+    _check(torch, kvq, gc, oc, q, start, od, dict(softcap=10.0))
+
+
 @pytest.mark.parametrize("flags", [2, 4, 6])
 @pytest.mark.parametrize("od", ["bf16", "f16"])
 def test_rotation_off(flags, od):

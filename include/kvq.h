@@ -491,7 +491,8 @@ typedef struct kvq_page_share {
  * and n outside [0, seq_len] give -1 and set KVQ_DEV_ERR_FORK.  Lengths are those
  * before the call.  A page id outside the pool sets KVQ_DEV_ERR_PAGE, as does a
  * state outside its ranges (all forks get -1 then).  With outlier channels
- * tail_len must be 0 (else KVQ_ERR_UNSUPPORTED).  n_forks 0 is refused with
+ * tail_len must be 0 (else KVQ_ERR_UNSUPPORTED).  A block index has dst's blocks after
+ * its next kvq_block_index_update with n_last 0.  n_forks 0 is refused with
  * seq_len_out or counts elsewhere, else a no-op.
  */
 KVQ_API kvq_status kvq_page_fork(const kvq_cache* c, const kvq_page_pool* pool, const kvq_page_share* share,

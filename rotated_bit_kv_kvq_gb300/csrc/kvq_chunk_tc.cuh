@@ -22,10 +22,10 @@
 // epilogue reads O in that order.  A key with a header or tail value that is not finite is zeroed and noted, and the rows
 // that see it are NaN at the end: 0 * NaN in the products would reach rows that do not.
 //
-// Measured (GB300, us): 2 x 4096 rows, 32/8 heads of 128, half of each prompt a prefix: 518, 663 TFLOP/s (34% of what a large
+// Measured (GB300, us): 2 x 4096 rows, 32/8 heads of 128, half of each prompt a prefix: 487, 706 TFLOP/s (37% of what a large
 // bf16 product reaches), bound by the softmax's exponentials and the roles' code, which the instruction cache does not hold
-// all of; 512 rows over 65,536 tokens, 24/4 heads of 256, with a bias: 1070, 767 TFLOP/s (40%), bound by the one group's chain
-// score - weight - product; 32 sequences of up to 8k tokens, one token each, 32/8 heads of 128: 250, 1.0 TB/s, bound by the
+// all of; 512 rows over 65,536 tokens, 24/4 heads of 256, with a bias: 1067, 770 TFLOP/s (40%), bound by the one group's chain
+// score - weight - product; 32 sequences of up to 8k tokens, one token each, 32/8 heads of 128: 245, 1.0 TB/s, bound by the
 // conversion of tiles of which 4 of 128 rows have use, 2 us a tile.
 //
 // Every wait is bounded: one that gives up sets the status word's timeout bit and a flag that ends the other waits; the

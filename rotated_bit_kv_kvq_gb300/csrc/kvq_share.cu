@@ -4,10 +4,12 @@
 // a count of 0 without knowing of it.  Only full pages are shared: a sequence appends to pages that it holds alone.
 //
 // All three are bound by what they move (fork and compact: page and tail bytes, read and written once) or by the latency of
-// their launches and scans (free).  Measured (GB300): 64 forks of 8 prompts, tails of 512 tokens, 162 MB: 50 us (3.3 TB/s; most of
-// it the decoding of tail rows that the source no longer has); half of a pool of 4096 pages moved, 234 MB: 52 us, 35 of
-// them the copy (6.7 TB/s); 256 of 512 sequences freed: 19 us.  Results do not depend on the order of atomics: counts are sums, and pages freed in one
-// call go into the ring in ascending order, from a scan over the counts.
+// their launches and scans (free).  Measured (GB300): 64 forks of 8 prompts, tails of 512 tokens, 162 MB: 50 us (3.3 TB/s;
+// most of it the decoding of tail rows that the source no longer has); half of a pool of 4096 pages moved, 234 MB: 52 us, 35
+// of them the copy (6.7 TB/s); 256 of 512 sequences freed: 19 us.
+//
+// Results do not depend on the order of atomics: counts are sums, and pages freed in one call go into the ring in ascending
+// order, from a scan over the bits that mark them.
 
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>

@@ -133,7 +133,7 @@ def forked_tail(oc, which, src, dst, n):
 
 
 def chunk(keys, values, rot_k, rot_v, q, row_start, seq_len, n_kv_heads, scale, softcap=0.0, slopes=None, first_key=None,
-          prefix_len=None, rounding=None):
+          prefix_len=None, rounding=None, least=None):
     """keys, values(b, h): rotated rows [n][d] in float64; q [rows][heads][d].  Zeros where no key is seen; rows that belong
     to no sequence are NaN here (nothing is written there).
 
@@ -141,7 +141,9 @@ def chunk(keys, values, rot_k, rot_v, q, row_start, seq_len, n_kv_heads, scale, 
     most e of themselves.  A score is off by at most D = ((1 + e)^2 - 1) scale sum |q_i k_i| (the cap has a slope of at most
     1, the bias is exact), its weight by a factor within exp(+-D), a normalised one within exp(+-2D); with the weight's and
     the value's rounding a channel of the rotated result is off by at most (exp(2D) (1 + e)^2 - 1) sum p |v|, and the
-    rotation back sums these over 1 / sqrt(G) of a group's channels."""
+    rotation back sums these over 1 / sqrt(G) of a group's channels.  least: functions like keys and values of how
+    far a channel may be off besides (numbers that a format does not hold in full): D has (1 + e) scale |q| . of the first
+    more, a channel of the result exp(2D) (1 + e) sum p of the second."""
     q = np.asarray(q, dtype=np.float64)
     rows, heads, d = q.shape
     G = heads // n_kv_heads
@@ -174,8 +176,13 @@ def chunk(keys, values, rot_k, rot_v, q, row_start, seq_len, n_kv_heads, scale, 
                 out[r, h * G:(h + 1) * G] = ko.rotate(y) if rot_v else y
                 if rounding:
                     e = rounding
-                    D = ((1 + e) ** 2 - 1) * scale * (np.abs(qr[r, h * G:(h + 1) * G]) @ np.abs(K[seen]).T).max(-1, keepdims=True)
-                    z = (np.exp(2 * D) * (1 + e) ** 2 - 1) * ((w / w.sum(-1, keepdims=True)) @ np.abs(V[seen]))
+                    size = np.abs(qr[r, h * G:(h + 1) * G])
+                    D = ((1 + e) ** 2 - 1) * scale * (size @ np.abs(K[seen]).T).max(-1, keepdims=True)
+                    z = 0.0
+                    if least:
+                        D = D + (1 + e) * scale * (size @ least[0](b, h)[seen].T).max(-1, keepdims=True)
+                        z = np.exp(2 * D) * (1 + e) * ((w / w.sum(-1, keepdims=True)) @ least[1](b, h)[seen])
+                    z = z + (np.exp(2 * D) * (1 + e) ** 2 - 1) * ((w / w.sum(-1, keepdims=True)) @ np.abs(V[seen]))
                     if rot_v:
                         g = ko.rotation_group(d)
                         z = np.repeat(z.reshape(G, d // g, g).sum(-1) / np.sqrt(g), g, -1).reshape(G, d)

@@ -12,11 +12,13 @@
 //                 them.  Of an item of more than 128 rows they take 128 each, so that a tile is converted once for both; of
 //                 a smaller one every other tile, and are joined at the item's end.
 //
-// PARTS 1 (bf16 outputs): queries, keys, values and weights rounded once to fp16, 2^-11, an eighth of the output's step;
-// PARTS 2 (fp16 and fp32): two fp16 parts each and three products, 22 bits.  Sums and softmax statistics are fp32.
-// fp16's range is no limit: a row's queries, a tile's keys and a segment's values are scaled by powers of two taken from
-// their largest values (a quantized tile's from its headers), and a segment's values keep the smallest scale met so far, O
-// being brought down with it.  Weights are times 2^8.
+// PARTS 1 (bf16 outputs): queries, keys, values and weights rounded once to fp16, 2^-11 of themselves, an eighth of the output's
+// step; PARTS 2 (fp16 and fp32): two fp16 parts each and three products, 22 bits.  Sums and softmax statistics are fp32.
+// fp16's range: a row's queries, a tile's keys and a tile's values are scaled by powers of two taken from their largest (a
+// quantized tile's from its headers), so that no more than 2^-12 of the largest of its block of 32 is lost of any number.  Where a
+// tile's tokens differ too much in size for that, it is converted from fp32 over the format's whole range, and 2^-34 of the
+// tile's largest is.  Values keep the scale of the tile before where it serves; O is brought along where it changes.
+// Weights are times 2^8.
 //
 // Channels lie in the order 0 2 1 3 within each four, as the codes' conversion leaves them, in Q, K and V alike; the
 // epilogue reads O in that order.  A key with a header or tail value that is not finite is zeroed and noted, and the rows
@@ -49,6 +51,7 @@ constexpr int kTcMaxStages = 8;
 constexpr int kTcSyncBytes = 7168;           // of TcSync, in front of everything else in shared memory
 constexpr int kTcMaxSlots = 4;
 constexpr int kTcMeta = 16;                  // (a tile's is read before the ring has come round and two more tiles are done)
+constexpr int kTcRise = 60;                  // see the scout
 constexpr int kTcConv = 8;                   // converter warps, the first half for keys, the others for values
 
 template <int D, int PARTS>
@@ -85,8 +88,8 @@ struct TcStage {  // offsets in a stage of the ring: K codes, V codes (1024-alig
 };
 
 struct __align__(16) TcMeta {
-  int t0, cnt, ks, vs;  // position of column 0, its keys, the powers of two that keys and values were multiplied by
-  uint32_t bad[2], pad[2];  // keys that are not finite
+  uint4 a;  // position of column 0, its keys, the powers of two that keys and values were multiplied by
+  uint4 b;  // keys that are not finite (two words); sides (1 keys, 2 values) that the quick conversion is not for, 4: a tail tile
 };
 
 struct TcSync {
@@ -152,6 +155,11 @@ __device__ __forceinline__ uint32_t tc_lds16(uint32_t a) {
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(a));
   return r;
 }
+__device__ __forceinline__ uint2 tc_lds64(uint32_t a) {
+  uint2 r;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
+  return r;
+}
 __device__ __forceinline__ uint4 tc_lds128(uint32_t a) {
   uint4 r;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
@@ -178,8 +186,9 @@ struct TcSide {
 
 // One fp16 part.  Codes enter as fp16 subnormals, code * 2^-24, a mask or byte permute away from what is stored, and one
 // fused operation gives code * d + m: exact before its one rounding, with d * 2^24 and the minimum (or -offset * d) exact.
-// That takes d below 2^-9 (the scale sees to it), and values below 2^-2 at most.  A lane has the keys lane and lane + 32: two
-// chains of loads, conversions and stores at once.
+// That takes d below 2^-8, and not so small that fp16's smallest step counts; the scout sees to both (tc_below_normal).  A lane
+// has the keys lane and lane + 32: two chains of loads, conversions and stores at once.  (Centred codes times d have fp16's whole
+// range for one operation a pair more, and with them 32 sequences of one token took 277 us for 255, 2 x 4096 prompt rows 533 for 488.)
 template <int D, bool Q8, bool HIGH>
 __device__ __forceinline__ void tc_unit1(const TcSide& u, int lane, int blk, const uint32_t (&d)[TC<D, 1>::KH],
                                          const uint32_t (&m)[TC<D, 1>::KH]) {
@@ -254,8 +263,8 @@ __device__ __forceinline__ void tc_unit1(const TcSide& u, int lane, int blk, con
   }
 }
 
-// Two fp16 parts: centred codes, exact; code * d rounded, and what that left (exact, or below fp16's smallest step); with a
-// minimum both from the sum in fp32.
+// Two fp16 parts: centred codes, exact; code * d rounded, and what that left, exact too where d is a normal number (the scout
+// sees to it); with a minimum both from the sum in fp32.
 template <int D, bool Q8, bool HIGH>
 __device__ __forceinline__ void tc_unit2(const TcSide& u, int key, int blk, uint32_t d, uint32_t m, uint32_t off, bool min) {
   using C = TC<D, 2>;
@@ -312,6 +321,61 @@ __device__ __forceinline__ void tc_unit2(const TcSide& u, int key, int blk, uint
     const uint32_t at = row + ((((blk & 1) * 4 + c) ^ (key & 7)) << 4);
     tc_sts128(at, hi);
     tc_sts128(at + C::part, lo);
+  }
+}
+
+// A key's block of any format from its sum in fp32: the whole range of headers, for tiles that mix far-off ones (a token a
+// thousand times as large as the others).  Rounded like the rest, once or in two parts.
+template <int D, int PARTS>
+__device__ __noinline__ void tc_wide_unit(uint32_t codes, uint32_t hdr, uint32_t qh, uint32_t dst, int type, int scale, bool is_k, int key,
+                                          int blk, bool ok) {
+  using C = TC<D, PARTS>;
+  constexpr int TK = C::TK, NB = C::NB;
+  const bool q8 = type == KVQ_TYPE_Q8_0;
+  const int off = q8 ? 128 : type_code_offset(type);
+  float fd, fm = 0.0f;
+  if (type_has_min(type)) {
+    const float2 f = __half22float2(u32_as_h2(tc_lds32(hdr + (key * NB + blk) * 4)));
+    fd = f.x;
+    fm = f.y;
+  } else {
+    fd = __half2float(__ushort_as_half(uint16_t(tc_lds16(hdr + (key * NB + blk) * 2))));
+  }
+  if (!ok || !(fabsf(fd) <= 65504.0f) || !(fabsf(fm) <= 65504.0f)) fd = fm = 0.0f;  // past the end, or noted as not finite
+  const float sc = tc_pow2(scale);
+  fd *= sc;
+  fm *= sc;
+  const uint32_t row = dst + (blk / 2) * (TK * 128) + key * 128;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t high = 0u;  // bits of pair e of word i at 2 i + e, 16 apart
+    if (type_has_qh(type)) {
+      if (is_k) {
+        const uint32_t x = tc_lds32(qh + (key * NB + blk) * 4);
+        const int at = 8 * (c & 1) + 4 * (c >> 1);
+        high = __funnelshift_r(x, x, at) & 0x000F000Fu;
+      } else {
+        const uint32_t x = tc_lds16(qh + ((((key >> 1) * NB + blk) * 2 + (c & 1)) * 2 + (key & 1)) * 2) >> (4 * (c >> 1));
+        high = (x & 3u) | (x >> 8 & 3u) << 2 | (x >> 2 & 3u) << 16 | (x >> 10 & 3u) << 18;
+      }
+    }
+    const uint2 v = tc_lds64(codes + (q8 ? swz_off<box_w(D)>(key, 32 * blk + 8 * c, TK)
+                                         : swz_off<box_w(D / 2)>(key, 16 * blk + 8 * (c & 1), TK)));
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t w = i ? v.y : v.x;
+        uint32_t t = q8 ? w >> (8 * e) & 0x00FF00FFu : w >> (4 * (c >> 1) + 8 * e) & 0x000F000Fu;
+        t |= (high >> (2 * i + e) & 0x00010001u) << 4;
+        const float x = fmaf(float(int(t & 0xFFFFu) - off), fd, fm), y = fmaf(float(int(t >> 16) - off), fd, fm);
+        if constexpr (PARTS == 2) split_h2(x, y, hi[2 * i + e], lo[2 * i + e]);
+        else hi[2 * i + e] = pack_h2(x, y);
+      }
+    const uint32_t at = row + ((((blk & 1) * 4 + c) ^ (key & 7)) << 4);
+    tc_sts128(at, hi);
+    if constexpr (PARTS == 2) tc_sts128(at + C::part, lo);
   }
 }
 
@@ -395,45 +459,99 @@ __device__ __noinline__ void tc_tail_unit(uint32_t rows, uint32_t dst, int pow, 
   }
 }
 
-// The power of two for a side with the largest scale d and minimum m: with one part d < 2^-9 and |minimum| < 2^14, with two
-// all values < 2^15; 120 where all are 0.
-template <int PARTS>
-__device__ __forceinline__ int tc_body_scale(int qt, uint32_t a, uint32_t b) {
-  if (!type_has_min(qt)) { a = max(a, b); b = 0; }
-  const float d = __half2float(__ushort_as_half(uint16_t(a))), m = __half2float(__ushort_as_half(uint16_t(b)));
-  int s = 120;
-  if constexpr (PARTS == 1) {
-    if (d > 0.0f) s = -9 - tc_exp(d);
-    if (m > 0.0f) s = min(s, 14 - tc_exp(m));
-  } else {
-    const float top = qt == KVQ_TYPE_Q8_0 ? 128.0f : qt == KVQ_TYPE_Q4_0 ? 8.0f : qt == KVQ_TYPE_Q5_0 ? 16.0f : qt == KVQ_TYPE_Q4_1 ? 15.0f : 31.0f;
-    const float v = fmaf(top, d, m);
-    if (v > 0.0f) s = 15 - tc_exp(v);
-  }
-  return s;
-}
-// What a tile holds: the largest header halves (scales, minima) of a side, or the largest tail value's bits; with `finite` of
-// those that are finite alone.
-__device__ __forceinline__ uint32_t tc_header_max(uint32_t hdr, int words, int lane) {
-  uint32_t mx = 0;
+// A warp's share of a side of a tile that the quick conversion is not for: bf16 rows, or headers too far apart.
+template <int D, int PARTS>
+__device__ __noinline__ void tc_slow_blocks(TcSide u, int first, int step, int cnt, bool tail, int lane) {
+  using C = TC<D, PARTS>;
 #pragma unroll 1
-  for (int i = lane; i < words / 4; i += 32) {
+  for (int blk = first; blk < C::NB; blk += step)
+#pragma unroll 1
+    for (int key = lane; key < C::TK; key += 32) {
+      if (!tail) tc_wide_unit<D, PARTS>(u.codes, u.hdr, u.qh, u.dst, u.type, u.scale, u.is_k, key, blk, key < cnt);
+      else if (!u.is_k || key - lane < cnt) tc_tail_unit<D, PARTS>(u.codes, u.dst, u.scale, key, blk, key < cnt);  // (scores past the end are masked)
+    }
+}
+
+// Values are below 2^this times their header's scale (with a minimum: twice the larger of that and the minimum).
+__device__ __forceinline__ int tc_code_bits(int qt) {
+  return qt == KVQ_TYPE_Q8_0 ? 7 : qt == KVQ_TYPE_Q5_0 || qt == KVQ_TYPE_Q4_1 ? 4 : qt == KVQ_TYPE_Q4_0 ? 3 : 5;
+}
+// A lane's share of a tile's headers: the largest and the smallest halves (scales, minima) in size, infinities and NaN going on in
+// the first.
+struct TcHeads {
+  uint32_t most, least;
+};
+__device__ __forceinline__ uint32_t tc_most(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("{\n\t.reg .b32 x;\n\tabs.f16x2 x, %2;\n\tmax.NaN.f16x2 %0, %1, x;\n\t}" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ TcHeads tc_heads(uint32_t hdr, int words, int sub) {
+  TcHeads t{0u, 0x7C007C00u};
+  auto look = [&](uint32_t w) {
+    t.most = tc_most(t.most, w);
+    asm("{\n\t.reg .b32 x;\n\tabs.f16x2 x, %1;\n\tmin.f16x2 %0, %0, x;\n\t}" : "+r"(t.least) : "r"(w));
+  };
+#pragma unroll 1
+  for (int i = sub; i < words / 4; i += 16) {
     const uint4 q = tc_lds128(hdr + 16 * i);
-    mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(q.x & 0x7FFF7FFFu, q.y & 0x7FFF7FFFu), __vmaxu2(q.z & 0x7FFF7FFFu, q.w & 0x7FFF7FFFu)));
+    look(q.x);
+    look(q.y);
+    look(q.z);
+    look(q.w);
   }
-  if (lane < (words & 3)) mx = __vmaxu2(mx, tc_lds32(hdr + 4 * (words / 4 * 4 + lane)) & 0x7FFF7FFFu);
-  return mx;
+  if (sub < (words & 3)) look(tc_lds32(hdr + 4 * (words / 4 * 4 + sub)));
+  return t;
 }
-__device__ __noinline__ uint32_t tc_header_max_finite(uint32_t hdr, int words, int lane) {
+__device__ __noinline__ uint32_t tc_most_finite(uint32_t hdr, int words, int sub) {
   uint32_t mx = 0;
 #pragma unroll 1
-  for (int i = lane; i < words; i += 32) {
+  for (int i = sub; i < words; i += 16) {
     uint32_t w = tc_lds32(hdr + 4 * i) & 0x7FFF7FFFu;
     if ((w & 0xFFFFu) >= 0x7C00u) w &= 0xFFFF0000u;
     if ((w >> 16) >= 0x7C00u) w &= 0xFFFFu;
-    mx = __vmaxu2(mx, w);
+    mx = tc_most(mx, w);
   }
   return mx;
+}
+// The quick conversion takes scales down to 2^-14 less this: half of fp16's smallest step, 2^-25, is 2^-12 of the largest of such
+// a block's values (with a minimum: of half their range).
+template <int PARTS>
+__device__ __forceinline__ int tc_below_normal(int qt) {
+  return PARTS == 2 ? 0 : qt == KVQ_TYPE_Q8_0 ? 5 : qt == KVQ_TYPE_Q5_0 ? 3 : qt == KVQ_TYPE_Q4_1 ? 1 : 2;
+}
+// The scales of a tile of which a header is 0 or too small for a first choice, s (all of a half warp): of each side one that has
+// all that are not 0, else one over fp16's whole range, for the conversion from fp32.  keep: the values' scale of the tile
+// before, top: how high it may go.  Returns the scales plus 512, ten bits each, and the sides for the conversion from fp32.
+template <int PARTS>
+__device__ __noinline__ uint32_t tc_scales(uint32_t hdr, int words, uint32_t most, int type, int s, int hi, int keep, int top,
+                                        int lane) {
+  const int side = lane >> 4, g = tc_below_normal<PARTS>(type), bits = tc_code_bits(type), p = most >> 10 & 31u, q = most >> 26;
+  const bool sum = type_has_min(type);
+  int least = 0x7FFF, full = sum ? max(p + bits, q) + 1 : max(p, q) + bits;
+#pragma unroll 1
+  for (int i = lane & 15; i < words * (sum ? 1 : 2); i += 16) {
+    const int x = tc_lds16(hdr + i * (sum ? 4 : 2)) & 0x7FFF;
+    if (x) least = min(least, x);
+  }
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) {
+    least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
+    full = max(full, __shfl_xor_sync(0xffffffffu, full, o));
+  }
+  full = 29 - full;
+  const int lo = (least < 0x400 ? 10 : 1 - (least >> 10)) - g;
+  uint32_t wide = 0u;
+  if (s < lo) {
+    wide = lo > hi;
+    s = !wide ? max(lo, hi - 2 * side) : keep <= full && keep >= full - 4 ? keep : full - 2 * side;
+    if (s > top) {
+      s = top;
+      wide = 1u;
+    }
+  }
+  const uint32_t x = uint32_t(s + 512), k = __shfl_sync(0xffffffffu, x, 0), v = __shfl_sync(0xffffffffu, x, 16);
+  return k | v << 10 | __shfl_sync(0xffffffffu, wide, 0) << 20 | __shfl_sync(0xffffffffu, wide, 16) << 21;
 }
 template <int D, int TT>
 __device__ __noinline__ uint32_t tc_tail_max(uint32_t rows, int cnt, int lane) {  // (bit 31: not all are finite)
@@ -482,11 +600,19 @@ __device__ __noinline__ uint2 tc_not_finite(uint32_t k, uint32_t v, int kh, int 
   return bad;
 }
 
-// The scout: looks a tile's raw contents over when they have landed and notes its scales and the keys that are not finite.
+// The scout: looks a tile's raw contents over when they have landed and notes its scales and the keys that are not finite.  (Every
+// tile waits for it: both sides at once, by half a warp each, and what seldom runs out of line.)
 template <int D, int PARTS>
 __device__ void tc_scout(const ChunkArgs& a, const TcStage& L, uint32_t ring, TcSync* sy, int lane) {
   using C = TC<D, PARTS>;
-  int vs = 0, r = 0;
+  // A header's exponents are raised by `up`, a minimum's by `upm`: 6 less the largest is the scale (PARTS 1:
+  // scales below 2^-8, minima below 2^14; else all values below 2^15).
+  const int side = lane >> 4, sub = lane & 15, type = side ? a.c.v_type : a.c.k_type;
+  const bool sum = type_has_min(type);
+  const int up = PARTS == 1 ? 0 : tc_code_bits(type) - (sum ? 22 : 23), upm = sum ? -22 : up;
+  const int hoff = side ? L.vd : L.kd, hrow = side ? L.vh : L.kh, g = tc_below_normal<PARTS>(type);
+  const uint32_t only = sum ? 0x7FFF0000u : 0u;
+  int vs = 0, low = 0, r = 0;
   uint32_t phase = 0;
 #pragma unroll 1
   for (int ct = 0;; ++ct) {
@@ -495,40 +621,46 @@ __device__ void tc_scout(const ChunkArgs& a, const TcStage& L, uint32_t ring, Tc
     const int cnt = int(job.y);
     const uint32_t st = ring + r * L.bytes;
     const bool tail = int(job.z) >= 0;
-    int kscale = 120, vscale = 120;
-    bool odd = false;
-    if (cnt > 0) {
-#pragma unroll 1
-      for (int side = 0; side < 2; ++side) {
-        int e = 120;
-        if (!tail) {
-          const uint32_t hdr = st + (side ? L.vd : L.kd);
-          const int words = cnt * (side ? L.vh : L.kh) / 4;
-          uint32_t m = tc_header_max(hdr, words, lane);
-          uint32_t m0 = __reduce_max_sync(0xffffffffu, m & 0xFFFFu), m1 = __reduce_max_sync(0xffffffffu, m >> 16);
-          if (max(m0, m1) >= 0x7C00u) {
-            odd = true;
-            m = tc_header_max_finite(hdr, words, lane);
-            m0 = __reduce_max_sync(0xffffffffu, m & 0xFFFFu);
-            m1 = __reduce_max_sync(0xffffffffu, m >> 16);
-          }
-          e = tc_body_scale<PARTS>(side ? a.c.v_type : a.c.k_type, m0, m1);
-        } else {
-          const uint32_t mx = tc_tail_max<D, C::TT>(st + (side ? L.vt : 0), cnt, lane);
-          odd |= mx >> 31 != 0;
-          if (mx << 1) e = min(120, 15 - tc_exp(bf16_bits_to_f32(mx & 0x7FFFu)));
-        }
-        if (side) vscale = e; else kscale = e;
-      }
+    int ks, hi;  // the largest scales
+    bool odd;
+    TcHeads t{0u, 0x7C007C00u};
+    if (!tail) {
+      const int words = cnt * hrow / 4;
+      t = tc_heads(st + hoff, words, sub);
+      odd = __any_sync(0xffffffffu, (t.most & 0x7C00u) == 0x7C00u || t.most >= 0x7C000000u);
+      if (odd) t.most = tc_most_finite(st + hoff, words, sub);
+      const int e = max(int(t.most >> 10 & 31u) + up, int(t.most >> 26) + upm);
+      ks = 6 - __reduce_max_sync(0xffffffffu, side ? -64 : e);
+      hi = 6 - __reduce_max_sync(0xffffffffu, side ? e : -64);
+    } else {
+      const uint32_t k = tc_tail_max<D, C::TT>(st, cnt, lane), v = tc_tail_max<D, C::TT>(st + L.vt, cnt, lane);
+      odd = (k | v) >> 31;
+      ks = min(141 - int(k >> 7 & 255u), 100);
+      hi = min(141 - int(v >> 7 & 255u), 100);
     }
+    // Values keep the scale of the tile before where it serves, since O is rescaled where it changes.  Else they take one with
+    // some room for a larger tile.  It goes up as well as down, so that rows that see small values alone have their bits
+    // whatever else the segment holds, but not above kTcRise over its lowest: a sum of 2^20 products below 2^30,
+    // 2^kTcRise times that, is within fp32.
+    const int keep = vs;
+    if (job.w || vs > hi || vs < hi - 4) vs = job.w ? hi - 2 : min(hi - 2, low + kTcRise);
+    uint32_t wide = tail ? 7u : 0u;  // (sides that the quick conversion is not for; 4: bf16 rows)
+    const int scale = side ? vs : ks;
+    if (__any_sync(0xffffffffu, int(min(t.least & 0xFFFFu, (t.least | only) >> 16)) < max(1 - g - scale, 1) << 10)) {
+      const bool first = side == 0 || job.w;
+      const uint32_t x = tc_scales<PARTS>(st + hoff, cnt * hrow / 4, t.most, type, scale, side ? hi : ks, first ? 1000 : keep,
+                                          first ? 1000 : low + kTcRise, lane);
+      ks = int(x & 1023u) - 512;
+      vs = int(x >> 10 & 1023u) - 512;
+      wide = x >> 20;
+    }
+    low = job.w ? vs : min(low, vs);
     uint2 bad = make_uint2(0u, 0u);
     if (odd) bad = tc_not_finite<D, C::TK, C::TT>(st + (tail ? 0 : L.kd), st + (tail ? L.vt : L.vd), L.kh, L.vh, cnt, tail, lane);
-    // values: the smallest scale of the segment so far, with some room when it has to come down
-    if (job.w || vs > vscale) vs = vscale - 2;
     if (lane == 0) {
-      volatile TcMeta* m = &sy->meta[ct % kTcMeta];
-      m->t0 = int(job.x); m->cnt = cnt; m->ks = kscale; m->vs = vs;
-      m->bad[0] = bad.x; m->bad[1] = bad.y;
+      const uint32_t at = smem_u32(&sy->meta[ct % kTcMeta]);
+      tc_sts128(at, {job.x, job.y, uint32_t(ks), uint32_t(vs)});
+      tc_sts128(at + 16, {bad.x, bad.y, wide, 0u});
       mbar_arrive(&sy->mfull[r]);
     }
     if (cnt < 0) return;  // (the end)
@@ -553,7 +685,8 @@ __device__ void tc_convert(const ChunkArgs& a, const TcStage& L, uint32_t sb, Tc
     const uint4 mt = tc_lds128(smem_u32(&sy->meta[ct % kTcMeta]));
     const int cnt = int(mt.y);
     if (cnt < 0) return;
-    const bool tail = int(tc_lds32(smem_u32(&sy->job[r].z))) >= 0;
+    const uint32_t how = tc_lds32(smem_u32(&sy->meta[ct % kTcMeta].b.z));
+    const bool tail = how & 4u;
     const uint32_t st = sb + C::off_ring + r * L.bytes;
     if (ct >= C::NS && !tc_wait(&empty[b], turn)) return;
     x.scale = int(side ? mt.w : mt.z);
@@ -561,15 +694,11 @@ __device__ void tc_convert(const ChunkArgs& a, const TcStage& L, uint32_t sb, Tc
     x.hdr = st + (side ? L.vd : L.kd);
     x.qh = st + (side ? L.vqh : L.kqh);
     x.dst = sb + (side ? C::off_v : C::off_k) + b * C::slot;
+    if (how >> side & 1u) {
+      tc_slow_blocks<D, PARTS>(x, warp % W, W, cnt, tail, lane);
+    } else {
 #pragma unroll 1
-    for (int blk = warp % W; blk < NB; blk += W) {
-      if (!tail) {
-        tc_body_unit<D, PARTS>(x, lane, blk, cnt);
-      } else {
-#pragma unroll 1
-        for (int key = lane; key < C::TK; key += 32)  // (scores past the end are masked)
-          if (side == 1 || key - lane < cnt) tc_tail_unit<D, PARTS>(x.codes, x.dst, x.scale, key, blk, key < cnt);
-      }
+      for (int blk = warp % W; blk < NB; blk += W) tc_body_unit<D, PARTS>(x, lane, blk, cnt);
     }
     fence_proxy_async_smem();
     __syncwarp();
@@ -836,7 +965,6 @@ template <int D, int PARTS>
 __device__ void tc_softmax(const ChunkArgs& a, const ChunkHeader& h, uint8_t* sm, uint32_t tmem, TcSync* sy, int warp, int lane) {
   using C = TC<D, PARTS>;
   constexpr int TK = C::TK, NG = C::NG;
-  uint32_t* status = a.c.status;
   const int grp = NG == 2 ? warp / 4 : 0, line = (warp & 3) * 32 + lane;
   uint32_t used = 0;  // the group's tiles
   const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16);
@@ -984,14 +1112,15 @@ __device__ void tc_softmax(const ChunkArgs& a, const ChunkHeader& h, uint8_t* sm
       ok = __all_sync(0xffffffffu, ok);
       if (ok && busy) {
         tc::fence_after_sync();
-        const volatile TcMeta* mt = &sy->meta[ct % kTcMeta];
-        const int t0 = mt->t0, cnt = mt->cnt, nvs = mt->vs;
-        float f = tc_pow2(-mt->ks - qs);
-        const uint32_t bad0 = mt->bad[0], bad1 = mt->bad[1];
+        const uint32_t meta = smem_u32(&sy->meta[ct % kTcMeta]);
+        const uint4 mt = tc_lds128(meta);
+        const uint2 bad = tc_lds64(meta + 16);
+        const int t0 = int(mt.x), cnt = int(mt.y), nvs = int(mt.w);
+        float f = tc_pow2(-int(mt.z) - qs);
         const int lo = span.lo - t0, hi = min(span.hi - t0, cnt);
         const bool edge = __any_sync(0xffffffffu, lo > 0 || hi < TK), changed = mods || edge;
         const bool ahead = __any_sync(0xffffffffu, t0 + TK - 1 > span.pos);  // keys behind a row's own position
-        if (bad0 | bad1) nan |= tc_sees(bad0, bad1, lo, hi);
+        if (bad.x | bad.y) nan |= tc_sees(bad.x, bad.y, lo, hi);
         // scores that are capped, biased or masked: 16 columns at a time, back to TMEM, times f
         const uint32_t sc0 = lanes + C::scol + b * TK;
         float mt2 = -INFINITY;

@@ -571,8 +571,8 @@ typedef struct kvq_score_mod {
  * taken from the largest values.  bf16 outputs take them rounded once, by at most 2^-11 of
  * themselves or 2^-12 of the largest of their block of 32; fp16 and fp32 outputs as two parts
  * (22 bits), as should who wants more than bf16 shows.  That holds for each key and value, whatever
- * others are beside it: what is lost besides is 2^-34 of the largest within 64 tokens.  Sums
- * and softmax are fp32.
+ * others are beside it: what is lost besides is 2^-34 of the largest within 64 tokens.  A cap
+ * of any size adds 2^-20 of the capped score.  Sums and softmax are fp32.
  * The first call for a head_dim, output type and pair of formats asks the device for
  * its limits; make it before a stream capture.
  * workspace: device memory, 16-byte aligned, kvq_chunk_workspace_bytes bytes, not

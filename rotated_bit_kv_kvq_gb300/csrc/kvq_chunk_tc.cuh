@@ -954,33 +954,43 @@ __device__ __forceinline__ void tc_fwht_chunks(float (&v)[GC][8]) {
         }
 }
 
-// v f capped: c tanh(v f / c), i = 1 / c, off by 2^-20.8 of itself at most.  With y = v f / c it is v f p(y^2) where |y| is below
+// Scores in TMEM times f, capped: s = c tanh(s / c), off by 2^-20.8 of itself at most.  With y = s / c it is s p(y^2) where |y| is below
 // 0.447, p being 1 and a fit of the smallest largest error (2^-21.8) to tanh(y) / y - 1 on y^2 from 0 to 0.2: a cap far above
 // the scores changes none.  Further on it is c - 2 c / (1 + e^(2 y)), which for small y would lose the digits of s in those of
-// c; most tiles have no such score.  (That form alone: 32 sequences of one token, capped, 255 us for 280, 2 x 4096 prompt
-// rows with a cap 807 for 823.)
-__device__ __forceinline__ void tc_cap(float (&v)[16], float f, float c, float i) {
+// c; most tiles have no such score.  (Out of line, so that calls without a cap do not fetch it: mixed chunks in fp16 183 us
+// for 199, 2 x 4096 prompt rows with a cap 753 for 821, without one 511 for 479.)
+template <int TK>
+__device__ __noinline__ void tc_cap(uint32_t at, float f, float cap) {
+  at = __shfl_sync(0xffffffffu, at, 0);
+  const float c = cap * kChunkLog2e, i = fminf(1.0f / c, 3.4e38f);  // (no infinity: times a score of 0)
   const float fi = fminf(f * i, 3.4e38f), c1 = -0.33330584f * f, c2 = 0.13248634f * f, c3 = -0.046406726f * f;
-  float top = 0.0f;
+#pragma unroll 1
+  for (int c0 = 0; c0 < TK; c0 += 16) {
+    float v[16];
+    tc::ld_x16(at + c0, v);
+    tc::wait_ld();
+    float top = 0.0f;
 #pragma unroll
-  for (int k = 0; k < 16; ++k) top = fmaxf(top, fabsf(v[k]));
-  const bool far = __any_sync(0xffffffffu, top * fi > 0.447f);
-  if (!far) {
+    for (int k = 0; k < 16; ++k) top = fmaxf(top, fabsf(v[k]));
+    if (!__any_sync(0xffffffffu, top * fi > 0.447f)) {
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const float y = v[k] * fi, u = y * y;
-      v[k] *= fmaf(fmaf(fmaf(c3, u, c2), u, c1), u, f);
+      for (int k = 0; k < 16; ++k) {
+        const float y = v[k] * fi, u = y * y;
+        v[k] *= fmaf(fmaf(fmaf(c3, u, c2), u, c1), u, f);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const float y = v[k] * fi, u = y * y;
+        float r;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + ex2_approx(2.0f * kChunkLog2e * y)));
+        const float low = v[k] * fmaf(fmaf(fmaf(c3, u, c2), u, c1), u, f);
+        v[k] = u < 0.2f ? low : fmaf(-2.0f * c, r, c);
+      }
     }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const float y = v[k] * fi, u = y * y;
-      float r;
-      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + ex2_approx(2.0f * kChunkLog2e * y)));
-      const float low = v[k] * fmaf(fmaf(fmaf(c3, u, c2), u, c1), u, f);
-      v[k] = u < 0.2f ? low : fmaf(-2.0f * c, r, c);
-    }
+    tc::st_x16(at + c0, v);
   }
+  tc::wait_st();
 }
 
 // Whether one of the keys in bad0, bad1 (columns 0-31, 32-63) lies in [lo, hi)
@@ -1002,8 +1012,6 @@ __device__ void tc_softmax(const ChunkArgs& a, const ChunkHeader& h, uint8_t* sm
     named_sync(1, C::kSoft);
     tc::fence_after_sync();
   };
-  const bool mods = a.mod.softcap > 0.0f || a.mod.slopes != nullptr;
-  const float cap2 = a.mod.softcap * kChunkLog2e, icap = fminf(1.0f / cap2, 3.4e38f);  // (no infinity: times a score of 0)
   ChunkWalk walk;
   walk.begin(a, h, blockIdx.x);
   ChunkItem it;
@@ -1147,32 +1155,32 @@ __device__ void tc_softmax(const ChunkArgs& a, const ChunkHeader& h, uint8_t* sm
         const int t0 = int(mt.x), cnt = int(mt.y), nvs = int(mt.w);
         float f = tc_pow2(-int(mt.z) - qs);
         const int lo = span.lo - t0, hi = min(span.hi - t0, cnt);
-        const bool edge = __any_sync(0xffffffffu, lo > 0 || hi < TK), changed = mods || edge;
+        const bool edge = __any_sync(0xffffffffu, lo > 0 || hi < TK), changed = a.mod.slopes || edge;
         const bool ahead = __any_sync(0xffffffffu, t0 + TK - 1 > span.pos);  // keys behind a row's own position
         if (bad.x | bad.y) nan |= tc_sees(bad.x, bad.y, lo, hi);
-        // scores that are capped, biased or masked: 16 columns at a time, back to TMEM, times f
+        // scores that are biased or masked: 16 columns at a time, back to TMEM, times f
         const uint32_t sc0 = lanes + C::scol + b * TK;
         float mt2 = -INFINITY;
+        if (a.mod.softcap > 0.0f) {
+          tc_cap<TK>(sc0, f, a.mod.softcap);
+          f = 1.0f;
+        }
         if (changed) {
+          mt2 = -INFINITY;
 #pragma unroll 1
           for (int c0 = 0; c0 < TK; c0 += 16) {
             float sv[16];
             tc::ld_x16(sc0 + c0, sv);
             tc::wait_ld();
-            if (a.mod.softcap > 0.0f) {
-              tc_cap(sv, f, cap2, icap);
-            }
-            const bool capped = a.mod.softcap > 0.0f;
-            const float g = capped ? 1.0f : f;
             const float d0 = float(t0 + c0 - span.pos);  // (exact up to 2^24; beyond, a step of it is 2^-24 of the bias)
             if (a.mod.slopes && !ahead) {  // -slope |position - t| is linear
               const float b0 = slope2 * d0;
 #pragma unroll
-              for (int c = 0; c < 16; ++c) sv[c] = fmaf(sv[c], g, fmaf(slope2, float(c), b0));
+              for (int c = 0; c < 16; ++c) sv[c] = fmaf(sv[c], f, fmaf(slope2, float(c), b0));
             } else if (a.mod.slopes) {
 #pragma unroll
-              for (int c = 0; c < 16; ++c) sv[c] = fmaf(sv[c], g, -slope2 * fabsf(d0 + float(c)));
-            } else if (!capped) {
+              for (int c = 0; c < 16; ++c) sv[c] = fmaf(sv[c], f, -slope2 * fabsf(d0 + float(c)));
+            } else {
 #pragma unroll
               for (int c = 0; c < 16; ++c) sv[c] *= f;
             }

@@ -17,9 +17,9 @@
 
 namespace kvq {
 
-// (2: 513 us for 2 x 4096 prompt rows, 248 for 32 sequences of one token; 4: 502, 244; 8: 487, 246; 14: 492, 251)
+// (4: 530 us for 2 x 4096 prompt rows, 194 for 16 mixed sequences; 8: 513, 184; 14: 513, 184)
 constexpr int kChunkGap = 8;       // tiles
-constexpr int kChunkMinPiece = 2;  // tiles of the shortest piece (a call of 1,000 tokens: 1 17.4 us, 2 16.8, 3 17.7, 4 19.2, 8 25.0)
+constexpr int kChunkMinPiece = 2;  // tiles of the shortest piece (a call of 1,000 tokens: 1 16.4 us, 2 15.9, 4 18.4, 8 23.8)
 constexpr float kChunkLog2e = 1.4426950408889634f;
 
 struct ChunkItem {

@@ -84,7 +84,7 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uin
 }
 
 // The same three issued by one thread of a converged warp, with operands that the compiler can tell to be the same in every
-// lane (six instructions an mma; it loops over the lanes' values otherwise, thirty).
+// lane (chunk attention's issuers with them, and with more operand slots, 0.94 ms for 1.07 in its prompt case).
 __device__ __forceinline__ void mma_f16_warp(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
